@@ -1,0 +1,714 @@
+// Writing, reading back and committing rows of the paged key/value cache:
+// kv_append, qkv_norm_rope_append, kv_gather, kv_commit (include/qlin.h).
+//
+// All four move data; a pass reads and writes each byte once and the memory
+// system is the bound.  A wave handles one head of four consecutive tokens,
+// 16 lanes to a row of D elements (D / 16 each).  Four tokens are what the
+// cache's V order keeps side by side: when their slots are one aligned
+// quad of a page -- every quad of a prompt that starts on one -- the wave
+// transposes its 4 x 4 units between the four rows and stores whole dwords;
+// otherwise each lane stores its elements one by one.
+#include "kv_cache.hpp"
+
+namespace qlin {
+namespace {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4;   // waves per block
+
+// --------------------------------------------------------------------------
+// 16-lane row reductions (DPP: xor 1, xor 2, mirrors of 8 and 16)
+// --------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF,
+                                                            0xF, true));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  v += dpp<0x141>(v);
+  v += dpp<0x140>(v);
+  return v;
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = __builtin_fmaxf(v, dpp<0xB1>(v));
+  v = __builtin_fmaxf(v, dpp<0x4E>(v));
+  v = __builtin_fmaxf(v, dpp<0x141>(v));
+  v = __builtin_fmaxf(v, dpp<0x140>(v));
+  return v;
+}
+
+// --------------------------------------------------------------------------
+// 4 x 4 transposes between the four rows of a wave (lanes 16 apart).  Both
+// are their own inverse.
+// --------------------------------------------------------------------------
+// Byte k of the result is byte j of row k's word; j is this lane's row.
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int j) {
+  const uint32_t a = __shfl_xor(w, 16, 64), b = __shfl_xor(w, 32, 64), c = __shfl_xor(w, 48, 64);
+  const uint32_t sel = 0x0C0C0000u | (j & 1 ? uint32_t(j | (4 + j) << 8) : uint32_t(4 + j | j << 8));
+  const uint32_t near = __builtin_amdgcn_perm(w, a, sel);   // rows j & ~1, j | 1
+  const uint32_t far = __builtin_amdgcn_perm(b, c, sel);
+  return j & 2 ? far | near << 16 : near | far << 16;
+}
+// Half k of the result (two words) is half j of row k's two words.
+__device__ __forceinline__ uint2 transpose_halves(uint32_t w0, uint32_t w1, int j) {
+  const uint32_t mine = j & 2 ? w1 : w0, other = j & 2 ? w0 : w1;
+  const uint32_t a = __shfl_xor(mine, 16, 64), b = __shfl_xor(other, 32, 64),
+                 c = __shfl_xor(other, 48, 64);
+  const uint32_t sel = j & 1 ? 0x07060302u : 0x01000504u;
+  const uint32_t near = __builtin_amdgcn_perm(mine, a, sel), far = __builtin_amdgcn_perm(b, c, sel);
+  return j & 2 ? make_uint2(far, near) : make_uint2(near, far);
+}
+
+// --------------------------------------------------------------------------
+// Rows in registers
+// --------------------------------------------------------------------------
+template <int N>
+__device__ __forceinline__ void load_row(const void* base, int64_t off, bool f32, float (&x)[N]) {
+  if (f32) {
+    const float* p = static_cast<const float*>(base) + off;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + i);
+      x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + off;
+    uint32_t w[N / 2];
+    if constexpr (N == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    *static_cast<uint32_t*>(p) = w[0];
+  } else if constexpr (N == 2) {
+    *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      static_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void store_row_bf16(void* base, int64_t off, const float (&x)[N]) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+  store_words(static_cast<uint16_t*>(base) + off, w);
+}
+
+// What a lane holds of an encoded row: `w` the row's bytes in order (16-bit
+// elements, 8-bit codes, or pairs of 4-bit codes), the E4M3 scale of the
+// group its elements lie in, and the row's stored exponent.
+template <int FMT, int D>
+struct EncRow {
+  static constexpr int N = D / 16;                                      // elements per lane
+  static constexpr int kBytes = KvLayout<FMT, D>::kRow / 16;            // of the row per lane
+  static constexpr int kWords = (kBytes + 3) / 4;
+  uint32_t w[kWords];
+  uint32_t scale, exp;
+};
+
+// Row exponent for a row of maximum amax (a bit pattern of a non-negative
+// float): the smallest e with amax <= Q 2^e, Q = 448 = 1.75 * 2^8 or
+// 2688 = 1.3125 * 2^11, as e + 127.
+template <int FMT>
+__device__ __forceinline__ uint32_t row_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax), m = u & 0x7FFFFFu;
+  constexpr int shift = FMT == QL_KV_E4M3 ? 8 : 11;
+  constexpr uint32_t top = FMT == QL_KV_E4M3 ? 0x600000u : 0x280000u;
+  const int b = int(u >> 23) - shift + (m > top ? 1 : 0);
+  return u == 0 ? 127u : uint32_t(b < kKvExpMin ? kKvExpMin : b);
+}
+
+// Encodes this lane's N elements of a row held by 16 lanes.  An infinity
+// saturates; a NaN stays one (8-bit: its own code; 4-bit: its group's scale).
+template <int FMT, int D>
+__device__ __forceinline__ EncRow<FMT, D> encode_row(const float (&x)[D / 16]) {
+  constexpr int N = D / 16;
+  EncRow<FMT, D> r;
+  r.scale = 0;
+  if constexpr (FMT == QL_KV_BF16) {
+    r.exp = 0;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) r.w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    return r;
+  } else {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) a = __builtin_fmaxf(a, __builtin_fabsf(x[i]));
+    const float amax = row_max(a);
+    r.exp = row_exponent<FMT>(amax);
+    const float p = __uint_as_float((254u - r.exp) << 23);   // 2^-e
+    float y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = x[i] * p;
+    if constexpr (FMT == QL_KV_E4M3) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = y[i] > 448.0f ? 448.0f : y[i] < -448.0f ? -448.0f : y[i];
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
+        r.w[i] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], v, true));
+      }
+    } else {
+      // group maximum over 16 elements: 16 / N lanes
+      float g = a;
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < N; ++i) nan |= x[i] != x[i];
+      float bad = nan ? 1.0f : 0.0f;
+      if constexpr (N < 16) {
+        g = __builtin_fmaxf(g, dpp<0xB1>(g));
+        bad = __builtin_fmaxf(bad, dpp<0xB1>(bad));
+      }
+      if constexpr (N < 8) {
+        g = __builtin_fmaxf(g, dpp<0x4E>(g));
+        bad = __builtin_fmaxf(bad, dpp<0x4E>(bad));
+      }
+      const float q = __builtin_fminf(g * p / 6.0f, 448.0f);
+      const uint32_t sc = __builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false) & 0xFFu;
+      const float sv = __builtin_amdgcn_cvt_f32_fp8(int(sc), 0);
+      const float inv = sv > 0.0f ? 1.0f / sv : 0.0f;
+      r.scale = bad > 0.0f ? 0x7Fu : sc;
+#pragma unroll
+      for (int i = 0; i < EncRow<FMT, D>::kWords; ++i) {
+        uint32_t v = 0;
+        v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i] * inv, y[8 * i + 1] * inv, 1.0f, 0);
+        v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i + 2] * inv, y[8 * i + 3] * inv, 1.0f, 1);
+        if constexpr (N > 4) {
+          v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i + 4] * inv, y[8 * i + 5] * inv, 1.0f, 2);
+          v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i + 6] * inv, y[8 * i + 7] * inv, 1.0f, 3);
+        }
+        r.w[i] = v;
+      }
+    }
+    return r;
+  }
+}
+
+// Where a token's row lies: the block's codes and scales, and the token in it.
+struct Place {
+  uint8_t* codes;
+  uint8_t* scales;
+  int t;
+};
+template <int FMT, int D>
+__device__ __forceinline__ Place place_of(const KvGeom& g, int64_t slot, int head) {
+  using L = KvLayout<FMT, D>;
+  const int64_t page = slot >> g.page_shift;
+  const int in = int(slot & ((int64_t(1) << g.page_shift) - 1));
+  const int64_t block = kv_block(g, page, head, in >> 4);
+  return {g.codes + block * L::kCodes, g.scales + block * L::kScales, in & 15};
+}
+__device__ __forceinline__ bool slot_ok(const KvGeom& g, int64_t slot) {
+  return slot >= 0 && (slot >> g.page_shift) < g.n_pages;
+}
+
+// Whether the wave's four tokens are one aligned quad of the cache; the same
+// in every lane (all lanes must call).
+__device__ __forceinline__ bool whole_quad(int64_t slot, bool ok, int j) {
+  const int64_t first = __shfl(slot, 0, 64);
+  return __all(ok && slot == first + j && (first & 3) == 0);
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void store_k(const Place& p, int i, const EncRow<FMT, D>& r) {
+  using L = KvLayout<FMT, D>;
+  using E = EncRow<FMT, D>;
+  if constexpr (E::kBytes == 2) {
+    *reinterpret_cast<uint16_t*>(p.codes + L::k_code(p.t, 2 * i)) = uint16_t(r.w[0]);
+  } else if constexpr (E::kBytes <= 16) {
+    store_words(p.codes + L::k_code(p.t, E::kBytes * i), r.w);
+  } else {
+#pragma unroll
+    for (int c = 0; c < E::kBytes / 16; ++c)
+      *reinterpret_cast<uint4*>(p.codes + L::k_code(p.t, E::kBytes * i + 16 * c)) =
+          make_uint4(r.w[4 * c], r.w[4 * c + 1], r.w[4 * c + 2], r.w[4 * c + 3]);
+  }
+  if constexpr (FMT == QL_KV_NVFP4) {
+    constexpr int lanes = 16 / E::N;   // lanes of a group
+    if (i % lanes == 0) p.scales[L::k_scale(p.t, i / lanes)] = uint8_t(r.scale);
+  }
+  if constexpr (FMT != QL_KV_BF16) {
+    if (i == 0) p.scales[L::k_exp(p.t)] = uint8_t(r.exp);
+  }
+}
+
+// `quad`: the wave's rows are one aligned quad (all lanes active then);
+// `ok`: this lane's row is stored.
+template <int FMT, int D>
+__device__ __forceinline__ void store_v(const Place& p, int i, int j, bool quad, bool ok,
+                                        const EncRow<FMT, D>& r) {
+  using L = KvLayout<FMT, D>;
+  using E = EncRow<FMT, D>;
+  if (quad) {
+    const int t0 = p.t & ~3;
+    if constexpr (FMT == QL_KV_BF16) {
+#pragma unroll
+      for (int w = 0; w < E::kWords / 2; ++w) {
+        const uint2 v = transpose_halves(r.w[2 * w], r.w[2 * w + 1], j);
+        *reinterpret_cast<uint2*>(p.codes + L::v_code(t0, E::N * i + 4 * w + j)) = v;
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < E::kWords; ++w) {
+        const uint32_t v = transpose_bytes(r.w[w], j);
+        if (E::kBytes >= 4 || j < E::kBytes)
+          *reinterpret_cast<uint32_t*>(p.codes + L::v_code(t0, E::kBytes * i + 4 * w + j)) = v;
+      }
+    }
+  } else if (ok) {
+    if constexpr (FMT == QL_KV_BF16) {
+#pragma unroll
+      for (int u = 0; u < E::N; ++u)
+        *reinterpret_cast<uint16_t*>(p.codes + L::v_code(p.t, E::N * i + u)) =
+            uint16_t(r.w[u / 2] >> (16 * (u & 1)));
+    } else {
+#pragma unroll
+      for (int u = 0; u < E::kBytes; ++u)
+        p.codes[L::v_code(p.t, E::kBytes * i + u)] = uint8_t(r.w[u / 4] >> (8 * (u & 3)));
+    }
+  }
+  if (!ok) return;
+  if constexpr (FMT == QL_KV_NVFP4) {
+    constexpr int lanes = 16 / E::N;
+    if (i % lanes == 0) p.scales[L::v_scale(p.t, i / lanes)] = uint8_t(r.scale);
+  }
+  if constexpr (FMT != QL_KV_BF16) {
+    if (i == 0) p.scales[L::v_exp(p.t)] = uint8_t(r.exp);
+  }
+}
+
+// --------------------------------------------------------------------------
+// kv_append
+// --------------------------------------------------------------------------
+template <int FMT, int D>
+__global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(
+    KvGeom g, const void* k, const void* v, bool f32, int64_t tokens, int64_t k_stride,
+    int64_t v_stride, const int64_t* slots) {
+  constexpr int N = D / 16;
+  const int lane = threadIdx.x & 63, i = lane & 15, j = lane >> 4;
+  const int item = int(blockIdx.y) * kWaves + int(threadIdx.x >> 6);   // K heads, then V heads
+  if (item >= 2 * g.n_kv) return;
+  const bool is_v = item >= g.n_kv;
+  const int head = is_v ? item - g.n_kv : item;
+  const int64_t token = int64_t(blockIdx.x) * 4 + j;
+  const int64_t slot = token < tokens ? slots[token] : -1;
+  const bool ok = slot_ok(g, slot);
+  float x[N] = {};
+  if (ok) load_row(is_v ? v : k, token * (is_v ? v_stride : k_stride) + head * D + i * N, f32, x);
+  const EncRow<FMT, D> r = encode_row<FMT, D>(x);
+  const Place p = place_of<FMT, D>(g, ok ? slot : 0, head);
+  if (is_v) {
+    store_v<FMT, D>(p, i, j, whole_quad(slot, ok, j), ok, r);
+  } else if (ok) {
+    store_k<FMT, D>(p, i, r);
+  }
+}
+
+// --------------------------------------------------------------------------
+// qkv_norm_rope_append
+// --------------------------------------------------------------------------
+struct NormArgs {
+  KvGeom g;
+  const void* qkv;
+  bool f32;
+  bool interleaved;
+  int64_t tokens;
+  int64_t row_stride;
+  int n_q;
+  int heads_per_wave;
+  const float* q_weight;
+  const float* k_weight;
+  float eps;
+  const int32_t* positions;
+  const float* rope;
+  int64_t max_pos;
+  int rot;
+  void* q_out;
+  const int64_t* slots;
+};
+
+template <int FMT, int D>
+__global__ __launch_bounds__(64 * kWaves) void qkv_norm_rope_append_kernel(NormArgs a) {
+  constexpr int N = D / 16;
+  // each wave's four rows, for the partner elements of half-split rotation
+  __shared__ float4 rows[kWaves][4][D / 4];
+  const int lane = threadIdx.x & 63, i = lane & 15, j = lane >> 4, wave = threadIdx.x >> 6;
+  const int64_t token = int64_t(blockIdx.x) * 4 + j;
+  const bool in = token < a.tokens;
+  const int64_t slot = in ? a.slots[token] : -1;
+  const bool ok = slot_ok(a.g, slot);
+  const bool quad = whole_quad(slot, ok, j);
+  const int heads = a.n_q + 2 * a.g.n_kv;
+  const int half = a.rot >> 1;
+
+  // element d of a row turns with partner pd: x[d] c[d] + x[pd] s[d]
+  float c[N], s[N];
+  {
+    int64_t pos = in ? a.positions[token] : 0;
+    pos = pos < 0 ? 0 : pos >= a.max_pos ? a.max_pos - 1 : pos;
+    const float* t = a.rope + pos * a.rot;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int d = i * N + u;
+      c[u] = 1.0f, s[u] = 0.0f;
+      if (d < a.rot) {
+        const int at = a.interleaved ? d >> 1 : d < half ? d : d - half;
+        const bool first = a.interleaved ? (d & 1) == 0 : d < half;
+        c[u] = t[at];
+        const float v = t[half + at];
+        s[u] = first ? -v : v;
+      }
+    }
+  }
+
+  const int first = (int(blockIdx.y) * kWaves + wave) * a.heads_per_wave;
+  for (int h = first; h < first + a.heads_per_wave && h < heads; ++h) {
+    float x[N] = {};
+    if (in) load_row(a.qkv, token * a.row_stride + int64_t(h) * D + i * N, a.f32, x);
+    const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.g.n_kv;
+    if (!is_v) {
+      const float* weight = is_q ? a.q_weight : a.k_weight;
+      if (weight) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < N; ++u) sum = __builtin_fmaf(x[u], x[u], sum);
+        const float r = 1.0f / __builtin_sqrtf(row_sum(sum) * (1.0f / D) + a.eps);
+#pragma unroll
+        for (int u = 0; u < N; ++u) x[u] = x[u] * r * weight[i * N + u];
+      }
+      if (a.rot) {
+        float partner[N];
+        if (a.interleaved) {
+#pragma unroll
+          for (int u = 0; u < N; ++u) partner[u] = x[u ^ 1];
+        } else {
+          // the wave's own rows: its LDS accesses run in order, the fences
+          // keep the compiler from moving them past each other
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int u = 0; u < N; u += 4)
+            rows[wave][j][(i * N + u) / 4] = make_float4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+          const float* row = reinterpret_cast<const float*>(rows[wave][j]);
+#pragma unroll
+          for (int u = 0; u < N; ++u) {
+            const int d = i * N + u;
+            partner[u] = row[d < half ? d + half : d < a.rot ? d - half : d];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u) x[u] = __builtin_fmaf(partner[u], s[u], x[u] * c[u]);
+      }
+    }
+    if (is_q) {
+      if (in) store_row_bf16(a.q_out, (token * a.n_q + h) * D + i * N, x);
+    } else {
+      const EncRow<FMT, D> r = encode_row<FMT, D>(x);
+      const Place p = place_of<FMT, D>(a.g, ok ? slot : 0, is_v ? h - a.n_q - a.g.n_kv : h - a.n_q);
+      if (is_v) {
+        store_v<FMT, D>(p, i, j, quad, ok, r);
+      } else if (ok) {
+        store_k<FMT, D>(p, i, r);
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------------------
+// kv_gather
+// --------------------------------------------------------------------------
+template <int FMT, int D>
+__device__ __forceinline__ void decode_row(const EncRow<FMT, D>& r, float (&x)[D / 16]) {
+  constexpr int N = D / 16;
+  if constexpr (FMT == QL_KV_BF16) {
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      x[u] = __uint_as_float(u & 1 ? r.w[u / 2] & 0xFFFF0000u : r.w[u / 2] << 16);
+  } else {
+    const float p = __uint_as_float(r.exp << 23);
+    if constexpr (FMT == QL_KV_E4M3) {
+#pragma unroll
+      for (int u = 0; u < N; u += 2) {
+        const f32x2 v = u & 2 ? __builtin_amdgcn_cvt_pk_f32_fp8(int(r.w[u / 4]), true)
+                              : __builtin_amdgcn_cvt_pk_f32_fp8(int(r.w[u / 4]), false);
+        x[u] = v[0] * p, x[u + 1] = v[1] * p;
+      }
+    } else {
+      const float sv = __builtin_amdgcn_cvt_f32_fp8(int(r.scale), 0);
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        f32x2 v;
+        switch (i & 3) {
+          case 0: v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r.w[i / 4], 1.0f, 0); break;
+          case 1: v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r.w[i / 4], 1.0f, 1); break;
+          case 2: v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r.w[i / 4], 1.0f, 2); break;
+          default: v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r.w[i / 4], 1.0f, 3); break;
+        }
+        x[2 * i] = v[0] * sv * p, x[2 * i + 1] = v[1] * sv * p;
+      }
+    }
+  }
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void load_k(const Place& p, int i, EncRow<FMT, D>& r) {
+  using L = KvLayout<FMT, D>;
+  using E = EncRow<FMT, D>;
+  if constexpr (E::kBytes == 2) {
+    r.w[0] = *reinterpret_cast<const uint16_t*>(p.codes + L::k_code(p.t, 2 * i));
+  } else {
+    constexpr int piece = E::kBytes < 16 ? E::kBytes : 16;
+#pragma unroll
+    for (int c = 0; c < E::kBytes / piece; ++c) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(
+          p.codes + L::k_code(p.t, E::kBytes * i + piece * c));
+#pragma unroll
+      for (int w = 0; w < piece / 4; ++w) r.w[c * (piece / 4) + w] = q[w];
+    }
+  }
+  if constexpr (FMT == QL_KV_NVFP4) r.scale = p.scales[L::k_scale(p.t, i * E::N / 16)];
+  if constexpr (FMT != QL_KV_BF16) r.exp = p.scales[L::k_exp(p.t)];
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void load_v(const Place& p, int i, int j, bool quad, bool ok,
+                                       EncRow<FMT, D>& r) {
+  using L = KvLayout<FMT, D>;
+  using E = EncRow<FMT, D>;
+  if (quad) {
+    const int t0 = p.t & ~3;
+    if constexpr (FMT == QL_KV_BF16) {
+#pragma unroll
+      for (int w = 0; w < E::kWords / 2; ++w) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p.codes + L::v_code(t0, E::N * i + 4 * w + j));
+        const uint2 o = transpose_halves(v.x, v.y, j);
+        r.w[2 * w] = o.x, r.w[2 * w + 1] = o.y;
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < E::kWords; ++w) {
+        uint32_t v = 0;
+        if (E::kBytes >= 4 || j < E::kBytes)
+          v = *reinterpret_cast<const uint32_t*>(p.codes + L::v_code(t0, E::kBytes * i + 4 * w + j));
+        r.w[w] = transpose_bytes(v, j);
+      }
+    }
+  } else if (ok) {
+#pragma unroll
+    for (int w = 0; w < E::kWords; ++w) r.w[w] = 0;
+    if constexpr (FMT == QL_KV_BF16) {
+#pragma unroll
+      for (int u = 0; u < E::N; ++u)
+        r.w[u / 2] |= uint32_t(*reinterpret_cast<const uint16_t*>(
+                          p.codes + L::v_code(p.t, E::N * i + u))) << (16 * (u & 1));
+    } else {
+#pragma unroll
+      for (int u = 0; u < E::kBytes; ++u)
+        r.w[u / 4] |= uint32_t(p.codes[L::v_code(p.t, E::kBytes * i + u)]) << (8 * (u & 3));
+    }
+  }
+  if (!ok) return;
+  if constexpr (FMT == QL_KV_NVFP4) r.scale = p.scales[L::v_scale(p.t, i * E::N / 16)];
+  if constexpr (FMT != QL_KV_BF16) r.exp = p.scales[L::v_exp(p.t)];
+}
+
+template <int FMT, int D>
+__global__ __launch_bounds__(64 * kWaves) void kv_gather_kernel(KvGeom g, const int64_t* slots,
+                                                                int64_t tokens, void* k, void* v,
+                                                                bool f32) {
+  constexpr int N = D / 16;
+  const int lane = threadIdx.x & 63, i = lane & 15, j = lane >> 4;
+  const int item = int(blockIdx.y) * kWaves + int(threadIdx.x >> 6);
+  if (item >= 2 * g.n_kv) return;
+  const bool is_v = item >= g.n_kv;
+  const int head = is_v ? item - g.n_kv : item;
+  const int64_t token = int64_t(blockIdx.x) * 4 + j;
+  const int64_t slot = token < tokens ? slots[token] : -1;
+  const bool ok = slot_ok(g, slot);
+  const Place p = place_of<FMT, D>(g, ok ? slot : 0, head);
+  EncRow<FMT, D> r = {};
+  if (is_v) {
+    load_v<FMT, D>(p, i, j, whole_quad(slot, ok, j), ok, r);
+  } else if (ok) {
+    load_k<FMT, D>(p, i, r);
+  }
+  float x[N] = {};
+  if (ok) decode_row<FMT, D>(r, x);
+  if (token >= tokens) return;
+  void* out = is_v ? v : k;
+  const int64_t off = (token * g.n_kv + head) * D + i * N;
+  if (f32) {
+    float* o = static_cast<float*>(out) + off;
+#pragma unroll
+    for (int u = 0; u < N; u += 4)
+      *reinterpret_cast<float4*>(o + u) = make_float4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+  } else {
+    store_row_bf16(out, off, x);
+  }
+}
+
+// --------------------------------------------------------------------------
+// kv_commit: one block per sequence, kv head and half (K or V).  Source and
+// target rows of a sequence overlap, so every row is read into LDS before
+// the first is written.
+// --------------------------------------------------------------------------
+constexpr int kMaxPath = 64;
+
+template <int FMT, int D>
+__global__ __launch_bounds__(256) void kv_commit_kernel(KvGeom g, const int32_t* cu_q,
+                                                        const int32_t* kv_lens,
+                                                        const int32_t* table, int64_t table_stride,
+                                                        int64_t table_cols, const int32_t* path,
+                                                        int max_path) {
+  using L = KvLayout<FMT, D>;
+  constexpr int kGroups = FMT == QL_KV_NVFP4 ? D / 16 : 0;
+  constexpr int kUnit = FMT == QL_KV_BF16 ? 2 : 1;     // bytes that stay together in V
+  __shared__ __align__(16) uint8_t codes[kMaxPath][L::kRow];
+  __shared__ uint8_t scales[kMaxPath][kGroups + 1];
+  __shared__ int64_t from[kMaxPath], to[kMaxPath];
+  const int head = blockIdx.x, tid = threadIdx.x;
+  const bool is_v = blockIdx.y != 0;
+  const int64_t b = blockIdx.z;
+  const int64_t nodes = cu_q[b + 1] - cu_q[b], len = kv_lens[b];
+  const int64_t ctx = len > nodes ? len - nodes : 0;
+  if (tid < max_path) {
+    auto slot_at = [&](int64_t pos) -> int64_t {
+      const int64_t col = pos >> g.page_shift;
+      if (col >= table_cols) return -1;
+      const int64_t page = table[b * table_stride + col];
+      if (page < 0 || page >= g.n_pages) return -1;
+      return (page << g.page_shift) + (pos & ((int64_t(1) << g.page_shift) - 1));
+    };
+    const int64_t node = path[b * max_path + tid];
+    int64_t s = -1, d = -1;
+    if (node >= 0 && node < nodes && ctx + node < len && node != tid && ctx + tid < len) {
+      s = slot_at(ctx + node);
+      d = slot_at(ctx + tid);
+    }
+    const bool both = s >= 0 && d >= 0;
+    from[tid] = both ? s : -1;
+    to[tid] = both ? d : -1;
+  }
+  __syncthreads();
+
+  auto rows = [&](const int64_t* slots, auto&& move) {
+    if (!is_v) {
+      constexpr int chunks = L::kRow / L::kLoad;
+      for (int u = tid; u < max_path * chunks; u += 256) {
+        const int n = u / chunks, c = u % chunks;
+        if (slots[n] < 0) continue;
+        const Place p = place_of<FMT, D>(g, slots[n], head);
+        if constexpr (L::kLoad == 16)
+          move(reinterpret_cast<uint4*>(p.codes + L::k_code(p.t, 16 * c)),
+               reinterpret_cast<uint4*>(codes[n] + 16 * c));
+        else
+          move(reinterpret_cast<uint2*>(p.codes + L::k_code(p.t, 8 * c)),
+               reinterpret_cast<uint2*>(codes[n] + 8 * c));
+      }
+    } else {
+      constexpr int units = L::kRow / kUnit;
+      for (int u = tid; u < max_path * units; u += 256) {
+        const int n = u / units, c = u % units;
+        if (slots[n] < 0) continue;
+        const Place p = place_of<FMT, D>(g, slots[n], head);
+        if constexpr (kUnit == 2)
+          move(reinterpret_cast<uint16_t*>(p.codes + L::v_code(p.t, c)),
+               reinterpret_cast<uint16_t*>(codes[n] + 2 * c));
+        else
+          move(p.codes + L::v_code(p.t, c), codes[n] + c);
+      }
+    }
+    if constexpr (FMT != QL_KV_BF16) {
+      for (int u = tid; u < max_path * (kGroups + 1); u += 256) {
+        const int n = u / (kGroups + 1), c = u % (kGroups + 1);
+        if (slots[n] < 0) continue;
+        const Place p = place_of<FMT, D>(g, slots[n], head);
+        const int off = c == kGroups ? (is_v ? L::v_exp(p.t) : L::k_exp(p.t))
+                                     : (is_v ? L::v_scale(p.t, c) : L::k_scale(p.t, c));
+        move(p.scales + off, &scales[n][c]);
+      }
+    }
+  };
+  rows(from, [](auto* cache, auto* lds) { *lds = *cache; });
+  __syncthreads();
+  rows(to, [](auto* cache, auto* lds) { *cache = *lds; });
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvGeom& g, int fmt, int d, const void* k, const void* v,
+                            int x_dtype, int64_t tokens, int64_t k_stride, int64_t v_stride,
+                            const int64_t* slots, hipStream_t s) {
+  const dim3 grid(unsigned((tokens + 3) / 4), unsigned((2 * g.n_kv + kWaves - 1) / kWaves));
+  return kv_dispatch(fmt, d, [&](auto f, auto n) {
+    kv_append_kernel<decltype(f)::value, decltype(n)::value><<<grid, 64 * kWaves, 0, s>>>(
+        g, k, v, x_dtype == QL_F32, tokens, k_stride, v_stride, slots);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_qkv_norm_rope_append(const KvGeom& g, int fmt, int d, const void* qkv,
+                                       int x_dtype, int64_t tokens, int64_t row_stride, int n_q,
+                                       const float* q_weight, const float* k_weight, float eps,
+                                       const int32_t* positions, const float* rope,
+                                       int64_t max_pos, int rot, bool interleaved, void* q_out,
+                                       const int64_t* slots, hipStream_t s) {
+  const int heads = n_q + 2 * g.n_kv;
+  const int hpw = 1;
+  const NormArgs a{g, qkv, x_dtype == QL_F32, interleaved, tokens, row_stride, n_q, hpw, q_weight,
+                   k_weight, eps, positions, rope, max_pos, rot, q_out, slots};
+  const dim3 grid(unsigned((tokens + 3) / 4), unsigned((heads + kWaves * hpw - 1) / (kWaves * hpw)));
+  return kv_dispatch(fmt, d, [&](auto f, auto n) {
+    qkv_norm_rope_append_kernel<decltype(f)::value, decltype(n)::value>
+        <<<grid, 64 * kWaves, 0, s>>>(a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_kv_gather(const KvGeom& g, int fmt, int d, const int64_t* slots, int64_t tokens,
+                            void* k, void* v, int y_dtype, hipStream_t s) {
+  const dim3 grid(unsigned((tokens + 3) / 4), unsigned((2 * g.n_kv + kWaves - 1) / kWaves));
+  return kv_dispatch(fmt, d, [&](auto f, auto n) {
+    kv_gather_kernel<decltype(f)::value, decltype(n)::value><<<grid, 64 * kWaves, 0, s>>>(
+        g, slots, tokens, k, v, y_dtype == QL_F32);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_kv_commit(const KvGeom& g, int fmt, int d, int64_t n_seqs, const int32_t* cu_q,
+                            const int32_t* kv_lens, const int32_t* table, int64_t table_stride,
+                            int64_t table_cols, const int32_t* path, int max_path, hipStream_t s) {
+  const dim3 grid(unsigned(g.n_kv), 2, unsigned(n_seqs));
+  return kv_dispatch(fmt, d, [&](auto f, auto n) {
+    kv_commit_kernel<decltype(f)::value, decltype(n)::value><<<grid, 256, 0, s>>>(
+        g, cu_q, kv_lens, table, table_stride, table_cols, path, max_path);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace qlin

@@ -26,6 +26,8 @@ QL_OK, QL_EINVAL, QL_ESHAPE, QL_EALIGN, QL_EDTYPE, QL_EWORKSPACE, QL_EHIP, QL_EF
 QL_F32, QL_BF16 = 0, 1
 QL_NVFP4, QL_INT4_G128, QL_LUT2, QL_INT4_SP24 = 0, 1, 2, 3
 QL_STATIC_SCALE = 1
+QL_KV_BF16, QL_KV_E4M3, QL_KV_NVFP4 = 0, 1, 2
+QL_ROPE_INTERLEAVED = 1
 
 _vp, _i64, _sz, _int, _uint = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint
 
@@ -56,6 +58,15 @@ _SIGS = {
     "quantize_gemm_w4a4": (_int, [_vp, _i64, _i64, _vp, _uint, _vp, _i64, _vp, _int, _vp, _sz,
                                   _vp]),
     "gemm_w4a16_sp24_ws": (_int, [_vp, _vp, _i64, _i64, _i64, _vp, _int, _vp, _sz, _vp]),
+    "kv_cache_bytes": (_sz, [_int, _i64, _i64, _i64, _i64]),
+    "kv_append": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp]),
+    "kv_gather": (_int, [_vp, _vp, _i64, _vp, _vp, _int, _vp]),
+    "qkv_norm_rope_append": (_int, [_vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, ctypes.c_float,
+                                    _vp, _vp, _i64, _i64, _uint, _vp, _vp, _vp]),
+    "kv_attention_workspace": (_sz, [_vp, _i64, _i64, _i64, _i64, _i64]),
+    "kv_attention": (_int, [_vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64,
+                            _i64, _vp, ctypes.c_float, _vp, _vp, _sz, _vp]),
+    "kv_commit": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -418,6 +429,242 @@ def gemm_w4a16_sp24(x, w_packed, n, k, y=None, out_dtype=torch.bfloat16, stream=
     workspace: as gemm_w4a16 (gemm_w4a16_sp24_workspace / gemm_w4a16_sp24_ws)."""
     return _decode("gemm_w4a16_sp24", QL_INT4_SP24, x, w_packed, n, k, y, out_dtype, stream,
                    workspace)
+
+
+# ---------------------------------------------------------------------------
+# Paged key/value cache (include/qlin.h describes formats and layout)
+# ---------------------------------------------------------------------------
+
+class _KVStruct(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("n_kv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", _i64), ("data", _vp), ("bytes", _sz)]
+
+
+def kv_cache_bytes(fmt, n_pages, page_size, n_kv, head_dim):
+    """Bytes of a cache; 0 for sizes or a format that are not supported."""
+    return _lib.kv_cache_bytes(fmt, n_pages, page_size, n_kv, head_dim)
+
+
+class KVCache:
+    """One layer's paged cache of keys and values: a uint8 GPU tensor ``data``
+    and what it holds.  fmt: QL_KV_BF16, QL_KV_E4M3 or QL_KV_NVFP4; page_size a
+    power of two of 16..4096; head_dim 64, 128 or 256.  ``data`` is allocated
+    when not given and needs no initialisation."""
+
+    def __init__(self, fmt, n_pages, page_size, n_kv, head_dim, data=None, device=None):
+        nbytes = _lib.kv_cache_bytes(fmt, n_pages, page_size, n_kv, head_dim)
+        if nbytes == 0:
+            raise ValueError(f"no cache of format {fmt}: {n_pages} pages of {page_size} tokens, "
+                             f"{n_kv} heads of {head_dim}")
+        if data is None:
+            data = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+        _bytes(data, "data", nbytes, torch.uint8)
+        self.fmt, self.n_pages, self.page_size = fmt, n_pages, page_size
+        self.n_kv, self.head_dim, self.data = n_kv, head_dim, data
+        self._struct = _KVStruct(fmt, n_kv, head_dim, page_size, n_pages, data.data_ptr(),
+                                 data.numel())
+        self._ref = ctypes.byref(self._struct)
+
+
+def _gpu(t, name, dtype, like):
+    """t is a GPU tensor of dtype on like's device."""
+    if t.device != like.device or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor on {like.device}, got {t.dtype} on "
+                         f"{t.device}")
+    return t
+
+
+def _vector(t, name, dtype, like, count):
+    _gpu(t, name, dtype, like)
+    if t.dim() != 1 or t.shape[0] != count or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{count}] tensor, got {list(t.shape)}")
+    return t
+
+
+_XDT = {torch.float32: QL_F32, torch.bfloat16: QL_BF16}
+
+
+def _heads(t, name, like, heads, d):
+    """t [tokens, heads, d] on like's device, a token's heads contiguous; its token stride."""
+    if t.device != like.device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}] on {like.device}, got "
+                         f"{list(t.shape)} on {t.device}")
+    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def _new(shape, dtype, like, stream):
+    """A buffer for a call on `stream`: memory of that stream's own pool, so
+    that work queued elsewhere on what the memory held before cannot meet it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _out3(t, name, like, shape, dtype, stream):
+    if t is None:
+        return _new(shape, dtype, like, stream)
+    _gpu(t, name, t.dtype, like)
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+    return t
+
+
+def kv_append(cache, k, v, slots, stream=None):
+    """Write k, v [tokens, n_kv, head_dim] (fp32 or bf16; slices of a fused qkv
+    tensor will do) to their slots (int64 [tokens]; negative: skipped)."""
+    ks = _heads(k, "k", cache.data, cache.n_kv, cache.head_dim)
+    vs = _heads(v, "v", cache.data, cache.n_kv, cache.head_dim)
+    dt = _XDT.get(k.dtype)
+    if dt is None or v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must be float32 or bfloat16, of one type and length")
+    tokens = k.shape[0]
+    _vector(slots, "slots", torch.int64, cache.data, tokens)
+    _check("kv_append", _lib.kv_append(cache._ref, k.data_ptr(), v.data_ptr(), dt, tokens, ks, vs,
+                                       slots.data_ptr(), _stream(stream)))
+
+
+def kv_gather(cache, slots, k=None, v=None, out_dtype=torch.bfloat16, stream=None):
+    """Read rows back: (k, v) [tokens, n_kv, head_dim] in out_dtype (fp32 or
+    bf16); a slot outside the cache gives zeros."""
+    tokens = slots.shape[0] if slots.dim() == 1 else -1
+    _vector(slots, "slots", torch.int64, cache.data, tokens)
+    shape = (tokens, cache.n_kv, cache.head_dim)
+    k = _out3(k, "k", cache.data, shape, out_dtype, stream)
+    v = _out3(v, "v", cache.data, shape, out_dtype, stream)
+    dt = _XDT.get(k.dtype)
+    if dt is None or v.dtype != k.dtype:
+        raise ValueError("k and v must be float32 or bfloat16, of one type")
+    _check("kv_gather", _lib.kv_gather(cache._ref, slots.data_ptr(), tokens, k.data_ptr(),
+                                       v.data_ptr(), dt, _stream(stream)))
+    return k, v
+
+
+def qkv_norm_rope_append(cache, qkv, n_q, slots, positions=None, rope=None, q_weight=None,
+                         k_weight=None, eps=1e-6, interleaved=False, q_out=None, stream=None):
+    """From a fused projection qkv [tokens, (n_q + 2 n_kv) * head_dim] (fp32 or
+    bf16): RMS norm of each query and key head (weights fp32 [head_dim], None:
+    no norm), rotation by the tokens' positions (rope fp32 [max_pos, rot]:
+    cosines, then sines, of rot / 2 pairs; None: no rotation; pairs (i, i +
+    rot / 2), or (2 i, 2 i + 1) if interleaved), and K and V written to slots
+    (int64 [tokens]; negative: skipped).  Returns the queries, bf16
+    [tokens, n_q, head_dim]."""
+    d = cache.head_dim
+    width = (n_q + 2 * cache.n_kv) * d
+    if qkv.device != cache.data.device or qkv.dim() != 2 or qkv.shape[1] != width:
+        raise ValueError(f"qkv must be [tokens, {width}] on {cache.data.device}, got "
+                         f"{list(qkv.shape)} on {qkv.device}")
+    tokens = qkv.shape[0]
+    if tokens and qkv.stride(1) != 1:
+        raise ValueError("qkv: a token's row must be contiguous")
+    dt = _XDT.get(qkv.dtype)
+    if dt is None:
+        raise ValueError("qkv must be float32 or bfloat16")
+    _vector(slots, "slots", torch.int64, cache.data, tokens)
+    max_pos = rot = 0
+    if rope is not None:
+        _gpu(rope, "rope", torch.float32, cache.data)
+        if rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous [max_pos, rot] tensor")
+        max_pos, rot = rope.shape
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _vector(positions, "positions", torch.int32, cache.data, tokens)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _vector(w, name, torch.float32, cache.data, d)
+    q_out = _out3(q_out, "q_out", cache.data, (tokens, n_q, d), torch.bfloat16, stream)
+    if q_out.dtype != torch.bfloat16:
+        raise ValueError("q_out must be bfloat16")
+    _check("qkv_norm_rope_append", _lib.qkv_norm_rope_append(
+        cache._ref, qkv.data_ptr(), dt, tokens, qkv.stride(0) if tokens > 1 else width, n_q,
+        _ptr(q_weight), _ptr(k_weight), eps, None if rope is None else positions.data_ptr(),
+        _ptr(rope), max_pos, rot, QL_ROPE_INTERLEAVED if interleaved else 0, q_out.data_ptr(),
+        slots.data_ptr(), _stream(stream)))
+    return q_out
+
+
+def kv_attention_workspace(cache, tokens, n_q, n_seqs, max_q, max_kv):
+    return _lib.kv_attention_workspace(cache._ref, tokens, n_q, n_seqs, max_q, max_kv)
+
+
+def _table(block_table, like, n_seqs):
+    _gpu(block_table, "block_table", torch.int32, like)
+    if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
+        raise ValueError(f"block_table must be [{n_seqs}, pages], got {list(block_table.shape)}")
+    cols = block_table.shape[1]
+    if cols > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table: a sequence's row must be contiguous")
+    return (block_table.stride(0) if n_seqs > 1 else cols), cols
+
+
+def kv_attention(cache, q, cu_q, kv_lens, block_table, max_q, max_kv, tree=None, scale=None,
+                 y=None, workspace=None, stream=None):
+    """Attention of each sequence's newest tokens over its cached context and
+    themselves.
+
+    q bf16 [tokens, n_q, head_dim], the sequences' tokens one after another;
+    cu_q int32 [n_seqs + 1] where each starts; kv_lens int32 [n_seqs] the keys
+    of each, the new tokens' own included (append them first); block_table
+    int32 [n_seqs, pages].  tree: int64 [tokens], bit j of token i's set where
+    it sees new token j of its sequence (at most 64); None: a causal chain, and
+    with one token ordinary decoding.  max_q: at least every sequence's new
+    tokens; max_kv: about the largest length.  scale: head_dim ** -0.5 when not
+    given.  workspace: uint8 of kv_attention_workspace(...) bytes, allocated
+    when not given.  Returns y bf16 [tokens, n_q, head_dim]."""
+    like = cache.data
+    n_q = q.shape[1] if q.dim() == 3 else -1
+    stride = _heads(q, "q", like, n_q, cache.head_dim)
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q must be bfloat16")
+    tokens = q.shape[0]
+    n_seqs = cu_q.shape[0] - 1 if cu_q.dim() == 1 else -1
+    if n_seqs < 0:
+        raise ValueError("cu_q must be an int32 [n_seqs + 1] tensor")
+    _vector(cu_q, "cu_q", torch.int32, like, n_seqs + 1)
+    _vector(kv_lens, "kv_lens", torch.int32, like, n_seqs)
+    tstride, cols = _table(block_table, like, n_seqs)
+    if tree is not None:
+        _vector(tree, "tree", torch.int64, like, tokens)
+    y = _out3(y, "y", like, (tokens, n_q, cache.head_dim), torch.bfloat16, stream)
+    if y.dtype != torch.bfloat16:
+        raise ValueError("y must be bfloat16")
+    if workspace is None:
+        need = _lib.kv_attention_workspace(cache._ref, tokens, n_q, n_seqs, max_q, max_kv)
+        if need:
+            workspace = _new(need, torch.uint8, like, stream)
+    else:
+        _bytes(workspace, "workspace", 0, torch.uint8)
+    _check("kv_attention", _lib.kv_attention(
+        cache._ref, q.data_ptr(), stride, tokens, n_q, n_seqs, cu_q.data_ptr(),
+        kv_lens.data_ptr(), block_table.data_ptr(), tstride, cols, max_q, max_kv, _ptr(tree),
+        cache.head_dim ** -0.5 if scale is None else scale, y.data_ptr(), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _stream(stream)))
+    return y
+
+
+def kv_commit(cache, cu_q, kv_lens, block_table, path, stream=None):
+    """Move the rows of each sequence's accepted drafts right behind its
+    context: path int32 [n_seqs, max_path <= 64], accepted draft indices, root
+    first, padded with -1; cu_q, kv_lens and block_table as the verification's
+    kv_attention call."""
+    like = cache.data
+    n_seqs = cu_q.shape[0] - 1 if cu_q.dim() == 1 else -1
+    if n_seqs < 0:
+        raise ValueError("cu_q must be an int32 [n_seqs + 1] tensor")
+    _vector(cu_q, "cu_q", torch.int32, like, n_seqs + 1)
+    _vector(kv_lens, "kv_lens", torch.int32, like, n_seqs)
+    tstride, cols = _table(block_table, like, n_seqs)
+    _gpu(path, "path", torch.int32, like)
+    if path.dim() != 2 or path.shape[0] != n_seqs or not path.is_contiguous():
+        raise ValueError(f"path must be a contiguous [{n_seqs}, max_path] tensor, got "
+                         f"{list(path.shape)}")
+    _check("kv_commit", _lib.kv_commit(
+        cache._ref, n_seqs, cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), tstride,
+        cols, path.data_ptr(), path.shape[1], _stream(stream)))
 
 
 def raw():

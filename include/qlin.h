@@ -397,6 +397,197 @@ int gemm_w4a16_sp24_ws(const void *x_bf16, const void *w_packed, int64_t m,
                        int64_t n, int64_t k, void *y, int y_dtype, void *workspace,
                        size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key/value cache.  Between a layer's qkv and output projections stand
+ * the head norms, the rotation of queries and keys by their positions, the
+ * cache of keys and values and the attention over it:
+ *
+ *   qkv_norm_rope_append(qkv) -> q, and K, V rows written to the cache
+ *   kv_attention(q, cache)    -> y, the input of the output projection
+ *   kv_commit                 -> after speculative decoding: the accepted
+ *                                drafts' rows move behind the context
+ *   kv_append, kv_gather         write and read rows without the norms
+ *
+ * The reference pages hand this cache from the prefill half to the decode
+ * half (Disaggregated Quantization; Mix-Quant, system-level deployment) and
+ * measure 8-bit against 16-bit caches (the qiita article on f16 and q8_0).
+ *
+ * A cache is one buffer of pages.  A page holds page_size consecutive tokens
+ * of one sequence for all n_kv heads; a slot is page * page_size + offset.
+ * Formats of one row (the K or V vector of one token and head):
+ *   QL_KV_BF16   the values, rounded to nearest even
+ *   QL_KV_E4M3   E4M3 codes of x / 2^e; e is the smallest integer >= -100 with
+ *                max|x| <= 448 * 2^e (0 for a row of zeros)
+ *   QL_KV_NVFP4  as quantize_nvfp4 with the row's own tensor scale 2^e: groups
+ *                of 16, s_g = E4M3(max|x_g| / 2^e / 6), code =
+ *                E2M1(x / 2^e * (1 / s_g)), each binary32 step rounded once;
+ *                e as above with 2688 = 6 * 448 in the place of 448
+ * In the two quantized formats an infinity saturates and a NaN stays a NaN
+ * (QL_KV_NVFP4: its whole group of 16 reads back as NaN).
+ *
+ * Layout: blocks of 16 tokens of one kv head, [n_pages][n_kv][page_size / 16].
+ * All blocks' codes come first, each block's 16 K rows and then its 16 V rows
+ * of R bytes (R = 2 d, d, d / 2); then, in the same order, all blocks' scales
+ * (0, 32, 2 d + 32 bytes).  Token t of a block, C = min(16, R / 4):
+ *   K codes        byte b of the row at (b / C) 16 C + t C + b % C
+ *   V codes        element u (QL_KV_NVFP4: byte u, a pair of elements) at
+ *                  (u / S) 16 S + (t / 4) 4 S + (u % S) 4 + t % 4, counted in
+ *                  elements (bytes); S = 32, 64, min(d, 128) / 2
+ *   NVFP4 scales   K group g at (g / P) 16 P + t P + g % P with P = C / 8;
+ *                  V group g at d + 16 g + t
+ *   row exponents  e + 127 in one byte, in the last 32 bytes of a block's
+ *                  scales: K at (t / 4) 8 + t % 4, V four bytes after it
+ *
+ * format     QL_KV_BF16, QL_KV_E4M3 or QL_KV_NVFP4.
+ * n_kv       key/value heads, 1..1024.
+ * head_dim   64, 128 or 256.
+ * page_size  a power of two, 16..4096.
+ * data       device buffer of at least kv_cache_bytes(...) bytes, 16-byte
+ *            aligned.  It needs no initialisation: only rows that were
+ *            written are ever used.
+ * The struct is read during the call only.  kv_cache_bytes returns 0 for
+ * arguments outside these ranges (or more than 2^40 blocks).
+ * Errors of every call that takes one: QL_EINVAL (null), QL_EFORMAT (format),
+ * QL_ESHAPE (sizes), QL_EWORKSPACE (bytes), QL_EALIGN (data).
+ * ---------------------------------------------------------------------- */
+typedef enum { QL_KV_BF16 = 0, QL_KV_E4M3 = 1, QL_KV_NVFP4 = 2 } ql_kv_format;
+
+typedef struct {
+  int32_t format;
+  int32_t n_kv;
+  int32_t head_dim;
+  int32_t page_size;
+  int64_t n_pages;
+  void *data;
+  size_t bytes;
+} ql_kv_cache;
+
+size_t kv_cache_bytes(int format, int64_t n_pages, int64_t page_size, int64_t n_kv,
+                      int64_t head_dim);
+
+/* ------------------------------------------------------------------------
+ * Write K and V rows to their slots, in the cache's format.
+ *
+ * k, v       [tokens, n_kv, head_dim], x_dtype QL_F32 or QL_BF16; a token's
+ *            heads are contiguous, tokens are k_stride / v_stride elements
+ *            apart (slices of a fused qkv buffer will do).  Rows start on 16
+ *            bytes: both strides and the pointers are multiples of 16 bytes.
+ * slots      int64 [tokens].  A slot outside the cache (any negative number)
+ *            is skipped; two tokens of one call must not share a slot.
+ * Errors: the cache's, QL_EINVAL, QL_ESHAPE (tokens < 0 is QL_EINVAL, more
+ * than 2^31 - 1, or a stride shorter than a token's heads), QL_EDTYPE,
+ * QL_EALIGN, QL_EHIP.
+ * ---------------------------------------------------------------------- */
+int kv_append(const ql_kv_cache *cache, const void *k, const void *v, int x_dtype,
+              int64_t tokens, int64_t k_stride, int64_t v_stride, const int64_t *slots,
+              void *stream);
+
+/* ------------------------------------------------------------------------
+ * Read rows back: k, v out [tokens, n_kv, head_dim] contiguous, the values
+ * the cached rows stand for, y_dtype QL_F32 or QL_BF16 (both exact: a code
+ * times its scales has at most 6 significant bits; rows of exponents near the
+ * end of the type's range excepted).  A slot outside the cache gives zeros.
+ * Errors: as kv_append.
+ * ---------------------------------------------------------------------- */
+int kv_gather(const ql_kv_cache *cache, const int64_t *slots, int64_t tokens, void *k, void *v,
+              int y_dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The step between the qkv projection and the attention, in one pass over
+ * the projection's output: RMS norm of every query and key head, rotation of
+ * both by the token's position, queries out, K and V written to the cache
+ * (as kv_append; K from its binary32 values, rounded once).
+ *   norm      x <- x / sqrt(mean(x^2) + eps) * weight     (binary32)
+ *   rotation  (a, b) <- (a c - b s, b c + a s) for rot / 2 pairs of a head,
+ *             a = x[i], b = x[i + rot / 2], or x[2 i], x[2 i + 1] with
+ *             QL_ROPE_INTERLEAVED; elements from rot on are left as they are
+ *
+ * qkv        [tokens, (n_q + 2 n_kv) * head_dim], QL_F32 or QL_BF16: queries,
+ *            keys, values; rows row_stride elements apart, 16-byte aligned.
+ * n_q        query heads, 1..65536.
+ * q_weight,  fp32 [head_dim] norm weights of queries and keys; NULL: no norm
+ * k_weight   of that kind.
+ * positions  int32 [tokens]; a position outside [0, max_pos) takes the
+ *            nearest row of the table.  May be NULL when rot == 0.
+ * rope       fp32 [max_pos, rot]: c[0..rot/2), then s[0..rot/2) of a position.
+ *            May be NULL when rot == 0.
+ * rot        0 (no rotation) or an even number up to head_dim.
+ * flags      0 or QL_ROPE_INTERLEAVED.
+ * q_out      out [tokens, n_q, head_dim] bf16 (RNE), for every token, also
+ *            one whose slot is skipped.
+ * Errors: the cache's, QL_EINVAL, QL_ESHAPE, QL_EDTYPE, QL_EALIGN, QL_EHIP.
+ * ---------------------------------------------------------------------- */
+#define QL_ROPE_INTERLEAVED 1u
+int qkv_norm_rope_append(const ql_kv_cache *cache, const void *qkv, int x_dtype, int64_t tokens,
+                         int64_t row_stride, int64_t n_q, const float *q_weight,
+                         const float *k_weight, float eps, const int32_t *positions,
+                         const float *rope, int64_t max_pos, int64_t rot, unsigned flags,
+                         void *q_out, const int64_t *slots, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of each sequence's newest tokens over its cached context and
+ * over themselves.  Sequence b has n_b = cu_q[b + 1] - cu_q[b] queries; its
+ * keys are the first kv_lens[b] positions of its pages, the last n_b of which
+ * are the rows of those same tokens (written beforehand).  Query i sees the
+ * context (every position before the last n_b) and, of the n_b new tokens,
+ *   tree != NULL  token j where bit j of tree[cu_q[b] + i] is set (a tree of
+ *                 drafted tokens: the bits of the path from the root to i,
+ *                 itself included), n_b <= 64
+ *   tree == NULL  tokens j <= i: one token is ordinary decoding, several are
+ *                 a chain of drafts or a chunk of a prompt
+ * and of those only positions whose page is in the cache: a block-table entry
+ * outside [0, n_pages) hides its page's tokens.
+ *   y = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale q.k_p - max_p scale q.k_p)
+ * A query that sees nothing gives zeros.  Rows that no query of a sequence
+ * sees do not matter, whatever they hold; a NaN or infinity in a row hidden
+ * from one query does not reach it.
+ *
+ * Products and sums are binary32; keys, values and queries enter exactly
+ * (queries rounded to a multiple of 2^-38 of their row's largest value for
+ * the quantized formats), weights rounded to 11 bits (QL_KV_BF16: 16 bits).
+ *
+ * q            bf16 [tokens, n_q, head_dim]; a token's heads are contiguous,
+ *              tokens q_stride elements apart; 16-byte aligned rows.
+ * tokens       rows of q and y; cu_q[n_seqs] <= tokens.
+ * n_q          query heads, a multiple of n_kv; heads h n_q / n_kv .. + n_q /
+ *              n_kv - 1 share kv head h.
+ * cu_q         int32 [n_seqs + 1], ascending from 0; kv_lens int32 [n_seqs].
+ * block_table  int32 [n_seqs, table_cols], rows table_stride elements apart:
+ *              the page of positions page_size * j .. of each sequence.
+ *              Positions past the table's last column are not read.
+ * max_q        at least every n_b (queries past it are not computed).
+ * max_kv       about the largest kv_lens[b]; the work split is planned by it,
+ *              the result is right for any value.
+ * y            out bf16 [tokens, n_q, head_dim] contiguous (RNE).
+ * workspace    >= kv_attention_workspace(...) bytes, 16-byte aligned (NULL when
+ *              that is 0).  Calls that share one must be ordered.
+ * Errors: the cache's, QL_EINVAL, QL_ESHAPE, QL_EALIGN, QL_EWORKSPACE,
+ * QL_EHIP.  tokens == 0, n_seqs == 0 or max_q == 0: QL_OK, nothing is done.
+ * ---------------------------------------------------------------------- */
+size_t kv_attention_workspace(const ql_kv_cache *cache, int64_t tokens, int64_t n_q,
+                              int64_t n_seqs, int64_t max_q, int64_t max_kv);
+int kv_attention(const ql_kv_cache *cache, const void *q_bf16, int64_t q_stride, int64_t tokens,
+                 int64_t n_q, int64_t n_seqs, const int32_t *cu_q, const int32_t *kv_lens,
+                 const int32_t *block_table, int64_t table_stride, int64_t table_cols,
+                 int64_t max_q, int64_t max_kv, const uint64_t *tree, float scale, void *y,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * After a tree of drafted tokens was verified: the rows of the accepted path
+ * move right behind the context, as they are (no requantization).  With ctx =
+ * kv_lens[b] - n_b, row ctx + path[b][j] goes to ctx + j, for every j at
+ * once: sources are read before targets are written.  The caller's new length
+ * is ctx plus the accepted count; cu_q and kv_lens are those of the
+ * verification.
+ *
+ * path  int32 [n_seqs, max_path]: accepted draft indices, root first; an
+ *       entry outside [0, n_b) moves nothing (pad with -1).  max_path <= 64.
+ * Errors: as kv_attention.
+ * ---------------------------------------------------------------------- */
+int kv_commit(const ql_kv_cache *cache, int64_t n_seqs, const int32_t *cu_q,
+              const int32_t *kv_lens, const int32_t *block_table, int64_t table_stride,
+              int64_t table_cols, const int32_t *path, int64_t max_path, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
