@@ -139,9 +139,9 @@ static int check_attention(const ql_kv_cache* cache, int64_t tokens, int64_t n_q
   if (tokens == 0 || n_seqs == 0 || max_q == 0) return QL_OK;
   const int64_t m = max_q < tokens ? max_q : tokens;
   if (m * n_q > kMost) return QL_ESHAPE;
-  const KvAttnPlan p = kv_attention_plan(cache->format, cache->head_dim, int(n_q), cache->n_kv,
-                                         n_seqs, m, max_kv);
-  if (p.row_blocks * n_seqs > kMost / (int64_t(cache->n_kv) * p.splits)) return QL_ESHAPE;
+  const KvAttnPlan p = kv_attention_plan(cache->head_dim, int(n_q), cache->n_kv, n_seqs, m,
+                                         max_kv);
+  if (p.row_blocks > (kMost / 16) / (n_seqs * cache->n_kv * p.splits)) return QL_ESHAPE;
   return -1;
 }
 
@@ -152,8 +152,8 @@ size_t kv_attention_workspace(const ql_kv_cache* cache, int64_t tokens, int64_t 
     return 0;
   if (check_attention(cache, tokens, n_q, n_seqs, max_q, max_kv) != -1) return 0;
   const int64_t m = max_q < tokens ? max_q : tokens;
-  const KvAttnPlan p = kv_attention_plan(cache->format, cache->head_dim, int(n_q), cache->n_kv,
-                                         n_seqs, m, max_kv);
+  const KvAttnPlan p = kv_attention_plan(cache->head_dim, int(n_q), cache->n_kv, n_seqs, m,
+                                         max_kv);
   return kv_attention_ws_bytes(p, tokens, int(n_q), cache->head_dim);
 }
 
@@ -181,8 +181,8 @@ int kv_attention(const ql_kv_cache* cache, const void* q_bf16, int64_t q_stride,
        reinterpret_cast<uintptr_t>(block_table)) & 3u)
     return QL_EALIGN;
   const int64_t m = max_q < tokens ? max_q : tokens;
-  const KvAttnPlan p = kv_attention_plan(cache->format, cache->head_dim, int(n_q), cache->n_kv,
-                                         n_seqs, m, max_kv);
+  const KvAttnPlan p = kv_attention_plan(cache->head_dim, int(n_q), cache->n_kv, n_seqs, m,
+                                         max_kv);
   const size_t need = kv_attention_ws_bytes(p, tokens, int(n_q), cache->head_dim);
   if (need) {
     if (!workspace) return QL_EINVAL;

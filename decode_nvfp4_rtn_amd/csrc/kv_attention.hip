@@ -2,31 +2,39 @@
 // over the paged, possibly quantized key/value cache: kv_attention
 // (include/qlin.h).
 //
-// One block takes up to 16 MT query rows (a row: one new token and one of the
-// n_q / n_kv query heads that share a kv head) of one sequence and kv head,
-// and one chunk of its keys; its four waves take the chunk's 32-key tiles in
-// turn.  A tile needs two products, computed transposed so that no operand
-// moves between lanes:
-//   S^T = K Q^T   A: 16 keys (lane % 16), 8 elements of d (lane / 16) per step
+// A row is one new token and one of the n_q / n_kv query heads that share a
+// kv head.  A block takes some rows of one sequence and kv head and one chunk
+// of its keys, 32 at a time, with the running maximum and sum of a softmax.
+// Both products of such a tile run transposed, so that no operand moves
+// between lanes:
+//   S^T = K Q^T     A: 16 keys (lane % 16), 8 elements of d (lane / 16) a step
 //   O^T += V^T P^T  A: 16 elements of d (lane % 16), 8 keys (lane / 16)
 // S^T leaves lane (n, g) the scores of query row n and keys 4 g .. 4 g + 3 of
 // each 16-key block.  The contraction index of the second product may run
-// over keys in any order as long as both operands agree: with index 8 g + j
-// standing for key 4 g + j % 4 of block j / 4, the probabilities already are
+// over the keys in any order as long as both operands agree: with index
+// 8 g + j standing for key 4 g + j % 4 of block j / 4, the weights already are
 // the B operand, and the cache keeps V so that a lane's registers are the A
-// operand (kv_cache.hpp).  Each row's statistics live in the four lanes of its
-// column, the accumulator is rescaled in place.
+// operand (kv_cache.hpp).  A row's statistics live in the four lanes of its
+// column, and the accumulator is rescaled in place.
 //
-// Quantized rows.  K's row scale 2^ke multiplies the row's score after the
-// product.  V's, 2^ve, joins the exponent: with z the score in units of
-// log 2 the weight that enters the product is 2^(z + ve - m), m a running
-// maximum of z + ve, and the sum of weights takes 2^(z + ve - m) 2^-ve.  So the
-// weights of the product are at most 2^8 however the rows' scales differ, and
-// codes (and NVFP4 codes times their group scales, at most 6 significant
-// bits) enter it exactly in fp16.  Queries are scaled by a power of two for
-// each row to fit fp16.  The weights' rounding to fp16 (relative 2^-12) is
-// below that of the bf16 result; a bf16 cache takes bf16 operands and its
-// weights as the sum of two bf16 values (16 bits).
+// Two kernels share this.
+// narrow (up to 16 rows): each of four waves takes tiles of its own straight
+//   from memory into registers and the four results are joined at the end;
+//   bound by the cache's bytes.
+// wide (more rows): four waves share each tile.  Each turns a quarter of it
+//   into matrix operands in LDS, once for all, and takes 16 or 32 rows of its
+//   own; bound by the softmax's vector instructions and the products.
+//
+// Quantized rows.  K's row scale 2^ke goes into the bf16 operand where that
+// is free (narrow, NVFP4: it multiplies the score).  V's, 2^ve, joins the
+// exponent: with z the score in units of log 2 the weight that enters the
+// product is w = 2^(z + ve - m), m a running maximum of z + ve, and the sum of
+// weights takes w 2^-ve.  So the weights are at most 2^8 however the rows'
+// scales differ, and V's codes (NVFP4: times their group scales, at most 6
+// significant bits) enter in fp16 exactly.  The weights' rounding to fp16
+// (relative 2^-12) is below that of the bf16 result.  A bf16 cache takes bf16
+// operands and its weights as the sum of two bf16 values (16 bits), because
+// one of 8 bits would add as much error as the rounding of the result.
 #include "kv_cache.hpp"
 
 namespace qlin {
@@ -34,6 +42,7 @@ namespace {
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -45,14 +54,14 @@ constexpr float kLowest = -3.0e38f;     // running maximum before the first key
 constexpr float kSlack = 8.0f;          // growth of the maximum that is let pass (weights <= 2^8)
 constexpr float kLog2e = 1.44269504088896340736f;
 
-template <int FMT>
+template <bool HALF>   // fp16 operands, or bf16
 __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (FMT == QL_KV_BF16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  else
+  if constexpr (HALF)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
 // Reductions over the four lanes of a column (16 apart).
@@ -74,6 +83,12 @@ __device__ __forceinline__ uint32_t fp8_pair(uint32_t w, int hi) {   // two E4M3
                      : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(int(w), 1.0f, false);
   return __builtin_bit_cast(uint32_t, v);
 }
+// two E4M3 codes times a power of two -> bf16
+__device__ __forceinline__ uint32_t fp8_pair_bf16(uint32_t w, float p, int hi) {
+  const bf16x2 v = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(int(w), p, true)
+                      : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(int(w), p, false);
+  return __builtin_bit_cast(uint32_t, v);
+}
 template <int B>
 __device__ __forceinline__ f16x2 fp4_pair(uint32_t w) {              // byte B's two E2M1 codes
   return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, B);
@@ -81,118 +96,179 @@ __device__ __forceinline__ f16x2 fp4_pair(uint32_t w) {              // byte B's
 __device__ __forceinline__ uint32_t times(f16x2 a, f16x2 s) {        // exact: 2 x 4 bits
   return __builtin_bit_cast(uint32_t, a * s);
 }
+// byte B's two E2M1 codes times a power of two and a group scale -> bf16
+template <int B>
+__device__ __forceinline__ uint32_t fp4_pair_bf16(uint32_t w, float p, float s) {
+  const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, p, B);
+  return pack_bf16x2(v[0] * s, v[1] * s);
+}
+__device__ __forceinline__ float power(uint32_t b) {                 // 2^(b - 127)
+  return __uint_as_float(b << 23);
+}
 
-// The raw bytes of one 32-key tile that a lane holds: two 16-key blocks.
+// Top bit of each half / byte that is a bf16 infinity or NaN / an E4M3 NaN.
+__device__ __forceinline__ uint32_t bad_halves(uint32_t w) {
+  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t bad_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_or(uint32_t v) {   // another lane of the same 16
+  return uint32_t(__builtin_amdgcn_mov_dpp(int(v), CTRL, 0xF, 0xF, true));
+}
+
+// One block's (16 keys') K or V bytes that a lane holds.
 template <int FMT, int D>
-struct Tile {
+struct Block {
   using L = KvLayout<FMT, D>;
   static constexpr int W = L::kLoad / 4;      // words per load
-  uint32_t k[2][L::kLoads * W], v[2][L::kLoads * W];
-  uint32_t ks[2][L::kLoads], vs[2][L::kLoads];   // NVFP4 group scales
-  uint32_t ke[2], ve[2];                         // row exponents of keys 4 g .. 4 g + 3
+  typedef uint32_t Words __attribute__((ext_vector_type(W)));
+  Words w[L::kLoads];
+  uint32_t sc[L::kLoads];                     // NVFP4 group scales (K: of the lane's key, V: of its quad)
 
-  __device__ __forceinline__ void load(int t, const uint8_t* codes, const uint8_t* scales, int lane) {
-    auto words = [&](const uint8_t* p, uint32_t* w) {
-      if constexpr (W == 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        w[0] = x.x, w[1] = x.y;
-      }
-    };
+  __device__ __forceinline__ void load_k(const uint8_t* codes, const uint8_t* scales, int lane) {
 #pragma unroll
     for (int i = 0; i < L::kLoads; ++i) {
-      words(codes + (64 * i + lane) * L::kLoad, &k[t][i * W]);
-      words(codes + 16 * L::kRow + (64 * i + lane) * L::kLoad, &v[t][i * W]);
-    }
-    if constexpr (FMT == QL_KV_NVFP4) {
-#pragma unroll
-      for (int i = 0; i < L::kLoads; ++i) {
+      w[i] = *reinterpret_cast<const Words*>(codes + (64 * i + lane) * L::kLoad);
+      if constexpr (FMT == QL_KV_NVFP4) {
         const uint8_t* p = scales + (64 * i + lane) * L::kGPC;
-        if constexpr (L::kGPC == 2) ks[t][i] = *reinterpret_cast<const uint16_t*>(p);
-        else ks[t][i] = *p;
+        if constexpr (L::kGPC == 2) sc[i] = *reinterpret_cast<const uint16_t*>(p);
+        else sc[i] = *p;
+      }
+    }
+  }
+  __device__ __forceinline__ void load_v(const uint8_t* codes, const uint8_t* scales, int lane) {
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i) {
+      w[i] = *reinterpret_cast<const Words*>(codes + 16 * L::kRow + (64 * i + lane) * L::kLoad);
+      if constexpr (FMT == QL_KV_NVFP4) {
         const int group = i * L::kDC + (lane & 15) * L::kDC / 16;
-        vs[t][i] = *reinterpret_cast<const uint32_t*>(scales + D + group * 16 + (lane >> 4) * 4);
+        sc[i] = *reinterpret_cast<const uint32_t*>(scales + D + group * 16 + (lane >> 4) * 4);
       }
     }
-    if constexpr (FMT != QL_KV_BF16) {
-      const uint2 e = *reinterpret_cast<const uint2*>(scales + L::kExp + (lane >> 4) * 8);
-      ke[t] = e.x, ve[t] = e.y;
+  }
+  __device__ __forceinline__ void take(const Block& o) {
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i) {
+      w[i] = o.w[i];
+      if constexpr (FMT == QL_KV_NVFP4) sc[i] = o.sc[i];
     }
   }
 
-  // K operand of block t, step s (elements d of a lane: see q_element).
-  __device__ __forceinline__ u32x4 k_operand(int t, int s) const {
-    u32x4 r;
+  // K operand of step s (its elements of d: q_element), bf16 with the row
+  // scale p; HALF (NVFP4): fp16 without it.
+  template <bool HALF>
+  __device__ __forceinline__ u32x4 k_operand(int s, float p) const {
+    constexpr int per = L::kEC / 8;           // steps per load
     if constexpr (FMT == QL_KV_BF16) {
-      for (int x = 0; x < 4; ++x) r[x] = k[t][4 * s + x];
+      return w[s];
     } else if constexpr (FMT == QL_KV_E4M3) {
-      const uint32_t a = k[t][2 * s], b = k[t][2 * s + 1];
-      r[0] = fp8_pair(a, 0), r[1] = fp8_pair(a, 1), r[2] = fp8_pair(b, 0), r[3] = fp8_pair(b, 1);
+      const uint32_t a = w[s / per][s % per * 2], b = w[s / per][s % per * 2 + 1];
+      return u32x4{fp8_pair_bf16(a, p, 0), fp8_pair_bf16(a, p, 1), fp8_pair_bf16(b, p, 0),
+                   fp8_pair_bf16(b, p, 1)};
     } else {
-      constexpr int per = L::kEC / 8;   // steps per load
-      const f16x2 sc = __builtin_bit_cast(f16x2, fp8_pair(ks[t][s / per], 0));
-      const _Float16 g = sc[s % per * 8 / 16];
-      const uint32_t a = k[t][s];
-      const f16x2 gg = {g, g};
-      r[0] = times(fp4_pair<0>(a), gg), r[1] = times(fp4_pair<1>(a), gg);
-      r[2] = times(fp4_pair<2>(a), gg), r[3] = times(fp4_pair<3>(a), gg);
-    }
-    return r;
-  }
-
-  // V operands of one load i: its kDC d-tiles, keys of both blocks.
-  __device__ __forceinline__ void v_operands(int i, u32x4 (&r)[L::kDC]) const {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if constexpr (FMT == QL_KV_BF16) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          r[q][2 * t] = v[t][4 * i + 2 * q];
-          r[q][2 * t + 1] = v[t][4 * i + 2 * q + 1];
-        }
-      } else if constexpr (FMT == QL_KV_E4M3) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          r[q][2 * t] = fp8_pair(v[t][4 * i + q], 0);
-          r[q][2 * t + 1] = fp8_pair(v[t][4 * i + q], 1);
-        }
+      const uint32_t a = w[s / per][s % per];
+      if constexpr (HALF) {
+        const f16x2 two = __builtin_bit_cast(f16x2, fp8_pair(sc[s / per], 0));
+        const _Float16 g = two[s % per / 2];
+        const f16x2 gg = {g, g};
+        return u32x4{times(fp4_pair<0>(a), gg), times(fp4_pair<1>(a), gg),
+                     times(fp4_pair<2>(a), gg), times(fp4_pair<3>(a), gg)};
       } else {
-        const f16x2 lo = __builtin_bit_cast(f16x2, fp8_pair(vs[t][i], 0));
-        const f16x2 hi = __builtin_bit_cast(f16x2, fp8_pair(vs[t][i], 1));
-#pragma unroll
-        for (int q = 0; q < W; ++q) {
-          // bytes (key 0..3) of a pair of elements -> bytes of two keys each:
-          // (d0: keys 0, 1), (d1: keys 0, 1), (d0: keys 2, 3), (d1: keys 2, 3)
-          const uint32_t x = v[t][W * i + q];
-          const uint32_t y = (x & 0xF00FF00Fu) | ((x << 4) & 0x0F000F00u) | ((x >> 4) & 0x00F000F0u);
-          r[2 * q][2 * t] = times(fp4_pair<0>(y), lo);
-          r[2 * q + 1][2 * t] = times(fp4_pair<1>(y), lo);
-          r[2 * q][2 * t + 1] = times(fp4_pair<2>(y), hi);
-          r[2 * q + 1][2 * t + 1] = times(fp4_pair<3>(y), hi);
-        }
+        const float g = s % per / 2 ? __builtin_amdgcn_cvt_f32_fp8(int(sc[s / per]), 1)
+                                    : __builtin_amdgcn_cvt_f32_fp8(int(sc[s / per]), 0);
+        return u32x4{fp4_pair_bf16<0>(a, p, g), fp4_pair_bf16<1>(a, p, g),
+                     fp4_pair_bf16<2>(a, p, g), fp4_pair_bf16<3>(a, p, g)};
       }
     }
   }
 
-  // Clears the V rows of block t's keys from `keys` (0..4 of this lane's
-  // quad) on: what lies there is not part of the sequence.
-  __device__ __forceinline__ void clear_v(int t, int keys) {
+  // This block's half (4 of a lane's 8 keys) of the V operands of load i's
+  // kDC d-tiles: bf16 values, or fp16 codes (NVFP4: times group scales).
+  __device__ __forceinline__ void v_operands(int i, uint2 (&r)[L::kDC]) const {
+    if constexpr (FMT == QL_KV_BF16) {
+      r[0] = make_uint2(w[i][0], w[i][1]);
+      r[1] = make_uint2(w[i][2], w[i][3]);
+    } else if constexpr (FMT == QL_KV_E4M3) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) r[q] = make_uint2(fp8_pair(w[i][q], 0), fp8_pair(w[i][q], 1));
+    } else {
+      const f16x2 lo = __builtin_bit_cast(f16x2, fp8_pair(sc[i], 0));
+      const f16x2 hi = __builtin_bit_cast(f16x2, fp8_pair(sc[i], 1));
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        // bytes (key 0..3) of a pair of elements -> bytes of two keys each:
+        // (d0: keys 0, 1), (d1: keys 0, 1), (d0: keys 2, 3), (d1: keys 2, 3)
+        const uint32_t x = w[i][q];
+        const uint32_t y = (x & 0xF00FF00Fu) | ((x << 4) & 0x0F000F00u) | ((x >> 4) & 0x00F000F0u);
+        r[2 * q] = make_uint2(times(fp4_pair<0>(y), lo), times(fp4_pair<2>(y), hi));
+        r[2 * q + 1] = make_uint2(times(fp4_pair<1>(y), lo), times(fp4_pair<3>(y), hi));
+      }
+    }
+  }
+
+  // V: clears the keys of the lane's quad from `keys` (0..4) on; what lies
+  // there is not part of the sequence.
+  __device__ __forceinline__ void clear_v(int keys) {
     if constexpr (FMT == QL_KV_BF16) {
       const uint32_t a = keys >= 2 ? ~0u : keys == 1 ? 0xFFFFu : 0u;
       const uint32_t b = keys >= 4 ? ~0u : keys == 3 ? 0xFFFFu : 0u;
 #pragma unroll
-      for (int x = 0; x < L::kLoads * W; ++x) v[t][x] &= x & 1 ? b : a;
+      for (int x = 0; x < L::kLoads * W; ++x) w[x / W][x % W] &= x & 1 ? b : a;
     } else {
       const uint32_t m = keys >= 4 ? ~0u : (1u << (8 * keys)) - 1u;
 #pragma unroll
-      for (int x = 0; x < L::kLoads * W; ++x) v[t][x] &= m;
-      if constexpr (FMT == QL_KV_NVFP4) {
-#pragma unroll
-        for (int i = 0; i < L::kLoads; ++i) vs[t][i] &= m;
+      for (int i = 0; i < L::kLoads; ++i) {
+        w[i] &= m;
+        if constexpr (FMT == QL_KV_NVFP4) sc[i] &= m;
       }
     }
+  }
+
+  // V: non-zero where a value that the lane holds is a NaN or an infinity.
+  __device__ __forceinline__ uint32_t non_finite() const {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i) {
+      if constexpr (FMT == QL_KV_NVFP4) {
+        r |= bad_bytes(sc[i]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < W; ++x) r |= FMT == QL_KV_BF16 ? bad_halves(w[i][x]) : bad_bytes(w[i][x]);
+      }
+    }
+    return r;
+  }
+  // V: clears them (NVFP4: their groups); bit k of the result: key k of the
+  // lane's quad had one, in an element of any of the 16 lanes that hold it.
+  __device__ __forceinline__ uint32_t clear_non_finite() {
+    uint32_t b = 0, c = 0, r;     // BF16: keys 0, 1 and keys 2, 3; others: b, a byte a key
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i) {
+      if constexpr (FMT == QL_KV_NVFP4) {
+        const uint32_t m = bad_bytes(sc[i]);
+        b |= m;
+        sc[i] &= ~((m >> 7) * 0xFFu);
+      } else {
+#pragma unroll
+        for (int x = 0; x < W; ++x) {
+          const uint32_t m = FMT == QL_KV_BF16 ? bad_halves(w[i][x]) : bad_bytes(w[i][x]);
+          if (FMT == QL_KV_BF16 && (x & 1)) c |= m;
+          else b |= m;
+          w[i][x] &= FMT == QL_KV_BF16 ? ~((m >> 15) * 0xFFFFu) : ~((m >> 7) * 0xFFu);
+        }
+      }
+    }
+    if constexpr (FMT == QL_KV_BF16)
+      r = (b >> 15 & 1u) | (b >> 30 & 2u) | (c >> 13 & 4u) | (c >> 28 & 8u);
+    else
+      r = (b >> 7 & 1u) | (b >> 14 & 2u) | (b >> 21 & 4u) | (b >> 28 & 8u);
+    r |= row_or<0xB1>(r);
+    r |= row_or<0x4E>(r);
+    r |= row_or<0x141>(r);
+    r |= row_or<0x140>(r);
+    return r;
   }
 };
 
@@ -203,171 +279,9 @@ __device__ __forceinline__ int q_element(int s, int g) {
   return (s / per * 4 + g) * EC + s % per * 8;
 }
 
-template <int FMT>
-__device__ __forceinline__ bool non_finite(u32x4 v) {
-  constexpr uint32_t e = FMT == QL_KV_BF16 ? 0x7F80u : 0x7C00u;
-  bool r = false;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) r |= (v[x] & e) == e || (v[x] >> 16 & e) == e;
-  return r;
-}
-
-template <int FMT, int D, int MT>
-struct State {
-  static constexpr int KS = D / 32;     // steps of the first product
-  static constexpr int DT = D / 16;     // d-tiles of the second
-  u32x4 q[MT][KS];
-  f32x4 o[MT][DT];
-  float qs[MT];                         // scale * log2(e) * the row's power of two
-  float m[MT], l[MT];
-};
-
-// Which keys a lane's row (column) sees in a masked tile, per m-tile.
-struct RowMask {
-  int last;          // chain: last visible position
-  uint64_t bits;     // tree: visible new tokens
-};
-
-// One tile.  MASKED: some key of it is hidden from some row: `base` its first
-// position, `n0`, `n1` how many of each block's 16 positions are there.
-template <bool MASKED, int FMT, int D, int MT>
-__device__ __forceinline__ void attend(State<FMT, D, MT>& st, Tile<FMT, D>& tile, int base, int n0,
-                                       int n1, int ctx, bool tree, const RowMask (&rm)[MT],
-                                       int lane) {
-  using L = KvLayout<FMT, D>;
-  constexpr int KS = State<FMT, D, MT>::KS;
-  const int g = lane >> 4;
-  f32x4 s[MT][2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) s[mt][t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const u32x4 a = tile.k_operand(t, k);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) s[mt][t] = mma<FMT>(a, st.q[mt][k], s[mt][t]);
-    }
-  }
-
-  // row scales of the lane's eight keys
-  float kf[2][4], vb[2][4], iv[2][4];
-  if constexpr (FMT != QL_KV_BF16) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t kb = tile.ke[t] >> (8 * r) & 0xFFu, b = tile.ve[t] >> (8 * r) & 0xFFu;
-        kf[t][r] = __uint_as_float(kb << 23);
-        vb[t][r] = static_cast<float>(b);
-        iv[t][r] = __uint_as_float((254u - b) << 23);
-      }
-  }
-
-  u32x4 p[MT], p_lo[MT];
-  uint32_t seen[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    float z[2][4];
-    seen[mt] = 0;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float v;
-        if constexpr (FMT == QL_KV_BF16) v = s[mt][t][r] * st.qs[mt];
-        else v = __builtin_fmaf(s[mt][t][r] * kf[t][r], st.qs[mt], vb[t][r]);
-        if constexpr (MASKED) {
-          const int in = 4 * g + r, pos = base + 16 * t + in, node = pos - ctx;
-          bool vis = in < (t ? n1 : n0);
-          if (tree) vis = vis && (node < 0 || (node < 64 && (rm[mt].bits >> (node & 63) & 1)));
-          else vis = vis && pos <= rm[mt].last;
-          if (!vis) v = -__builtin_inff();
-          seen[mt] |= vis ? 1u << (4 * t + r) : 0u;
-        }
-        z[t][r] = v;
-      }
-    float mx = z[0][0];
-#pragma unroll
-    for (int x = 1; x < 8; ++x) mx = __builtin_fmaxf(mx, z[x >> 2][x & 3]);
-    mx = column_max(mx);
-    if (__any(mx > st.m[mt] + kSlack)) {
-      const float mn = __builtin_fmaxf(st.m[mt], mx);
-      const float f = __builtin_amdgcn_exp2f(st.m[mt] - mn);
-      st.m[mt] = mn;
-      st.l[mt] *= f;
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) st.o[mt][d] *= f;
-    }
-    float w[8];
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      w[x] = __builtin_amdgcn_exp2f(z[x >> 2][x & 3] - st.m[mt]);
-      float add = w[x];
-      if constexpr (FMT != QL_KV_BF16) {
-        add *= iv[x >> 2][x & 3];
-        if constexpr (MASKED) add = seen[mt] >> x & 1 ? add : 0.0f;   // iv may be anything there
-      }
-      st.l[mt] += add;
-    }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if constexpr (FMT == QL_KV_BF16) {
-        p[mt][x] = pack_bf16x2(w[2 * x], w[2 * x + 1]);
-        p_lo[mt][x] = pack_bf16x2(w[2 * x] - __uint_as_float(p[mt][x] << 16),
-                                  w[2 * x + 1] - __uint_as_float(p[mt][x] & 0xFFFF0000u));
-      } else {
-        const f32x2 v = {w[2 * x], w[2 * x + 1]};
-        p[mt][x] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
-      }
-    }
-  }
-
-  if constexpr (MASKED) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int left = (t ? n1 : n0) - 4 * g;
-      tile.clear_v(t, left < 0 ? 0 : left > 4 ? 4 : left);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < L::kLoads; ++i) {
-    u32x4 v[L::kDC];
-    tile.v_operands(i, v);
-#pragma unroll
-    for (int q = 0; q < L::kDC; ++q) {
-      const int d = i * L::kDC + q;
-      if constexpr (MASKED) {
-        if (__any(non_finite<FMT>(v[q]))) {
-          // A zero weight does not hide a NaN or infinity in the product, so
-          // the keys enter one by one, each only in the rows that see it.
-          for (int x = 0; x < 32; ++x) {
-            const int gk = x >> 3, j = x & 7;
-            const uint32_t half = j & 1 ? 0xFFFF0000u : 0xFFFFu;
-            u32x4 one, sel;
-            for (int y = 0; y < 4; ++y) sel[y] = g == gk && y == j >> 1 ? half : 0u;
-            one = v[q] & sel;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              f32x4 c = mma<FMT>(one, p[mt] & sel, st.o[mt][d]);
-              if constexpr (FMT == QL_KV_BF16) c = mma<FMT>(one, p_lo[mt] & sel, c);
-              const bool vis = __shfl(seen[mt], gk * 16 + (lane & 15), 64) >> j & 1;
-#pragma unroll
-              for (int y = 0; y < 4; ++y) st.o[mt][d][y] = vis ? c[y] : st.o[mt][d][y];
-            }
-          }
-          continue;
-        }
-      }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        st.o[mt][d] = mma<FMT>(v[q], p[mt], st.o[mt][d]);
-        if constexpr (FMT == QL_KV_BF16) st.o[mt][d] = mma<FMT>(v[q], p_lo[mt], st.o[mt][d]);
-      }
-    }
-  }
-}
-
+// ---------------------------------------------------------------------------
+// Sequences, rows, splits
+// ---------------------------------------------------------------------------
 // Keys of one split of a sequence of `len` keys: the planned chunk, or more
 // where the sequence is longer than the plan's splits cover.
 __device__ __forceinline__ int chunk_of(int len, int chunk, int splits) {
@@ -380,213 +294,634 @@ __device__ __forceinline__ int splits_of(int len, int chunk) {
 }
 
 struct Seq {
-  int q0, nodes, rows_q, len, ctx;   // rows_q: its queries that lie in q and y
+  int q0, rows_q, len, ctx;   // rows_q: its queries that lie in q and y
 };
 __device__ __forceinline__ Seq sequence(const KvAttnArgs& a, int b) {
   Seq s;
   s.q0 = a.cu_q[b];
-  s.nodes = a.cu_q[b + 1] - s.q0;
+  const int nodes = a.cu_q[b + 1] - s.q0;
   const int64_t room = a.tokens - s.q0;
-  s.rows_q = s.q0 < 0 || s.nodes < 0 || room <= 0 ? 0 : room < s.nodes ? int(room) : s.nodes;
+  s.rows_q = s.q0 < 0 || nodes < 0 || room <= 0 ? 0 : room < nodes ? int(room) : nodes;
   if (s.rows_q > a.max_q) s.rows_q = a.max_q;
   const int64_t cap = a.table_cols << a.g.page_shift;
   const int len = a.kv_lens[b];
   s.len = len < 0 ? 0 : len < cap ? len : int(cap);
-  s.ctx = s.len > s.nodes ? s.len - s.nodes : 0;
+  s.ctx = nodes < 0 ? s.len : s.len > nodes ? s.len - nodes : 0;
   return s;
 }
 
-template <int FMT, int D, int MT>
-__global__ __launch_bounds__(64 * kWaves) void kv_attention_kernel(KvAttnArgs a, int row_blocks) {
+// What a thread block works on.
+struct Work {
+  Seq sq;
+  int b, head, split, nsplit, group;
+  int64_t rows, row0;
+  int k0, k1;            // its keys
+  bool any;
+};
+// Row blocks of one unit (sequence, head, split) read the same keys: their
+// ids are 8 apart, so that they run on one XCD and share its L2.
+template <int ROWS>
+__device__ __forceinline__ Work work_of(const KvAttnArgs& a) {
+  Work w;
+  const int slot = int(blockIdx.x >> 3);
+  int unit = slot / a.row_blocks * 8 + int(blockIdx.x & 7);
+  w.row0 = int64_t(slot % a.row_blocks) * ROWS;
+  w.any = unit < a.units;
+  if (!w.any) return w;
+  w.split = unit % a.splits;
+  unit /= a.splits;
+  w.head = unit % a.g.n_kv;
+  w.b = unit / a.g.n_kv;
+  w.group = a.n_q / a.g.n_kv;
+  w.sq = sequence(a, w.b);
+  w.rows = int64_t(w.sq.rows_q) * w.group;
+  const int chunk = chunk_of(w.sq.len, a.chunk, a.splits);
+  w.nsplit = splits_of(w.sq.len, chunk);
+  w.any = w.row0 < w.rows && w.split < w.nsplit;
+  w.k0 = w.split * chunk;
+  w.k1 = w.sq.len - w.k0 < chunk ? w.sq.len : w.k0 + chunk;
+  if (!a.tree) {
+    // of a chain, no row sees past the block's last token
+    const int64_t last = (w.row0 + ROWS < w.rows ? w.row0 + ROWS : w.rows) - 1;
+    const int64_t lim = int64_t(w.sq.ctx) + last / w.group + 1;
+    if (lim < w.k1) w.k1 = int(lim);
+  }
+  return w;
+}
+// Positions that every row from `row0` on sees.
+__device__ __forceinline__ int open_to(const KvAttnArgs& a, const Work& w, int64_t row0) {
+  const int64_t o = a.tree ? w.sq.ctx : w.sq.ctx + row0 / w.group + 1;
+  return o < w.k1 ? int(o) : w.k1;
+}
+
+// Which new tokens a row sees.
+struct RowMask {
+  int last;          // chain: last visible position
+  uint64_t bits;     // tree: visible new tokens
+};
+// Bit 4 t + r: the row sees key 4 g + r of block t of the tile at `base`.
+__device__ __forceinline__ uint32_t visible(const RowMask& rm, bool tree, int base, int ctx, int g) {
+  uint32_t seen = 0;
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const int pos = base + 16 * (x >> 2) + 4 * g + (x & 3), node = pos - ctx;
+    const bool vis = tree ? node < 0 || (node < 64 && (rm.bits >> (node & 63) & 1)) : pos <= rm.last;
+    seen |= vis ? 1u << x : 0u;
+  }
+  return seen;
+}
+
+// A row's query operands; HALF: scaled by a power of two to fit fp16.
+template <int FMT, int D, bool HALF>
+__device__ __forceinline__ void load_query(const KvAttnArgs& a, const Work& w, int64_t row, int g,
+                                           u32x4 (&q)[D / 32], float& qs, RowMask& rm) {
+  constexpr int KS = D / 32;
+  const bool in = row < w.rows;
+  const int node = in ? int(row / w.group) : 0;
+  const uint16_t* p = static_cast<const uint16_t*>(a.q) + int64_t(w.sq.q0 + node) * a.q_stride +
+                      int64_t(w.head * w.group + (in ? int(row % w.group) : 0)) * D;
+  rm.last = w.sq.ctx + node;
+  rm.bits = a.tree ? a.tree[w.sq.q0 + node] : 0;
+  qs = a.scale * kLog2e;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    q[s] = u32x4{0, 0, 0, 0};
+    if (in) q[s] = *reinterpret_cast<const u32x4*>(p + q_element<FMT, D>(s, g));
+  }
+  if constexpr (HALF) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        amax = __builtin_fmaxf(amax, __builtin_fabsf(__uint_as_float(q[s][x] << 16)));
+        amax = __builtin_fmaxf(amax, __builtin_fabsf(__uint_as_float(q[s][x] & 0xFFFF0000u)));
+      }
+    amax = column_max(amax);
+    // the row's largest value goes to [2^14, 2^15)
+    int e = int(__float_as_uint(amax) >> 23);
+    e = e < 40 ? 40 : e > 254 ? 254 : e;
+    const float down = power(254 + 14 - e);               // 2^(14 - (e - 127))
+    qs *= power(e - 14);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const f32x2 v = {__uint_as_float(q[s][x] << 16) * down,
+                         __uint_as_float(q[s][x] & 0xFFFF0000u) * down};
+        q[s][x] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One row tile's softmax step over a tile of keys
+// ---------------------------------------------------------------------------
+template <int D>
+struct Rows {
+  f32x4 o[D / 16];
+  float m, l;
+  __device__ __forceinline__ void clear() {
+    m = kLowest, l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) o[d] = f32x4{0, 0, 0, 0};
+  }
+};
+
+// From z (scores, V's row exponent added) to the weights' operand p (BF16:
+// and p_lo); iv: 2^-ve.  MASKED: `seen` says which keys count.
+template <int FMT, int D, bool MASKED, bool IV>
+__device__ __forceinline__ void softmax_step(Rows<D>& r, float (&z)[8], const float (&iv)[8],
+                                             uint32_t seen, u32x4& p, u32x4& p_lo) {
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) z[x] = seen >> x & 1 ? z[x] : -__builtin_inff();
+  }
+  float mx = z[0];
+#pragma unroll
+  for (int x = 1; x < 8; ++x) mx = __builtin_fmaxf(mx, z[x]);
+  mx = column_max(mx);
+  if (__any(mx > r.m + kSlack)) {
+    const float mn = __builtin_fmaxf(r.m, mx);
+    const float f = __builtin_amdgcn_exp2f(r.m - mn);
+    r.m = mn;
+    r.l *= f;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) r.o[d] *= f;
+  }
+  float w[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    w[x] = __builtin_amdgcn_exp2f(z[x] - r.m);
+    if constexpr (IV) {
+      if constexpr (MASKED) r.l += seen >> x & 1 ? w[x] * iv[x] : 0.0f;   // iv may be NaN
+      else r.l = __builtin_fmaf(w[x], iv[x], r.l);
+    } else {
+      r.l += w[x];
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    if constexpr (FMT == QL_KV_BF16) {
+      p[x] = pack_bf16x2(w[2 * x], w[2 * x + 1]);
+      p_lo[x] = pack_bf16x2(w[2 * x] - __uint_as_float(p[x] << 16),
+                            w[2 * x + 1] - __uint_as_float(p[x] & 0xFFFF0000u));
+    } else {
+      const f32x2 v = {w[2 * x], w[2 * x + 1]};
+      p[x] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+    }
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ f32x4 weigh(u32x4 v, u32x4 p, u32x4 p_lo, f32x4 o) {
+  o = mma<FMT != QL_KV_BF16>(v, p, o);
+  if constexpr (FMT == QL_KV_BF16) o = mma<false>(v, p_lo, o);
+  return o;
+}
+
+// Row `row`'s place in y and in the partial results.
+__device__ __forceinline__ int64_t out_row(const KvAttnArgs& a, const Work& w, int64_t row) {
+  return int64_t(w.sq.q0 + int(row / w.group)) * a.n_q + w.head * w.group + int(row % w.group);
+}
+
+// ---------------------------------------------------------------------------
+// narrow: 16 rows, keys split over the waves
+// ---------------------------------------------------------------------------
+template <int FMT, int D>
+struct Tile {
   using L = KvLayout<FMT, D>;
-  constexpr int KS = D / 32, DT = D / 16;
-  constexpr int DCH = D < 128 ? D : 128;        // elements of d merged at a time
-  __shared__ float sm_m[kWaves][16 * MT], sm_l[kWaves][16 * MT];
+  Block<FMT, D> k[2], v[2];
+  uint32_t ke[2];      // E4M3: row exponent of key lane % 16; NVFP4: of keys 4 g .. 4 g + 3
+  uint32_t ve[2];      // of keys 4 g .. 4 g + 3
+  __device__ __forceinline__ void load(int t, const uint8_t* codes, const uint8_t* scales, int lane) {
+    k[t].load_k(codes, scales, lane);
+    v[t].load_v(codes, scales, lane);
+    if constexpr (FMT == QL_KV_E4M3) {
+      ke[t] = scales[L::k_exp(lane & 15)];
+      ve[t] = *reinterpret_cast<const uint32_t*>(scales + L::v_exp(lane >> 4 << 2));
+    } else if constexpr (FMT == QL_KV_NVFP4) {
+      const uint2 e = *reinterpret_cast<const uint2*>(scales + L::k_exp(lane >> 4 << 2));
+      ke[t] = e.x, ve[t] = e.y;
+    }
+  }
+  __device__ __forceinline__ void take(const Tile& o) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      k[t].take(o.k[t]);
+      v[t].take(o.v[t]);
+      if constexpr (FMT != QL_KV_BF16) ke[t] = o.ke[t], ve[t] = o.ve[t];
+    }
+  }
+};
+
+// One tile.  n0, n1: how many of each block's 16 keys are there.  MASKED: some
+// are hidden from some row, or missing; otherwise n0 or n1 is 0 only where a
+// block's page is absent, and the tile holds the other block in its place.
+template <int FMT, int D, bool MASKED>
+__device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&q)[D / 32], float qs,
+                                            Tile<FMT, D>& tile, int n0, int n1, uint32_t seen,
+                                            int g) {
+  using L = KvLayout<FMT, D>;
+  constexpr bool HALF = FMT == QL_KV_NVFP4;
+  f32x4 s[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    float p = 1.0f;
+    if constexpr (FMT == QL_KV_E4M3) p = power(tile.ke[t]);
+    s[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+      s[t] = mma<HALF>(tile.k[t].template k_operand<HALF>(k, p), q[k], s[t]);
+  }
+  const float hide0 = MASKED || n0 ? 0.0f : -__builtin_inff();
+  const float hide1 = MASKED || n1 ? 0.0f : -__builtin_inff();
+  float z[8], iv[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const int t = x >> 2, k = x & 3;
+    const float hide = t ? hide1 : hide0;
+    if constexpr (FMT == QL_KV_BF16) {
+      z[x] = __builtin_fmaf(s[t][k], qs, hide);
+    } else {
+      const uint32_t b = tile.ve[t] >> (8 * k) & 0xFFu;
+      iv[x] = power(254u - b);
+      float v = s[t][k];
+      if constexpr (HALF) v *= power(tile.ke[t] >> (8 * k) & 0xFFu);
+      z[x] = __builtin_fmaf(v, qs, static_cast<float>(b) + hide);
+    }
+  }
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int left = (t ? n1 : n0) - 4 * g, keys = left < 0 ? 0 : left > 4 ? 4 : left;
+      seen &= ~(0xFu << (4 * t)) | ((1u << keys) - 1u) << (4 * t);
+      tile.v[t].clear_v(keys);
+    }
+  }
+  u32x4 p, p_lo;
+  softmax_step<FMT, D, MASKED, FMT != QL_KV_BF16>(r, z, iv, seen, p, p_lo);
+  if constexpr (MASKED) {
+    // A zero weight does not hide a NaN or an infinity in the product: they
+    // are cleared, and the sum of weights of a row that sees one is made NaN.
+    if (__any((tile.v[0].non_finite() | tile.v[1].non_finite()) != 0)) {
+      const uint32_t bad = tile.v[0].clear_non_finite() | tile.v[1].clear_non_finite() << 4;
+      if (seen & bad) r.l = __builtin_nanf("");
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < L::kLoads; ++i) {
+    uint2 a[L::kDC], b[L::kDC];
+    tile.v[0].v_operands(i, a);
+    tile.v[1].v_operands(i, b);
+#pragma unroll
+    for (int x = 0; x < L::kDC; ++x) {
+      f32x4& o = r.o[i * L::kDC + x];
+      o = weigh<FMT>(u32x4{a[x].x, a[x].y, b[x].x, b[x].y}, p, p_lo, o);
+    }
+  }
+}
+
+// Waves per SIMD that the register budget is set for (fewer spill).
+constexpr int narrow_waves(int fmt, int d) {
+  return d == 64 ? 3 : d == 128 ? (fmt == QL_KV_BF16 ? 2 : 3) : fmt == QL_KV_NVFP4 ? 2 : 1;
+}
+
+template <int FMT, int D>
+__global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attention_narrow_kernel(
+    KvAttnArgs a) {
+  using L = KvLayout<FMT, D>;
+  constexpr int DCH = D < 128 ? D : 128;        // elements of d joined at a time
+  __shared__ float sm_m[kWaves][16], sm_l[kWaves][16];
   __shared__ __align__(16) float sm_o[kWaves][16][DCH + 4];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  int id = blockIdx.x;
-  const int rb = id % row_blocks;
-  id /= row_blocks;
-  const int split = id % a.splits;
-  id /= a.splits;
-  const int head = id % a.g.n_kv, b = id / a.g.n_kv;
-  const int group = a.n_q / a.g.n_kv;
-  const Seq sq = sequence(a, b);
-  const int64_t rows = int64_t(sq.rows_q) * group, row0 = int64_t(rb) * (16 * MT);
-  if (row0 >= rows) return;
-  const int chunk = chunk_of(sq.len, a.chunk, a.splits), nsplit = splits_of(sq.len, chunk);
-  if (split >= nsplit) return;
-  const int k0 = split * chunk;
-  int k1 = sq.len - k0 < chunk ? sq.len : k0 + chunk;
-  if (!a.tree) {
-    // no row of this block sees past its last token
-    const int64_t last = (row0 + 16 * MT < rows ? row0 + 16 * MT : rows) - 1;
-    const int64_t lim = int64_t(sq.ctx) + last / group + 1;
-    if (lim < k1) k1 = int(lim);
-  }
-
-  State<FMT, D, MT> st;
-  RowMask rm[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int64_t r = row0 + 16 * mt + n;
-    const bool in = r < rows;
-    const int node = in ? int(r / group) : 0;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + int64_t(sq.q0 + node) * a.q_stride +
-                        int64_t(head * group + (in ? int(r % group) : 0)) * D;
-    rm[mt].last = sq.ctx + node;
-    rm[mt].bits = a.tree ? a.tree[sq.q0 + node] : 0;
-    u32x4 w[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      w[s] = u32x4{0, 0, 0, 0};
-      if (in) w[s] = *reinterpret_cast<const u32x4*>(q + q_element<FMT, D>(s, g));
-    }
-    st.qs[mt] = a.scale * kLog2e;
-    if constexpr (FMT == QL_KV_BF16) {
-#pragma unroll
-      for (int s = 0; s < KS; ++s) st.q[mt][s] = w[s];
-    } else {
-      float amax = 0.0f;
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          amax = __builtin_fmaxf(amax, __builtin_fabsf(__uint_as_float(w[s][x] << 16)));
-          amax = __builtin_fmaxf(amax, __builtin_fabsf(__uint_as_float(w[s][x] & 0xFFFF0000u)));
-        }
-      amax = column_max(amax);
-      // the row's largest value goes to [2^14, 2^15)
-      int e = int(__float_as_uint(amax) >> 23);
-      e = e < 40 ? 40 : e > 254 ? 254 : e;
-      const float down = __uint_as_float(uint32_t(254 + 14 - e) << 23);   // 2^(14 - (e - 127))
-      st.qs[mt] *= __uint_as_float(uint32_t(e - 14) << 23);
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const f32x2 v = {__uint_as_float(w[s][x] << 16) * down,
-                           __uint_as_float(w[s][x] & 0xFFFF0000u) * down};
-          st.q[mt][s][x] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
-        }
-    }
-    st.m[mt] = kLowest;
-    st.l[mt] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) st.o[mt][d] = f32x4{0, 0, 0, 0};
-  }
+  const Work w = work_of<16>(a);
+  if (!w.any) return;
+  u32x4 q[D / 32];
+  float qs;
+  RowMask rm;
+  load_query<FMT, D, FMT == QL_KV_NVFP4>(a, w, w.row0 + n, g, q, qs, rm);
+  Rows<D> r;
+  r.clear();
 
   // tiles first, first + 4, ... of the split
-  const int first = k0 / kTile + wave;
-  const int tiles = (k1 + kTile - 1) / kTile;
+  const int first = w.k0 / kTile + wave;
+  const int tiles = (w.k1 + kTile - 1) / kTile;
   const int count = tiles > first ? (tiles - first + kWaves - 1) / kWaves : 0;
   const int per_page = a.g.page_shift - 4;             // log2(blocks of a page)
-  const int32_t* table = a.table + int64_t(b) * a.table_stride;
+  const int32_t* table = a.table + int64_t(w.b) * a.table_stride;
   int pages = -1;   // of 32 iterations' two blocks, one per lane
-  auto fetch_pages = [&](int it) {
-    const int block = 2 * (first + kWaves * (it + (lane >> 1))) + (lane & 1);
-    pages = -1;
-    if (int64_t(block) * 16 < k1) {
-      pages = table[block >> per_page];
-      if (pages >= a.g.n_pages) pages = -1;
-    }
-  };
+  // An absent block of a tile is read from the tile's other block.
   auto load = [&](int it, Tile<FMT, D>& tile, int& p0, int& p1) {
-    if ((it & 31) == 0) fetch_pages(it);
+    if ((it & 31) == 0) {
+      const int mine = 2 * (first + kWaves * (it + (lane >> 1))) + (lane & 1);
+      pages = -1;
+      if (int64_t(mine) * 16 < w.k1) {
+        pages = table[mine >> per_page];
+        if (pages >= a.g.n_pages) pages = -1;
+      }
+    }
     const int block = 2 * (first + kWaves * it);
     p0 = __builtin_amdgcn_readlane(pages, 2 * (it & 31));
     p1 = __builtin_amdgcn_readlane(pages, 2 * (it & 31) + 1);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int page = t ? p1 : p0;
-      const int64_t at = kv_block(a.g, page < 0 ? 0 : page, head, (block + t) & ((1 << per_page) - 1));
+      const int own = t ? p1 : p0, other = t ? p0 : p1;
+      const int page = own >= 0 ? own : other >= 0 ? other : 0;
+      const int in = (own >= 0 ? block + t : block + 1 - t) & ((1 << per_page) - 1);
+      const int64_t at = kv_block(a.g, page, w.head, in);
       tile.load(t, a.g.codes + at * L::kCodes, a.g.scales + at * L::kScales, lane);
     }
   };
   if (count > 0) {
+    // first the tiles that every row sees, then those with hidden keys
+    const int open = open_to(a, w, w.row0) / kTile;
+    const int whole = open > first ? (open - first + kWaves - 1) / kWaves : 0;
     Tile<FMT, D> cur, nxt;
-    int c0, c1, x0 = 0, x1 = 0;
+    int c0, c1, x0 = 0, x1 = 0, it = 0;
     load(0, cur, c0, c1);
-    for (int it = 0; it < count; ++it) {
+    for (; it < whole; ++it) {
       if (it + 1 < count) load(it + 1, nxt, x0, x1);
-      const int base = (first + kWaves * it) * kTile;
-      if (base + kTile > sq.ctx || base + kTile > k1 || (c0 | c1) < 0) {
-        const int left = k1 - base;
-        const int n0 = c0 < 0 ? 0 : left, n1 = c1 < 0 ? 0 : left - 16;
-        attend<true, FMT, D, MT>(st, cur, base, n0, n1, sq.ctx, a.tree != nullptr, rm, lane);
-      } else {
-        attend<false, FMT, D, MT>(st, cur, base, 16, 16, sq.ctx, false, rm, lane);
-      }
-      cur = nxt;
+      if (c0 >= 0 || c1 >= 0)
+        narrow_tile<FMT, D, false>(r, q, qs, cur, c0 >= 0, c1 >= 0, 0, g);
+      cur.take(nxt);
+      c0 = x0, c1 = x1;
+    }
+    for (; it < count; ++it) {
+      if (it + 1 < count) load(it + 1, nxt, x0, x1);
+      const int base = (first + kWaves * it) * kTile, left = w.k1 - base;
+      narrow_tile<FMT, D, true>(r, q, qs, cur, c0 < 0 ? 0 : left, c1 < 0 ? 0 : left - 16,
+                                visible(rm, a.tree != nullptr, base, w.sq.ctx, g), g);
+      cur.take(nxt);
       c0 = x0, c1 = x1;
     }
   }
 
   // the four waves' parts, in wave order
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    st.l[mt] = column_sum(st.l[mt]);
-    if (g == 0) sm_m[wave][16 * mt + n] = st.m[mt], sm_l[wave][16 * mt + n] = st.l[mt];
-  }
+  r.l = column_sum(r.l);
+  if (g == 0) sm_m[wave][n] = r.m, sm_l[wave][n] = r.l;
   __syncthreads();
+  float top = sm_m[0][n];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    float top = sm_m[0][16 * mt + n];
+  for (int x = 1; x < kWaves; ++x) top = __builtin_fmaxf(top, sm_m[x][n]);
+  const float f = __builtin_amdgcn_exp2f(r.m - top);
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = __builtin_fmaxf(top, sm_m[w][16 * mt + n]);
-    const float f = __builtin_amdgcn_exp2f(st.m[mt] - top);
+  for (int part = 0; part < D / DCH; ++part) {
+    // lane (n, g) holds, of each load i, the 4 kDC elements from
+    // 16 kDC i + 4 kDC g on: element kDC r + q is row r of d-tile kDC i + q
 #pragma unroll
-    for (int part = 0; part < D / DCH; ++part) {
-      // lane (n, g) holds, of each load i, the 4 kDC elements from
-      // 16 kDC i + 4 kDC g on: element kDC r + q is row r of d-tile kDC i + q
+    for (int i = 0; i < L::kLoads; ++i) {
+      const int d0 = 16 * L::kDC * i;
+      if (d0 / DCH != part) continue;
+#pragma unroll
+      for (int x = 0; x < 4 * L::kDC; x += 4) {
+        f32x4 v;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) v[y] = r.o[L::kDC * i + (x + y) % L::kDC][(x + y) / L::kDC] * f;
+        *reinterpret_cast<f32x4*>(&sm_o[wave][n][d0 % DCH + 4 * L::kDC * g + x]) = v;
+      }
+    }
+    __syncthreads();
+    constexpr int kCols = DCH / 8;      // threads per row, 8 elements each
+    const int row = threadIdx.x / kCols, c = threadIdx.x % kCols * 8;
+    if (row < 16 && w.row0 + row < w.rows) {
+      float tm = sm_m[0][row];
+#pragma unroll
+      for (int x = 1; x < kWaves; ++x) tm = __builtin_fmaxf(tm, sm_m[x][row]);
+      float l = 0.0f, v[8] = {};
+#pragma unroll
+      for (int x = 0; x < kWaves; ++x) {
+        l += sm_l[x][row] * __builtin_amdgcn_exp2f(sm_m[x][row] - tm);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) v[y] += sm_o[x][row][c + y];
+      }
+      const int64_t out = out_row(a, w, w.row0 + row);
+      if (w.nsplit == 1) {
+        uint32_t y[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          y[x] = l == 0.0f ? 0u : pack_bf16x2(v[2 * x] / l, v[2 * x + 1] / l);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out * D + part * DCH + c) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+      } else {
+        const int64_t at = int64_t(w.split) * a.tokens * a.n_q + out;
+        float4* o = reinterpret_cast<float4*>(a.part_o + at * D + part * DCH + c);
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        if (part == 0 && c == 0) a.part_ml[2 * at] = tm, a.part_ml[2 * at + 1] = l;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// wide: 64 MT rows, tiles shared through LDS
+// ---------------------------------------------------------------------------
+template <int FMT, int D>
+struct Shared {        // one tile's operands
+  u32x4 k[2][D / 32][64];
+  u32x4 v[D / 16][64];
+  float ve[kTile];     // V's row exponent + 127; -inf: the key is missing
+  float iv[kTile];     // 2^-that; NaN: the row holds a NaN or an infinity
+};
+
+// The quarter of a tile that a wave turns into operands: block t's K or V.
+template <int FMT, int D>
+struct Quarter {
+  using L = KvLayout<FMT, D>;
+  Block<FMT, D> x;
+  uint32_t e;          // row exponent of key lane % 16
+  int keys;            // keys of the block that are there
+
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, bool is_v,
+                                       int lane) {
+    if (is_v) x.load_v(codes, scales, lane);
+    else x.load_k(codes, scales, lane);
+    if constexpr (FMT != QL_KV_BF16) e = scales[L::k_exp(lane & 15) + (is_v ? 4 : 0)];
+  }
+  // CHECK: keys of this tile may be hidden from some row.
+  __device__ __forceinline__ void store(Shared<FMT, D>& sh, int t, bool is_v, bool check, int lane) {
+    const int n = lane & 15, g = lane >> 4;
+    if (!is_v) {
+      float p = 1.0f;
+      if constexpr (FMT != QL_KV_BF16) p = power(e);
+      const uint32_t keep = n < keys ? ~0u : 0u;
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s)
+        sh.k[t][s][lane] = x.template k_operand<false>(s, p) & keep;
+    } else {
+      uint32_t bad = 0;
+      if (keys < 16) {
+        const int left = keys - 4 * g;
+        x.clear_v(left < 0 ? 0 : left > 4 ? 4 : left);
+      }
+      if (check && __any(x.non_finite() != 0)) {
+        // as in narrow_tile; lane n's key is in quad n / 4
+        bad = x.clear_non_finite();
+        bad = __shfl(bad, (n >> 2) * 16, 64) >> (n & 3) & 1u;
+      }
 #pragma unroll
       for (int i = 0; i < L::kLoads; ++i) {
-        const int d0 = 16 * L::kDC * i;
-        if (d0 / DCH != part) continue;
+        uint2 r[L::kDC];
+        x.v_operands(i, r);
 #pragma unroll
-        for (int x = 0; x < 4 * L::kDC; x += 4) {
-          f32x4 v;
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            v[y] = st.o[mt][L::kDC * i + (x + y) % L::kDC][(x + y) / L::kDC] * f;
-          *reinterpret_cast<f32x4*>(&sm_o[wave][n][d0 % DCH + 4 * L::kDC * g + x]) = v;
-        }
+        for (int q = 0; q < L::kDC; ++q)
+          reinterpret_cast<uint2*>(&sh.v[i * L::kDC + q][lane])[t] = r[q];
       }
-      __syncthreads();
-      constexpr int kCols = DCH / 8;      // threads per row, 8 elements each
-      const int row = threadIdx.x / kCols, c = threadIdx.x % kCols * 8;
-      const int64_t r = row0 + 16 * mt + row;
-      if (row < 16 && r < rows) {
-        float tm = sm_m[0][16 * mt + row];
+      if (g == 0) {
+        float ve = 0.0f, iv = 1.0f;
+        if constexpr (FMT != QL_KV_BF16) ve = static_cast<float>(e), iv = power(254u - e);
+        sh.ve[16 * t + n] = n < keys ? ve : -__builtin_inff();
+        sh.iv[16 * t + n] = n >= keys ? 0.0f : bad ? __builtin_nanf("") : iv;
+      }
+    }
+  }
+};
+
+template <int FMT, int D, int MT, bool MASKED>
+__device__ __forceinline__ void wide_tile(Rows<D> (&r)[MT], const u32x4 (&q)[MT][D / 32],
+                                          const float (&qs)[MT], const Shared<FMT, D>& sh,
+                                          const uint32_t (&seen)[MT], int lane) {
+  const int g = lane >> 4;
+  f32x4 s[MT][2];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) tm = __builtin_fmaxf(tm, sm_m[w][16 * mt + row]);
-        float l = 0.0f, v[8] = {};
+  for (int t = 0; t < 2; ++t) {
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          l += sm_l[w][16 * mt + row] * __builtin_amdgcn_exp2f(sm_m[w][16 * mt + row] - tm);
+    for (int mt = 0; mt < MT; ++mt) s[mt][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int x = 0; x < 8; ++x) v[x] += sm_o[w][row][c + x];
-        }
-        const int64_t out = int64_t(sq.q0 + int(r / group)) * a.n_q + head * group + int(r % group);
-        if (nsplit == 1) {
-          uint32_t y[4];
+    for (int k = 0; k < D / 32; ++k) {
+      const u32x4 a = sh.k[t][k][lane];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            y[x] = l == 0.0f ? 0u : pack_bf16x2(v[2 * x] / l, v[2 * x + 1] / l);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out * D + part * DCH + c) =
-              make_uint4(y[0], y[1], y[2], y[3]);
-        } else {
-          const int64_t at = int64_t(split) * a.tokens * a.n_q + out;
-          float4* o = reinterpret_cast<float4*>(a.part_o + at * D + part * DCH + c);
-          o[0] = make_float4(v[0], v[1], v[2], v[3]);
-          o[1] = make_float4(v[4], v[5], v[6], v[7]);
-          if (part == 0 && c == 0) a.part_ml[2 * at] = tm, a.part_ml[2 * at + 1] = l;
-        }
+      for (int mt = 0; mt < MT; ++mt) s[mt][t] = mma<false>(a, q[mt][k], s[mt][t]);
+    }
+  }
+  float ve[8], iv[8];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(&sh.ve[16 * t + 4 * g]);
+    const f32x4 b = *reinterpret_cast<const f32x4*>(&sh.iv[16 * t + 4 * g]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) ve[4 * t + k] = a[k], iv[4 * t + k] = b[k];
+  }
+  u32x4 p[MT], p_lo[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    float z[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) z[x] = __builtin_fmaf(s[mt][x >> 2][x & 3], qs[mt], ve[x]);
+    softmax_step<FMT, D, MASKED, true>(r[mt], z, iv, seen[mt], p[mt], p_lo[mt]);
+  }
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d) {
+    const u32x4 v = sh.v[d][lane];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) r[mt].o[d] = weigh<FMT>(v, p[mt], p_lo[mt], r[mt].o[d]);
+  }
+}
+
+template <int FMT, int D, int MT>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void kv_attention_wide_kernel(KvAttnArgs a) {
+  using L = KvLayout<FMT, D>;
+  extern __shared__ __align__(16) uint8_t lds[];
+  Shared<FMT, D>* sh = reinterpret_cast<Shared<FMT, D>*>(lds);      // two tiles
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const Work w = work_of<64 * MT>(a);
+  if (!w.any) return;
+  const int64_t row0 = w.row0 + wave * (16 * MT);
+  const bool active = row0 < w.rows;
+  u32x4 q[MT][D / 32];
+  float qs[MT];
+  RowMask rm[MT];
+  Rows<D> r[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    load_query<FMT, D, false>(a, w, row0 + 16 * mt + n, g, q[mt], qs[mt], rm[mt]);
+    r[mt].clear();
+  }
+
+  const int first = w.k0 / kTile, tiles = (w.k1 + kTile - 1) / kTile;
+  const int open = open_to(a, w, w.row0) / kTile;                    // of the whole block
+  const int mine = active ? open_to(a, w, row0) / kTile : 0;         // of this wave
+  const int t = wave & 1;
+  const bool is_v = wave >> 1;
+  const int per_page = a.g.page_shift - 4;
+  const int32_t* table = a.table + int64_t(w.b) * a.table_stride;
+  int pages = -1;   // of block t of 64 tiles, one per lane
+  auto load = [&](int tile, Quarter<FMT, D>& x) {
+    const int it = tile - first, block = 2 * tile + t;
+    if ((it & 63) == 0) {
+      const int ahead = block + 2 * lane;
+      pages = -1;
+      if (int64_t(ahead) * 16 < w.k1) {
+        pages = table[ahead >> per_page];
+        if (pages >= a.g.n_pages) pages = -1;
+      }
+    }
+    const int page = __builtin_amdgcn_readlane(pages, it & 63);
+    const int left = w.k1 - 16 * block;
+    x.keys = page < 0 || left < 0 ? 0 : left < 16 ? left : 16;
+    const int64_t at = kv_block(a.g, page < 0 ? 0 : page, w.head, block & ((1 << per_page) - 1));
+    x.load(a.g.codes + at * L::kCodes, a.g.scales + at * L::kScales, is_v, lane);
+  };
+  if (first < tiles) {
+    Quarter<FMT, D> x;
+    load(first, x);
+    x.store(sh[0], t, is_v, first >= open, lane);
+    if (first + 1 < tiles) load(first + 1, x);
+    __syncthreads();
+    for (int i = first; i < tiles; ++i) {
+      const int at = (i - first) & 1;
+      if (i + 1 < tiles) {
+        // the other buffer: every wave has left it before the last barrier
+        x.store(sh[at ^ 1], t, is_v, i + 1 >= open, lane);
+        if (i + 2 < tiles) load(i + 2, x);
+      }
+      uint32_t seen[MT] = {};
+      if (i < mine) {
+        wide_tile<FMT, D, MT, false>(r, q, qs, sh[at], seen, lane);
+      } else if (active) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          seen[mt] = visible(rm[mt], a.tree != nullptr, i * kTile, w.sq.ctx, g);
+        wide_tile<FMT, D, MT, true>(r, q, qs, sh[at], seen, lane);
       }
       __syncthreads();
     }
+  }
+  if (!active) return;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int64_t row = row0 + 16 * mt + n;
+    const float l = column_sum(r[mt].l);
+    if (row >= w.rows) continue;
+    const int64_t out = out_row(a, w, row);
+    const int64_t at = int64_t(w.split) * a.tokens * a.n_q + out;
+    if (w.nsplit > 1 && g == 0) a.part_ml[2 * at] = r[mt].m, a.part_ml[2 * at + 1] = l;
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i)
+#pragma unroll
+      for (int x = 0; x < 4 * L::kDC; x += 8) {
+        const int d = 16 * L::kDC * i + 4 * L::kDC * g + x;
+        float v[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) v[y] = r[mt].o[L::kDC * i + (x + y) % L::kDC][(x + y) / L::kDC];
+        if (w.nsplit == 1) {
+          uint32_t y[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            y[z] = l == 0.0f ? 0u : pack_bf16x2(v[2 * z] / l, v[2 * z + 1] / l);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out * D + d) =
+              make_uint4(y[0], y[1], y[2], y[3]);
+        } else {
+          float4* o = reinterpret_cast<float4*>(a.part_o + at * D + d);
+          o[0] = make_float4(v[0], v[1], v[2], v[3]);
+          o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      }
   }
 }
 
@@ -619,14 +954,13 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attention_join_kernel(KvAttnAr
 
 }  // namespace
 
-KvAttnPlan kv_attention_plan(int fmt, int d, int n_q, int n_kv, int64_t n_seqs, int64_t max_q,
+KvAttnPlan kv_attention_plan(int d, int n_q, int n_kv, int64_t n_seqs, int64_t max_q,
                              int64_t max_kv) {
-  (void)fmt;
+  (void)d;
   KvAttnPlan p;
   const int64_t rows = max_q * (n_q / n_kv);
-  const int most = d == 256 ? 2 : 4;
-  p.mt = rows <= 16 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
-  p.row_blocks = (rows + 16 * p.mt - 1) / (16 * p.mt);
+  p.rows = rows <= 16 ? 16 : rows <= 64 ? 64 : 128;
+  p.row_blocks = (rows + p.rows - 1) / p.rows;
   // enough blocks for two on each compute unit, and at least 256 keys in one
   const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
   const int64_t blocks = n_seqs * n_kv * p.row_blocks;
@@ -647,19 +981,29 @@ size_t kv_attention_ws_bytes(const KvAttnPlan& p, int64_t tokens, int n_q, int d
   return size_t(p.splits) * size_t(tokens) * size_t(n_q) * size_t(d + 2) * sizeof(float);
 }
 
+template <int FMT, int D, int MT>
+static hipError_t launch_wide(const KvAttnArgs& a, unsigned blocks, hipStream_t s) {
+  constexpr int bytes = 2 * sizeof(Shared<FMT, D>);
+  if constexpr (bytes > 64 * 1024) {
+    static std::atomic<int> done[64];
+    const hipError_t e = lds_limit_once(
+        done, reinterpret_cast<const void*>(kv_attention_wide_kernel<FMT, D, MT>), bytes);
+    if (e != hipSuccess) return e;
+  }
+  kv_attention_wide_kernel<FMT, D, MT><<<blocks, 64 * kWaves, bytes, s>>>(a);
+  return hipGetLastError();
+}
+
 hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a, hipStream_t s) {
-  const int64_t blocks = int64_t(a.n_seqs) * a.g.n_kv * p.row_blocks * p.splits;
+  const int64_t units = int64_t(a.n_seqs) * a.g.n_kv * p.splits;
+  a.units = int(units);
+  a.row_blocks = int(p.row_blocks);
+  const unsigned blocks = unsigned((units + 7) / 8 * 8 * p.row_blocks);
   const hipError_t e = kv_dispatch(fmt, d, [&](auto f, auto n) {
     constexpr int FMT = decltype(f)::value, D = decltype(n)::value;
-    const dim3 grid(static_cast<unsigned>(blocks));
-    const int rb = int(p.row_blocks);
-    if (p.mt == 1) {
-      kv_attention_kernel<FMT, D, 1><<<grid, 64 * kWaves, 0, s>>>(a, rb);
-    } else if (p.mt == 2) {
-      kv_attention_kernel<FMT, D, 2><<<grid, 64 * kWaves, 0, s>>>(a, rb);
-    } else if constexpr (D != 256) {
-      kv_attention_kernel<FMT, D, 4><<<grid, 64 * kWaves, 0, s>>>(a, rb);
-    }
+    if (p.rows == 64) return launch_wide<FMT, D, 1>(a, blocks, s);
+    if (p.rows == 128) return launch_wide<FMT, D, 2>(a, blocks, s);
+    kv_attention_narrow_kernel<FMT, D><<<blocks, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
   });
   if (e != hipSuccess || p.splits < 2) return e;

@@ -134,14 +134,16 @@ struct KvAttnArgs {
   float* part_ml;         // [splits][tokens * n_q][2]
   int splits;
   int chunk;              // keys per split (a multiple of 128)
+  int units;              // n_seqs * n_kv * splits
+  int row_blocks;
 };
 struct KvAttnPlan {
-  int mt;                 // row tiles of 16 per block
+  int rows;               // query rows per block: 16, 64 or 128
   int64_t row_blocks;
   int splits;
   int chunk;
 };
-KvAttnPlan kv_attention_plan(int fmt, int d, int n_q, int n_kv, int64_t n_seqs, int64_t max_q,
+KvAttnPlan kv_attention_plan(int d, int n_q, int n_kv, int64_t n_seqs, int64_t max_q,
                              int64_t max_kv);
 size_t kv_attention_ws_bytes(const KvAttnPlan& p, int64_t tokens, int n_q, int d);
 hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a, hipStream_t s);
