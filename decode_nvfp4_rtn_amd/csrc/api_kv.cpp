@@ -138,7 +138,7 @@ static int check_attention(const ql_kv_cache* cache, int64_t tokens, int64_t n_q
   if (tokens > kMost || n_seqs > 65535 || max_q > kMost || max_kv > kMost - 4096) return QL_ESHAPE;
   if (tokens == 0 || n_seqs == 0 || max_q == 0) return QL_OK;
   const int64_t m = max_q < tokens ? max_q : tokens;
-  if (m * n_q > kMost) return QL_ESHAPE;
+  if (m * n_q > kMost - 4096) return QL_ESHAPE;   // rows are counted in 32 bits
   const KvAttnPlan p = kv_attention_plan(cache->head_dim, int(n_q), cache->n_kv, n_seqs, m,
                                          max_kv);
   if (p.row_blocks > (kMost / 16) / (n_seqs * cache->n_kv * p.splits)) return QL_ESHAPE;

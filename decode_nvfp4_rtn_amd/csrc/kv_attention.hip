@@ -118,6 +118,24 @@ __device__ __forceinline__ uint32_t row_or(uint32_t v) {   // another lane of th
   return uint32_t(__builtin_amdgcn_mov_dpp(int(v), CTRL, 0xF, 0xF, true));
 }
 
+// A block's codes and scales as buffer resources: the base is uniform, so a
+// lane's address is one 32-bit offset.
+struct Source {
+  __amdgpu_buffer_rsrc_t codes, scales;
+};
+template <int FMT, int D>
+__device__ __forceinline__ Source source(const KvGeom& g, int64_t block) {
+  using L = KvLayout<FMT, D>;
+  constexpr int kWord3 = 0x00020000;      // raw buffer
+  Source s;
+  s.codes = __builtin_amdgcn_make_buffer_rsrc(g.codes + block * L::kCodes, 0, L::kCodes, kWord3);
+  s.scales = __builtin_amdgcn_make_buffer_rsrc(g.scales + block * L::kScales, 0, L::kScales, kWord3);
+  return s;
+}
+__device__ __forceinline__ uint32_t load32(__amdgpu_buffer_rsrc_t r, int at) {
+  return __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+}
+
 // One block's (16 keys') K or V bytes that a lane holds.
 template <int FMT, int D>
 struct Block {
@@ -127,25 +145,27 @@ struct Block {
   Words w[L::kLoads];
   uint32_t sc[L::kLoads];                     // NVFP4 group scales (K: of the lane's key, V: of its quad)
 
-  __device__ __forceinline__ void load_k(const uint8_t* codes, const uint8_t* scales, int lane) {
+  __device__ __forceinline__ Words words(const Source& s, int at) {
+    if constexpr (W == 4) return __builtin_amdgcn_raw_buffer_load_b128(s.codes, at, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b64(s.codes, at, 0, 0);
+  }
+  __device__ __forceinline__ void load_k(const Source& s, int lane) {
 #pragma unroll
     for (int i = 0; i < L::kLoads; ++i) {
-      w[i] = *reinterpret_cast<const Words*>(codes + (64 * i + lane) * L::kLoad);
+      w[i] = words(s, lane * L::kLoad + 64 * i * L::kLoad);
       if constexpr (FMT == QL_KV_NVFP4) {
-        const uint8_t* p = scales + (64 * i + lane) * L::kGPC;
-        if constexpr (L::kGPC == 2) sc[i] = *reinterpret_cast<const uint16_t*>(p);
-        else sc[i] = *p;
+        const int at = lane * L::kGPC + 64 * i * L::kGPC;
+        if constexpr (L::kGPC == 2) sc[i] = __builtin_amdgcn_raw_buffer_load_b16(s.scales, at, 0, 0);
+        else sc[i] = __builtin_amdgcn_raw_buffer_load_b8(s.scales, at, 0, 0);
       }
     }
   }
-  __device__ __forceinline__ void load_v(const uint8_t* codes, const uint8_t* scales, int lane) {
+  __device__ __forceinline__ void load_v(const Source& s, int lane) {
 #pragma unroll
     for (int i = 0; i < L::kLoads; ++i) {
-      w[i] = *reinterpret_cast<const Words*>(codes + 16 * L::kRow + (64 * i + lane) * L::kLoad);
-      if constexpr (FMT == QL_KV_NVFP4) {
-        const int group = i * L::kDC + (lane & 15) * L::kDC / 16;
-        sc[i] = *reinterpret_cast<const uint32_t*>(scales + D + group * 16 + (lane >> 4) * 4);
-      }
+      w[i] = words(s, lane * L::kLoad + (16 * L::kRow + 64 * i * L::kLoad));
+      if constexpr (FMT == QL_KV_NVFP4)      // group i kDC + (lane % 16) kDC / 16
+        sc[i] = load32(s.scales, (lane & 15) * L::kDC / 16 * 16 + (lane >> 4) * 4 + (D + i * L::kDC * 16));
     }
   }
   __device__ __forceinline__ void take(const Block& o) {
@@ -184,27 +204,27 @@ struct Block {
     }
   }
 
-  // This block's half (4 of a lane's 8 keys) of the V operands of load i's
-  // kDC d-tiles: bf16 values, or fp16 codes (NVFP4: times group scales).
-  __device__ __forceinline__ void v_operands(int i, uint2 (&r)[L::kDC]) const {
+  // This block's half (4 of a lane's 8 keys) of the V operands of kPer d-tiles
+  // from kPer j on: bf16 values, or fp16 codes (NVFP4: times group scales).
+  static constexpr int kPer = FMT == QL_KV_E4M3 ? 1 : 2;
+  __device__ __forceinline__ void v_operands(int j, uint2 (&r)[kPer]) const {
+    constexpr int per = L::kDC / kPer;        // such pieces of a load
+    const int i = j / per, q = j % per;
     if constexpr (FMT == QL_KV_BF16) {
       r[0] = make_uint2(w[i][0], w[i][1]);
       r[1] = make_uint2(w[i][2], w[i][3]);
     } else if constexpr (FMT == QL_KV_E4M3) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) r[q] = make_uint2(fp8_pair(w[i][q], 0), fp8_pair(w[i][q], 1));
+      r[0] = make_uint2(fp8_pair(w[i][q], 0), fp8_pair(w[i][q], 1));
     } else {
       const f16x2 lo = __builtin_bit_cast(f16x2, fp8_pair(sc[i], 0));
       const f16x2 hi = __builtin_bit_cast(f16x2, fp8_pair(sc[i], 1));
-#pragma unroll
-      for (int q = 0; q < W; ++q) {
-        // bytes (key 0..3) of a pair of elements -> bytes of two keys each:
-        // (d0: keys 0, 1), (d1: keys 0, 1), (d0: keys 2, 3), (d1: keys 2, 3)
-        const uint32_t x = w[i][q];
-        const uint32_t y = (x & 0xF00FF00Fu) | ((x << 4) & 0x0F000F00u) | ((x >> 4) & 0x00F000F0u);
-        r[2 * q] = make_uint2(times(fp4_pair<0>(y), lo), times(fp4_pair<2>(y), hi));
-        r[2 * q + 1] = make_uint2(times(fp4_pair<1>(y), lo), times(fp4_pair<3>(y), hi));
-      }
+      // bytes (key 0..3) of a pair of elements -> bytes of two keys each:
+      // (d0: keys 0, 1), (d1: keys 0, 1), (d0: keys 2, 3), (d1: keys 2, 3)
+      const uint32_t x = w[i][q];
+      uint32_t y = (x & ~0x0F000F00u) | ((x << 4) & 0x0F000F00u);
+      y = (y & ~0x00F000F0u) | ((x >> 4) & 0x00F000F0u);
+      r[0] = make_uint2(times(fp4_pair<0>(y), lo), times(fp4_pair<2>(y), hi));
+      r[1] = make_uint2(times(fp4_pair<1>(y), lo), times(fp4_pair<3>(y), hi));
     }
   }
 
@@ -314,27 +334,29 @@ __device__ __forceinline__ Seq sequence(const KvAttnArgs& a, int b) {
 struct Work {
   Seq sq;
   int b, head, split, nsplit, group;
-  int64_t rows, row0;
+  int rows, row0;
   int k0, k1;            // its keys
   bool any;
 };
-// Row blocks of one unit (sequence, head, split) read the same keys: their
-// ids are 8 apart, so that they run on one XCD and share its L2.
+// Row blocks of one unit (split, sequence, head) read the same keys: their ids
+// are 8 apart, so that they run on one XCD and share its L2.  Heads come
+// fastest and splits last, so that the late splits, which only long sequences
+// have, spread over all XCDs.
 template <int ROWS>
 __device__ __forceinline__ Work work_of(const KvAttnArgs& a) {
   Work w;
   const int slot = int(blockIdx.x >> 3);
   int unit = slot / a.row_blocks * 8 + int(blockIdx.x & 7);
-  w.row0 = int64_t(slot % a.row_blocks) * ROWS;
+  w.row0 = slot % a.row_blocks * ROWS;
   w.any = unit < a.units;
   if (!w.any) return w;
-  w.split = unit % a.splits;
-  unit /= a.splits;
   w.head = unit % a.g.n_kv;
-  w.b = unit / a.g.n_kv;
+  unit /= a.g.n_kv;
+  w.b = unit % a.n_seqs;
+  w.split = unit / a.n_seqs;
   w.group = a.n_q / a.g.n_kv;
   w.sq = sequence(a, w.b);
-  w.rows = int64_t(w.sq.rows_q) * w.group;
+  w.rows = w.sq.rows_q * w.group;
   const int chunk = chunk_of(w.sq.len, a.chunk, a.splits);
   w.nsplit = splits_of(w.sq.len, chunk);
   w.any = w.row0 < w.rows && w.split < w.nsplit;
@@ -342,16 +364,16 @@ __device__ __forceinline__ Work work_of(const KvAttnArgs& a) {
   w.k1 = w.sq.len - w.k0 < chunk ? w.sq.len : w.k0 + chunk;
   if (!a.tree) {
     // of a chain, no row sees past the block's last token
-    const int64_t last = (w.row0 + ROWS < w.rows ? w.row0 + ROWS : w.rows) - 1;
-    const int64_t lim = int64_t(w.sq.ctx) + last / w.group + 1;
-    if (lim < w.k1) w.k1 = int(lim);
+    const int last = (w.row0 + ROWS < w.rows ? w.row0 + ROWS : w.rows) - 1;
+    const int lim = w.sq.ctx + last / w.group + 1;
+    if (lim < w.k1) w.k1 = lim;
   }
   return w;
 }
 // Positions that every row from `row0` on sees.
-__device__ __forceinline__ int open_to(const KvAttnArgs& a, const Work& w, int64_t row0) {
-  const int64_t o = a.tree ? w.sq.ctx : w.sq.ctx + row0 / w.group + 1;
-  return o < w.k1 ? int(o) : w.k1;
+__device__ __forceinline__ int open_to(const KvAttnArgs& a, const Work& w, int row0) {
+  const int o = a.tree ? w.sq.ctx : w.sq.ctx + row0 / w.group + 1;
+  return o < w.k1 ? o : w.k1;
 }
 
 // Which new tokens a row sees.
@@ -373,13 +395,13 @@ __device__ __forceinline__ uint32_t visible(const RowMask& rm, bool tree, int ba
 
 // A row's query operands; HALF: scaled by a power of two to fit fp16.
 template <int FMT, int D, bool HALF>
-__device__ __forceinline__ void load_query(const KvAttnArgs& a, const Work& w, int64_t row, int g,
+__device__ __forceinline__ void load_query(const KvAttnArgs& a, const Work& w, int row, int g,
                                            u32x4 (&q)[D / 32], float& qs, RowMask& rm) {
   constexpr int KS = D / 32;
   const bool in = row < w.rows;
-  const int node = in ? int(row / w.group) : 0;
+  const int node = in ? row / w.group : 0, sub = in ? row - node * w.group : 0;
   const uint16_t* p = static_cast<const uint16_t*>(a.q) + int64_t(w.sq.q0 + node) * a.q_stride +
-                      int64_t(w.head * w.group + (in ? int(row % w.group) : 0)) * D;
+                      int64_t(w.head * w.group + sub) * D;
   rm.last = w.sq.ctx + node;
   rm.bits = a.tree ? a.tree[w.sq.q0 + node] : 0;
   qs = a.scale * kLog2e;
@@ -473,6 +495,10 @@ __device__ __forceinline__ void softmax_step(Rows<D>& r, float (&z)[8], const fl
   }
 }
 
+// Operands are made right before the product that takes them: made further
+// ahead (as the compiler would) they cost registers, and so waves.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 template <int FMT>
 __device__ __forceinline__ f32x4 weigh(u32x4 v, u32x4 p, u32x4 p_lo, f32x4 o) {
   o = mma<FMT != QL_KV_BF16>(v, p, o);
@@ -480,9 +506,13 @@ __device__ __forceinline__ f32x4 weigh(u32x4 v, u32x4 p, u32x4 p_lo, f32x4 o) {
   return o;
 }
 
+// 1 / (sum of weights); 0 for a row that sees nothing, whose result is zero.
+__device__ __forceinline__ float reciprocal(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+
 // Row `row`'s place in y and in the partial results.
-__device__ __forceinline__ int64_t out_row(const KvAttnArgs& a, const Work& w, int64_t row) {
-  return int64_t(w.sq.q0 + int(row / w.group)) * a.n_q + w.head * w.group + int(row % w.group);
+__device__ __forceinline__ int64_t out_row(const KvAttnArgs& a, const Work& w, int row) {
+  const int node = row / w.group;
+  return int64_t(w.sq.q0 + node) * a.n_q + w.head * w.group + (row - node * w.group);
 }
 
 // ---------------------------------------------------------------------------
@@ -494,15 +524,15 @@ struct Tile {
   Block<FMT, D> k[2], v[2];
   uint32_t ke[2];      // E4M3: row exponent of key lane % 16; NVFP4: of keys 4 g .. 4 g + 3
   uint32_t ve[2];      // of keys 4 g .. 4 g + 3
-  __device__ __forceinline__ void load(int t, const uint8_t* codes, const uint8_t* scales, int lane) {
-    k[t].load_k(codes, scales, lane);
-    v[t].load_v(codes, scales, lane);
+  __device__ __forceinline__ void load(int t, const Source& s, int lane) {
+    k[t].load_k(s, lane);
+    v[t].load_v(s, lane);
     if constexpr (FMT == QL_KV_E4M3) {
-      ke[t] = scales[L::k_exp(lane & 15)];
-      ve[t] = *reinterpret_cast<const uint32_t*>(scales + L::v_exp(lane >> 4 << 2));
+      ke[t] = __builtin_amdgcn_raw_buffer_load_b8(s.scales, L::k_exp(lane & 15), 0, 0);
+      ve[t] = load32(s.scales, L::v_exp(lane >> 4 << 2));
     } else if constexpr (FMT == QL_KV_NVFP4) {
-      const uint2 e = *reinterpret_cast<const uint2*>(scales + L::k_exp(lane >> 4 << 2));
-      ke[t] = e.x, ve[t] = e.y;
+      const auto e = __builtin_amdgcn_raw_buffer_load_b64(s.scales, L::k_exp(lane >> 4 << 2), 0, 0);
+      ke[t] = e[0], ve[t] = e[1];
     }
   }
   __device__ __forceinline__ void take(const Tile& o) {
@@ -519,20 +549,25 @@ struct Tile {
 // are hidden from some row, or missing; otherwise n0 or n1 is 0 only where a
 // block's page is absent, and the tile holds the other block in its place.
 template <int FMT, int D, bool MASKED>
-__device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&q)[D / 32], float qs,
+__device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&sm_q)[D / 32][64], float qs,
                                             Tile<FMT, D>& tile, int n0, int n1, uint32_t seen,
-                                            int g) {
-  using L = KvLayout<FMT, D>;
+                                            int lane) {
   constexpr bool HALF = FMT == QL_KV_NVFP4;
-  f32x4 s[2];
+  const int g = lane >> 4;
+  // read again for every tile: held in registers they would cost waves
+  asm volatile("" ::: "memory");
+  u32x4 q[D / 32];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    float p = 1.0f;
-    if constexpr (FMT == QL_KV_E4M3) p = power(tile.ke[t]);
-    s[t] = f32x4{0, 0, 0, 0};
+  for (int k = 0; k < D / 32; ++k) q[k] = sm_q[k][lane];
+  f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  float kp[2] = {1.0f, 1.0f};
+  if constexpr (FMT == QL_KV_E4M3) kp[0] = power(tile.ke[0]), kp[1] = power(tile.ke[1]);
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k)
-      s[t] = mma<HALF>(tile.k[t].template k_operand<HALF>(k, p), q[k], s[t]);
+  for (int k = 0; k < D / 32; ++k) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      s[t] = mma<HALF>(tile.k[t].template k_operand<HALF>(k, kp[t]), q[k], s[t]);
+    in_order();
   }
   const float hide0 = MASKED || n0 ? 0.0f : -__builtin_inff();
   const float hide1 = MASKED || n1 ? 0.0f : -__builtin_inff();
@@ -545,7 +580,7 @@ __device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&q)[D / 32]
       z[x] = __builtin_fmaf(s[t][k], qs, hide);
     } else {
       const uint32_t b = tile.ve[t] >> (8 * k) & 0xFFu;
-      iv[x] = power(254u - b);
+      iv[x] = power((0xFEFEFEFEu - tile.ve[t]) >> (8 * k) & 0xFFu);   // 254 - b
       float v = s[t][k];
       if constexpr (HALF) v *= power(tile.ke[t] >> (8 * k) & 0xFFu);
       z[x] = __builtin_fmaf(v, qs, static_cast<float>(b) + hide);
@@ -569,23 +604,28 @@ __device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&q)[D / 32]
       if (seen & bad) r.l = __builtin_nanf("");
     }
   }
+  constexpr int per = Block<FMT, D>::kPer;
 #pragma unroll
-  for (int i = 0; i < L::kLoads; ++i) {
-    uint2 a[L::kDC], b[L::kDC];
-    tile.v[0].v_operands(i, a);
-    tile.v[1].v_operands(i, b);
+  for (int j = 0; j < D / 16 / per; ++j) {
+    uint2 a[per], b[per];
+    tile.v[0].v_operands(j, a);
+    tile.v[1].v_operands(j, b);
 #pragma unroll
-    for (int x = 0; x < L::kDC; ++x) {
-      f32x4& o = r.o[i * L::kDC + x];
+    for (int x = 0; x < per; ++x) {
+      f32x4& o = r.o[j * per + x];
       o = weigh<FMT>(u32x4{a[x].x, a[x].y, b[x].x, b[x].y}, p, p_lo, o);
     }
+    in_order();
   }
 }
 
 // Waves per SIMD that the register budget is set for (fewer spill).
 constexpr int narrow_waves(int fmt, int d) {
-  return d == 64 ? 3 : d == 128 ? (fmt == QL_KV_BF16 ? 2 : 3) : fmt == QL_KV_NVFP4 ? 2 : 1;
+  return d == 64 ? (fmt == QL_KV_BF16 ? 4 : 5) : d == 128 ? (fmt == QL_KV_BF16 ? 2 : 4) : 2;
 }
+
+// Tiles that are under way while one is worked on.
+constexpr int narrow_ahead(int fmt, int d) { return 0; }
 
 template <int FMT, int D>
 __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attention_narrow_kernel(
@@ -594,36 +634,47 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
   constexpr int DCH = D < 128 ? D : 128;        // elements of d joined at a time
   __shared__ float sm_m[kWaves][16], sm_l[kWaves][16];
   __shared__ __align__(16) float sm_o[kWaves][16][DCH + 4];
+  __shared__ u32x4 sm_q[D / 32][64];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const Work w = work_of<16>(a);
   if (!w.any) return;
-  u32x4 q[D / 32];
   float qs;
   RowMask rm;
-  load_query<FMT, D, FMT == QL_KV_NVFP4>(a, w, w.row0 + n, g, q, qs, rm);
+  {
+    u32x4 q[D / 32];
+    load_query<FMT, D, FMT == QL_KV_NVFP4>(a, w, w.row0 + n, g, q, qs, rm);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+      if (k % kWaves == wave) sm_q[k][lane] = q[k];
+  }
+  __syncthreads();
   Rows<D> r;
   r.clear();
 
-  // tiles first, first + 4, ... of the split
+  // Tiles first, first + 4, ... of the split, the last first: those with
+  // hidden keys come before those that every row sees.
   const int first = w.k0 / kTile + wave;
   const int tiles = (w.k1 + kTile - 1) / kTile;
   const int count = tiles > first ? (tiles - first + kWaves - 1) / kWaves : 0;
+  const int open = open_to(a, w, w.row0) / kTile;
+  const int whole = open > first ? (open - first + kWaves - 1) / kWaves : 0;
   const int per_page = a.g.page_shift - 4;             // log2(blocks of a page)
   const int32_t* table = a.table + int64_t(w.b) * a.table_stride;
   int pages = -1;   // of 32 iterations' two blocks, one per lane
   // An absent block of a tile is read from the tile's other block.
   auto load = [&](int it, Tile<FMT, D>& tile, int& p0, int& p1) {
+    if (it >= count) return;
     if ((it & 31) == 0) {
-      const int mine = 2 * (first + kWaves * (it + (lane >> 1))) + (lane & 1);
+      const int mine = 2 * (first + kWaves * (count - 1 - it - (lane >> 1))) + (lane & 1);
       pages = -1;
-      if (int64_t(mine) * 16 < w.k1) {
+      if (mine >= 0 && int64_t(mine) * 16 < w.k1) {
         pages = table[mine >> per_page];
         if (pages >= a.g.n_pages) pages = -1;
       }
     }
-    const int block = 2 * (first + kWaves * it);
+    const int block = 2 * (first + kWaves * (count - 1 - it));
     p0 = __builtin_amdgcn_readlane(pages, 2 * (it & 31));
     p1 = __builtin_amdgcn_readlane(pages, 2 * (it & 31) + 1);
 #pragma unroll
@@ -631,31 +682,35 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
       const int own = t ? p1 : p0, other = t ? p0 : p1;
       const int page = own >= 0 ? own : other >= 0 ? other : 0;
       const int in = (own >= 0 ? block + t : block + 1 - t) & ((1 << per_page) - 1);
-      const int64_t at = kv_block(a.g, page, w.head, in);
-      tile.load(t, a.g.codes + at * L::kCodes, a.g.scales + at * L::kScales, lane);
+      tile.load(t, source<FMT, D>(a.g, kv_block(a.g, page, w.head, in)), lane);
     }
   };
   if (count > 0) {
-    // first the tiles that every row sees, then those with hidden keys
-    const int open = open_to(a, w, w.row0) / kTile;
-    const int whole = open > first ? (open - first + kWaves - 1) / kWaves : 0;
-    Tile<FMT, D> cur, nxt;
-    int c0, c1, x0 = 0, x1 = 0, it = 0;
-    load(0, cur, c0, c1);
-    for (; it < whole; ++it) {
-      if (it + 1 < count) load(it + 1, nxt, x0, x1);
-      if (c0 >= 0 || c1 >= 0)
-        narrow_tile<FMT, D, false>(r, q, qs, cur, c0 >= 0, c1 >= 0, 0, g);
-      cur.take(nxt);
-      c0 = x0, c1 = x1;
+    constexpr int N = narrow_ahead(FMT, D) + 1;       // tiles in registers
+    Tile<FMT, D> buf[N];
+    int p0[N], p1[N];
+#pragma unroll
+    for (int x = 0; x < N - 1; ++x) load(x, buf[x], p0[x], p1[x]);
+    int it = 0;
+    for (; it < count - whole; ++it) {
+      load(it + N - 1, buf[N - 1], p0[N - 1], p1[N - 1]);
+      const int base = (first + kWaves * (count - 1 - it)) * kTile, left = w.k1 - base;
+      narrow_tile<FMT, D, true>(r, sm_q, qs, buf[0], p0[0] < 0 ? 0 : left, p1[0] < 0 ? 0 : left - 16,
+                                visible(rm, a.tree != nullptr, base, w.sq.ctx, g), lane);
+#pragma unroll
+      for (int x = 0; x < N - 1; ++x) buf[x].take(buf[x + 1]), p0[x] = p0[x + 1], p1[x] = p1[x + 1];
     }
-    for (; it < count; ++it) {
-      if (it + 1 < count) load(it + 1, nxt, x0, x1);
-      const int base = (first + kWaves * it) * kTile, left = w.k1 - base;
-      narrow_tile<FMT, D, true>(r, q, qs, cur, c0 < 0 ? 0 : left, c1 < 0 ? 0 : left - 16,
-                                visible(rm, a.tree != nullptr, base, w.sq.ctx, g), g);
-      cur.take(nxt);
-      c0 = x0, c1 = x1;
+    while (it < count) {
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+        if (it < count) {
+          const int y = (x + N - 1) % N;
+          load(it + N - 1, buf[y], p0[y], p1[y]);
+          if (p0[x] >= 0 || p1[x] >= 0)
+            narrow_tile<FMT, D, false>(r, sm_q, qs, buf[x], p0[x] >= 0, p1[x] >= 0, 0, lane);
+        }
+        ++it;
+      }
     }
   }
 
@@ -699,10 +754,10 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
       }
       const int64_t out = out_row(a, w, w.row0 + row);
       if (w.nsplit == 1) {
+        const float inv = reciprocal(l);
         uint32_t y[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          y[x] = l == 0.0f ? 0u : pack_bf16x2(v[2 * x] / l, v[2 * x + 1] / l);
+        for (int x = 0; x < 4; ++x) y[x] = pack_bf16x2(v[2 * x] * inv, v[2 * x + 1] * inv);
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out * D + part * DCH + c) =
             make_uint4(y[0], y[1], y[2], y[3]);
       } else {
@@ -736,11 +791,11 @@ struct Quarter {
   uint32_t e;          // row exponent of key lane % 16
   int keys;            // keys of the block that are there
 
-  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, bool is_v,
-                                       int lane) {
-    if (is_v) x.load_v(codes, scales, lane);
-    else x.load_k(codes, scales, lane);
-    if constexpr (FMT != QL_KV_BF16) e = scales[L::k_exp(lane & 15) + (is_v ? 4 : 0)];
+  __device__ __forceinline__ void load(const Source& s, bool is_v, int lane) {
+    if (is_v) x.load_v(s, lane);
+    else x.load_k(s, lane);
+    if constexpr (FMT != QL_KV_BF16)
+      e = __builtin_amdgcn_raw_buffer_load_b8(s.scales, L::k_exp(lane & 15) + (is_v ? 4 : 0), 0, 0);
   }
   // CHECK: keys of this tile may be hidden from some row.
   __device__ __forceinline__ void store(Shared<FMT, D>& sh, int t, bool is_v, bool check, int lane) {
@@ -763,13 +818,13 @@ struct Quarter {
         bad = x.clear_non_finite();
         bad = __shfl(bad, (n >> 2) * 16, 64) >> (n & 3) & 1u;
       }
+      constexpr int per = Block<FMT, D>::kPer;
 #pragma unroll
-      for (int i = 0; i < L::kLoads; ++i) {
-        uint2 r[L::kDC];
-        x.v_operands(i, r);
+      for (int j = 0; j < D / 16 / per; ++j) {
+        uint2 r[per];
+        x.v_operands(j, r);
 #pragma unroll
-        for (int q = 0; q < L::kDC; ++q)
-          reinterpret_cast<uint2*>(&sh.v[i * L::kDC + q][lane])[t] = r[q];
+        for (int q = 0; q < per; ++q) reinterpret_cast<uint2*>(&sh.v[j * per + q][lane])[t] = r[q];
       }
       if (g == 0) {
         float ve = 0.0f, iv = 1.0f;
@@ -831,7 +886,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void kv_attention_wi
   const int n = lane & 15, g = lane >> 4;
   const Work w = work_of<64 * MT>(a);
   if (!w.any) return;
-  const int64_t row0 = w.row0 + wave * (16 * MT);
+  const int row0 = w.row0 + wave * (16 * MT);
   const bool active = row0 < w.rows;
   u32x4 q[MT][D / 32];
   float qs[MT];
@@ -864,8 +919,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void kv_attention_wi
     const int page = __builtin_amdgcn_readlane(pages, it & 63);
     const int left = w.k1 - 16 * block;
     x.keys = page < 0 || left < 0 ? 0 : left < 16 ? left : 16;
-    const int64_t at = kv_block(a.g, page < 0 ? 0 : page, w.head, block & ((1 << per_page) - 1));
-    x.load(a.g.codes + at * L::kCodes, a.g.scales + at * L::kScales, is_v, lane);
+    x.load(source<FMT, D>(a.g, kv_block(a.g, page < 0 ? 0 : page, w.head,
+                                        block & ((1 << per_page) - 1))), is_v, lane);
   };
   if (first < tiles) {
     Quarter<FMT, D> x;
@@ -895,8 +950,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void kv_attention_wi
   if (!active) return;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const int64_t row = row0 + 16 * mt + n;
-    const float l = column_sum(r[mt].l);
+    const int row = row0 + 16 * mt + n;
+    const float l = column_sum(r[mt].l), inv = reciprocal(l);
     if (row >= w.rows) continue;
     const int64_t out = out_row(a, w, row);
     const int64_t at = int64_t(w.split) * a.tokens * a.n_q + out;
@@ -912,8 +967,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void kv_attention_wi
         if (w.nsplit == 1) {
           uint32_t y[4];
 #pragma unroll
-          for (int z = 0; z < 4; ++z)
-            y[z] = l == 0.0f ? 0u : pack_bf16x2(v[2 * z] / l, v[2 * z + 1] / l);
+          for (int z = 0; z < 4; ++z) y[z] = pack_bf16x2(v[2 * z] * inv, v[2 * z + 1] * inv);
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out * D + d) =
               make_uint4(y[0], y[1], y[2], y[3]);
         } else {
@@ -925,31 +979,47 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void kv_attention_wi
   }
 }
 
-// Joins the splits of every row that has more than one, in split order: a
-// wave per row.
+// Joins the splits of every row that has more than one, in a fixed order.
+// D / 4 lanes (4 elements each) take one of `parts` shares of a row's splits,
+// every parts-th split; the shares are then added in order.
 template <int D>
-__global__ __launch_bounds__(64 * kWaves) void kv_attention_join_kernel(KvAttnArgs a) {
-  constexpr int N = D / 64;
-  const int lane = threadIdx.x & 63, b = blockIdx.y;
-  const int64_t r = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);   // token of the sequence, head
+__global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttnArgs a, int parts) {
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+  __shared__ f32x4 sm_o[kGroups][kLanes];
+  __shared__ float sm_l[kGroups];
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int b = blockIdx.y, part = group % parts;
   const Seq sq = sequence(a, b);
-  if (r >= int64_t(sq.rows_q) * a.n_q) return;
   const int nsplit = splits_of(sq.len, chunk_of(sq.len, a.chunk, a.splits));
   if (nsplit == 1) return;
+  const int64_t r = int64_t(blockIdx.x) * (kGroups / parts) + group / parts;   // token, head
+  const bool in = r < int64_t(sq.rows_q) * a.n_q;
   const int64_t row = int64_t(sq.q0) * a.n_q + r, step = a.tokens * a.n_q;
-  float top = kLowest;
-  for (int s = 0; s < nsplit; ++s) top = __builtin_fmaxf(top, a.part_ml[2 * (s * step + row)]);
-  float l = 0.0f, v[N] = {};
-  for (int s = 0; s < nsplit; ++s) {
-    const int64_t at = s * step + row;
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - top);
-    l += a.part_ml[2 * at + 1] * f;
+  float l = 0.0f;
+  f32x4 v = {0, 0, 0, 0};
+  if (in) {
+    float top = kLowest;
+    for (int s = lane; s < nsplit; s += kLanes) top = __builtin_fmaxf(top, a.part_ml[2 * (s * step + row)]);
 #pragma unroll
-    for (int x = 0; x < N; ++x) v[x] = __builtin_fmaf(a.part_o[at * D + lane * N + x], f, v[x]);
+    for (int off = 1; off < kLanes; off *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, off, 64));
+    for (int s = part; s < nsplit; s += parts) {
+      const int64_t at = s * step + row;
+      const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - top);
+      l = __builtin_fmaf(a.part_ml[2 * at + 1], f, l);
+      v += *reinterpret_cast<const f32x4*>(a.part_o + at * D + 4 * lane) * f;
+    }
   }
-  uint16_t* y = static_cast<uint16_t*>(a.y) + row * D + lane * N;
-#pragma unroll
-  for (int x = 0; x < N; ++x) y[x] = l == 0.0f ? uint16_t(0) : to_bf16(v[x] / l);
+  if (parts > 1) {
+    sm_o[group][lane] = v;
+    if (lane == 0) sm_l[group] = l;
+    __syncthreads();
+    if (part) return;
+    for (int x = 1; x < parts; ++x) v += sm_o[group + x][lane], l += sm_l[group + x];
+  }
+  if (!in) return;
+  v *= reciprocal(l);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + row * D + 4 * lane) =
+      make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
 }  // namespace
@@ -964,8 +1034,8 @@ KvAttnPlan kv_attention_plan(int d, int n_q, int n_kv, int64_t n_seqs, int64_t m
   // enough blocks for two on each compute unit, and at least 256 keys in one
   const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
   const int64_t blocks = n_seqs * n_kv * p.row_blocks;
-  int64_t splits = (2 * cus + blocks - 1) / blocks;
-  const int64_t most_splits = (max_kv + 255) / 256;
+  int64_t splits = (4 * cus + blocks - 1) / blocks;
+  const int64_t most_splits = max_kv <= 512 ? 1 : (max_kv + 255) / 256;
   if (splits > most_splits) splits = most_splits;
   if (splits < 1) splits = 1;
   if (splits > 256) splits = 256;
@@ -1007,11 +1077,14 @@ hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a
     return hipGetLastError();
   });
   if (e != hipSuccess || p.splits < 2) return e;
-  const dim3 grid(unsigned((int64_t(a.max_q) * a.n_q + kWaves - 1) / kWaves), unsigned(a.n_seqs));
+  // shares of a row: all of a block's groups where there are many splits
+  const int groups = 1024 / d, parts = p.splits >= 2 * groups ? groups : p.splits >= 4 ? 2 : 1;
+  const int64_t rows = int64_t(a.max_q) * a.n_q, per_block = groups / parts;
+  const dim3 grid(unsigned((rows + per_block - 1) / per_block), unsigned(a.n_seqs));
   switch (d) {
-    case 64: kv_attention_join_kernel<64><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    case 128: kv_attention_join_kernel<128><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    default: kv_attention_join_kernel<256><<<grid, 64 * kWaves, 0, s>>>(a); break;
+    case 64: kv_attention_join_kernel<64><<<grid, 256, 0, s>>>(a, parts); break;
+    case 128: kv_attention_join_kernel<128><<<grid, 256, 0, s>>>(a, parts); break;
+    default: kv_attention_join_kernel<256><<<grid, 256, 0, s>>>(a, parts); break;
   }
   return hipGetLastError();
 }
