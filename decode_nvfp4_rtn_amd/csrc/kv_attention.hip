@@ -149,37 +149,32 @@ struct Block {
     if constexpr (W == 4) return __builtin_amdgcn_raw_buffer_load_b128(s.codes, at, 0, 0);
     else return __builtin_amdgcn_raw_buffer_load_b64(s.codes, at, 0, 0);
   }
-  __device__ __forceinline__ void load_k(const Source& s, int lane) {
+  // The functions below work on COUNT loads, those from `first` on of a block.
+  template <int COUNT = L::kLoads>
+  __device__ __forceinline__ void load_k(const Source& s, int lane, int first = 0) {
 #pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) {
-      w[i] = words(s, lane * L::kLoad + 64 * i * L::kLoad);
+    for (int i = 0; i < COUNT; ++i) {
+      w[i] = words(s, lane * L::kLoad + 64 * (first + i) * L::kLoad);
       if constexpr (FMT == QL_KV_NVFP4) {
-        const int at = lane * L::kGPC + 64 * i * L::kGPC;
-        if constexpr (L::kGPC == 2) sc[i] = __builtin_amdgcn_raw_buffer_load_b16(s.scales, at, 0, 0);
-        else sc[i] = __builtin_amdgcn_raw_buffer_load_b8(s.scales, at, 0, 0);
+        // whole words: a narrower load's result is extended at once, and waited for
+        sc[i] = load32(s.scales, (lane * L::kGPC & ~3) + 64 * (first + i) * L::kGPC);
       }
     }
   }
-  __device__ __forceinline__ void load_v(const Source& s, int lane) {
+  template <int COUNT = L::kLoads>
+  __device__ __forceinline__ void load_v(const Source& s, int lane, int first = 0) {
 #pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) {
-      w[i] = words(s, lane * L::kLoad + (16 * L::kRow + 64 * i * L::kLoad));
-      if constexpr (FMT == QL_KV_NVFP4)      // group i kDC + (lane % 16) kDC / 16
-        sc[i] = load32(s.scales, (lane & 15) * L::kDC / 16 * 16 + (lane >> 4) * 4 + (D + i * L::kDC * 16));
+    for (int i = 0; i < COUNT; ++i) {
+      w[i] = words(s, lane * L::kLoad + (16 * L::kRow + 64 * (first + i) * L::kLoad));
+      if constexpr (FMT == QL_KV_NVFP4)      // group (first + i) kDC + (lane % 16) kDC / 16
+        sc[i] = load32(s.scales, (lane & 15) * L::kDC / 16 * 16 + (lane >> 4) * 4 +
+                                     (D + (first + i) * L::kDC * 16));
     }
   }
-  __device__ __forceinline__ void take(const Block& o) {
-#pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) {
-      w[i] = o.w[i];
-      if constexpr (FMT == QL_KV_NVFP4) sc[i] = o.sc[i];
-    }
-  }
-
   // K operand of step s (its elements of d: q_element), bf16 with the row
   // scale p; HALF (NVFP4): fp16 without it.
   template <bool HALF>
-  __device__ __forceinline__ u32x4 k_operand(int s, float p) const {
+  __device__ __forceinline__ u32x4 k_operand(int s, float p, int lane) const {
     constexpr int per = L::kEC / 8;           // steps per load
     if constexpr (FMT == QL_KV_BF16) {
       return w[s];
@@ -189,15 +184,16 @@ struct Block {
                    fp8_pair_bf16(b, p, 1)};
     } else {
       const uint32_t a = w[s / per][s % per];
+      const uint32_t groups = sc[s / per] >> 8 * (lane * L::kGPC & 3);
       if constexpr (HALF) {
-        const f16x2 two = __builtin_bit_cast(f16x2, fp8_pair(sc[s / per], 0));
+        const f16x2 two = __builtin_bit_cast(f16x2, fp8_pair(groups, 0));
         const _Float16 g = two[s % per / 2];
         const f16x2 gg = {g, g};
         return u32x4{times(fp4_pair<0>(a), gg), times(fp4_pair<1>(a), gg),
                      times(fp4_pair<2>(a), gg), times(fp4_pair<3>(a), gg)};
       } else {
-        const float g = s % per / 2 ? __builtin_amdgcn_cvt_f32_fp8(int(sc[s / per]), 1)
-                                    : __builtin_amdgcn_cvt_f32_fp8(int(sc[s / per]), 0);
+        const float g = s % per / 2 ? __builtin_amdgcn_cvt_f32_fp8(int(groups), 1)
+                                    : __builtin_amdgcn_cvt_f32_fp8(int(groups), 0);
         return u32x4{fp4_pair_bf16<0>(a, p, g), fp4_pair_bf16<1>(a, p, g),
                      fp4_pair_bf16<2>(a, p, g), fp4_pair_bf16<3>(a, p, g)};
       }
@@ -230,16 +226,17 @@ struct Block {
 
   // V: clears the keys of the lane's quad from `keys` (0..4) on; what lies
   // there is not part of the sequence.
+  template <int COUNT = L::kLoads>
   __device__ __forceinline__ void clear_v(int keys) {
     if constexpr (FMT == QL_KV_BF16) {
       const uint32_t a = keys >= 2 ? ~0u : keys == 1 ? 0xFFFFu : 0u;
       const uint32_t b = keys >= 4 ? ~0u : keys == 3 ? 0xFFFFu : 0u;
 #pragma unroll
-      for (int x = 0; x < L::kLoads * W; ++x) w[x / W][x % W] &= x & 1 ? b : a;
+      for (int x = 0; x < COUNT * W; ++x) w[x / W][x % W] &= x & 1 ? b : a;
     } else {
       const uint32_t m = keys >= 4 ? ~0u : (1u << (8 * keys)) - 1u;
 #pragma unroll
-      for (int i = 0; i < L::kLoads; ++i) {
+      for (int i = 0; i < COUNT; ++i) {
         w[i] &= m;
         if constexpr (FMT == QL_KV_NVFP4) sc[i] &= m;
       }
@@ -247,10 +244,11 @@ struct Block {
   }
 
   // V: non-zero where a value that the lane holds is a NaN or an infinity.
+  template <int COUNT = L::kLoads>
   __device__ __forceinline__ uint32_t non_finite() const {
     uint32_t r = 0;
 #pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) {
+    for (int i = 0; i < COUNT; ++i) {
       if constexpr (FMT == QL_KV_NVFP4) {
         r |= bad_bytes(sc[i]);
       } else {
@@ -262,10 +260,11 @@ struct Block {
   }
   // V: clears them (NVFP4: their groups); bit k of the result: key k of the
   // lane's quad had one, in an element of any of the 16 lanes that hold it.
+  template <int COUNT = L::kLoads>
   __device__ __forceinline__ uint32_t clear_non_finite() {
     uint32_t b = 0, c = 0, r;     // BF16: keys 0, 1 and keys 2, 3; others: b, a byte a key
 #pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) {
+    for (int i = 0; i < COUNT; ++i) {
       if constexpr (FMT == QL_KV_NVFP4) {
         const uint32_t m = bad_bytes(sc[i]);
         b |= m;
@@ -522,25 +521,18 @@ template <int FMT, int D>
 struct Tile {
   using L = KvLayout<FMT, D>;
   Block<FMT, D> k[2], v[2];
-  uint32_t ke[2];      // E4M3: row exponent of key lane % 16; NVFP4: of keys 4 g .. 4 g + 3
+  uint32_t ke[2];      // row exponents: E4M3 of the four keys around key lane % 16,
+                       // NVFP4 of keys 4 g .. 4 g + 3
   uint32_t ve[2];      // of keys 4 g .. 4 g + 3
   __device__ __forceinline__ void load(int t, const Source& s, int lane) {
     k[t].load_k(s, lane);
     v[t].load_v(s, lane);
     if constexpr (FMT == QL_KV_E4M3) {
-      ke[t] = __builtin_amdgcn_raw_buffer_load_b8(s.scales, L::k_exp(lane & 15), 0, 0);
+      ke[t] = load32(s.scales, L::k_exp(lane & 12));
       ve[t] = load32(s.scales, L::v_exp(lane >> 4 << 2));
     } else if constexpr (FMT == QL_KV_NVFP4) {
       const auto e = __builtin_amdgcn_raw_buffer_load_b64(s.scales, L::k_exp(lane >> 4 << 2), 0, 0);
       ke[t] = e[0], ve[t] = e[1];
-    }
-  }
-  __device__ __forceinline__ void take(const Tile& o) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      k[t].take(o.k[t]);
-      v[t].take(o.v[t]);
-      if constexpr (FMT != QL_KV_BF16) ke[t] = o.ke[t], ve[t] = o.ve[t];
     }
   }
 };
@@ -561,12 +553,15 @@ __device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&sm_q)[D / 
   for (int k = 0; k < D / 32; ++k) q[k] = sm_q[k][lane];
   f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
   float kp[2] = {1.0f, 1.0f};
-  if constexpr (FMT == QL_KV_E4M3) kp[0] = power(tile.ke[0]), kp[1] = power(tile.ke[1]);
+  if constexpr (FMT == QL_KV_E4M3) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) kp[t] = power(tile.ke[t] >> 8 * (lane & 3) & 0xFFu);
+  }
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
-      s[t] = mma<HALF>(tile.k[t].template k_operand<HALF>(k, kp[t]), q[k], s[t]);
+      s[t] = mma<HALF>(tile.k[t].template k_operand<HALF>(k, kp[t], lane), q[k], s[t]);
     in_order();
   }
   const float hide0 = MASKED || n0 ? 0.0f : -__builtin_inff();
@@ -621,7 +616,7 @@ __device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&sm_q)[D / 
 
 // Waves per SIMD that the register budget is set for (fewer spill).
 constexpr int narrow_waves(int fmt, int d) {
-  return d == 64 ? (fmt == QL_KV_BF16 ? 4 : 5) : d == 128 ? (fmt == QL_KV_BF16 ? 2 : 4) : 2;
+  return d == 64 ? 5 : d == 128 ? (fmt == QL_KV_BF16 ? 3 : 4) : 2;
 }
 
 // Tiles that are under way while one is worked on.
@@ -660,23 +655,27 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
   const int count = tiles > first ? (tiles - first + kWaves - 1) / kWaves : 0;
   const int open = open_to(a, w, w.row0) / kTile;
   const int whole = open > first ? (open - first + kWaves - 1) / kWaves : 0;
+  constexpr int N = narrow_ahead(FMT, D) + 1;          // tiles in registers
+  int partly = count - whole;
+  partly = (partly + N - 1) / N * N < count ? (partly + N - 1) / N * N : count;
+  auto tile_of = [&](int i) { return first + kWaves * (count - 1 - i); };
   const int per_page = a.g.page_shift - 4;             // log2(blocks of a page)
   const int32_t* table = a.table + int64_t(w.b) * a.table_stride;
   int pages = -1;   // of 32 iterations' two blocks, one per lane
   // An absent block of a tile is read from the tile's other block.
-  auto load = [&](int it, Tile<FMT, D>& tile, int& p0, int& p1) {
-    if (it >= count) return;
-    if ((it & 31) == 0) {
-      const int mine = 2 * (first + kWaves * (count - 1 - it - (lane >> 1))) + (lane & 1);
+  auto load = [&](int i, Tile<FMT, D>& tile, int& p0, int& p1) {
+    if (i >= count) i = count - 1;      // once more: a load that may not happen costs a move
+    if ((i & 31) == 0) {
+      const int mine = i + (lane >> 1) < count ? 2 * tile_of(i + (lane >> 1)) + (lane & 1) : -1;
       pages = -1;
       if (mine >= 0 && int64_t(mine) * 16 < w.k1) {
         pages = table[mine >> per_page];
         if (pages >= a.g.n_pages) pages = -1;
       }
     }
-    const int block = 2 * (first + kWaves * (count - 1 - it));
-    p0 = __builtin_amdgcn_readlane(pages, 2 * (it & 31));
-    p1 = __builtin_amdgcn_readlane(pages, 2 * (it & 31) + 1);
+    const int block = 2 * tile_of(i);
+    p0 = __builtin_amdgcn_readlane(pages, 2 * (i & 31));
+    p1 = __builtin_amdgcn_readlane(pages, 2 * (i & 31) + 1);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int own = t ? p1 : p0, other = t ? p0 : p1;
@@ -686,30 +685,28 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
     }
   };
   if (count > 0) {
-    constexpr int N = narrow_ahead(FMT, D) + 1;       // tiles in registers
     Tile<FMT, D> buf[N];
     int p0[N], p1[N];
 #pragma unroll
-    for (int x = 0; x < N - 1; ++x) load(x, buf[x], p0[x], p1[x]);
-    int it = 0;
-    for (; it < count - whole; ++it) {
-      load(it + N - 1, buf[N - 1], p0[N - 1], p1[N - 1]);
-      const int base = (first + kWaves * (count - 1 - it)) * kTile, left = w.k1 - base;
-      narrow_tile<FMT, D, true>(r, sm_q, qs, buf[0], p0[0] < 0 ? 0 : left, p1[0] < 0 ? 0 : left - 16,
-                                visible(rm, a.tree != nullptr, base, w.sq.ctx, g), lane);
+    for (int y = 0; y < N - 1; ++y) load(y, buf[y], p0[y], p1[y]);
+    for (int i = 0; i < partly; i += N) {
 #pragma unroll
-      for (int x = 0; x < N - 1; ++x) buf[x].take(buf[x + 1]), p0[x] = p0[x + 1], p1[x] = p1[x + 1];
+      for (int y = 0; y < N; ++y) {
+        if (i + y >= partly) break;
+        load(i + y + N - 1, buf[(y + N - 1) % N], p0[(y + N - 1) % N], p1[(y + N - 1) % N]);
+        const int base = tile_of(i + y) * kTile, left = w.k1 - base;
+        narrow_tile<FMT, D, true>(r, sm_q, qs, buf[y], p0[y] < 0 ? 0 : left,
+                                  p1[y] < 0 ? 0 : left - 16,
+                                  visible(rm, a.tree != nullptr, base, w.sq.ctx, g), lane);
+      }
     }
-    while (it < count) {
+    for (int i = partly; i < count; i += N) {
 #pragma unroll
-      for (int x = 0; x < N; ++x) {
-        if (it < count) {
-          const int y = (x + N - 1) % N;
-          load(it + N - 1, buf[y], p0[y], p1[y]);
-          if (p0[x] >= 0 || p1[x] >= 0)
-            narrow_tile<FMT, D, false>(r, sm_q, qs, buf[x], p0[x] >= 0, p1[x] >= 0, 0, lane);
-        }
-        ++it;
+      for (int y = 0; y < N; ++y) {
+        if (i + y >= count) break;
+        load(i + y + N - 1, buf[(y + N - 1) % N], p0[(y + N - 1) % N], p1[(y + N - 1) % N]);
+        if (p0[y] >= 0 || p1[y] >= 0)
+          narrow_tile<FMT, D, false>(r, sm_q, qs, buf[y], p0[y] >= 0, p1[y] >= 0, 0, lane);
       }
     }
   }
@@ -773,91 +770,108 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
 }
 
 // ---------------------------------------------------------------------------
-// wide: 64 MT rows, tiles shared through LDS
+// wide: 16 MT rows for each of NW waves, tiles shared through LDS
 // ---------------------------------------------------------------------------
 template <int FMT, int D>
 struct Shared {        // one tile's operands
   u32x4 k[2][D / 32][64];
   u32x4 v[D / 16][64];
   float ve[kTile];     // V's row exponent + 127; -inf: the key is missing
-  float iv[kTile];     // 2^-that; NaN: the row holds a NaN or an infinity
+  float iv[kTile];     // 2^-that
+  float bad[2][kTile]; // tiles with hidden keys: NaN where a half of the row holds one, or an infinity
 };
 
-// The quarter of a tile that a wave turns into operands: block t's K or V.
-template <int FMT, int D>
-struct Quarter {
+// The part of a tile that a wave turns into operands: block t's K or V, or
+// (eight waves) one half of its loads.
+template <int FMT, int D, int NW>
+struct Part {
   using L = KvLayout<FMT, D>;
-  Block<FMT, D> x;
-  uint32_t e;          // row exponent of key lane % 16
+  static constexpr int H = NW / 4;                 // parts of a block's K (or V)
+  static constexpr int kMine = L::kLoads / H;      // loads
+  Block<FMT, D> x;     // loads 0 .. kMine - 1 are used
+  uint32_t e;          // row exponents of the four keys around key lane % 16
   int keys;            // keys of the block that are there
 
-  __device__ __forceinline__ void load(const Source& s, bool is_v, int lane) {
-    if (is_v) x.load_v(s, lane);
-    else x.load_k(s, lane);
+  __device__ __forceinline__ void load(const Source& s, bool is_v, int half, int lane) {
+    if (is_v) x.template load_v<kMine>(s, lane, half * kMine);
+    else x.template load_k<kMine>(s, lane, half * kMine);
     if constexpr (FMT != QL_KV_BF16)
-      e = __builtin_amdgcn_raw_buffer_load_b8(s.scales, L::k_exp(lane & 15) + (is_v ? 4 : 0), 0, 0);
+      e = load32(s.scales, L::k_exp(lane & 12) + (is_v ? 4 : 0));
   }
-  // CHECK: keys of this tile may be hidden from some row.
-  __device__ __forceinline__ void store(Shared<FMT, D>& sh, int t, bool is_v, bool check, int lane) {
+  // check: keys of this tile may be hidden from some row.
+  __device__ __forceinline__ void store(Shared<FMT, D>& sh, int t, bool is_v, int half, bool check,
+                                        int lane) {
     const int n = lane & 15, g = lane >> 4;
+    uint32_t mine = 0;
+    if constexpr (FMT != QL_KV_BF16) mine = e >> 8 * (n & 3) & 0xFFu;
     if (!is_v) {
       float p = 1.0f;
-      if constexpr (FMT != QL_KV_BF16) p = power(e);
+      if constexpr (FMT != QL_KV_BF16) p = power(mine);
       const uint32_t keep = n < keys ? ~0u : 0u;
+      constexpr int steps = D / 32 / H;
 #pragma unroll
-      for (int s = 0; s < D / 32; ++s)
-        sh.k[t][s][lane] = x.template k_operand<false>(s, p) & keep;
+      for (int s = 0; s < steps; ++s)
+        sh.k[t][half * steps + s][lane] = x.template k_operand<false>(s, p, lane) & keep;
     } else {
-      uint32_t bad = 0;
       if (keys < 16) {
         const int left = keys - 4 * g;
-        x.clear_v(left < 0 ? 0 : left > 4 ? 4 : left);
+        x.template clear_v<kMine>(left < 0 ? 0 : left > 4 ? 4 : left);
       }
-      if (check && __any(x.non_finite() != 0)) {
+      if (check) {
         // as in narrow_tile; lane n's key is in quad n / 4
-        bad = x.clear_non_finite();
-        bad = __shfl(bad, (n >> 2) * 16, 64) >> (n & 3) & 1u;
+        uint32_t bad = 0;
+        if (__any(x.template non_finite<kMine>() != 0)) {
+          bad = x.template clear_non_finite<kMine>();
+          bad = __shfl(bad, (n >> 2) * 16, 64) >> (n & 3) & 1u;
+        }
+        if (g == 0) sh.bad[half][16 * t + n] = bad ? __builtin_nanf("") : 0.0f;
       }
-      constexpr int per = Block<FMT, D>::kPer;
+      constexpr int per = Block<FMT, D>::kPer, tiles = D / 16 / H;
 #pragma unroll
-      for (int j = 0; j < D / 16 / per; ++j) {
+      for (int j = 0; j < tiles / per; ++j) {
         uint2 r[per];
         x.v_operands(j, r);
 #pragma unroll
-        for (int q = 0; q < per; ++q) reinterpret_cast<uint2*>(&sh.v[j * per + q][lane])[t] = r[q];
+        for (int q = 0; q < per; ++q)
+          reinterpret_cast<uint2*>(&sh.v[half * tiles + j * per + q][lane])[t] = r[q];
       }
-      if (g == 0) {
+      if (g == 0 && half == 0) {
         float ve = 0.0f, iv = 1.0f;
-        if constexpr (FMT != QL_KV_BF16) ve = static_cast<float>(e), iv = power(254u - e);
+        if constexpr (FMT != QL_KV_BF16) ve = static_cast<float>(mine), iv = power(254u - mine);
         sh.ve[16 * t + n] = n < keys ? ve : -__builtin_inff();
-        sh.iv[16 * t + n] = n >= keys ? 0.0f : bad ? __builtin_nanf("") : iv;
+        sh.iv[16 * t + n] = n < keys ? iv : 0.0f;
       }
     }
   }
 };
 
-template <int FMT, int D, int MT, bool MASKED>
+template <int FMT, int D, int MT, int NW, bool MASKED>
 __device__ __forceinline__ void wide_tile(Rows<D> (&r)[MT], const u32x4 (&q)[MT][D / 32],
                                           const float (&qs)[MT], const Shared<FMT, D>& sh,
                                           const uint32_t (&seen)[MT], int lane) {
   const int g = lane >> 4;
   f32x4 s[MT][2];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) s[mt][t] = f32x4{0, 0, 0, 0};
+  for (int k = 0; k < D / 32; ++k) {
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
+    for (int t = 0; t < 2; ++t) {
       const u32x4 a = sh.k[t][k][lane];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) s[mt][t] = mma<false>(a, q[mt][k], s[mt][t]);
     }
+    if (k % 2) in_order();
   }
   float ve[8], iv[8];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const f32x4 a = *reinterpret_cast<const f32x4*>(&sh.ve[16 * t + 4 * g]);
-    const f32x4 b = *reinterpret_cast<const f32x4*>(&sh.iv[16 * t + 4 * g]);
+    f32x4 b = *reinterpret_cast<const f32x4*>(&sh.iv[16 * t + 4 * g]);
+    if constexpr (MASKED) {
+#pragma unroll
+      for (int h = 0; h < NW / 4; ++h) b += *reinterpret_cast<const f32x4*>(&sh.bad[h][16 * t + 4 * g]);
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) ve[4 * t + k] = a[k], iv[4 * t + k] = b[k];
   }
@@ -874,17 +888,21 @@ __device__ __forceinline__ void wide_tile(Rows<D> (&r)[MT], const u32x4 (&q)[MT]
     const u32x4 v = sh.v[d][lane];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) r[mt].o[d] = weigh<FMT>(v, p[mt], p_lo[mt], r[mt].o[d]);
+    if (d % 4 == 3) in_order();
   }
 }
 
-template <int FMT, int D, int MT>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void kv_attention_wide_kernel(KvAttnArgs a) {
+// Waves per SIMD that the register budget is set for.
+constexpr int wide_waves(int d, int mt, int nw) { return d == 256 && mt == 2 && nw == 4 ? 1 : 2; }
+
+template <int FMT, int D, int MT, int NW>
+__global__ __launch_bounds__(64 * NW, wide_waves(D, MT, NW)) void kv_attention_wide_kernel(KvAttnArgs a) {
   using L = KvLayout<FMT, D>;
   extern __shared__ __align__(16) uint8_t lds[];
   Shared<FMT, D>* sh = reinterpret_cast<Shared<FMT, D>*>(lds);      // two tiles
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const Work w = work_of<64 * MT>(a);
+  const Work w = work_of<16 * MT * NW>(a);
   if (!w.any) return;
   const int row0 = w.row0 + wave * (16 * MT);
   const bool active = row0 < w.rows;
@@ -898,51 +916,79 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void kv_attention_wi
     r[mt].clear();
   }
 
+  // The tiles in the order they are taken: the last ones, of which some key is
+  // hidden from some row, before those that every row sees.
   const int first = w.k0 / kTile, tiles = (w.k1 + kTile - 1) / kTile;
-  const int open = open_to(a, w, w.row0) / kTile;                    // of the whole block
-  const int mine = active ? open_to(a, w, row0) / kTile : 0;         // of this wave
-  const int t = wave & 1;
-  const bool is_v = wave >> 1;
+  const int open = open_to(a, w, w.row0) / kTile;
+  const int count = tiles > first ? tiles - first : 0;
+  constexpr int P = 2;      // tiles whose bytes are under way, and buffers in LDS
+  int partly = open > first ? tiles - open : count;
+  partly = partly + partly % P < count ? partly + partly % P : count;
+  auto tile_of = [&](int i) { return i < partly ? tiles - partly + i : first + i - partly; };
+  const int t = wave & 1, half = wave >> 2;
+  const bool is_v = wave >> 1 & 1;
   const int per_page = a.g.page_shift - 4;
   const int32_t* table = a.table + int64_t(w.b) * a.table_stride;
   int pages = -1;   // of block t of 64 tiles, one per lane
-  auto load = [&](int tile, Quarter<FMT, D>& x) {
-    const int it = tile - first, block = 2 * tile + t;
-    if ((it & 63) == 0) {
-      const int ahead = block + 2 * lane;
+  auto load = [&](int i, Part<FMT, D, NW>& x) {
+    if (i >= count) i = count - 1;      // once more: a load that may not happen costs a move
+    if ((i & 63) == 0) {
+      const int ahead = 2 * tile_of(i + lane) + t;
       pages = -1;
-      if (int64_t(ahead) * 16 < w.k1) {
+      if (i + lane < count && int64_t(ahead) * 16 < w.k1) {
         pages = table[ahead >> per_page];
         if (pages >= a.g.n_pages) pages = -1;
       }
     }
-    const int page = __builtin_amdgcn_readlane(pages, it & 63);
+    const int block = 2 * tile_of(i) + t;
+    const int page = __builtin_amdgcn_readlane(pages, i & 63);
     const int left = w.k1 - 16 * block;
     x.keys = page < 0 || left < 0 ? 0 : left < 16 ? left : 16;
     x.load(source<FMT, D>(a.g, kv_block(a.g, page < 0 ? 0 : page, w.head,
-                                        block & ((1 << per_page) - 1))), is_v, lane);
+                                        block & ((1 << per_page) - 1))), is_v, half, lane);
   };
-  if (first < tiles) {
-    Quarter<FMT, D> x;
-    load(first, x);
-    x.store(sh[0], t, is_v, first >= open, lane);
-    if (first + 1 < tiles) load(first + 1, x);
-    __syncthreads();
-    for (int i = first; i < tiles; ++i) {
-      const int at = (i - first) & 1;
-      if (i + 1 < tiles) {
-        // the other buffer: every wave has left it before the last barrier
-        x.store(sh[at ^ 1], t, is_v, i + 1 >= open, lane);
-        if (i + 2 < tiles) load(i + 2, x);
-      }
-      uint32_t seen[MT] = {};
-      if (i < mine) {
-        wide_tile<FMT, D, MT, false>(r, q, qs, sh[at], seen, lane);
-      } else if (active) {
+  // Tile i's bytes are in x[i % P] and its operands in sh[i % P]; the loops go
+  // P tiles at a time, because registers that are loaded must not be moved
+  // (the move would wait for the load).
+  Part<FMT, D, NW> x[P];
+  if (count > 0) {
+#pragma unroll
+    for (int y = 0; y < P; ++y) load(y, x[y]);
+  }
+  // Makes tile i's operands (y = i % P).  Every wave has left that buffer,
+  // which held tile i - P, before the last barrier.
+  auto prepare = [&](int i, int y) {
+    if (i < count) x[y].store(sh[y], t, is_v, half, i < partly, lane);
+    load(i + P, x[y]);
+  };
+  if (count > 0) prepare(0, 0);
+  __syncthreads();
+  // A loop for each kind of tile: where two ways meet, the accumulators would
+  // be copied.
+  for (int i = 0; i < partly; i += P) {
+#pragma unroll
+    for (int y = 0; y < P; ++y) {
+      if (i + y >= partly) break;
+      prepare(i + y + 1, (y + 1) % P);
+      if (active) {
+        uint32_t seen[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-          seen[mt] = visible(rm[mt], a.tree != nullptr, i * kTile, w.sq.ctx, g);
-        wide_tile<FMT, D, MT, true>(r, q, qs, sh[at], seen, lane);
+          seen[mt] = visible(rm[mt], a.tree != nullptr, tile_of(i + y) * kTile, w.sq.ctx, g);
+        in_order();
+        wide_tile<FMT, D, MT, NW, true>(r, q, qs, sh[y], seen, lane);
+      }
+      __syncthreads();
+    }
+  }
+  for (int i = partly; i < count; i += P) {
+#pragma unroll
+    for (int y = 0; y < P; ++y) {
+      if (i + y >= count) break;
+      prepare(i + y + 1, (y + 1) % P);
+      if (active) {
+        const uint32_t seen[MT] = {};
+        wide_tile<FMT, D, MT, NW, false>(r, q, qs, sh[y], seen, lane);
       }
       __syncthreads();
     }
@@ -1029,7 +1075,7 @@ KvAttnPlan kv_attention_plan(int d, int n_q, int n_kv, int64_t n_seqs, int64_t m
   (void)d;
   KvAttnPlan p;
   const int64_t rows = max_q * (n_q / n_kv);
-  p.rows = rows <= 16 ? 16 : rows <= 64 ? 64 : 128;
+  p.rows = rows <= 16 ? 16 : 64;
   p.row_blocks = (rows + p.rows - 1) / p.rows;
   // enough blocks for two on each compute unit, and at least 256 keys in one
   const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
@@ -1051,16 +1097,16 @@ size_t kv_attention_ws_bytes(const KvAttnPlan& p, int64_t tokens, int n_q, int d
   return size_t(p.splits) * size_t(tokens) * size_t(n_q) * size_t(d + 2) * sizeof(float);
 }
 
-template <int FMT, int D, int MT>
+template <int FMT, int D, int MT, int NW>
 static hipError_t launch_wide(const KvAttnArgs& a, unsigned blocks, hipStream_t s) {
   constexpr int bytes = 2 * sizeof(Shared<FMT, D>);
   if constexpr (bytes > 64 * 1024) {
     static std::atomic<int> done[64];
     const hipError_t e = lds_limit_once(
-        done, reinterpret_cast<const void*>(kv_attention_wide_kernel<FMT, D, MT>), bytes);
+        done, reinterpret_cast<const void*>(kv_attention_wide_kernel<FMT, D, MT, NW>), bytes);
     if (e != hipSuccess) return e;
   }
-  kv_attention_wide_kernel<FMT, D, MT><<<blocks, 64 * kWaves, bytes, s>>>(a);
+  kv_attention_wide_kernel<FMT, D, MT, NW><<<blocks, 64 * NW, bytes, s>>>(a);
   return hipGetLastError();
 }
 
@@ -1071,8 +1117,12 @@ hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a
   const unsigned blocks = unsigned((units + 7) / 8 * 8 * p.row_blocks);
   const hipError_t e = kv_dispatch(fmt, d, [&](auto f, auto n) {
     constexpr int FMT = decltype(f)::value, D = decltype(n)::value;
-    if (p.rows == 64) return launch_wide<FMT, D, 1>(a, blocks, s);
-    if (p.rows == 128) return launch_wide<FMT, D, 2>(a, blocks, s);
+    if (p.rows == 64) return launch_wide<FMT, D, 1, 4>(a, blocks, s);
+    if (p.rows == 128) return launch_wide<FMT, D, 2, 4>(a, blocks, s);
+    if constexpr (D == 256) {
+      if (p.rows == 129) return launch_wide<FMT, D, 1, 8>(a, blocks, s);
+      if (p.rows == 256) return launch_wide<FMT, D, 2, 8>(a, blocks, s);
+    }
     kv_attention_narrow_kernel<FMT, D><<<blocks, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
   });
