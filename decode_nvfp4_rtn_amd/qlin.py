@@ -461,85 +461,113 @@ class KVCache:
             data = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
         _bytes(data, "data", nbytes, torch.uint8)
         self.fmt, self.n_pages, self.page_size = fmt, n_pages, page_size
-        self.n_kv, self.head_dim, self.data = n_kv, head_dim, data
+        self.n_kv, self.head_dim, self.data, self.device = n_kv, head_dim, data, data.device
         self._struct = _KVStruct(fmt, n_kv, head_dim, page_size, n_pages, data.data_ptr(),
                                  data.numel())
         self._ref = ctypes.byref(self._struct)
 
 
-def _gpu(t, name, dtype, like):
-    """t is a GPU tensor of dtype on like's device."""
-    if t.device != like.device or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor on {like.device}, got {t.dtype} on "
-                         f"{t.device}")
-    return t
-
-
-def _vector(t, name, dtype, like, count):
-    _gpu(t, name, dtype, like)
-    if t.dim() != 1 or t.shape[0] != count or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [{count}] tensor, got {list(t.shape)}")
-    return t
-
+# The calls below are a few microseconds of GPU work each at decode sizes, so
+# their Python side is kept short: integers for pointers, no per-call stream
+# object (torch.cuda.current_stream() alone takes 2.8 us).
 
 _XDT = {torch.float32: QL_F32, torch.bfloat16: QL_BF16}
 
 
-def _heads(t, name, like, heads, d):
-    """t [tokens, heads, d] on like's device, a token's heads contiguous; its token stride."""
-    if t.device != like.device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}] on {like.device}, got "
-                         f"{list(t.shape)} on {t.device}")
-    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+def _queue(stream, dev):
+    """Address of the stream a call on `dev` goes to."""
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _vector(t, name, dtype, dev, count):
+    """Address of t, a contiguous [count] tensor of dtype on dev."""
+    if t.device != dev or t.dtype != dtype or t.shape != (count,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} [{count}] tensor on {dev}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _heads(t, name, dev, heads, d):
+    """Token stride of t [tokens, heads, d] on dev, a token's heads contiguous."""
+    shape = t.shape
+    if t.device != dev or len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}] on {dev}, got {list(shape)} on "
+                         f"{t.device}")
+    if shape[0] == 0:
+        return heads * d
+    a, b, c = t.stride()
+    if c != 1 or (heads > 1 and b != d):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    return a if shape[0] > 1 else heads * d
 
 
-def _new(shape, dtype, like, stream):
+def _new(shape, dtype, dev, stream):
     """A buffer for a call on `stream`: memory of that stream's own pool, so
     that work queued elsewhere on what the memory held before cannot meet it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _out3(t, name, like, shape, dtype, stream):
-    if t is None:
-        return _new(shape, dtype, like, stream)
-    _gpu(t, name, t.dtype, like)
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+def _rows_out(t, name, shape, dtypes, dev):
+    if t.device != dev or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on {dev} of "
+                         f"{' or '.join(map(str, dtypes))}, got {t.dtype} {list(t.shape)} on "
+                         f"{t.device}")
     return t
+
+
+def _table(t, dev, n_seqs):
+    """Row stride and columns of a block table."""
+    if t.device != dev or t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != n_seqs:
+        raise ValueError(f"block_table must be an int32 [{n_seqs}, pages] tensor on {dev}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+    rows, cols = t.stride()
+    if t.shape[1] > 1 and cols != 1:
+        raise ValueError("block_table: a sequence's row must be contiguous")
+    return (rows if n_seqs > 1 else t.shape[1]), t.shape[1]
+
+
+def _seqs(cu_q):
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        raise ValueError("cu_q must be an int32 [n_seqs + 1] tensor")
+    return cu_q.shape[0] - 1
 
 
 def kv_append(cache, k, v, slots, stream=None):
     """Write k, v [tokens, n_kv, head_dim] (fp32 or bf16; slices of a fused qkv
     tensor will do) to their slots (int64 [tokens]; negative: skipped)."""
-    ks = _heads(k, "k", cache.data, cache.n_kv, cache.head_dim)
-    vs = _heads(v, "v", cache.data, cache.n_kv, cache.head_dim)
-    dt = _XDT.get(k.dtype)
-    if dt is None or v.dtype != k.dtype or v.shape[0] != k.shape[0]:
-        raise ValueError("k and v must be float32 or bfloat16, of one type and length")
+    dev = cache.device
+    ks = _heads(k, "k", dev, cache.n_kv, cache.head_dim)
+    vs = _heads(v, "v", dev, cache.n_kv, cache.head_dim)
     tokens = k.shape[0]
-    _vector(slots, "slots", torch.int64, cache.data, tokens)
-    _check("kv_append", _lib.kv_append(cache._ref, k.data_ptr(), v.data_ptr(), dt, tokens, ks, vs,
-                                       slots.data_ptr(), _stream(stream)))
+    dt = _XDT.get(k.dtype)
+    if dt is None or v.dtype != k.dtype or v.shape[0] != tokens:
+        raise ValueError("k and v must be float32 or bfloat16, of one type and length")
+    at = _vector(slots, "slots", torch.int64, dev, tokens)
+    st = _lib.kv_append(cache._ref, k.data_ptr(), v.data_ptr(), dt, tokens, ks, vs, at,
+                        _queue(stream, dev))
+    if st:
+        raise QlinError("kv_append", st)
 
 
 def kv_gather(cache, slots, k=None, v=None, out_dtype=torch.bfloat16, stream=None):
     """Read rows back: (k, v) [tokens, n_kv, head_dim] in out_dtype (fp32 or
     bf16); a slot outside the cache gives zeros."""
+    dev = cache.device
     tokens = slots.shape[0] if slots.dim() == 1 else -1
-    _vector(slots, "slots", torch.int64, cache.data, tokens)
+    at = _vector(slots, "slots", torch.int64, dev, tokens)
     shape = (tokens, cache.n_kv, cache.head_dim)
-    k = _out3(k, "k", cache.data, shape, out_dtype, stream)
-    v = _out3(v, "v", cache.data, shape, out_dtype, stream)
+    k = _new(shape, out_dtype, dev, stream) if k is None else _rows_out(k, "k", shape, _XDT, dev)
+    v = _new(shape, k.dtype, dev, stream) if v is None else _rows_out(v, "v", shape, _XDT, dev)
     dt = _XDT.get(k.dtype)
     if dt is None or v.dtype != k.dtype:
         raise ValueError("k and v must be float32 or bfloat16, of one type")
-    _check("kv_gather", _lib.kv_gather(cache._ref, slots.data_ptr(), tokens, k.data_ptr(),
-                                       v.data_ptr(), dt, _stream(stream)))
+    st = _lib.kv_gather(cache._ref, at, tokens, k.data_ptr(), v.data_ptr(), dt,
+                        _queue(stream, dev))
+    if st:
+        raise QlinError("kv_gather", st)
     return k, v
 
 
@@ -552,53 +580,46 @@ def qkv_norm_rope_append(cache, qkv, n_q, slots, positions=None, rope=None, q_we
     rot / 2), or (2 i, 2 i + 1) if interleaved), and K and V written to slots
     (int64 [tokens]; negative: skipped).  Returns the queries, bf16
     [tokens, n_q, head_dim]."""
-    d = cache.head_dim
+    dev, d = cache.device, cache.head_dim
     width = (n_q + 2 * cache.n_kv) * d
-    if qkv.device != cache.data.device or qkv.dim() != 2 or qkv.shape[1] != width:
-        raise ValueError(f"qkv must be [tokens, {width}] on {cache.data.device}, got "
-                         f"{list(qkv.shape)} on {qkv.device}")
-    tokens = qkv.shape[0]
-    if tokens and qkv.stride(1) != 1:
-        raise ValueError("qkv: a token's row must be contiguous")
     dt = _XDT.get(qkv.dtype)
-    if dt is None:
-        raise ValueError("qkv must be float32 or bfloat16")
-    _vector(slots, "slots", torch.int64, cache.data, tokens)
+    if dt is None or qkv.device != dev or qkv.dim() != 2 or qkv.shape[1] != width:
+        raise ValueError(f"qkv must be a float32 or bfloat16 [tokens, {width}] tensor on {dev}, "
+                         f"got {qkv.dtype} {list(qkv.shape)} on {qkv.device}")
+    tokens = qkv.shape[0]
+    stride, inner = qkv.stride()
+    if tokens and inner != 1:
+        raise ValueError("qkv: a token's row must be contiguous")
+    slot_at = _vector(slots, "slots", torch.int64, dev, tokens)
     max_pos = rot = 0
+    pos_at = rope_at = None
     if rope is not None:
-        _gpu(rope, "rope", torch.float32, cache.data)
-        if rope.dim() != 2 or not rope.is_contiguous():
-            raise ValueError("rope must be a contiguous [max_pos, rot] tensor")
-        max_pos, rot = rope.shape
+        if (rope.device != dev or rope.dtype != torch.float32 or rope.dim() != 2
+                or not rope.is_contiguous()):
+            raise ValueError(f"rope must be a contiguous float32 [max_pos, rot] tensor on {dev}")
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _vector(positions, "positions", torch.int32, cache.data, tokens)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _vector(w, name, torch.float32, cache.data, d)
-    q_out = _out3(q_out, "q_out", cache.data, (tokens, n_q, d), torch.bfloat16, stream)
-    if q_out.dtype != torch.bfloat16:
-        raise ValueError("q_out must be bfloat16")
-    _check("qkv_norm_rope_append", _lib.qkv_norm_rope_append(
-        cache._ref, qkv.data_ptr(), dt, tokens, qkv.stride(0) if tokens > 1 else width, n_q,
-        _ptr(q_weight), _ptr(k_weight), eps, None if rope is None else positions.data_ptr(),
-        _ptr(rope), max_pos, rot, QL_ROPE_INTERLEAVED if interleaved else 0, q_out.data_ptr(),
-        slots.data_ptr(), _stream(stream)))
+        max_pos, rot = rope.shape
+        rope_at = rope.data_ptr()
+        pos_at = _vector(positions, "positions", torch.int32, dev, tokens)
+    qw = None if q_weight is None else _vector(q_weight, "q_weight", torch.float32, dev, d)
+    kw = None if k_weight is None else _vector(k_weight, "k_weight", torch.float32, dev, d)
+    shape = (tokens, n_q, d)
+    if q_out is None:
+        q_out = _new(shape, torch.bfloat16, dev, stream)
+    else:
+        _rows_out(q_out, "q_out", shape, (torch.bfloat16,), dev)
+    st = _lib.qkv_norm_rope_append(
+        cache._ref, qkv.data_ptr(), dt, tokens, stride if tokens > 1 else width, n_q, qw, kw, eps,
+        pos_at, rope_at, max_pos, rot, QL_ROPE_INTERLEAVED if interleaved else 0,
+        q_out.data_ptr(), slot_at, _queue(stream, dev))
+    if st:
+        raise QlinError("qkv_norm_rope_append", st)
     return q_out
 
 
 def kv_attention_workspace(cache, tokens, n_q, n_seqs, max_q, max_kv):
     return _lib.kv_attention_workspace(cache._ref, tokens, n_q, n_seqs, max_q, max_kv)
-
-
-def _table(block_table, like, n_seqs):
-    _gpu(block_table, "block_table", torch.int32, like)
-    if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
-        raise ValueError(f"block_table must be [{n_seqs}, pages], got {list(block_table.shape)}")
-    cols = block_table.shape[1]
-    if cols > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table: a sequence's row must be contiguous")
-    return (block_table.stride(0) if n_seqs > 1 else cols), cols
 
 
 def kv_attention(cache, q, cu_q, kv_lens, block_table, max_q, max_kv, tree=None, scale=None,
@@ -615,34 +636,36 @@ def kv_attention(cache, q, cu_q, kv_lens, block_table, max_q, max_kv, tree=None,
     tokens; max_kv: about the largest length.  scale: head_dim ** -0.5 when not
     given.  workspace: uint8 of kv_attention_workspace(...) bytes, allocated
     when not given.  Returns y bf16 [tokens, n_q, head_dim]."""
-    like = cache.data
+    dev, d = cache.device, cache.head_dim
     n_q = q.shape[1] if q.dim() == 3 else -1
-    stride = _heads(q, "q", like, n_q, cache.head_dim)
+    stride = _heads(q, "q", dev, n_q, d)
     if q.dtype != torch.bfloat16:
         raise ValueError("q must be bfloat16")
-    tokens = q.shape[0]
-    n_seqs = cu_q.shape[0] - 1 if cu_q.dim() == 1 else -1
-    if n_seqs < 0:
-        raise ValueError("cu_q must be an int32 [n_seqs + 1] tensor")
-    _vector(cu_q, "cu_q", torch.int32, like, n_seqs + 1)
-    _vector(kv_lens, "kv_lens", torch.int32, like, n_seqs)
-    tstride, cols = _table(block_table, like, n_seqs)
-    if tree is not None:
-        _vector(tree, "tree", torch.int64, like, tokens)
-    y = _out3(y, "y", like, (tokens, n_q, cache.head_dim), torch.bfloat16, stream)
-    if y.dtype != torch.bfloat16:
-        raise ValueError("y must be bfloat16")
+    tokens, n_seqs = q.shape[0], _seqs(cu_q)
+    cu_at = _vector(cu_q, "cu_q", torch.int32, dev, n_seqs + 1)
+    lens_at = _vector(kv_lens, "kv_lens", torch.int32, dev, n_seqs)
+    tstride, cols = _table(block_table, dev, n_seqs)
+    tree_at = None if tree is None else _vector(tree, "tree", torch.int64, dev, tokens)
+    shape = (tokens, n_q, d)
+    if y is None:
+        y = _new(shape, torch.bfloat16, dev, stream)
+    else:
+        _rows_out(y, "y", shape, (torch.bfloat16,), dev)
+    ws_at, have = None, 0
     if workspace is None:
-        need = _lib.kv_attention_workspace(cache._ref, tokens, n_q, n_seqs, max_q, max_kv)
-        if need:
-            workspace = _new(need, torch.uint8, like, stream)
+        have = _lib.kv_attention_workspace(cache._ref, tokens, n_q, n_seqs, max_q, max_kv)
+        if have:
+            workspace = _new((have,), torch.uint8, dev, stream)
+            ws_at = workspace.data_ptr()
     else:
         _bytes(workspace, "workspace", 0, torch.uint8)
-    _check("kv_attention", _lib.kv_attention(
-        cache._ref, q.data_ptr(), stride, tokens, n_q, n_seqs, cu_q.data_ptr(),
-        kv_lens.data_ptr(), block_table.data_ptr(), tstride, cols, max_q, max_kv, _ptr(tree),
-        cache.head_dim ** -0.5 if scale is None else scale, y.data_ptr(), _ptr(workspace),
-        0 if workspace is None else workspace.numel(), _stream(stream)))
+        ws_at, have = workspace.data_ptr(), workspace.numel()
+    st = _lib.kv_attention(
+        cache._ref, q.data_ptr(), stride, tokens, n_q, n_seqs, cu_at, lens_at,
+        block_table.data_ptr(), tstride, cols, max_q, max_kv, tree_at,
+        d ** -0.5 if scale is None else scale, y.data_ptr(), ws_at, have, _queue(stream, dev))
+    if st:
+        raise QlinError("kv_attention", st)
     return y
 
 
@@ -651,20 +674,18 @@ def kv_commit(cache, cu_q, kv_lens, block_table, path, stream=None):
     context: path int32 [n_seqs, max_path <= 64], accepted draft indices, root
     first, padded with -1; cu_q, kv_lens and block_table as the verification's
     kv_attention call."""
-    like = cache.data
-    n_seqs = cu_q.shape[0] - 1 if cu_q.dim() == 1 else -1
-    if n_seqs < 0:
-        raise ValueError("cu_q must be an int32 [n_seqs + 1] tensor")
-    _vector(cu_q, "cu_q", torch.int32, like, n_seqs + 1)
-    _vector(kv_lens, "kv_lens", torch.int32, like, n_seqs)
-    tstride, cols = _table(block_table, like, n_seqs)
-    _gpu(path, "path", torch.int32, like)
-    if path.dim() != 2 or path.shape[0] != n_seqs or not path.is_contiguous():
-        raise ValueError(f"path must be a contiguous [{n_seqs}, max_path] tensor, got "
-                         f"{list(path.shape)}")
-    _check("kv_commit", _lib.kv_commit(
-        cache._ref, n_seqs, cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), tstride,
-        cols, path.data_ptr(), path.shape[1], _stream(stream)))
+    dev, n_seqs = cache.device, _seqs(cu_q)
+    cu_at = _vector(cu_q, "cu_q", torch.int32, dev, n_seqs + 1)
+    lens_at = _vector(kv_lens, "kv_lens", torch.int32, dev, n_seqs)
+    tstride, cols = _table(block_table, dev, n_seqs)
+    if (path.device != dev or path.dtype != torch.int32 or path.dim() != 2
+            or path.shape[0] != n_seqs or not path.is_contiguous()):
+        raise ValueError(f"path must be a contiguous int32 [{n_seqs}, max_path] tensor on {dev}, "
+                         f"got {path.dtype} {list(path.shape)} on {path.device}")
+    st = _lib.kv_commit(cache._ref, n_seqs, cu_at, lens_at, block_table.data_ptr(), tstride, cols,
+                        path.data_ptr(), path.shape[1], _queue(stream, dev))
+    if st:
+        raise QlinError("kv_commit", st)
 
 
 def raw():
