@@ -22,8 +22,8 @@
 //   from memory into registers and the four results are joined at the end;
 //   bound by the cache's bytes.
 // wide (more rows): four waves share each tile.  Each turns a quarter of it
-//   into matrix operands in LDS, once for all, and takes 16 or 32 rows of its
-//   own; bound by the softmax's vector instructions and the products.
+//   into matrix operands in LDS, once for all, and takes 16 rows of its own;
+//   bound by the chain of LDS reads, products and softmax of a tile.
 //
 // Quantized rows.  K's row scale 2^ke goes into the bf16 operand where that
 // is free (narrow, NVFP4: it multiplies the score).  V's, 2^ve, joins the
@@ -149,26 +149,23 @@ struct Block {
     if constexpr (W == 4) return __builtin_amdgcn_raw_buffer_load_b128(s.codes, at, 0, 0);
     else return __builtin_amdgcn_raw_buffer_load_b64(s.codes, at, 0, 0);
   }
-  // The functions below work on COUNT loads, those from `first` on of a block.
-  template <int COUNT = L::kLoads>
-  __device__ __forceinline__ void load_k(const Source& s, int lane, int first = 0) {
+  __device__ __forceinline__ void load_k(const Source& s, int lane) {
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      w[i] = words(s, lane * L::kLoad + 64 * (first + i) * L::kLoad);
+    for (int i = 0; i < L::kLoads; ++i) {
+      w[i] = words(s, lane * L::kLoad + 64 * i * L::kLoad);
       if constexpr (FMT == QL_KV_NVFP4) {
         // whole words: a narrower load's result is extended at once, and waited for
-        sc[i] = load32(s.scales, (lane * L::kGPC & ~3) + 64 * (first + i) * L::kGPC);
+        sc[i] = load32(s.scales, (lane * L::kGPC & ~3) + 64 * i * L::kGPC);
       }
     }
   }
-  template <int COUNT = L::kLoads>
-  __device__ __forceinline__ void load_v(const Source& s, int lane, int first = 0) {
+  __device__ __forceinline__ void load_v(const Source& s, int lane) {
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      w[i] = words(s, lane * L::kLoad + (16 * L::kRow + 64 * (first + i) * L::kLoad));
-      if constexpr (FMT == QL_KV_NVFP4)      // group (first + i) kDC + (lane % 16) kDC / 16
+    for (int i = 0; i < L::kLoads; ++i) {
+      w[i] = words(s, lane * L::kLoad + (16 * L::kRow + 64 * i * L::kLoad));
+      if constexpr (FMT == QL_KV_NVFP4)      // group i kDC + (lane % 16) kDC / 16
         sc[i] = load32(s.scales, (lane & 15) * L::kDC / 16 * 16 + (lane >> 4) * 4 +
-                                     (D + (first + i) * L::kDC * 16));
+                                     (D + i * L::kDC * 16));
     }
   }
   // K operand of step s (its elements of d: q_element), bf16 with the row
@@ -226,17 +223,16 @@ struct Block {
 
   // V: clears the keys of the lane's quad from `keys` (0..4) on; what lies
   // there is not part of the sequence.
-  template <int COUNT = L::kLoads>
   __device__ __forceinline__ void clear_v(int keys) {
     if constexpr (FMT == QL_KV_BF16) {
       const uint32_t a = keys >= 2 ? ~0u : keys == 1 ? 0xFFFFu : 0u;
       const uint32_t b = keys >= 4 ? ~0u : keys == 3 ? 0xFFFFu : 0u;
 #pragma unroll
-      for (int x = 0; x < COUNT * W; ++x) w[x / W][x % W] &= x & 1 ? b : a;
+      for (int x = 0; x < L::kLoads * W; ++x) w[x / W][x % W] &= x & 1 ? b : a;
     } else {
       const uint32_t m = keys >= 4 ? ~0u : (1u << (8 * keys)) - 1u;
 #pragma unroll
-      for (int i = 0; i < COUNT; ++i) {
+      for (int i = 0; i < L::kLoads; ++i) {
         w[i] &= m;
         if constexpr (FMT == QL_KV_NVFP4) sc[i] &= m;
       }
@@ -244,11 +240,10 @@ struct Block {
   }
 
   // V: non-zero where a value that the lane holds is a NaN or an infinity.
-  template <int COUNT = L::kLoads>
   __device__ __forceinline__ uint32_t non_finite() const {
     uint32_t r = 0;
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
+    for (int i = 0; i < L::kLoads; ++i) {
       if constexpr (FMT == QL_KV_NVFP4) {
         r |= bad_bytes(sc[i]);
       } else {
@@ -260,11 +255,10 @@ struct Block {
   }
   // V: clears them (NVFP4: their groups); bit k of the result: key k of the
   // lane's quad had one, in an element of any of the 16 lanes that hold it.
-  template <int COUNT = L::kLoads>
   __device__ __forceinline__ uint32_t clear_non_finite() {
     uint32_t b = 0, c = 0, r;     // BF16: keys 0, 1 and keys 2, 3; others: b, a byte a key
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
+    for (int i = 0; i < L::kLoads; ++i) {
       if constexpr (FMT == QL_KV_NVFP4) {
         const uint32_t m = bad_bytes(sc[i]);
         b |= m;
@@ -770,37 +764,31 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
 }
 
 // ---------------------------------------------------------------------------
-// wide: 16 MT rows for each of NW waves, tiles shared through LDS
+// wide: 64 rows, 16 for each wave; tiles shared through LDS
 // ---------------------------------------------------------------------------
 template <int FMT, int D>
 struct Shared {        // one tile's operands
   u32x4 k[2][D / 32][64];
   u32x4 v[D / 16][64];
   float ve[kTile];     // V's row exponent + 127; -inf: the key is missing
-  float iv[kTile];     // 2^-that
-  float bad[2][kTile]; // tiles with hidden keys: NaN where a half of the row holds one, or an infinity
+  float iv[kTile];     // 2^-that; NaN: the row holds a NaN or an infinity
 };
 
-// The part of a tile that a wave turns into operands: block t's K or V, or
-// (eight waves) one half of its loads.
-template <int FMT, int D, int NW>
-struct Part {
+// The quarter of a tile that a wave turns into operands: block t's K or V.
+template <int FMT, int D>
+struct Quarter {
   using L = KvLayout<FMT, D>;
-  static constexpr int H = NW / 4;                 // parts of a block's K (or V)
-  static constexpr int kMine = L::kLoads / H;      // loads
-  Block<FMT, D> x;     // loads 0 .. kMine - 1 are used
+  Block<FMT, D> x;
   uint32_t e;          // row exponents of the four keys around key lane % 16
   int keys;            // keys of the block that are there
 
-  __device__ __forceinline__ void load(const Source& s, bool is_v, int half, int lane) {
-    if (is_v) x.template load_v<kMine>(s, lane, half * kMine);
-    else x.template load_k<kMine>(s, lane, half * kMine);
-    if constexpr (FMT != QL_KV_BF16)
-      e = load32(s.scales, L::k_exp(lane & 12) + (is_v ? 4 : 0));
+  __device__ __forceinline__ void load(const Source& s, bool is_v, int lane) {
+    if (is_v) x.load_v(s, lane);
+    else x.load_k(s, lane);
+    if constexpr (FMT != QL_KV_BF16) e = load32(s.scales, L::k_exp(lane & 12) + (is_v ? 4 : 0));
   }
   // check: keys of this tile may be hidden from some row.
-  __device__ __forceinline__ void store(Shared<FMT, D>& sh, int t, bool is_v, int half, bool check,
-                                        int lane) {
+  __device__ __forceinline__ void store(Shared<FMT, D>& sh, int t, bool is_v, bool check, int lane) {
     const int n = lane & 15, g = lane >> 4;
     uint32_t mine = 0;
     if constexpr (FMT != QL_KV_BF16) mine = e >> 8 * (n & 3) & 0xFFu;
@@ -808,129 +796,107 @@ struct Part {
       float p = 1.0f;
       if constexpr (FMT != QL_KV_BF16) p = power(mine);
       const uint32_t keep = n < keys ? ~0u : 0u;
-      constexpr int steps = D / 32 / H;
 #pragma unroll
-      for (int s = 0; s < steps; ++s)
-        sh.k[t][half * steps + s][lane] = x.template k_operand<false>(s, p, lane) & keep;
+      for (int s = 0; s < D / 32; ++s)
+        sh.k[t][s][lane] = x.template k_operand<false>(s, p, lane) & keep;
     } else {
+      uint32_t bad = 0;
       if (keys < 16) {
         const int left = keys - 4 * g;
-        x.template clear_v<kMine>(left < 0 ? 0 : left > 4 ? 4 : left);
+        x.clear_v(left < 0 ? 0 : left > 4 ? 4 : left);
       }
-      if (check) {
+      if (check && __any(x.non_finite() != 0)) {
         // as in narrow_tile; lane n's key is in quad n / 4
-        uint32_t bad = 0;
-        if (__any(x.template non_finite<kMine>() != 0)) {
-          bad = x.template clear_non_finite<kMine>();
-          bad = __shfl(bad, (n >> 2) * 16, 64) >> (n & 3) & 1u;
-        }
-        if (g == 0) sh.bad[half][16 * t + n] = bad ? __builtin_nanf("") : 0.0f;
+        bad = x.clear_non_finite();
+        bad = __shfl(bad, (n >> 2) * 16, 64) >> (n & 3) & 1u;
       }
-      constexpr int per = Block<FMT, D>::kPer, tiles = D / 16 / H;
+      constexpr int per = Block<FMT, D>::kPer;
 #pragma unroll
-      for (int j = 0; j < tiles / per; ++j) {
+      for (int j = 0; j < D / 16 / per; ++j) {
         uint2 r[per];
         x.v_operands(j, r);
 #pragma unroll
-        for (int q = 0; q < per; ++q)
-          reinterpret_cast<uint2*>(&sh.v[half * tiles + j * per + q][lane])[t] = r[q];
+        for (int q = 0; q < per; ++q) reinterpret_cast<uint2*>(&sh.v[j * per + q][lane])[t] = r[q];
       }
-      if (g == 0 && half == 0) {
+      if (g == 0) {
         float ve = 0.0f, iv = 1.0f;
         if constexpr (FMT != QL_KV_BF16) ve = static_cast<float>(mine), iv = power(254u - mine);
         sh.ve[16 * t + n] = n < keys ? ve : -__builtin_inff();
-        sh.iv[16 * t + n] = n < keys ? iv : 0.0f;
+        sh.iv[16 * t + n] = n >= keys ? 0.0f : bad ? __builtin_nanf("") : iv;
       }
     }
   }
 };
 
-template <int FMT, int D, int MT, int NW, bool MASKED>
-__device__ __forceinline__ void wide_tile(Rows<D> (&r)[MT], const u32x4 (&q)[MT][D / 32],
-                                          const float (&qs)[MT], const Shared<FMT, D>& sh,
-                                          const uint32_t (&seen)[MT], int lane) {
+template <int FMT, int D, bool MASKED>
+__device__ __forceinline__ void wide_tile(Rows<D>& r, const u32x4 (&q)[D / 32], float qs,
+                                          const Shared<FMT, D>& sh, uint32_t seen, int lane) {
   const int g = lane >> 4;
-  f32x4 s[MT][2];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = f32x4{0, 0, 0, 0};
+  f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const u32x4 a = sh.k[t][k][lane];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) s[mt][t] = mma<false>(a, q[mt][k], s[mt][t]);
-    }
+    for (int t = 0; t < 2; ++t) s[t] = mma<false>(sh.k[t][k][lane], q[k], s[t]);
     if (k % 2) in_order();
   }
-  float ve[8], iv[8];
+  float z[8], iv[8];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const f32x4 a = *reinterpret_cast<const f32x4*>(&sh.ve[16 * t + 4 * g]);
-    f32x4 b = *reinterpret_cast<const f32x4*>(&sh.iv[16 * t + 4 * g]);
-    if constexpr (MASKED) {
+    const f32x4 b = *reinterpret_cast<const f32x4*>(&sh.iv[16 * t + 4 * g]);
 #pragma unroll
-      for (int h = 0; h < NW / 4; ++h) b += *reinterpret_cast<const f32x4*>(&sh.bad[h][16 * t + 4 * g]);
+    for (int k = 0; k < 4; ++k) {
+      z[4 * t + k] = __builtin_fmaf(s[t][k], qs, a[k]);
+      iv[4 * t + k] = b[k];
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) ve[4 * t + k] = a[k], iv[4 * t + k] = b[k];
   }
-  u32x4 p[MT], p_lo[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    float z[8];
-#pragma unroll
-    for (int x = 0; x < 8; ++x) z[x] = __builtin_fmaf(s[mt][x >> 2][x & 3], qs[mt], ve[x]);
-    softmax_step<FMT, D, MASKED, true>(r[mt], z, iv, seen[mt], p[mt], p_lo[mt]);
-  }
+  u32x4 p, p_lo;
+  softmax_step<FMT, D, MASKED, true>(r, z, iv, seen, p, p_lo);
 #pragma unroll
   for (int d = 0; d < D / 16; ++d) {
-    const u32x4 v = sh.v[d][lane];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) r[mt].o[d] = weigh<FMT>(v, p[mt], p_lo[mt], r[mt].o[d]);
+    r.o[d] = weigh<FMT>(sh.v[d][lane], p, p_lo, r.o[d]);
     if (d % 4 == 3) in_order();
   }
 }
 
-// Waves per SIMD that the register budget is set for.
-constexpr int wide_waves(int d, int mt, int nw) { return d == 256 && mt == 2 && nw == 4 ? 1 : 2; }
-
-template <int FMT, int D, int MT, int NW>
-__global__ __launch_bounds__(64 * NW, wide_waves(D, MT, NW)) void kv_attention_wide_kernel(KvAttnArgs a) {
+// 16 rows to a wave, and so two or three waves on a SIMD, beat 32: a tile is a
+// chain of LDS reads, products and the softmax that takes a wave 2000 cycles,
+// 3 times what it issues, so it is the other waves that fill the SIMD (16
+// sequences of 63 drafts over 2000 8-bit keys, 32 / 8 128-wide heads: 56 us,
+// and 77 us with 32 rows to a wave; eight waves to a block: 78 us).
+template <int FMT, int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAttnArgs a) {
   using L = KvLayout<FMT, D>;
+  constexpr int P = 2;      // tiles whose bytes are under way, and buffers in LDS
   extern __shared__ __align__(16) uint8_t lds[];
-  Shared<FMT, D>* sh = reinterpret_cast<Shared<FMT, D>*>(lds);      // two tiles
+  Shared<FMT, D>* sh = reinterpret_cast<Shared<FMT, D>*>(lds);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const Work w = work_of<16 * MT * NW>(a);
+  const Work w = work_of<64>(a);
   if (!w.any) return;
-  const int row0 = w.row0 + wave * (16 * MT);
+  const int row0 = w.row0 + wave * 16;
   const bool active = row0 < w.rows;
-  u32x4 q[MT][D / 32];
-  float qs[MT];
-  RowMask rm[MT];
-  Rows<D> r[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    load_query<FMT, D, false>(a, w, row0 + 16 * mt + n, g, q[mt], qs[mt], rm[mt]);
-    r[mt].clear();
-  }
+  u32x4 q[D / 32];
+  float qs;
+  RowMask rm;
+  load_query<FMT, D, false>(a, w, row0 + n, g, q, qs, rm);
+  Rows<D> r;
+  r.clear();
 
   // The tiles in the order they are taken: the last ones, of which some key is
   // hidden from some row, before those that every row sees.
   const int first = w.k0 / kTile, tiles = (w.k1 + kTile - 1) / kTile;
   const int open = open_to(a, w, w.row0) / kTile;
   const int count = tiles > first ? tiles - first : 0;
-  constexpr int P = 2;      // tiles whose bytes are under way, and buffers in LDS
   int partly = open > first ? tiles - open : count;
   partly = partly + partly % P < count ? partly + partly % P : count;
   auto tile_of = [&](int i) { return i < partly ? tiles - partly + i : first + i - partly; };
-  const int t = wave & 1, half = wave >> 2;
-  const bool is_v = wave >> 1 & 1;
+  const int t = wave & 1;
+  const bool is_v = wave >> 1;
   const int per_page = a.g.page_shift - 4;
   const int32_t* table = a.table + int64_t(w.b) * a.table_stride;
   int pages = -1;   // of block t of 64 tiles, one per lane
-  auto load = [&](int i, Part<FMT, D, NW>& x) {
+  auto load = [&](int i, Quarter<FMT, D>& x) {
     if (i >= count) i = count - 1;      // once more: a load that may not happen costs a move
     if ((i & 63) == 0) {
       const int ahead = 2 * tile_of(i + lane) + t;
@@ -945,12 +911,12 @@ __global__ __launch_bounds__(64 * NW, wide_waves(D, MT, NW)) void kv_attention_w
     const int left = w.k1 - 16 * block;
     x.keys = page < 0 || left < 0 ? 0 : left < 16 ? left : 16;
     x.load(source<FMT, D>(a.g, kv_block(a.g, page < 0 ? 0 : page, w.head,
-                                        block & ((1 << per_page) - 1))), is_v, half, lane);
+                                        block & ((1 << per_page) - 1))), is_v, lane);
   };
   // Tile i's bytes are in x[i % P] and its operands in sh[i % P]; the loops go
   // P tiles at a time, because registers that are loaded must not be moved
   // (the move would wait for the load).
-  Part<FMT, D, NW> x[P];
+  Quarter<FMT, D> x[P];
   if (count > 0) {
 #pragma unroll
     for (int y = 0; y < P; ++y) load(y, x[y]);
@@ -958,7 +924,7 @@ __global__ __launch_bounds__(64 * NW, wide_waves(D, MT, NW)) void kv_attention_w
   // Makes tile i's operands (y = i % P).  Every wave has left that buffer,
   // which held tile i - P, before the last barrier.
   auto prepare = [&](int i, int y) {
-    if (i < count) x[y].store(sh[y], t, is_v, half, i < partly, lane);
+    if (i < count) x[y].store(sh[y], t, is_v, i < partly, lane);
     load(i + P, x[y]);
   };
   if (count > 0) prepare(0, 0);
@@ -971,12 +937,9 @@ __global__ __launch_bounds__(64 * NW, wide_waves(D, MT, NW)) void kv_attention_w
       if (i + y >= partly) break;
       prepare(i + y + 1, (y + 1) % P);
       if (active) {
-        uint32_t seen[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-          seen[mt] = visible(rm[mt], a.tree != nullptr, tile_of(i + y) * kTile, w.sq.ctx, g);
+        const uint32_t seen = visible(rm, a.tree != nullptr, tile_of(i + y) * kTile, w.sq.ctx, g);
         in_order();
-        wide_tile<FMT, D, MT, NW, true>(r, q, qs, sh[y], seen, lane);
+        wide_tile<FMT, D, true>(r, q, qs, sh[y], seen, lane);
       }
       __syncthreads();
     }
@@ -986,43 +949,36 @@ __global__ __launch_bounds__(64 * NW, wide_waves(D, MT, NW)) void kv_attention_w
     for (int y = 0; y < P; ++y) {
       if (i + y >= count) break;
       prepare(i + y + 1, (y + 1) % P);
-      if (active) {
-        const uint32_t seen[MT] = {};
-        wide_tile<FMT, D, MT, NW, false>(r, q, qs, sh[y], seen, lane);
-      }
+      if (active) wide_tile<FMT, D, false>(r, q, qs, sh[y], 0, lane);
       __syncthreads();
     }
   }
-  if (!active) return;
+  const int row = row0 + n;
+  const float l = column_sum(r.l), inv = reciprocal(l);
+  if (row >= w.rows) return;
+  const int64_t out = out_row(a, w, row);
+  const int64_t at = int64_t(w.split) * a.tokens * a.n_q + out;
+  if (w.nsplit > 1 && g == 0) a.part_ml[2 * at] = r.m, a.part_ml[2 * at + 1] = l;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int row = row0 + 16 * mt + n;
-    const float l = column_sum(r[mt].l), inv = reciprocal(l);
-    if (row >= w.rows) continue;
-    const int64_t out = out_row(a, w, row);
-    const int64_t at = int64_t(w.split) * a.tokens * a.n_q + out;
-    if (w.nsplit > 1 && g == 0) a.part_ml[2 * at] = r[mt].m, a.part_ml[2 * at + 1] = l;
+  for (int i = 0; i < L::kLoads; ++i)
 #pragma unroll
-    for (int i = 0; i < L::kLoads; ++i)
+    for (int x8 = 0; x8 < 4 * L::kDC; x8 += 8) {
+      const int d = 16 * L::kDC * i + 4 * L::kDC * g + x8;
+      float v[8];
 #pragma unroll
-      for (int x = 0; x < 4 * L::kDC; x += 8) {
-        const int d = 16 * L::kDC * i + 4 * L::kDC * g + x;
-        float v[8];
+      for (int y = 0; y < 8; ++y) v[y] = r.o[L::kDC * i + (x8 + y) % L::kDC][(x8 + y) / L::kDC];
+      if (w.nsplit == 1) {
+        uint32_t y[4];
 #pragma unroll
-        for (int y = 0; y < 8; ++y) v[y] = r[mt].o[L::kDC * i + (x + y) % L::kDC][(x + y) / L::kDC];
-        if (w.nsplit == 1) {
-          uint32_t y[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) y[z] = pack_bf16x2(v[2 * z] * inv, v[2 * z + 1] * inv);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out * D + d) =
-              make_uint4(y[0], y[1], y[2], y[3]);
-        } else {
-          float4* o = reinterpret_cast<float4*>(a.part_o + at * D + d);
-          o[0] = make_float4(v[0], v[1], v[2], v[3]);
-          o[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
+        for (int z = 0; z < 4; ++z) y[z] = pack_bf16x2(v[2 * z] * inv, v[2 * z + 1] * inv);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out * D + d) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+      } else {
+        float4* o = reinterpret_cast<float4*>(a.part_o + at * D + d);
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
-  }
+    }
 }
 
 // Joins the splits of every row that has more than one, in a fixed order.
@@ -1072,18 +1028,35 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttnArgs a, in
 
 KvAttnPlan kv_attention_plan(int d, int n_q, int n_kv, int64_t n_seqs, int64_t max_q,
                              int64_t max_kv) {
-  (void)d;
   KvAttnPlan p;
   const int64_t rows = max_q * (n_q / n_kv);
   p.rows = rows <= 16 ? 16 : 64;
   p.row_blocks = (rows + p.rows - 1) / p.rows;
-  // enough blocks for two on each compute unit, and at least 256 keys in one
-  const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
+  // Splits of the longest sequence.  A second launch joins them (3 to 10 us),
+  // and a block takes about as long as 128 keys of a narrow wave to start, so
+  // up to 512 keys stay whole (500 keys, one sequence: 8 us against 12), and
+  // no split is under 256 keys.
+  const int64_t cus = device_cu_count() > 0 ? device_cu_count() : 256;
   const int64_t blocks = n_seqs * n_kv * p.row_blocks;
-  int64_t splits = (4 * cus + blocks - 1) / blocks;
-  const int64_t most_splits = max_kv <= 512 ? 1 : (max_kv + 255) / 256;
-  if (splits > most_splits) splits = most_splits;
-  if (splits < 1) splits = 1;
+  auto splits_for = [&](int64_t per_cu) {
+    const int64_t most = max_kv <= 512 ? 1 : (max_kv + 255) / 256;
+    const int64_t n = (per_cu * cus + blocks - 1) / blocks;
+    return n < 1 ? 1 : n > most ? most : n;
+  };
+  int64_t splits;
+  if (p.rows == 64) {
+    // as many blocks as run at once: three on a compute unit, two of 256-wide
+    // heads (the tree cases of 128- and 256-wide heads: 30 and 111 us; with 2
+    // and 3: 33 and 139 us)
+    splits = splits_for(d == 256 ? 2 : 3);
+  } else {
+    // two on a compute unit (one sequence of 131071 8-bit keys: 56 us; with
+    // four 61 us), four while the splits are longer than 2048 keys (32
+    // sequences of up to 8192 4-bit keys: 56 us; with two 65 us)
+    splits = splits_for(2);
+    const int64_t four = splits_for(4), need = (max_kv + 2047) / 2048;
+    if (splits < need) splits = need < four ? need : four;
+  }
   if (splits > 256) splits = 256;
   const int64_t chunk = ((max_kv + splits - 1) / splits + 127) / 128 * 128;
   p.chunk = chunk > 128 ? int(chunk) : 128;
@@ -1097,16 +1070,16 @@ size_t kv_attention_ws_bytes(const KvAttnPlan& p, int64_t tokens, int n_q, int d
   return size_t(p.splits) * size_t(tokens) * size_t(n_q) * size_t(d + 2) * sizeof(float);
 }
 
-template <int FMT, int D, int MT, int NW>
+template <int FMT, int D>
 static hipError_t launch_wide(const KvAttnArgs& a, unsigned blocks, hipStream_t s) {
   constexpr int bytes = 2 * sizeof(Shared<FMT, D>);
   if constexpr (bytes > 64 * 1024) {
     static std::atomic<int> done[64];
     const hipError_t e = lds_limit_once(
-        done, reinterpret_cast<const void*>(kv_attention_wide_kernel<FMT, D, MT, NW>), bytes);
+        done, reinterpret_cast<const void*>(kv_attention_wide_kernel<FMT, D>), bytes);
     if (e != hipSuccess) return e;
   }
-  kv_attention_wide_kernel<FMT, D, MT, NW><<<blocks, 64 * NW, bytes, s>>>(a);
+  kv_attention_wide_kernel<FMT, D><<<blocks, 64 * kWaves, bytes, s>>>(a);
   return hipGetLastError();
 }
 
@@ -1117,12 +1090,7 @@ hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a
   const unsigned blocks = unsigned((units + 7) / 8 * 8 * p.row_blocks);
   const hipError_t e = kv_dispatch(fmt, d, [&](auto f, auto n) {
     constexpr int FMT = decltype(f)::value, D = decltype(n)::value;
-    if (p.rows == 64) return launch_wide<FMT, D, 1, 4>(a, blocks, s);
-    if (p.rows == 128) return launch_wide<FMT, D, 2, 4>(a, blocks, s);
-    if constexpr (D == 256) {
-      if (p.rows == 129) return launch_wide<FMT, D, 1, 8>(a, blocks, s);
-      if (p.rows == 256) return launch_wide<FMT, D, 2, 8>(a, blocks, s);
-    }
+    if (p.rows == 64) return launch_wide<FMT, D>(a, blocks, s);
     kv_attention_narrow_kernel<FMT, D><<<blocks, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
   });

@@ -138,7 +138,7 @@ struct KvAttnArgs {
   int row_blocks;
 };
 struct KvAttnPlan {
-  int rows;               // query rows per block: 16, 64 or 128
+  int rows;               // query rows per block: 16 (narrow) or 64 (wide)
   int64_t row_blocks;
   int splits;
   int chunk;
