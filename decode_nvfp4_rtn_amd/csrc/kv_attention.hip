@@ -28,11 +28,12 @@
 // Quantized rows.  K's row scale 2^ke goes into the bf16 operand where that
 // is free (narrow, NVFP4: it multiplies the score).  V's, 2^ve, joins the
 // exponent: with z the score in units of log 2 the weight that enters the
-// product is w = 2^(z + ve - m), m a running maximum of z + ve, and the sum of
-// weights takes w 2^-ve.  So the weights are at most 2^8 however the rows'
-// scales differ, and V's codes (NVFP4: times their group scales, at most 6
-// significant bits) enter in fp16 exactly.  The weights' rounding to fp16
-// (relative 2^-12) is below that of the bf16 result.  A bf16 cache takes bf16
+// product is w = 2^(z + ve - m), m + 7 a running maximum of z + ve, and the
+// sum of weights takes w 2^-ve.  So the weights are at most 2^15 however the
+// rows' scales differ, and V's codes (NVFP4: times their group scales, at most
+// 6 significant bits) enter in fp16 exactly.  The weights' rounding to fp16
+// (relative 2^-12, and of weights below 2^-21 of the largest a multiple of at
+// most 2^-31 of it) is below that of the bf16 result.  A bf16 cache takes bf16
 // operands and its weights as the sum of two bf16 values (16 bits), because
 // one of 8 bits would add as much error as the rounding of the result.
 #include "kv_cache.hpp"
@@ -51,7 +52,12 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kWaves = 4;
 constexpr int kTile = 32;               // keys per tile
 constexpr float kLowest = -3.0e38f;     // running maximum before the first key
-constexpr float kSlack = 8.0f;          // growth of the maximum that is let pass (weights <= 2^8)
+// Weights are 2^(z - m).  The largest is 2^kUp when m is set, and m is set anew
+// when one would pass 2^kMost: fp16 ends at 2^16, and the further up the
+// weights are the fewer fall below its normal range.
+constexpr float kUp = 7.0f, kMost = 15.0f;
+// The sum of weights of quantized rows is kept times 2^-7: 2^-ve reaches 2^100.
+constexpr float kUnit = 1.0f / 128;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <bool HALF>   // fp16 operands, or bf16
@@ -444,7 +450,7 @@ struct Rows {
 };
 
 // From z (scores, V's row exponent added) to the weights' operand p (BF16:
-// and p_lo); iv: 2^-ve.  MASKED: `seen` says which keys count.
+// and p_lo); iv: 2 2^-ve.  MASKED: `seen` says which keys count.
 template <int FMT, int D, bool MASKED, bool IV>
 __device__ __forceinline__ void softmax_step(Rows<D>& r, float (&z)[8], const float (&iv)[8],
                                              uint32_t seen, u32x4& p, u32x4& p_lo) {
@@ -456,25 +462,26 @@ __device__ __forceinline__ void softmax_step(Rows<D>& r, float (&z)[8], const fl
 #pragma unroll
   for (int x = 1; x < 8; ++x) mx = __builtin_fmaxf(mx, z[x]);
   mx = column_max(mx);
-  if (__any(mx > r.m + kSlack)) {
-    const float mn = __builtin_fmaxf(r.m, mx);
+  if (__any(mx > r.m + kMost)) {
+    const float mn = __builtin_fmaxf(r.m, mx - kUp);
     const float f = __builtin_amdgcn_exp2f(r.m - mn);
     r.m = mn;
     r.l *= f;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) r.o[d] *= f;
   }
-  float w[8];
+  float w[8], l = 0.0f;
 #pragma unroll
   for (int x = 0; x < 8; ++x) {
     w[x] = __builtin_amdgcn_exp2f(z[x] - r.m);
     if constexpr (IV) {
-      if constexpr (MASKED) r.l += seen >> x & 1 ? w[x] * iv[x] : 0.0f;   // iv may be NaN
-      else r.l = __builtin_fmaf(w[x], iv[x], r.l);
+      if constexpr (MASKED) l += seen >> x & 1 ? w[x] * iv[x] : 0.0f;   // iv may be NaN
+      else l = __builtin_fmaf(w[x], iv[x], l);
     } else {
-      r.l += w[x];
+      l += w[x];
     }
   }
+  r.l = FMT == QL_KV_BF16 ? r.l + l : __builtin_fmaf(l, kUnit / 2, r.l);   // iv: 2 2^-ve
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     if constexpr (FMT == QL_KV_BF16) {
@@ -499,8 +506,12 @@ __device__ __forceinline__ f32x4 weigh(u32x4 v, u32x4 p, u32x4 p_lo, f32x4 o) {
   return o;
 }
 
-// 1 / (sum of weights); 0 for a row that sees nothing, whose result is zero.
-__device__ __forceinline__ float reciprocal(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+// 1 / (sum of weights), from the sum as it is kept (in units of 1 / unit); 0
+// for a row that sees nothing, whose result is zero.
+__device__ __forceinline__ float reciprocal(float l, float unit) {
+  return l == 0.0f ? 0.0f : unit / l;
+}
+constexpr float unit_of(int fmt) { return fmt == QL_KV_BF16 ? 1.0f : kUnit; }
 
 // Row `row`'s place in y and in the partial results.
 __device__ __forceinline__ int64_t out_row(const KvAttnArgs& a, const Work& w, int row) {
@@ -569,7 +580,7 @@ __device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&sm_q)[D / 
       z[x] = __builtin_fmaf(s[t][k], qs, hide);
     } else {
       const uint32_t b = tile.ve[t] >> (8 * k) & 0xFFu;
-      iv[x] = power((0xFEFEFEFEu - tile.ve[t]) >> (8 * k) & 0xFFu);   // 254 - b
+      iv[x] = power(~tile.ve[t] >> (8 * k) & 0xFFu);   // 2^(128 - b)
       float v = s[t][k];
       if constexpr (HALF) v *= power(tile.ke[t] >> (8 * k) & 0xFFu);
       z[x] = __builtin_fmaf(v, qs, static_cast<float>(b) + hide);
@@ -613,9 +624,6 @@ constexpr int narrow_waves(int fmt, int d) {
   return d == 64 ? 5 : d == 128 ? (fmt == QL_KV_BF16 ? 3 : 4) : 2;
 }
 
-// Tiles that are under way while one is worked on.
-constexpr int narrow_ahead(int fmt, int d) { return 0; }
-
 template <int FMT, int D>
 __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attention_narrow_kernel(
     KvAttnArgs a) {
@@ -649,16 +657,13 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
   const int count = tiles > first ? (tiles - first + kWaves - 1) / kWaves : 0;
   const int open = open_to(a, w, w.row0) / kTile;
   const int whole = open > first ? (open - first + kWaves - 1) / kWaves : 0;
-  constexpr int N = narrow_ahead(FMT, D) + 1;          // tiles in registers
-  int partly = count - whole;
-  partly = (partly + N - 1) / N * N < count ? (partly + N - 1) / N * N : count;
+  const int partly = count - whole;
   auto tile_of = [&](int i) { return first + kWaves * (count - 1 - i); };
   const int per_page = a.g.page_shift - 4;             // log2(blocks of a page)
   const int32_t* table = a.table + int64_t(w.b) * a.table_stride;
   int pages = -1;   // of 32 iterations' two blocks, one per lane
   // An absent block of a tile is read from the tile's other block.
   auto load = [&](int i, Tile<FMT, D>& tile, int& p0, int& p1) {
-    if (i >= count) i = count - 1;      // once more: a load that may not happen costs a move
     if ((i & 31) == 0) {
       const int mine = i + (lane >> 1) < count ? 2 * tile_of(i + (lane >> 1)) + (lane & 1) : -1;
       pages = -1;
@@ -678,31 +683,17 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
       tile.load(t, source<FMT, D>(a.g, kv_block(a.g, page, w.head, in)), lane);
     }
   };
-  if (count > 0) {
-    Tile<FMT, D> buf[N];
-    int p0[N], p1[N];
-#pragma unroll
-    for (int y = 0; y < N - 1; ++y) load(y, buf[y], p0[y], p1[y]);
-    for (int i = 0; i < partly; i += N) {
-#pragma unroll
-      for (int y = 0; y < N; ++y) {
-        if (i + y >= partly) break;
-        load(i + y + N - 1, buf[(y + N - 1) % N], p0[(y + N - 1) % N], p1[(y + N - 1) % N]);
-        const int base = tile_of(i + y) * kTile, left = w.k1 - base;
-        narrow_tile<FMT, D, true>(r, sm_q, qs, buf[y], p0[y] < 0 ? 0 : left,
-                                  p1[y] < 0 ? 0 : left - 16,
-                                  visible(rm, a.tree != nullptr, base, w.sq.ctx, g), lane);
-      }
-    }
-    for (int i = partly; i < count; i += N) {
-#pragma unroll
-      for (int y = 0; y < N; ++y) {
-        if (i + y >= count) break;
-        load(i + y + N - 1, buf[(y + N - 1) % N], p0[(y + N - 1) % N], p1[(y + N - 1) % N]);
-        if (p0[y] >= 0 || p1[y] >= 0)
-          narrow_tile<FMT, D, false>(r, sm_q, qs, buf[y], p0[y] >= 0, p1[y] >= 0, 0, lane);
-      }
-    }
+  Tile<FMT, D> tile;
+  int p0, p1;
+  for (int i = 0; i < partly; ++i) {
+    load(i, tile, p0, p1);
+    const int base = tile_of(i) * kTile, left = w.k1 - base;
+    narrow_tile<FMT, D, true>(r, sm_q, qs, tile, p0 < 0 ? 0 : left, p1 < 0 ? 0 : left - 16,
+                              visible(rm, a.tree != nullptr, base, w.sq.ctx, g), lane);
+  }
+  for (int i = partly; i < count; ++i) {
+    load(i, tile, p0, p1);
+    if (p0 >= 0 || p1 >= 0) narrow_tile<FMT, D, false>(r, sm_q, qs, tile, p0 >= 0, p1 >= 0, 0, lane);
   }
 
   // the four waves' parts, in wave order
@@ -745,7 +736,7 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
       }
       const int64_t out = out_row(a, w, w.row0 + row);
       if (w.nsplit == 1) {
-        const float inv = reciprocal(l);
+        const float inv = reciprocal(l, unit_of(FMT));
         uint32_t y[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) y[x] = pack_bf16x2(v[2 * x] * inv, v[2 * x + 1] * inv);
@@ -771,7 +762,7 @@ struct Shared {        // one tile's operands
   u32x4 k[2][D / 32][64];
   u32x4 v[D / 16][64];
   float ve[kTile];     // V's row exponent + 127; -inf: the key is missing
-  float iv[kTile];     // 2^-that; NaN: the row holds a NaN or an infinity
+  float iv[kTile];     // 2 2^-that exponent; NaN: the row holds a NaN or an infinity
 };
 
 // The quarter of a tile that a wave turns into operands: block t's K or V.
@@ -820,7 +811,7 @@ struct Quarter {
       }
       if (g == 0) {
         float ve = 0.0f, iv = 1.0f;
-        if constexpr (FMT != QL_KV_BF16) ve = static_cast<float>(mine), iv = power(254u - mine);
+        if constexpr (FMT != QL_KV_BF16) ve = static_cast<float>(mine), iv = power(255u - mine);
         sh.ve[16 * t + n] = n < keys ? ve : -__builtin_inff();
         sh.iv[16 * t + n] = n >= keys ? 0.0f : bad ? __builtin_nanf("") : iv;
       }
@@ -954,7 +945,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAtt
     }
   }
   const int row = row0 + n;
-  const float l = column_sum(r.l), inv = reciprocal(l);
+  const float l = column_sum(r.l), inv = reciprocal(l, unit_of(FMT));
   if (row >= w.rows) return;
   const int64_t out = out_row(a, w, row);
   const int64_t at = int64_t(w.split) * a.tokens * a.n_q + out;
@@ -985,7 +976,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAtt
 // D / 4 lanes (4 elements each) take one of `parts` shares of a row's splits,
 // every parts-th split; the shares are then added in order.
 template <int D>
-__global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttnArgs a, int parts) {
+__global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttnArgs a, int parts,
+                                                                     float unit) {
   constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
   __shared__ f32x4 sm_o[kGroups][kLanes];
   __shared__ float sm_l[kGroups];
@@ -1019,7 +1011,7 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttnArgs a, in
     for (int x = 1; x < parts; ++x) v += sm_o[group + x][lane], l += sm_l[group + x];
   }
   if (!in) return;
-  v *= reciprocal(l);
+  v *= reciprocal(l, unit);
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + row * D + 4 * lane) =
       make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
@@ -1100,9 +1092,9 @@ hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a
   const int64_t rows = int64_t(a.max_q) * a.n_q, per_block = groups / parts;
   const dim3 grid(unsigned((rows + per_block - 1) / per_block), unsigned(a.n_seqs));
   switch (d) {
-    case 64: kv_attention_join_kernel<64><<<grid, 256, 0, s>>>(a, parts); break;
-    case 128: kv_attention_join_kernel<128><<<grid, 256, 0, s>>>(a, parts); break;
-    default: kv_attention_join_kernel<256><<<grid, 256, 0, s>>>(a, parts); break;
+    case 64: kv_attention_join_kernel<64><<<grid, 256, 0, s>>>(a, parts, unit_of(fmt)); break;
+    case 128: kv_attention_join_kernel<128><<<grid, 256, 0, s>>>(a, parts, unit_of(fmt)); break;
+    default: kv_attention_join_kernel<256><<<grid, 256, 0, s>>>(a, parts, unit_of(fmt)); break;
   }
   return hipGetLastError();
 }

@@ -422,8 +422,10 @@ int gemm_w4a16_sp24_ws(const void *x_bf16, const void *w_packed, int64_t m,
  *                of 16, s_g = E4M3(max|x_g| / 2^e / 6), code =
  *                E2M1(x / 2^e * (1 / s_g)), each binary32 step rounded once;
  *                e as above with 2688 = 6 * 448 in the place of 448
- * In the two quantized formats an infinity saturates and a NaN stays a NaN
- * (QL_KV_NVFP4: its whole group of 16 reads back as NaN).
+ * In the two quantized formats an infinity takes the largest code, counted as
+ * 2^128 for e, and reads back as an infinity (finite elements beside it lose
+ * their bits to that e); a NaN stays a NaN (QL_KV_NVFP4: its whole group of 16
+ * reads back as NaN).
  *
  * Layout: blocks of 16 tokens of one kv head, [n_pages][n_kv][page_size / 16].
  * All blocks' codes come first, each block's 16 K rows and then its 16 V rows
@@ -496,8 +498,9 @@ int kv_gather(const ql_kv_cache *cache, const int64_t *slots, int64_t tokens, vo
  * The step between the qkv projection and the attention, in one pass over
  * the projection's output: RMS norm of every query and key head, rotation of
  * both by the token's position, queries out, K and V written to the cache
- * (as kv_append; K from its binary32 values, rounded once).
- *   norm      x <- x / sqrt(mean(x^2) + eps) * weight     (binary32)
+ * (as kv_append).  Queries are computed in binary32, keys in binary64 up to
+ * the one rounding to binary32 that the row's format starts from.
+ *   norm      x <- x / sqrt(mean(x^2) + eps) * weight
  *   rotation  (a, b) <- (a c - b s, b c + a s) for rot / 2 pairs of a head,
  *             a = x[i], b = x[i + rot / 2], or x[2 i], x[2 i + 1] with
  *             QL_ROPE_INTERLEAVED; elements from rot on are left as they are
@@ -540,11 +543,14 @@ int qkv_norm_rope_append(const ql_kv_cache *cache, const void *qkv, int x_dtype,
  *   y = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale q.k_p - max_p scale q.k_p)
  * A query that sees nothing gives zeros.  Rows that no query of a sequence
  * sees do not matter, whatever they hold; a NaN or infinity in a row hidden
- * from one query does not reach it.
+ * from one query does not reach it.  One that a query sees makes its result
+ * NaN in that element at least, and possibly in all.
  *
- * Products and sums are binary32; keys, values and queries enter exactly
- * (queries rounded to a multiple of 2^-38 of their row's largest value for
- * the quantized formats), weights rounded to 11 bits (QL_KV_BF16: 16 bits).
+ * Sums are binary32.  Keys, values and queries enter exactly (queries over
+ * QL_KV_NVFP4 rounded to a multiple of 2^-38 of their row's largest value).
+ * Weights are rounded to 16 bits (QL_KV_BF16), or to 11 bits, those below
+ * 2^-21 of the largest w_p 2^e_p (e_p: the exponent of V's row) to a multiple
+ * of at most 2^-31 of it.
  *
  * q            bf16 [tokens, n_q, head_dim]; a token's heads are contiguous,
  *              tokens q_stride elements apart; 16-byte aligned rows.
