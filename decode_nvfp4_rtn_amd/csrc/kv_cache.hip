@@ -174,11 +174,31 @@ __device__ __forceinline__ uint32_t row_exponent(float amax) {
   return u == 0 ? 127u : uint32_t(b < kKvExpMin ? kKvExpMin : b);
 }
 
-// Encodes this lane's N elements of a row held by 16 lanes.  An infinity
-// saturates; a NaN stays one (8-bit: its own code; 4-bit: its group's scale).
-template <int FMT, int D>
-__device__ __forceinline__ EncRow<FMT, D> encode_row(const float (&x)[D / 16]) {
+// A value in binary32 that rounds on to fewer bits as v itself does: where it
+// is not exact the last bit is set (and what was rounded up is taken back).
+__device__ __forceinline__ float sticky(float v) { return v; }
+__device__ __forceinline__ float sticky(double v) {
+  const float f = static_cast<float>(v);
+  const double back = f;
+  uint32_t u = __float_as_uint(f);
+  if (__builtin_fabs(back) > __builtin_fabs(v)) u -= 1;
+  return __uint_as_float(back != v ? u | 1u : u);
+}
+template <typename T>
+__device__ __forceinline__ T greater(T a, T b) {
+  if constexpr (sizeof(T) == 8) return __builtin_fmax(a, b);
+  else return __builtin_fmaxf(a, b);
+}
+
+// Encodes this lane's N elements (binary32, or keys in binary64) of a row held
+// by 16 lanes.  An infinity takes the largest code; a NaN stays one (8-bit: its
+// own code; 4-bit: its group's scale).
+template <int FMT, int D, typename T>
+__device__ __forceinline__ EncRow<FMT, D> encode_row(const T (&v)[D / 16]) {
   constexpr int N = D / 16;
+  float x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = FMT == QL_KV_BF16 ? static_cast<float>(v[i]) : sticky(v[i]);
   EncRow<FMT, D> r;
   r.scale = 0;
   if constexpr (FMT == QL_KV_BF16) {
@@ -206,32 +226,34 @@ __device__ __forceinline__ EncRow<FMT, D> encode_row(const float (&x)[D / 16]) {
       }
     } else {
       // group maximum over 16 elements: 16 / N lanes
-      float g = a;
+      T g = 0;
       bool nan = false;
 #pragma unroll
-      for (int i = 0; i < N; ++i) nan |= x[i] != x[i];
+      for (int i = 0; i < N; ++i) g = greater<T>(g, std::fabs(v[i])), nan |= x[i] != x[i];
       float bad = nan ? 1.0f : 0.0f;
       if constexpr (N < 16) {
-        g = __builtin_fmaxf(g, dpp<0xB1>(g));
+        g = greater<T>(g, dpp<0xB1>(g));
         bad = __builtin_fmaxf(bad, dpp<0xB1>(bad));
       }
       if constexpr (N < 8) {
-        g = __builtin_fmaxf(g, dpp<0x4E>(g));
+        g = greater<T>(g, dpp<0x4E>(g));
         bad = __builtin_fmaxf(bad, dpp<0x4E>(bad));
       }
-      const float q = __builtin_fminf(g * p / 6.0f, 448.0f);
+      const float q = __builtin_fminf(static_cast<float>(g * T(p) / T(6)), 448.0f);
       const uint32_t sc = __builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false) & 0xFFu;
       const float sv = __builtin_amdgcn_cvt_f32_fp8(int(sc), 0);
       const float inv = sv > 0.0f ? 1.0f / sv : 0.0f;
       r.scale = bad > 0.0f ? 0x7Fu : sc;
 #pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = static_cast<float>(v[i] * T(p) * T(inv));
+#pragma unroll
       for (int i = 0; i < EncRow<FMT, D>::kWords; ++i) {
         uint32_t v = 0;
-        v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i] * inv, y[8 * i + 1] * inv, 1.0f, 0);
-        v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i + 2] * inv, y[8 * i + 3] * inv, 1.0f, 1);
+        v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i], y[8 * i + 1], 1.0f, 0);
+        v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i + 2], y[8 * i + 3], 1.0f, 1);
         if constexpr (N > 4) {
-          v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i + 4] * inv, y[8 * i + 5] * inv, 1.0f, 2);
-          v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i + 6] * inv, y[8 * i + 7] * inv, 1.0f, 3);
+          v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i + 4], y[8 * i + 5], 1.0f, 2);
+          v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, y[8 * i + 6], y[8 * i + 7], 1.0f, 3);
         }
         r.w[i] = v;
       }
@@ -462,7 +484,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void qkv_norm_rope_a
     }
   };
 
-  auto norm_rope = [&](float (&x)[N], bool norm, const auto& wc, const auto& ws) {
+  auto norm_rope = [&](const float (&x)[N], bool norm, const auto& wc, const auto& ws, auto& y) {
     typedef std::remove_const_t<std::remove_reference_t<decltype(wc[0])>> T;
     T r = 1;
     if (norm) {
@@ -498,7 +520,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void qkv_norm_rope_a
     }
 #pragma unroll
     for (int u = 0; u < N; ++u)
-      x[u] = static_cast<float>(fma_of(static_cast<T>(partner[u]), ws[u], x[u] * wc[u]) * r);
+      y[u] = fma_of(static_cast<T>(partner[u]), ws[u], x[u] * wc[u]) * r;
   };
 
   // A loop of its own for each kind of head: with one of three kinds of stores
@@ -525,14 +547,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void qkv_norm_rope_a
   float qc[N], qs[N];
   if (first < k0) factors(a.q_weight, qc, qs);
   sweep(0, k0, [&](int h, float (&x)[N]) {
-    norm_rope(x, a.q_weight != nullptr, qc, qs);
-    if (in) store_row_bf16(a.q_out, (token * a.n_q + h) * D + i * N, x);
+    float y[N];
+    norm_rope(x, a.q_weight != nullptr, qc, qs, y);
+    if (in) store_row_bf16(a.q_out, (token * a.n_q + h) * D + i * N, y);
   });
   double kc[N], ks[N];
   if (end > k0 && first < v0) factors(a.k_weight, kc, ks);
   sweep(k0, v0, [&](int h, float (&x)[N]) {
-    norm_rope(x, a.k_weight != nullptr, kc, ks);
-    const EncRow<FMT, D> r = encode_row<FMT, D>(x);
+    double y[N];
+    norm_rope(x, a.k_weight != nullptr, kc, ks, y);
+    const EncRow<FMT, D> r = encode_row<FMT, D>(y);
     if (ok) store_k<FMT, D>(place_of<FMT, D>(a.g, slot, h - k0), i, r);
   });
   sweep(v0, heads, [&](int h, float (&x)[N]) {

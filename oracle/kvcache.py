@@ -10,7 +10,8 @@ NVFP4 reading of ``nvfp4.py`` with a power of two for each row in the place of
 the tensor scale, and the 8-bit ones are E4M3 codes under the same kind of
 scale.
 
-Steps for a row x of d values, all binary32 and rounded once:
+Steps for a row x of d values, binary32 (keys that were just normed: binary64),
+each rounded once to binary32:
   e = the smallest integer >= -100 with max|x| <= Q 2^e, 0 for a row of zeros;
       Q = 448 (E4M3) or 2688 = 6 * 448 (NVFP4); stored as the byte e + 127
   E4M3:  code = E4M3(x 2^-e)
@@ -49,6 +50,14 @@ def row_exponent(amax, top):
     return e
 
 
+def sticky32(v):
+    """Binary32 values that round on to fewer bits as the float64 v do: the last
+    bit says that something was dropped."""
+    f = np.asarray(v, dtype=np.float64).astype(np.float32)
+    f = np.where(np.abs(f.astype(np.float64)) > np.abs(v), np.nextafter(f, np.float32(0)), f)
+    return (f.view(np.uint32) | (f.astype(np.float64) != v)).view(np.float32)
+
+
 def enc_e4m3_signed(v):
     """E4M3 codes of binary32 values, sign included, saturating at 448."""
     v = np.asarray(v, dtype=np.float32)
@@ -61,21 +70,23 @@ def dec_e4m3_signed(c):
 
 
 def quantize(fmt, x):
-    """Rows x [n, d] (binary32 values) -> dict with "row" (bytes [n, row_bytes]),
+    """Rows x [n, d] (binary32 or, as float64, binary64 values) -> dict with "row" (bytes [n, row_bytes]),
     "scales" ([n, d/16] or None), "exp" ([n] stored bytes or None) and "value"
     (float64 [n, d], what the bytes stand for)."""
-    x = np.asarray(x, dtype=np.float32)
+    x = np.asarray(x)
+    x = x if x.dtype == np.float64 else x.astype(np.float32)
     n, d = x.shape
     if fmt == BF16:
+        x = x.astype(np.float32)
         bits = rn_bf16_bits(x)
         return dict(row=bits.view(np.uint8).reshape(n, 2 * d), scales=None, exp=None,
                     value=bf16_bits_to_f32(bits).astype(np.float64))
     e = row_exponent(np.max(np.abs(x), axis=1), TOP[fmt])
-    y = rn32(x.astype(np.float64) * 2.0 ** -e[:, None])
+    y = x.astype(np.float64) * 2.0 ** -e[:, None]
     stored = (e + 127).astype(np.uint8)
     p = 2.0 ** e[:, None].astype(np.float64)
     if fmt == E4M3:
-        c = enc_e4m3_signed(y)
+        c = enc_e4m3_signed(sticky32(y))
         return dict(row=c, scales=None, exp=stored, value=dec_e4m3_signed(c) * p)
     g = y.reshape(n, d // 16, 16)
     s = enc_e4m3(rn32(np.max(np.abs(g), axis=2).astype(np.float64) / 6.0))
@@ -146,7 +157,7 @@ class Cache:
 
     def write(self, which, x, slots):
         """Rows x [tokens, n_kv, d] (binary32) to slots; slots < 0 are skipped."""
-        x = np.asarray(x, dtype=np.float32)
+        x = np.asarray(x)
         for h in range(self.n_kv):
             q = quantize(self.fmt, x[:, h])
             for i, s in enumerate(slots):

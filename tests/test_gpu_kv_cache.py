@@ -159,9 +159,9 @@ def test_norm_rope_append(fmt, d, tokens, n_q, n_kv, rot, pairs, norm, bf16):
     normed = np.abs(kv.norm_rope(qkv[:, :n_q], wq, 1e-5, None, pos, pairs)).max(-1, keepdims=True)
     bound = 2.0 ** -8 * np.abs(want) + (8 + d / 2 + 4) * 2.0 ** -24 * 2 * normed
     assert np.all(np.abs(got.double().cpu().numpy() - want) <= bound)
-    # keys: binary64 before the one rounding to binary32 that the format takes
+    # keys: binary64 up to the roundings of the format
     c = kv.Cache(FMTS[fmt], 4, 16, n_kv, d)
-    keys = kv.norm_rope(qkv[:, n_q:n_q + n_kv], wk, 1e-5, table, pos, pairs).astype(np.float32)
+    keys = kv.norm_rope(qkv[:, n_q:n_q + n_kv], wk, 1e-5, table, pos, pairs)
     c.write("k", keys, slots)
     c.write("v", qkv[:, n_q + n_kv:], slots)
     assert np.array_equal(cache.data.cpu().numpy(), c.bytes)
