@@ -23,6 +23,8 @@ int4     Symmetric INT4 quantizer with 128-element groups and bf16 scales.
 sparse24 2:4 magnitude pruning along k on top of int4.
 lut2     2-bit per-row codebook (K-means, Lloyd iterations).
 gemm     Matrix products on dequantized operands and the pass rule.
+kvcache  Row formats and layout of the paged key/value cache, head norm and
+         rotation, attention over chains and trees of new tokens.
 
 Pins (what ties each function to something other than itself) live in
 ``tests/test_oracle_*.py``.  ``lut2.lloyd`` is pinned to scikit-learn's
@@ -32,4 +34,4 @@ rule, final rounding and re-assignment are pinned by closed forms, brute
 force and special cases.
 """
 
-from . import formats, nvfp4, int4, sparse24, lut2, gemm  # noqa: F401
+from . import formats, nvfp4, int4, sparse24, lut2, gemm, kvcache  # noqa: F401
