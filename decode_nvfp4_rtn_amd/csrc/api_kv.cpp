@@ -139,9 +139,9 @@ static int check_attention(const ql_kv_cache* cache, int64_t tokens, int64_t n_q
   if (tokens == 0 || n_seqs == 0 || max_q == 0) return QL_OK;
   const int64_t m = max_q < tokens ? max_q : tokens;
   if (m * n_q > kMost - 4096) return QL_ESHAPE;   // rows are counted in 32 bits
-  const KvAttnPlan p = kv_attention_plan(cache->head_dim, int(n_q), cache->n_kv, n_seqs, m,
-                                         max_kv);
-  if (p.row_blocks > (kMost / 16) / (n_seqs * cache->n_kv * p.splits)) return QL_ESHAPE;
+  const KvAttnPlan p = kv_attention_plan(cache->format, cache->head_dim, int(n_q), cache->n_kv, n_seqs,
+                                         m, max_kv);
+  if (p.row_blocks > (kMost / 16) / (p.parts * cache->n_kv)) return QL_ESHAPE;
   return -1;
 }
 
@@ -152,9 +152,9 @@ size_t kv_attention_workspace(const ql_kv_cache* cache, int64_t tokens, int64_t 
     return 0;
   if (check_attention(cache, tokens, n_q, n_seqs, max_q, max_kv) != -1) return 0;
   const int64_t m = max_q < tokens ? max_q : tokens;
-  const KvAttnPlan p = kv_attention_plan(cache->head_dim, int(n_q), cache->n_kv, n_seqs, m,
-                                         max_kv);
-  return kv_attention_ws_bytes(p, tokens, int(n_q), cache->head_dim);
+  const KvAttnPlan p = kv_attention_plan(cache->format, cache->head_dim, int(n_q), cache->n_kv, n_seqs,
+                                         m, max_kv);
+  return kv_attention_ws_bytes(p, n_seqs, m, int(n_q), cache->head_dim);
 }
 
 int kv_attention(const ql_kv_cache* cache, const void* q_bf16, int64_t q_stride, int64_t tokens,
@@ -181,9 +181,9 @@ int kv_attention(const ql_kv_cache* cache, const void* q_bf16, int64_t q_stride,
        reinterpret_cast<uintptr_t>(block_table)) & 3u)
     return QL_EALIGN;
   const int64_t m = max_q < tokens ? max_q : tokens;
-  const KvAttnPlan p = kv_attention_plan(cache->head_dim, int(n_q), cache->n_kv, n_seqs, m,
-                                         max_kv);
-  const size_t need = kv_attention_ws_bytes(p, tokens, int(n_q), cache->head_dim);
+  const KvAttnPlan p = kv_attention_plan(cache->format, cache->head_dim, int(n_q), cache->n_kv, n_seqs,
+                                         m, max_kv);
+  const size_t need = kv_attention_ws_bytes(p, n_seqs, m, int(n_q), cache->head_dim);
   if (need) {
     if (!workspace) return QL_EINVAL;
     if (!aligned16(workspace)) return QL_EALIGN;
@@ -207,9 +207,11 @@ int kv_attention(const ql_kv_cache* cache, const void* q_bf16, int64_t q_stride,
   a.scale = scale;
   a.y = y;
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = need ? a.part_o + int64_t(p.splits) * tokens * n_q * cache->head_dim : nullptr;
-  a.splits = p.splits;
-  a.chunk = p.chunk;
+  if (need) {
+    a.part_ml = a.part_o + p.parts * m * n_q * cache->head_dim;
+    a.first = reinterpret_cast<int32_t*>(a.part_ml + p.parts * m * n_q * 2);
+  }
+  a.parts = int(p.parts);
   return launch_status(launch_kv_attention(cache->format, cache->head_dim, p, a,
                                            as_stream(stream)));
 }

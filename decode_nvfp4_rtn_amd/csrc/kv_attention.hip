@@ -301,15 +301,10 @@ __device__ __forceinline__ int q_element(int s, int g) {
 // ---------------------------------------------------------------------------
 // Sequences, rows, splits
 // ---------------------------------------------------------------------------
-// Keys of one split of a sequence of `len` keys: the planned chunk, or more
-// where the sequence is longer than the plan's splits cover.
-__device__ __forceinline__ int chunk_of(int len, int chunk, int splits) {
-  const int need = (len + splits - 1) / splits;
-  return need <= chunk ? chunk : (need + 127) / 128 * 128;
-}
-// Splits that hold keys (at least one, so that every row is written).
-__device__ __forceinline__ int splits_of(int len, int chunk) {
-  return len > chunk ? (len + chunk - 1) / chunk : 1;
+__device__ __forceinline__ int length(const KvAttnArgs& a, int b) {
+  const int64_t cap = a.table_cols << a.g.page_shift;
+  const int len = a.kv_lens[b];
+  return len < 0 ? 0 : len < cap ? len : int(cap);
 }
 
 struct Seq {
@@ -322,25 +317,98 @@ __device__ __forceinline__ Seq sequence(const KvAttnArgs& a, int b) {
   const int64_t room = a.tokens - s.q0;
   s.rows_q = s.q0 < 0 || nodes < 0 || room <= 0 ? 0 : room < nodes ? int(room) : nodes;
   if (s.rows_q > a.max_q) s.rows_q = a.max_q;
-  const int64_t cap = a.table_cols << a.g.page_shift;
-  const int len = a.kv_lens[b];
-  s.len = len < 0 ? 0 : len < cap ? len : int(cap);
+  s.len = length(a, b);
   s.ctx = nodes < 0 ? s.len : s.len > nodes ? s.len - nodes : 0;
   return s;
+}
+
+// Sum over the wave, in every lane.
+__device__ __forceinline__ uint32_t wave_sum(uint32_t v) {
+  v += row_or<0xB1>(v);
+  v += row_or<0x4E>(v);
+  v += row_or<0x141>(v);
+  v += row_or<0x140>(v);
+  auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = r[0] + r[1];
+  r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return r[0] + r[1];
+}
+
+// The keys of all sequences are cut into at most a.parts parts, every sequence
+// into pieces of one length, which is the shortest (nearly) that does: so the
+// parts are even however uneven the sequences are, and the grid, which is
+// planned without the lengths, is full.  (Planned by the longest sequence
+// alone, uneven ones left a third of the chip idle: 32 sequences of up to 8192
+// 4-bit keys 52 us, 4 of up to 16000 256-wide ones 110 us.)
+struct Part {
+  int b, split, nsplit, keys;    // sequence (none if < 0), place in it, its parts, keys of one
+};
+// Part u; every wave works it out alone, with a sequence to a lane.
+__device__ __forceinline__ Part part_of(const KvAttnArgs& a, int u) {
+  if (a.parts == a.n_seqs) return {u, 0, 1, 0x7FFFFFFF};
+  const int lane = threadIdx.x & 63;
+  // in steps of 128 keys
+  auto steps_of = [&](int b) { return b < a.n_seqs ? (uint32_t(length(a, b)) + 127) >> 7 : 0u; };
+  const uint32_t mine = steps_of(lane);
+  uint64_t total = wave_sum(mine);
+  for (int b = 64; b < a.n_seqs; b += 64) total += wave_sum(steps_of(b + lane));
+  // parts that a sequence of w steps needs at c steps each: one at least, so
+  // that every row is written
+  auto need = [&](uint32_t w, uint32_t c) { return w > c ? (w + c - 1) / c : 1u; };
+  auto fits = [&](uint32_t c) {
+    uint32_t n = lane < a.n_seqs ? need(mine, c) : 0u;
+    for (int b = 64 + lane; b < a.n_seqs; b += 64) n += need(steps_of(b), c);
+    return __builtin_amdgcn_readfirstlane(wave_sum(n)) <= uint32_t(a.parts);
+  };
+  // between the mean part and what surely fits; 256 keys at least
+  const uint32_t spare = uint32_t(a.parts - a.n_seqs);
+  uint64_t least = (total + a.parts - 1) / uint32_t(a.parts), most = (total + spare - 1) / spare;
+  uint32_t lo = least < 2 ? 2u : uint32_t(least), hi = most > 1u << 24 ? 1u << 24 : uint32_t(most);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi < lo ? lo : hi);
+  if (fits(lo)) hi = lo;
+  for (int i = 0; i < 6 && lo < hi; ++i) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (fits(mid)) hi = mid;
+    else lo = mid + 1;
+  }
+  Part p = {-1, 0, 1, hi >> 24 ? 0x7FFFFFFF : int(hi) << 7};
+  uint32_t before = 0;
+  for (int b0 = 0; b0 < a.n_seqs; b0 += 64) {
+    const uint32_t n = b0 + lane < a.n_seqs ? need(b0 ? steps_of(b0 + lane) : mine, hi) : 0u;
+    uint32_t upto = n;
+#pragma unroll
+    for (int off = 1; off < 64; off *= 2) {
+      const uint32_t v = __shfl_up(upto, off, 64);
+      if (lane >= off) upto += v;
+    }
+    if (blockIdx.x == 0 && threadIdx.x < 64 && b0 + lane < a.n_seqs) {
+      a.first[b0 + lane] = int(before + upto - n);
+      if (b0 + lane == a.n_seqs - 1) a.first[a.n_seqs] = int(before + upto);
+    }
+    const int ahead = __popcll(__ballot(before + upto <= uint32_t(u)));   // lanes whose parts come first
+    if (p.b < 0 && ahead < 64 && b0 + ahead < a.n_seqs) {
+      p.b = b0 + ahead;
+      p.nsplit = __builtin_amdgcn_readlane(n, ahead);
+      p.split = u - int(before + __builtin_amdgcn_readlane(upto, ahead) - p.nsplit);
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return p;
 }
 
 // What a thread block works on.
 struct Work {
   Seq sq;
-  int b, head, split, nsplit, group;
+  int part, head, split, nsplit, group;
+  int b;
   int rows, row0;
   int k0, k1;            // its keys
   bool any;
 };
 // Row blocks of one unit (split, sequence, head) read the same keys: their ids
 // are 8 apart, so that they run on one XCD and share its L2.  Heads come
-// fastest and splits last, so that the late splits, which only long sequences
-// have, spread over all XCDs.
+// fastest, so that what is not used at the end spreads over all XCDs.
 template <int ROWS>
 __device__ __forceinline__ Work work_of(const KvAttnArgs& a) {
   Work w;
@@ -350,17 +418,17 @@ __device__ __forceinline__ Work work_of(const KvAttnArgs& a) {
   w.any = unit < a.units;
   if (!w.any) return w;
   w.head = unit % a.g.n_kv;
-  unit /= a.g.n_kv;
-  w.b = unit % a.n_seqs;
-  w.split = unit / a.n_seqs;
+  w.part = unit / a.g.n_kv;
+  const Part p = part_of(a, w.part);
+  w.any = p.b >= 0;
+  if (!w.any) return w;
+  w.b = p.b, w.split = p.split, w.nsplit = p.nsplit;
   w.group = a.n_q / a.g.n_kv;
   w.sq = sequence(a, w.b);
   w.rows = w.sq.rows_q * w.group;
-  const int chunk = chunk_of(w.sq.len, a.chunk, a.splits);
-  w.nsplit = splits_of(w.sq.len, chunk);
-  w.any = w.row0 < w.rows && w.split < w.nsplit;
-  w.k0 = w.split * chunk;
-  w.k1 = w.sq.len - w.k0 < chunk ? w.sq.len : w.k0 + chunk;
+  w.any = w.row0 < w.rows;
+  w.k0 = w.split * p.keys;
+  w.k1 = w.sq.len - w.k0 < p.keys ? w.sq.len : w.k0 + p.keys;
   if (!a.tree) {
     // of a chain, no row sees past the block's last token
     const int last = (w.row0 + ROWS < w.rows ? w.row0 + ROWS : w.rows) - 1;
@@ -513,10 +581,11 @@ __device__ __forceinline__ float reciprocal(float l, float unit) {
 }
 constexpr float unit_of(int fmt) { return fmt == QL_KV_BF16 ? 1.0f : kUnit; }
 
-// Row `row`'s place in y and in the partial results.
+// Row `row`'s place in y, or among the partial results of a split sequence.
 __device__ __forceinline__ int64_t out_row(const KvAttnArgs& a, const Work& w, int row) {
-  const int node = row / w.group;
-  return int64_t(w.sq.q0 + node) * a.n_q + w.head * w.group + (row - node * w.group);
+  const int node = row / w.group, head = w.head * w.group + (row - node * w.group);
+  return w.nsplit == 1 ? int64_t(w.sq.q0 + node) * a.n_q + head
+                       : (int64_t(w.part) * a.max_q + node) * a.n_q + head;
 }
 
 // ---------------------------------------------------------------------------
@@ -743,11 +812,10 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out * D + part * DCH + c) =
             make_uint4(y[0], y[1], y[2], y[3]);
       } else {
-        const int64_t at = int64_t(w.split) * a.tokens * a.n_q + out;
-        float4* o = reinterpret_cast<float4*>(a.part_o + at * D + part * DCH + c);
+        float4* o = reinterpret_cast<float4*>(a.part_o + out * D + part * DCH + c);
         o[0] = make_float4(v[0], v[1], v[2], v[3]);
         o[1] = make_float4(v[4], v[5], v[6], v[7]);
-        if (part == 0 && c == 0) a.part_ml[2 * at] = tm, a.part_ml[2 * at + 1] = l;
+        if (part == 0 && c == 0) a.part_ml[2 * out] = tm, a.part_ml[2 * out + 1] = l;
       }
     }
     __syncthreads();
@@ -948,8 +1016,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAtt
   const float l = column_sum(r.l), inv = reciprocal(l, unit_of(FMT));
   if (row >= w.rows) return;
   const int64_t out = out_row(a, w, row);
-  const int64_t at = int64_t(w.split) * a.tokens * a.n_q + out;
-  if (w.nsplit > 1 && g == 0) a.part_ml[2 * at] = r.m, a.part_ml[2 * at + 1] = l;
+  if (w.nsplit > 1 && g == 0) a.part_ml[2 * out] = r.m, a.part_ml[2 * out + 1] = l;
 #pragma unroll
   for (int i = 0; i < L::kLoads; ++i)
 #pragma unroll
@@ -965,7 +1032,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAtt
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out * D + d) =
             make_uint4(y[0], y[1], y[2], y[3]);
       } else {
-        float4* o = reinterpret_cast<float4*>(a.part_o + at * D + d);
+        float4* o = reinterpret_cast<float4*>(a.part_o + out * D + d);
         o[0] = make_float4(v[0], v[1], v[2], v[3]);
         o[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
@@ -984,11 +1051,11 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttnArgs a, in
   const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   const int b = blockIdx.y, part = group % parts;
   const Seq sq = sequence(a, b);
-  const int nsplit = splits_of(sq.len, chunk_of(sq.len, a.chunk, a.splits));
+  const int first = a.first[b], nsplit = a.first[b + 1] - first;
   if (nsplit == 1) return;
   const int64_t r = int64_t(blockIdx.x) * (kGroups / parts) + group / parts;   // token, head
   const bool in = r < int64_t(sq.rows_q) * a.n_q;
-  const int64_t row = int64_t(sq.q0) * a.n_q + r, step = a.tokens * a.n_q;
+  const int64_t step = int64_t(a.max_q) * a.n_q, row = first * step + r;
   float l = 0.0f;
   f32x4 v = {0, 0, 0, 0};
   if (in) {
@@ -1012,54 +1079,59 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttnArgs a, in
   }
   if (!in) return;
   v *= reciprocal(l, unit);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + row * D + 4 * lane) =
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + (int64_t(sq.q0) * a.n_q + r) * D + 4 * lane) =
       make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
 }  // namespace
 
-KvAttnPlan kv_attention_plan(int d, int n_q, int n_kv, int64_t n_seqs, int64_t max_q,
+KvAttnPlan kv_attention_plan(int fmt, int d, int n_q, int n_kv, int64_t n_seqs, int64_t max_q,
                              int64_t max_kv) {
   KvAttnPlan p;
   const int64_t rows = max_q * (n_q / n_kv);
   p.rows = rows <= 16 ? 16 : 64;
   p.row_blocks = (rows + p.rows - 1) / p.rows;
-  // Splits of the longest sequence.  A second launch joins them (3 to 10 us),
-  // and a block takes about as long as 128 keys of a narrow wave to start, so
-  // up to 512 keys stay whole (500 keys, one sequence: 8 us against 12), and
-  // no split is under 256 keys.
+  // Parts of all keys together.  A second launch joins those of one sequence (3
+  // to 10 us), and a block takes about as long as 128 keys of a narrow wave to
+  // start, so up to 512 keys stay whole (500 keys, one sequence: 8 us against
+  // 12), and no part of a longer one is planned under 256 keys.
   const int64_t cus = device_cu_count() > 0 ? device_cu_count() : 256;
-  const int64_t blocks = n_seqs * n_kv * p.row_blocks;
-  auto splits_for = [&](int64_t per_cu) {
-    const int64_t most = max_kv <= 512 ? 1 : (max_kv + 255) / 256;
-    const int64_t n = (per_cu * cus + blocks - 1) / blocks;
-    return n < 1 ? 1 : n > most ? most : n;
+  auto parts_for = [&](int64_t per_cu, int64_t least) {
+    const int64_t most = max_kv <= 512 ? n_seqs : n_seqs * ((max_kv + least - 1) / least);
+    // what each XCD's eighth of the units leaves room for in one round
+    const int64_t n = per_cu * (cus / 8) / p.row_blocks * 8 / n_kv;
+    return n > most ? most : n < n_seqs ? n_seqs : n;
   };
-  int64_t splits;
   if (p.rows == 64) {
-    // as many blocks as run at once: three on a compute unit, two of 256-wide
-    // heads (the tree cases of 128- and 256-wide heads: 30 and 111 us; with 2
-    // and 3: 33 and 139 us)
-    splits = splits_for(d == 256 ? 2 : 3);
+    // as many blocks as run at once: two of 256-wide heads on a compute unit, of
+    // others three where the parts stay over 512 keys (16 sequences of 63 drafts
+    // over up to 2000 8-bit keys: 60 us, and 65 with two; 8 of 16 drafts over up
+    // to 4096: 31 us, and 28 with two; 256-wide over up to 16000: 121 and 100 us)
+    p.parts = parts_for(2, 256);
+    if (d < 256) {
+      const int64_t three = parts_for(3, 512);
+      if (p.parts < three) p.parts = three;
+    }
   } else {
-    // two on a compute unit (one sequence of 131071 8-bit keys: 56 us; with
-    // four 61 us), four while the splits are longer than 2048 keys (32
-    // sequences of up to 8192 4-bit keys: 56 us; with two 65 us)
-    splits = splits_for(2);
-    const int64_t four = splits_for(4), need = (max_kv + 2047) / 2048;
-    if (splits < need) splits = need < four ? need : four;
+    // two on a compute unit (one sequence of 131072 8-bit keys: 57 us, with
+    // four 62); of rows of at most 64 bytes, whose instructions count for more
+    // than their bytes, up to four while the parts are long (32 sequences of up
+    // to 8192 4-bit 128-wide keys: 51 us, with two 61; 8-bit 64-wide: 60 and 69;
+    // but 8-bit 128-wide: 71 and 70)
+    p.parts = parts_for(2, 256);
+    const int row_bytes = fmt == QL_KV_BF16 ? 2 * d : fmt == QL_KV_E4M3 ? d : d / 2;
+    if (row_bytes <= 64) {
+      const int64_t four = parts_for(4, 256), need = n_seqs * ((max_kv + 2047) / 2048);
+      if (p.parts < need) p.parts = need < four ? need : four;
+    }
   }
-  if (splits > 256) splits = 256;
-  const int64_t chunk = ((max_kv + splits - 1) / splits + 127) / 128 * 128;
-  p.chunk = chunk > 128 ? int(chunk) : 128;
-  p.splits = int((max_kv + p.chunk - 1) / p.chunk);
-  if (p.splits < 1) p.splits = 1;
   return p;
 }
 
-size_t kv_attention_ws_bytes(const KvAttnPlan& p, int64_t tokens, int n_q, int d) {
-  if (p.splits < 2) return 0;
-  return size_t(p.splits) * size_t(tokens) * size_t(n_q) * size_t(d + 2) * sizeof(float);
+size_t kv_attention_ws_bytes(const KvAttnPlan& p, int64_t n_seqs, int64_t max_q, int n_q, int d) {
+  if (p.parts == n_seqs) return 0;
+  return size_t(p.parts) * size_t(max_q) * size_t(n_q) * size_t(d + 2) * sizeof(float) +
+         (size_t(n_seqs) + 1) * sizeof(int32_t);
 }
 
 template <int FMT, int D>
@@ -1076,7 +1148,7 @@ static hipError_t launch_wide(const KvAttnArgs& a, unsigned blocks, hipStream_t 
 }
 
 hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a, hipStream_t s) {
-  const int64_t units = int64_t(a.n_seqs) * a.g.n_kv * p.splits;
+  const int64_t units = p.parts * a.g.n_kv;
   a.units = int(units);
   a.row_blocks = int(p.row_blocks);
   const unsigned blocks = unsigned((units + 7) / 8 * 8 * p.row_blocks);
@@ -1086,9 +1158,10 @@ hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a
     kv_attention_narrow_kernel<FMT, D><<<blocks, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
   });
-  if (e != hipSuccess || p.splits < 2) return e;
+  if (e != hipSuccess || p.parts == a.n_seqs) return e;
   // shares of a row: all of a block's groups where there are many splits
-  const int groups = 1024 / d, parts = p.splits >= 2 * groups ? groups : p.splits >= 4 ? 2 : 1;
+  const int groups = 1024 / d, splits = int(p.parts / a.n_seqs);
+  const int parts = splits >= 2 * groups ? groups : splits >= 4 ? 2 : 1;
   const int64_t rows = int64_t(a.max_q) * a.n_q, per_block = groups / parts;
   const dim3 grid(unsigned((rows + per_block - 1) / per_block), unsigned(a.n_seqs));
   switch (d) {

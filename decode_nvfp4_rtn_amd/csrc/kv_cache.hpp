@@ -130,22 +130,21 @@ struct KvAttnArgs {
   const uint64_t* tree;
   float scale;
   void* y;                // bf16 [tokens, n_q, d]
-  float* part_o;          // [splits][tokens * n_q][d]
-  float* part_ml;         // [splits][tokens * n_q][2]
-  int splits;
-  int chunk;              // keys per split (a multiple of 128)
-  int units;              // n_seqs * n_kv * splits
+  float* part_o;          // [parts][max_q * n_q][d]
+  float* part_ml;         // [parts][max_q * n_q][2]
+  int32_t* first;         // [n_seqs + 1]: each sequence's first part
+  int parts;              // parts of the keys of all sequences; n_seqs: none is split
+  int units;              // parts * n_kv
   int row_blocks;
 };
 struct KvAttnPlan {
   int rows;               // query rows per block: 16 (narrow) or 64 (wide)
   int64_t row_blocks;
-  int splits;
-  int chunk;
+  int64_t parts;
 };
-KvAttnPlan kv_attention_plan(int d, int n_q, int n_kv, int64_t n_seqs, int64_t max_q,
+KvAttnPlan kv_attention_plan(int fmt, int d, int n_q, int n_kv, int64_t n_seqs, int64_t max_q,
                              int64_t max_kv);
-size_t kv_attention_ws_bytes(const KvAttnPlan& p, int64_t tokens, int n_q, int d);
+size_t kv_attention_ws_bytes(const KvAttnPlan& p, int64_t n_seqs, int64_t max_q, int n_q, int d);
 hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a, hipStream_t s);
 
 }  // namespace qlin

@@ -562,8 +562,9 @@ int qkv_norm_rope_append(const ql_kv_cache *cache, const void *qkv, int x_dtype,
  *              the page of positions page_size * j .. of each sequence.
  *              Positions past the table's last column are not read.
  * max_q        at least every n_b (queries past it are not computed).
- * max_kv       about the largest kv_lens[b]; the work split is planned by it,
- *              the result is right for any value.
+ * max_kv       about the largest kv_lens[b]; whether and into how many parts
+ *              keys are split goes by it, where goes by the lengths
+ *              themselves.  The result is right for any value.
  * y            out bf16 [tokens, n_q, head_dim] contiguous (RNE).
  * workspace    >= kv_attention_workspace(...) bytes, 16-byte aligned (NULL when
  *              that is 0).  Calls that share one must be ordered.

@@ -141,7 +141,7 @@ def test_attention(lib):
     # a workspace is asked for where keys are split, and only there
     assert lib.kv_attention_workspace(c, 3, 4, 1, 1, 512) == 0
     need = lib.kv_attention_workspace(c, 3, 4, 1, 1, 100000)
-    assert need > 0 and need % (3 * 4 * (128 + 2) * 4) == 0
+    assert need > 8 and (need - 8) % (4 * (128 + 2) * 4) == 0
     assert run(max_kv=100000) == QL_EINVAL
     assert run(max_kv=100000, ws=A + 8, wsb=need) == QL_EALIGN
     assert run(max_kv=100000, ws=A, wsb=need - 1) == QL_EWORKSPACE

@@ -302,3 +302,22 @@ def test_bytes_of_a_hidden_row_do_not_reach_its_neighbours(fmt, nodes):
                     b.c.bytes[p] = 0xFF
         tree = np.array([int(m) & ~(1 << gone) for m in random_tree([nodes], 17)], dtype=object)
         b.check(b.run(q, tree), tree)
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("nodes", [1, 17])
+def test_many_uneven_sequences_share_the_parts(fmt, nodes):
+    """More sequences than a wave has lanes, most of them short or empty, some
+    long: parts go to the long ones."""
+    q = require_gpu()
+    say("uneven", fmt, nodes)
+    lens = [nodes + (5 * i) % 40 for i in range(70)]
+    lens[0] = lens[66] = 1900
+    lens[69], lens[30] = 2700, 600
+    count = [nodes if i % 9 else 0 for i in range(70)]
+    lens[9] = lens[18] = 0
+    b = Batch(FMTS[fmt], lens, count, 2, 1, 64, 32, seed=18)
+    y = b.run(q)
+    b.check(y)
+    assert torch.equal(y, b.run(q)) and q.kv_attention_workspace(
+        device_cache(q, b.c), sum(count), 2, 70, nodes, max(lens)) > 0
