@@ -3,8 +3,8 @@
 // (include/qlin.h).
 //
 // A row is one new token and one of the n_q / n_kv query heads that share a
-// kv head.  A block takes some rows of one sequence and kv head and one chunk
-// of its keys, 32 at a time, with the running maximum and sum of a softmax.
+// kv head.  A block takes some rows of one sequence and kv head and one part of
+// its keys, 32 at a time, with the running maximum and sum of a softmax.
 // Both products of such a tile run transposed, so that no operand moves
 // between lanes:
 //   S^T = K Q^T     A: 16 keys (lane % 16), 8 elements of d (lane / 16) a step
@@ -20,10 +20,19 @@
 // Two kernels share this.
 // narrow (up to 16 rows): each of four waves takes tiles of its own straight
 //   from memory into registers and the four results are joined at the end;
-//   bound by the cache's bytes.
+//   bound by the cache's bytes (32 sequences of 2048 to 8192 keys, 32 / 8
+//   128-wide heads, with the join: bf16 130 us, 685 MB at 5.3 TB/s; 8-bit
+//   71 us, 4.9 TB/s), at 4 bits by each wave's chain of loads, unpacking,
+//   products and softmax (51 us, 195 MB at 3.8 TB/s; the vector unit issues in
+//   47 % of the cycles).
 // wide (more rows): four waves share each tile.  Each turns a quarter of it
 //   into matrix operands in LDS, once for all, and takes 16 rows of its own;
-//   bound by the chain of LDS reads, products and softmax of a tile.
+//   bound by what a tile takes a wave from barrier to barrier: operands made
+//   and stored, LDS reads, products, softmax (4 sequences of 6893 to 16063
+//   4-bit 256-wide keys, 63 drafts, 15 / 5 heads: 98 us and 9 for the join,
+//   47 GFLOP).  A wave issues 45 % of that time; without the operands' making
+//   and storing the case takes 76 us, without LDS reads 101, without the
+//   softmax 99.
 //
 // Quantized rows.  K's row scale 2^ke goes into the bf16 operand where that
 // is free (narrow, NVFP4: it multiplies the score).  V's, 2^ve, joins the
@@ -688,7 +697,12 @@ __device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&sm_q)[D / 
   }
 }
 
-// Waves per SIMD that the register budget is set for (fewer spill).
+// Waves per SIMD that the register budget is set for: what fits without
+// spills that matter.  It is the number of waves, not loads under way in each,
+// that covers the memory's latency: with the next tile's loads issued ahead,
+// and half the waves for want of registers, 16 sequences of up to 8192 8-bit
+// 256-wide keys took 62 us instead of 49, 64 of up to 1024 128-wide ones 22.6
+// instead of 21.8.
 constexpr int narrow_waves(int fmt, int d) {
   return d == 64 ? 5 : d == 128 ? (fmt == QL_KV_BF16 ? 3 : 4) : 2;
 }
@@ -919,8 +933,8 @@ __device__ __forceinline__ void wide_tile(Rows<D>& r, const u32x4 (&q)[D / 32], 
 }
 
 // 16 rows to a wave, and so two or three waves on a SIMD, beat 32: a tile is a
-// chain of LDS reads, products and the softmax that takes a wave 2000 cycles,
-// 3 times what it issues, so it is the other waves that fill the SIMD (16
+// chain of LDS reads, products and the softmax that takes a wave more than
+// twice the cycles it issues, so it is the other waves that fill the SIMD (16
 // sequences of 63 drafts over 2000 8-bit keys, 32 / 8 128-wide heads: 56 us,
 // and 77 us with 32 rows to a wave; eight waves to a block: 78 us).
 template <int FMT, int D>
@@ -989,29 +1003,33 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAtt
   if (count > 0) prepare(0, 0);
   __syncthreads();
   // A loop for each kind of tile: where two ways meet, the accumulators would
-  // be copied.
-  for (int i = 0; i < partly; i += P) {
-#pragma unroll
-    for (int y = 0; y < P; ++y) {
-      if (i + y >= partly) break;
-      prepare(i + y + 1, (y + 1) % P);
-      if (active) {
-        const uint32_t seen = visible(rm, a.tree != nullptr, tile_of(i + y) * kTile, w.sq.ctx, g);
-        in_order();
-        wide_tile<FMT, D, true>(r, q, qs, sh[y], seen, lane);
-      }
-      __syncthreads();
+  // be copied.  No way out of a loop but its end: where one in the middle met
+  // the others, the compiler would wait for all loads on every turn.
+  auto hidden = [&](int i, int y) {
+    prepare(i + 1, (y + 1) % P);
+    if (active) {
+      const uint32_t seen = visible(rm, a.tree != nullptr, tile_of(i) * kTile, w.sq.ctx, g);
+      in_order();
+      wide_tile<FMT, D, true>(r, q, qs, sh[y], seen, lane);
     }
-  }
-  for (int i = partly; i < count; i += P) {
+    __syncthreads();
+  };
+  auto open_tile = [&](int i, int y) {
+    prepare(i + 1, (y + 1) % P);
+    if (active) wide_tile<FMT, D, false>(r, q, qs, sh[y], 0, lane);
+    __syncthreads();
+  };
+  int i = 0;
+  for (; i + P <= partly; i += P) {
 #pragma unroll
-    for (int y = 0; y < P; ++y) {
-      if (i + y >= count) break;
-      prepare(i + y + 1, (y + 1) % P);
-      if (active) wide_tile<FMT, D, false>(r, q, qs, sh[y], 0, lane);
-      __syncthreads();
-    }
+    for (int y = 0; y < P; ++y) hidden(i + y, y);
   }
+  if (i < partly) hidden(i, 0);      // then partly == count
+  for (i = partly; i + P <= count; i += P) {
+#pragma unroll
+    for (int y = 0; y < P; ++y) open_tile(i + y, y);
+  }
+  if (i < count) open_tile(i, 0);
   const int row = row0 + n;
   const float l = column_sum(r.l), inv = reciprocal(l, unit_of(FMT));
   if (row >= w.rows) return;

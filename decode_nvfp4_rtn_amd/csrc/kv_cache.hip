@@ -365,7 +365,11 @@ __device__ __forceinline__ void store_v(const Place& p, int i, int j, bool quad,
 }
 
 // --------------------------------------------------------------------------
-// kv_append
+// kv_append: a wave takes four tokens of one K or V head, 16 lanes a row, so
+// that an aligned quad of V rows can be transposed in registers and stored as
+// words (the layout keeps four tokens of an element together).  Bound by the
+// bytes: 16384 tokens of 8 128-wide heads to 4 bits, 86 MB read and written in
+// 23.4 us, 3.7 TB/s; a few tokens are one launch (3.4 us).
 // --------------------------------------------------------------------------
 template <int FMT, int D>
 __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(
@@ -397,7 +401,11 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(
 }
 
 // --------------------------------------------------------------------------
-// qkv_norm_rope_append
+// qkv_norm_rope_append: a wave takes four tokens and a run of heads, whose
+// rotation factors times weights it makes once; 16 lanes hold a row, so the sum
+// of squares is four steps within them.  Bound by the bytes: 8192 tokens of 32
+// query and 8 key heads of 128, bf16 in, 8-bit cache: 185 MB in 44.7 us,
+// 4.1 TB/s; a few tokens are one launch (3.9 us).
 // --------------------------------------------------------------------------
 struct NormArgs {
   KvGeom g;
@@ -566,7 +574,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void qkv_norm_rope_a
 }
 
 // --------------------------------------------------------------------------
-// kv_gather
+// kv_gather: as kv_append the other way (16384 tokens of 8 128-wide heads from 4
+// bits: 86 MB in 18.9 us, 4.5 TB/s).
 // --------------------------------------------------------------------------
 template <int FMT, int D>
 __device__ __forceinline__ void decode_row(const EncRow<FMT, D>& r, float (&x)[D / 16]) {
