@@ -24,7 +24,7 @@
 //   128-wide heads, with the join: bf16 130 us, 685 MB at 5.3 TB/s; 8-bit
 //   71 us, 4.9 TB/s), at 4 bits by each wave's chain of loads, unpacking,
 //   products and softmax (51 us, 195 MB at 3.8 TB/s; the vector unit issues in
-//   47 % of the cycles).
+//   43 % of the cycles).
 // wide (more rows): four waves share each tile.  Each turns a quarter of it
 //   into matrix operands in LDS, once for all, and takes 16 rows of its own;
 //   bound by what a tile takes a wave from barrier to barrier: operands made
@@ -346,9 +346,9 @@ __device__ __forceinline__ uint32_t wave_sum(uint32_t v) {
 // The keys of all sequences are cut into at most a.parts parts, every sequence
 // into pieces of one length, which is the shortest (nearly) that does: so the
 // parts are even however uneven the sequences are, and the grid, which is
-// planned without the lengths, is full.  (Planned by the longest sequence
-// alone, uneven ones left a third of the chip idle: 32 sequences of up to 8192
-// 4-bit keys 52 us, 4 of up to 16000 256-wide ones 110 us.)
+// planned without the lengths, is full.  (Against parts planned by the longest
+// sequence alone: 32 sequences of 2260 to 8193 4-bit keys 51 us for 56, 16 of
+// up to 8192 8-bit 256-wide ones 40 for 49.)
 struct Part {
   int b, split, nsplit, keys;    // sequence (none if < 0), place in it, its parts, keys of one
 };
