@@ -17,7 +17,7 @@
 // operand (kv_cache.hpp).  A row's statistics live in the four lanes of its
 // column, and the accumulator is rescaled in place.
 //
-// Two kernels share this.
+// Three kernels share this.
 // narrow (up to 16 rows): each of four waves takes tiles of its own straight
 //   from memory into registers and the four results are joined at the end;
 //   bound by the cache's bytes (32 sequences of 2048 to 8192 keys, 32 / 8
@@ -25,14 +25,19 @@
 //   71 us, 4.9 TB/s), at 4 bits by each wave's chain of loads, unpacking,
 //   products and softmax (51 us, 195 MB at 3.8 TB/s; the vector unit issues in
 //   43 % of the cycles).
-// wide (more rows): four waves share each tile.  Each turns a quarter of it
-//   into matrix operands in LDS, once for all, and takes 16 rows of its own;
-//   bound by what a tile takes a wave from barrier to barrier: operands made
-//   and stored, LDS reads, products, softmax (4 sequences of 6893 to 16063
-//   4-bit 256-wide keys, 63 drafts, 15 / 5 heads: 98 us and 9 for the join,
-//   47 GFLOP).  A wave issues 45 % of that time; without the operands' making
-//   and storing the case takes 76 us, without LDS reads 101, without the
-//   softmax 99.
+// pair (more rows, 64- and 128-wide heads): as narrow with 32 rows, so that a
+//   tile's operands serve two products each; bound by the chain of a tile as
+//   well (16 sequences of 63 drafts over up to 2000 8-bit 128-wide keys, 32 / 8
+//   heads: 51 us).
+// wide (256-wide heads, whose 32 rows do not fit the registers, and more than
+//   32 rows over 4-bit 128-wide keys, whose unpacking counts for more): four
+//   waves share each tile.  Each turns a quarter of it into matrix operands in
+//   LDS, once for all, and takes 16 rows of its own; bound by what a tile takes
+//   a wave from barrier to barrier: operands made and stored, LDS reads,
+//   products, softmax (4 sequences of 6893 to 16063 4-bit 256-wide keys, 63
+//   drafts, 15 / 5 heads: 98 us and 9 for the join, 47 GFLOP).  A wave issues
+//   45 % of that time; without the operands' making and storing the case takes
+//   76 us, without LDS reads 101, without the softmax 99.
 //
 // Quantized rows.  K's row scale 2^ke goes into the bf16 operand where that
 // is free (narrow, NVFP4: it multiplies the score).  V's, 2^ve, joins the
@@ -707,46 +712,31 @@ constexpr int narrow_waves(int fmt, int d) {
   return d == 64 ? 5 : d == 128 ? (fmt == QL_KV_BF16 ? 3 : 4) : 2;
 }
 
+// The tiles that one wave takes of a block's keys: first, first + 4, ..., the
+// last first, so that those with hidden keys come before those that every row
+// sees.
 template <int FMT, int D>
-__global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attention_narrow_kernel(
-    KvAttnArgs a) {
-  using L = KvLayout<FMT, D>;
-  constexpr int DCH = D < 128 ? D : 128;        // elements of d joined at a time
-  __shared__ float sm_m[kWaves][16], sm_l[kWaves][16];
-  __shared__ __align__(16) float sm_o[kWaves][16][DCH + 4];
-  __shared__ u32x4 sm_q[D / 32][64];
-
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 15, g = lane >> 4;
-  const Work w = work_of<16>(a);
-  if (!w.any) return;
-  float qs;
-  RowMask rm;
-  {
-    u32x4 q[D / 32];
-    load_query<FMT, D, FMT == QL_KV_NVFP4>(a, w, w.row0 + n, g, q, qs, rm);
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k)
-      if (k % kWaves == wave) sm_q[k][lane] = q[k];
+struct Walk {
+  const KvAttnArgs& a;
+  const Work& w;
+  int lane, first, count, partly;      // tiles; of them, the first `partly` with hidden keys
+  int per_page;                        // log2(blocks of a page)
+  const int32_t* table;
+  int pages = -1;                      // of 32 tiles' two blocks, one per lane
+  __device__ __forceinline__ Walk(const KvAttnArgs& args, const Work& work, int wave, int ln)
+      : a(args), w(work), lane(ln) {
+    first = w.k0 / kTile + wave;
+    const int tiles = (w.k1 + kTile - 1) / kTile;
+    count = tiles > first ? (tiles - first + kWaves - 1) / kWaves : 0;
+    const int open = open_to(a, w, w.row0) / kTile;
+    partly = count - (open > first ? (open - first + kWaves - 1) / kWaves : 0);
+    per_page = a.g.page_shift - 4;
+    table = a.table + int64_t(w.b) * a.table_stride;
   }
-  __syncthreads();
-  Rows<D> r;
-  r.clear();
-
-  // Tiles first, first + 4, ... of the split, the last first: those with
-  // hidden keys come before those that every row sees.
-  const int first = w.k0 / kTile + wave;
-  const int tiles = (w.k1 + kTile - 1) / kTile;
-  const int count = tiles > first ? (tiles - first + kWaves - 1) / kWaves : 0;
-  const int open = open_to(a, w, w.row0) / kTile;
-  const int whole = open > first ? (open - first + kWaves - 1) / kWaves : 0;
-  const int partly = count - whole;
-  auto tile_of = [&](int i) { return first + kWaves * (count - 1 - i); };
-  const int per_page = a.g.page_shift - 4;             // log2(blocks of a page)
-  const int32_t* table = a.table + int64_t(w.b) * a.table_stride;
-  int pages = -1;   // of 32 iterations' two blocks, one per lane
-  // An absent block of a tile is read from the tile's other block.
-  auto load = [&](int i, Tile<FMT, D>& tile, int& p0, int& p1) {
+  __device__ __forceinline__ int tile_of(int i) const { return first + kWaves * (count - 1 - i); }
+  // Reads tile i; p0, p1: its blocks' pages, negative if absent.  An absent
+  // block is read from the tile's other block.
+  __device__ __forceinline__ void load(int i, Tile<FMT, D>& tile, int& p0, int& p1) {
     if ((i & 31) == 0) {
       const int mine = i + (lane >> 1) < count ? 2 * tile_of(i + (lane >> 1)) + (lane & 1) : -1;
       pages = -1;
@@ -765,21 +755,17 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
       const int in = (own >= 0 ? block + t : block + 1 - t) & ((1 << per_page) - 1);
       tile.load(t, source<FMT, D>(a.g, kv_block(a.g, page, w.head, in)), lane);
     }
-  };
-  Tile<FMT, D> tile;
-  int p0, p1;
-  for (int i = 0; i < partly; ++i) {
-    load(i, tile, p0, p1);
-    const int base = tile_of(i) * kTile, left = w.k1 - base;
-    narrow_tile<FMT, D, true>(r, sm_q, qs, tile, p0 < 0 ? 0 : left, p1 < 0 ? 0 : left - 16,
-                              visible(rm, a.tree != nullptr, base, w.sq.ctx, g), lane);
   }
-  for (int i = partly; i < count; ++i) {
-    load(i, tile, p0, p1);
-    if (p0 >= 0 || p1 >= 0) narrow_tile<FMT, D, false>(r, sm_q, qs, tile, p0 >= 0, p1 >= 0, 0, lane);
-  }
+};
 
-  // the four waves' parts, in wave order
+// Joins the four waves' parts of 16 rows, in wave order, and stores them.
+template <int FMT, int D, int DCH>
+__device__ __forceinline__ void finish(const KvAttnArgs& a, const Work& w, Rows<D>& r, int row0,
+                                       float (&sm_m)[kWaves][16], float (&sm_l)[kWaves][16],
+                                       float (&sm_o)[kWaves][16][DCH + 4]) {
+  using L = KvLayout<FMT, D>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
   r.l = column_sum(r.l);
   if (g == 0) sm_m[wave][n] = r.m, sm_l[wave][n] = r.l;
   __syncthreads();
@@ -806,7 +792,7 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
     __syncthreads();
     constexpr int kCols = DCH / 8;      // threads per row, 8 elements each
     const int row = threadIdx.x / kCols, c = threadIdx.x % kCols * 8;
-    if (row < 16 && w.row0 + row < w.rows) {
+    if (row < 16 && row0 + row < w.rows) {
       float tm = sm_m[0][row];
 #pragma unroll
       for (int x = 1; x < kWaves; ++x) tm = __builtin_fmaxf(tm, sm_m[x][row]);
@@ -817,7 +803,7 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
 #pragma unroll
         for (int y = 0; y < 8; ++y) v[y] += sm_o[x][row][c + y];
       }
-      const int64_t out = out_row(a, w, w.row0 + row);
+      const int64_t out = out_row(a, w, row0 + row);
       if (w.nsplit == 1) {
         const float inv = reciprocal(l, unit_of(FMT));
         uint32_t y[4];
@@ -834,6 +820,196 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
     }
     __syncthreads();
   }
+}
+
+template <int FMT, int D>
+__global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attention_narrow_kernel(
+    KvAttnArgs a) {
+  using L = KvLayout<FMT, D>;
+  constexpr int DCH = D < 128 ? D : 128;        // elements of d joined at a time
+  __shared__ float sm_m[kWaves][16], sm_l[kWaves][16];
+  __shared__ __align__(16) float sm_o[kWaves][16][DCH + 4];
+  __shared__ u32x4 sm_q[D / 32][64];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const Work w = work_of<16>(a);
+  if (!w.any) return;
+  float qs;
+  RowMask rm;
+  {
+    u32x4 q[D / 32];
+    load_query<FMT, D, FMT == QL_KV_NVFP4>(a, w, w.row0 + n, g, q, qs, rm);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+      if (k % kWaves == wave) sm_q[k][lane] = q[k];
+  }
+  __syncthreads();
+  Rows<D> r;
+  r.clear();
+
+  Walk<FMT, D> walk(a, w, wave, lane);
+  Tile<FMT, D> tile;
+  int p0, p1;
+  for (int i = 0; i < walk.partly; ++i) {
+    walk.load(i, tile, p0, p1);
+    const int base = walk.tile_of(i) * kTile, left = w.k1 - base;
+    narrow_tile<FMT, D, true>(r, sm_q, qs, tile, p0 < 0 ? 0 : left, p1 < 0 ? 0 : left - 16,
+                              visible(rm, a.tree != nullptr, base, w.sq.ctx, g), lane);
+  }
+  for (int i = walk.partly; i < walk.count; ++i) {
+    walk.load(i, tile, p0, p1);
+    if (p0 >= 0 || p1 >= 0) narrow_tile<FMT, D, false>(r, sm_q, qs, tile, p0 >= 0, p1 >= 0, 0, lane);
+  }
+
+  finish<FMT, D, DCH>(a, w, r, w.row0, sm_m, sm_l, sm_o);
+}
+
+// ---------------------------------------------------------------------------
+// pair: 32 rows, keys split over the waves
+// ---------------------------------------------------------------------------
+// Waves per SIMD: 64 elements of o and two blocks' bytes of 128-wide heads fill
+// the registers of two (with three they spill: 51 us become 126); of 64-wide
+// heads four fit, three at 8 bits (32 sequences of up to 4096 keys, 4 drafts,
+// 60 / 12 heads: 4 bits 40 us, and 43 with three; 8 bits 37 us either way, 16
+// sequences of up to 8192 22 us and 24 with four).
+constexpr int pair_waves(int fmt, int d) {
+  return d == 128 ? 2 : fmt == QL_KV_E4M3 ? 3 : 4;
+}
+
+// One tile for two row tiles; arguments as narrow_tile.
+template <int FMT, int D, bool MASKED>
+__device__ __forceinline__ void pair_tile(Rows<D> (&r)[2], const u32x4 (&sm_q)[2][D / 32][64],
+                                          const float (&qs)[2], Tile<FMT, D>& tile, int n0, int n1,
+                                          uint32_t (&seen)[2], int lane) {
+  constexpr bool HALF = FMT == QL_KV_NVFP4;
+  const int g = lane >> 4;
+  // read again for every tile: held in registers they would cost waves
+  asm volatile("" ::: "memory");
+  f32x4 s[2][2] = {};
+  float kp[2] = {1.0f, 1.0f};
+  if constexpr (FMT == QL_KV_E4M3) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) kp[t] = power(tile.ke[t] >> 8 * (lane & 3) & 0xFFu);
+  }
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) {
+    u32x4 q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) q[i] = sm_q[i][k][lane];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const u32x4 a = tile.k[t].template k_operand<HALF>(k, kp[t], lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s[i][t] = mma<HALF>(a, q[i], s[i][t]);
+    }
+    in_order();
+  }
+  const float hide0 = MASKED || n0 ? 0.0f : -__builtin_inff();
+  const float hide1 = MASKED || n1 ? 0.0f : -__builtin_inff();
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int left = (t ? n1 : n0) - 4 * g, keys = left < 0 ? 0 : left > 4 ? 4 : left;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) seen[i] &= ~(0xFu << (4 * t)) | ((1u << keys) - 1u) << (4 * t);
+      tile.v[t].clear_v(keys);
+    }
+  }
+  u32x4 p[2], p_lo[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float z[8], iv[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int t = x >> 2, k = x & 3;
+      const float hide = t ? hide1 : hide0;
+      if constexpr (FMT == QL_KV_BF16) {
+        z[x] = __builtin_fmaf(s[i][t][k], qs[i], hide);
+      } else {
+        const uint32_t b = tile.ve[t] >> (8 * k) & 0xFFu;
+        iv[x] = power(~tile.ve[t] >> (8 * k) & 0xFFu);   // 2^(128 - b)
+        float v = s[i][t][k];
+        if constexpr (HALF) v *= power(tile.ke[t] >> (8 * k) & 0xFFu);
+        z[x] = __builtin_fmaf(v, qs[i], static_cast<float>(b) + hide);
+      }
+    }
+    softmax_step<FMT, D, MASKED, FMT != QL_KV_BF16>(r[i], z, iv, seen[i], p[i], p_lo[i]);
+    in_order();
+  }
+  if constexpr (MASKED) {
+    // A zero weight does not hide a NaN or an infinity in the product: they
+    // are cleared, and the sum of weights of a row that sees one is made NaN.
+    if (__any((tile.v[0].non_finite() | tile.v[1].non_finite()) != 0)) {
+      const uint32_t bad = tile.v[0].clear_non_finite() | tile.v[1].clear_non_finite() << 4;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (seen[i] & bad) r[i].l = __builtin_nanf("");
+    }
+  }
+  constexpr int per = Block<FMT, D>::kPer;
+#pragma unroll
+  for (int j = 0; j < D / 16 / per; ++j) {
+    uint2 a[per], b[per];
+    tile.v[0].v_operands(j, a);
+    tile.v[1].v_operands(j, b);
+#pragma unroll
+    for (int x = 0; x < per; ++x) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f32x4& o = r[i].o[j * per + x];
+        o = weigh<FMT>(u32x4{a[x].x, a[x].y, b[x].x, b[x].y}, p[i], p_lo[i], o);
+      }
+    }
+    in_order();
+  }
+}
+
+template <int FMT, int D>
+__global__ __launch_bounds__(64 * kWaves, pair_waves(FMT, D)) void kv_attention_pair_kernel(
+    KvAttnArgs a) {
+  constexpr int DCH = D < 128 ? D : 128;
+  __shared__ float sm_m[kWaves][16], sm_l[kWaves][16];
+  __shared__ __align__(16) float sm_o[kWaves][16][DCH + 4];
+  __shared__ u32x4 sm_q[2][D / 32][64];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const Work w = work_of<32>(a);
+  if (!w.any) return;
+  float qs[2];
+  RowMask rm[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    u32x4 q[D / 32];
+    load_query<FMT, D, FMT == QL_KV_NVFP4>(a, w, w.row0 + 16 * x + n, g, q, qs[x], rm[x]);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+      if (k % kWaves == wave) sm_q[x][k][lane] = q[k];
+  }
+  __syncthreads();
+  Rows<D> r[2];
+  r[0].clear();
+  r[1].clear();
+  Walk<FMT, D> walk(a, w, wave, lane);
+  Tile<FMT, D> tile;
+  int p0, p1;
+  uint32_t seen[2] = {0, 0};
+  for (int i = 0; i < walk.partly; ++i) {
+    walk.load(i, tile, p0, p1);
+    const int base = walk.tile_of(i) * kTile, left = w.k1 - base;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) seen[x] = visible(rm[x], a.tree != nullptr, base, w.sq.ctx, g);
+    pair_tile<FMT, D, true>(r, sm_q, qs, tile, p0 < 0 ? 0 : left, p1 < 0 ? 0 : left - 16, seen,
+                              lane);
+  }
+  for (int i = walk.partly; i < walk.count; ++i) {
+    walk.load(i, tile, p0, p1);
+    if (p0 >= 0 || p1 >= 0)
+      pair_tile<FMT, D, false>(r, sm_q, qs, tile, p0 >= 0, p1 >= 0, seen, lane);
+  }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) finish<FMT, D, DCH>(a, w, r[x], w.row0 + 16 * x, sm_m, sm_l, sm_o);
 }
 
 // ---------------------------------------------------------------------------
@@ -935,8 +1111,8 @@ __device__ __forceinline__ void wide_tile(Rows<D>& r, const u32x4 (&q)[D / 32], 
 // 16 rows to a wave, and so two or three waves on a SIMD, beat 32: a tile is a
 // chain of LDS reads, products and the softmax that takes a wave more than
 // twice the cycles it issues, so it is the other waves that fill the SIMD (16
-// sequences of 63 drafts over 2000 8-bit keys, 32 / 8 128-wide heads: 56 us,
-// and 77 us with 32 rows to a wave; eight waves to a block: 78 us).
+// sequences of 63 drafts over 2000 8-bit 128-wide keys: 56 us, and 77 us with 32
+// rows to a wave; eight waves to a block: 78 us).
 template <int FMT, int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAttnArgs a) {
   using L = KvLayout<FMT, D>;
@@ -1103,11 +1279,20 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttnArgs a, in
 
 }  // namespace
 
+// Whether the kernel of 64 rows is built for a format and head.
+static constexpr bool wide_fits(int fmt, int d) {
+  return d == 256 || (fmt == QL_KV_NVFP4 && d == 128);
+}
+
 KvAttnPlan kv_attention_plan(int fmt, int d, int n_q, int n_kv, int64_t n_seqs, int64_t max_q,
                              int64_t max_kv) {
   KvAttnPlan p;
   const int64_t rows = max_q * (n_q / n_kv);
-  p.rows = rows <= 16 ? 16 : 64;
+  // 32 rows straight from memory, or 64 through LDS (8-bit keys, 128-wide heads:
+  // 16 sequences of 63 drafts over up to 2000 keys 51 us, and 59; a 512-token
+  // chunk of a prompt 25 and 41; 4-bit: 32 drafts over 60000 keys 79 and 72, 8
+  // sequences of up to 8192 and 8 drafts in 5 heads 39 and 36)
+  p.rows = rows <= 16 ? 16 : wide_fits(fmt, d) && (d == 256 || rows > 32) ? 64 : 32;
   p.row_blocks = (rows + p.rows - 1) / p.rows;
   // Parts of all keys together.  A second launch joins those of one sequence (3
   // to 10 us), and a block takes about as long as 128 keys of a narrow wave to
@@ -1120,16 +1305,15 @@ KvAttnPlan kv_attention_plan(int fmt, int d, int n_q, int n_kv, int64_t n_seqs, 
     const int64_t n = per_cu * (cus / 8) / p.row_blocks * 8 / n_kv;
     return n > most ? most : n < n_seqs ? n_seqs : n;
   };
-  if (p.rows == 64) {
-    // as many blocks as run at once: two of 256-wide heads on a compute unit, of
-    // others three where the parts stay over 512 keys (16 sequences of 63 drafts
-    // over up to 2000 8-bit keys: 60 us, and 65 with two; 8 of 16 drafts over up
-    // to 4096: 31 us, and 28 with two; 256-wide over up to 16000: 121 and 100 us)
+  if (p.rows >= 32) {
+    // as many blocks as run at once where the parts stay over 512 keys, two on a
+    // compute unit otherwise (4-bit 128-wide keys through LDS, three run: 16
+    // sequences of 63 drafts over up to 2000 keys 67 us, and 70 with two; 8 of
+    // 16 drafts over up to 4096 keys 31 us, and 28 with two)
+    const int at_once = p.rows == 32 ? pair_waves(fmt, d) : d == 256 ? 2 : 3;
+    const int64_t all = parts_for(at_once, 512);
     p.parts = parts_for(2, 256);
-    if (d < 256) {
-      const int64_t three = parts_for(3, 512);
-      if (p.parts < three) p.parts = three;
-    }
+    if (p.parts < all) p.parts = all;
   } else {
     // two on a compute unit (one sequence of 131072 8-bit keys: 57 us, with
     // four 62); of rows of at most 64 bytes, whose instructions count for more
@@ -1172,8 +1356,13 @@ hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a
   const unsigned blocks = unsigned((units + 7) / 8 * 8 * p.row_blocks);
   const hipError_t e = kv_dispatch(fmt, d, [&](auto f, auto n) {
     constexpr int FMT = decltype(f)::value, D = decltype(n)::value;
-    if (p.rows == 64) return launch_wide<FMT, D>(a, blocks, s);
-    kv_attention_narrow_kernel<FMT, D><<<blocks, 64 * kWaves, 0, s>>>(a);
+    if constexpr (wide_fits(FMT, D)) {
+      if (p.rows == 64) return launch_wide<FMT, D>(a, blocks, s);
+    }
+    if constexpr (D < 256) {
+      if (p.rows == 32) kv_attention_pair_kernel<FMT, D><<<blocks, 64 * kWaves, 0, s>>>(a);
+    }
+    if (p.rows == 16) kv_attention_narrow_kernel<FMT, D><<<blocks, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
   });
   if (e != hipSuccess || p.parts == a.n_seqs) return e;

@@ -138,7 +138,7 @@ struct KvAttnArgs {
   int row_blocks;
 };
 struct KvAttnPlan {
-  int rows;               // query rows per block: 16 (narrow) or 64 (wide)
+  int rows;               // query rows per block: 16 (narrow), 32 (pair), 64 (wide)
   int64_t row_blocks;
   int64_t parts;
 };

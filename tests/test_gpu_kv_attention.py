@@ -321,3 +321,26 @@ def test_many_uneven_sequences_share_the_parts(fmt, nodes):
     b.check(y)
     assert torch.equal(y, b.run(q)) and q.kv_attention_workspace(
         device_cache(q, b.c), sum(count), 2, 70, nodes, max(lens)) > 0
+
+
+@pytest.mark.parametrize("fmt,d", FD)
+@pytest.mark.parametrize("n_q,n_kv,nodes", [(4, 1, 5), (8, 1, 4), (3, 1, 11), (6, 2, 14), (1, 1, 48)])
+def test_rows_around_the_blocks(fmt, d, n_q, n_kv, nodes):
+    """20, 32, 33, 42 and 48 rows of a kv head: blocks of 16, 32 and 64 rows, the
+    last one full or not."""
+    q = require_gpu()
+    say("row blocks", fmt, d, n_q, n_kv, nodes)
+    lens = [nodes, nodes + 31, 640]
+    b = Batch(FMTS[fmt], lens, [nodes] * 3, n_q, n_kv, d, 32, seed=19)
+    tree = random_tree([nodes] * 3, 19)
+    b.check(b.run(q, tree), tree)
+    b.check(b.run(q))
+
+
+def test_sequences_that_share_pages():
+    """Two sequences with a common prompt's pages."""
+    q = require_gpu()
+    say("shared pages")
+    b = Batch(kv.E4M3, [100, 90], [1, 1], 4, 2, 128, 16, seed=20)
+    b.table[1, :5] = b.table[0, :5]
+    b.check(b.run(q))
