@@ -29,8 +29,8 @@
 //   tile's operands serve two products each; bound by the chain of a tile as
 //   well (16 sequences of 63 drafts over up to 2000 8-bit 128-wide keys, 32 / 8
 //   heads: 51 us).
-// wide (256-wide heads, whose 32 rows do not fit the registers, and more than
-//   32 rows over 4-bit 128-wide keys, whose unpacking counts for more): four
+// wide (256-wide heads, whose 32 rows do not fit the registers, and mostly more
+//   than 32 rows over 4-bit 128-wide keys, whose unpacking counts for more): four
 //   waves share each tile.  Each turns a quarter of it into matrix operands in
 //   LDS, once for all, and takes 16 rows of its own; bound by what a tile takes
 //   a wave from barrier to barrier: operands made and stored, LDS reads,
@@ -1291,14 +1291,18 @@ KvAttnPlan kv_attention_plan(int fmt, int d, int n_q, int n_kv, int64_t n_seqs, 
   // 32 rows straight from memory, or 64 through LDS (8-bit keys, 128-wide heads:
   // 16 sequences of 63 drafts over up to 2000 keys 51 us, and 59; a 512-token
   // chunk of a prompt 25 and 41; 4-bit: 32 drafts over 60000 keys 79 and 72, 8
-  // sequences of up to 8192 and 8 drafts in 5 heads 39 and 36)
-  p.rows = rows <= 16 ? 16 : wide_fits(fmt, d) && (d == 256 || rows > 32) ? 64 : 32;
+  // sequences of up to 8192 and 8 drafts in 5 heads 39 and 36; but a chunk of a
+  // prompt whose blocks of 64 rows would not fill a round, which is not split
+  // either, 33 and 44 at 512 tokens over 1000; at 4096 tokens 291 and 259)
+  const int64_t cus = device_cu_count() > 0 ? device_cu_count() : 256;
+  const bool few = max_q > 64 && n_seqs * n_kv * ((rows + 63) / 64) <= 3 * cus;
+  const bool wide = wide_fits(fmt, d) && (d == 256 || (rows > 32 && !few));
+  p.rows = rows <= 16 ? 16 : wide ? 64 : 32;
   p.row_blocks = (rows + p.rows - 1) / p.rows;
   // Parts of all keys together.  A second launch joins those of one sequence (3
   // to 10 us), and a block takes about as long as 128 keys of a narrow wave to
   // start, so up to 512 keys stay whole (500 keys, one sequence: 8 us against
   // 12), and no part of a longer one is planned under 256 keys.
-  const int64_t cus = device_cu_count() > 0 ? device_cu_count() : 256;
   auto parts_for = [&](int64_t per_cu, int64_t least) {
     const int64_t most = max_kv <= 512 ? n_seqs : n_seqs * ((max_kv + least - 1) / least);
     // what each XCD's eighth of the units leaves room for in one round

@@ -588,7 +588,8 @@ int kv_attention(const ql_kv_cache *cache, const void *q_bf16, int64_t q_stride,
  * verification.
  *
  * path  int32 [n_seqs, max_path]: accepted draft indices, root first; an
- *       entry outside [0, n_b) moves nothing (pad with -1).  max_path <= 64.
+ *       entry outside [0, n_b) moves nothing (pad with -1), nor does one of
+ *       whose two rows the page is not in the cache.  max_path <= 64.
  * Errors: as kv_attention.
  * ---------------------------------------------------------------------- */
 int kv_commit(const ql_kv_cache *cache, int64_t n_seqs, const int32_t *cu_q,

@@ -344,3 +344,12 @@ def test_sequences_that_share_pages():
     b = Batch(kv.E4M3, [100, 90], [1, 1], 4, 2, 128, 16, seed=20)
     b.table[1, :5] = b.table[0, :5]
     b.check(b.run(q))
+
+
+@pytest.mark.parametrize("n_kv,tokens", [(1, 65), (2, 300), (8, 700)])
+def test_chunks_over_four_bits(n_kv, tokens):
+    """A prompt's chunk over 4-bit 128-wide keys: few blocks and many."""
+    q = require_gpu()
+    say("4-bit chunk", n_kv, tokens)
+    b = Batch(kv.NVFP4, [tokens + 40], [tokens], 4 * n_kv if n_kv < 8 else 8, n_kv, 128, 64, seed=21)
+    b.check(b.run(q))

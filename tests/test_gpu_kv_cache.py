@@ -204,6 +204,26 @@ def test_commit_moves_rows(fmt, d):
     assert np.array_equal(cache.data.cpu().numpy(), b.c.bytes)
 
 
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_commit_leaves_rows_of_absent_pages(fmt):
+    q = require_gpu()
+    say("commit absent pages", fmt)
+    lens, nodes = [40, 40], [30, 30]                  # drafts at 10..39, over three pages
+    b = Batch(FMTS[fmt], lens, nodes, 2, 2, 64, page=16, seed=4)
+    path = np.array([[3, 8, 20, 25]] * 2, dtype=np.int32)
+    gone = b.table.copy()
+    gone[0, 1], gone[1, 0] = -1, b.c.n_pages          # sources 13, 18, 30, 35
+    cache = device_cache(q, b.c)
+    q.kv_commit(cache, torch.from_numpy(b.cu).cuda(), _dev(lens, torch.int32),
+                torch.from_numpy(gone).cuda(), torch.from_numpy(path).cuda())
+    torch.cuda.synchronize()
+    # of the first sequence only sources on pages 0 and 2 move, of the second
+    # none: all targets (10..13) lie on its page 0
+    at = b.slots(0, [13, 35, 10, 13])
+    b.c.move([(at[0], at[2]), (at[1], at[3])])
+    assert np.array_equal(cache.data.cpu().numpy(), b.c.bytes)
+
+
 def test_reads_back_what_a_reappend_keeps():
     """E4M3 rows survive reading back and appending again unchanged."""
     q = require_gpu()
