@@ -315,6 +315,7 @@ __device__ __forceinline__ int q_element(int s, int g) {
 // ---------------------------------------------------------------------------
 // Sequences, rows, splits
 // ---------------------------------------------------------------------------
+// Keys of sequence b that its row of the table reaches.
 __device__ __forceinline__ int length(const KvAttnArgs& a, int b) {
   const int64_t cap = a.table_cols << a.g.page_shift;
   const int len = a.kv_lens[b];
@@ -322,7 +323,9 @@ __device__ __forceinline__ int length(const KvAttnArgs& a, int b) {
 }
 
 struct Seq {
-  int q0, rows_q, len, ctx;   // rows_q: its queries that lie in q and y
+  int q0, rows_q;   // rows_q: its queries that lie in q and y
+  int len;          // its keys, as far as the table goes
+  int ctx;          // of all its keys, those before the new tokens' (may pass len)
 };
 __device__ __forceinline__ Seq sequence(const KvAttnArgs& a, int b) {
   Seq s;
@@ -332,7 +335,8 @@ __device__ __forceinline__ Seq sequence(const KvAttnArgs& a, int b) {
   s.rows_q = s.q0 < 0 || nodes < 0 || room <= 0 ? 0 : room < nodes ? int(room) : nodes;
   if (s.rows_q > a.max_q) s.rows_q = a.max_q;
   s.len = length(a, b);
-  s.ctx = nodes < 0 ? s.len : s.len > nodes ? s.len - nodes : 0;
+  const int all = a.kv_lens[b] > 0 ? a.kv_lens[b] : 0;
+  s.ctx = nodes < 0 ? all : all > nodes ? all - nodes : 0;
   return s;
 }
 

@@ -560,7 +560,8 @@ int qkv_norm_rope_append(const ql_kv_cache *cache, const void *qkv, int x_dtype,
  * cu_q         int32 [n_seqs + 1], ascending from 0; kv_lens int32 [n_seqs].
  * block_table  int32 [n_seqs, table_cols], rows table_stride elements apart:
  *              the page of positions page_size * j .. of each sequence.
- *              Positions past the table's last column are not read.
+ *              Positions past the table's last column are not read: they are
+ *              hidden, like those of a page that is not in the cache.
  * max_q        at least every n_b (queries past it are not computed).
  * max_kv       about the largest kv_lens[b]; whether and into how many parts
  *              keys are split goes by it, where goes by the lengths
