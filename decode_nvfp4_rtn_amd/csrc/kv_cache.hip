@@ -501,10 +501,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void qkv_norm_rope_a
       for (int u = 0; u < N; ++u) sum = fma_of(static_cast<T>(x[u]), static_cast<T>(x[u]), sum);
       r = rsqrt_of(fma_of(row_sum(sum), static_cast<T>(1.0f / D), static_cast<T>(a.eps)));
     }
+    // Elements from rot on have none: -0 times their factor 0 adds -0, which
+    // leaves every value as it is, an infinity and a -0 as well.
     float partner[N];
     if constexpr (ROT == kRotPairs) {
 #pragma unroll
-      for (int u = 0; u < N; ++u) partner[u] = x[u ^ 1];
+      for (int u = 0; u < N; ++u) partner[u] = i * N + u < a.rot ? x[u ^ 1] : -0.0f;
     } else if constexpr (ROT == kRotWhole) {
       // half a row on is 8 of its 16 lanes on
 #pragma unroll
@@ -523,7 +525,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void qkv_norm_rope_a
 #pragma unroll
       for (int u = 0; u < N; ++u) {
         const int d = i * N + u;
-        partner[u] = row[d < half ? d + half : d < a.rot ? d - half : d];
+        const float other = row[d < half ? d + half : d < a.rot ? d - half : d];
+        partner[u] = d < a.rot ? other : -0.0f;
       }
     }
 #pragma unroll

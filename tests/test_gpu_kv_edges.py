@@ -36,3 +36,35 @@ def test_tables_shorter_than_a_length(fmt, d, n_q, n_kv, nodes):
                 got = b.run(q, tree).double().cpu().numpy()
                 b.table = whole
                 assert np.all(np.abs(got - want) <= bound)
+
+
+@pytest.mark.parametrize("fmt,d", FD)
+@pytest.mark.parametrize("rot", [0, 16, 26])
+@pytest.mark.parametrize("pairs", [False, True])
+def test_elements_past_the_rotation_stay_as_they_are(fmt, d, rot, pairs):
+    """Without norm weights, an infinity or a NaN past `rot` reaches no other
+    element and stays what it is; a rotation by 0 changes nothing before it."""
+    q = require_gpu()
+    say("past the rotation", fmt, d, rot, pairs)
+    n_q, n_kv, tokens = 3, 2, 6
+    x = rows(41, tokens, n_q + 2 * n_kv, d)
+    for t, at, value in ((0, rot, np.inf), (1, d - 1, -np.inf), (2, d // 2 + 1, np.nan), (3, rot + 1, np.nan)):
+        x[t, :, at] = value
+    x[4, :, rot:] = -0.0
+    table = np.concatenate([np.ones((1, rot // 2)), np.zeros((1, rot // 2))], 1)
+    slots = torch.arange(tokens, device="cuda")
+    for bf16 in (True, False):
+        got, want = (q.KVCache(FMTS[fmt], 1, 16, n_kv, d) for _ in range(2))
+        qkv = on_gpu(x, bf16)
+        queries = q.qkv_norm_rope_append(
+            got, qkv.flatten(1), n_q, slots, slots.int() if rot else None,
+            _dev(table, torch.float32) if rot else None, interleaved=pairs)
+        q.kv_append(want, qkv[:, n_q:n_q + n_kv], qkv[:, n_q + n_kv:], slots)
+        same = [(queries.float().cpu().numpy(), x[:, :n_q])]
+        same += [(a.cpu().numpy(), b.cpu().numpy()) for a, b in
+                 zip(q.kv_gather(got, slots, out_dtype=torch.float32),
+                     q.kv_gather(want, slots, out_dtype=torch.float32))]
+        for a, b in same:
+            assert np.array_equal(a, b, equal_nan=True)
+            real = ~np.isnan(b)
+            assert np.array_equal(np.signbit(a)[real], np.signbit(b)[real])
