@@ -198,7 +198,7 @@ __device__ __forceinline__ EncRow<FMT, D> encode_row(const T (&v)[D / 16]) {
   constexpr int N = D / 16;
   float x[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = FMT == QL_KV_BF16 ? static_cast<float>(v[i]) : sticky(v[i]);
+  for (int i = 0; i < N; ++i) x[i] = sticky(v[i]);
   EncRow<FMT, D> r;
   r.scale = 0;
   if constexpr (FMT == QL_KV_BF16) {

@@ -77,8 +77,7 @@ def quantize(fmt, x):
     x = x if x.dtype == np.float64 else x.astype(np.float32)
     n, d = x.shape
     if fmt == BF16:
-        x = x.astype(np.float32)
-        bits = rn_bf16_bits(x)
+        bits = rn_bf16_bits(sticky32(x))
         return dict(row=bits.view(np.uint8).reshape(n, 2 * d), scales=None, exp=None,
                     value=bf16_bits_to_f32(bits).astype(np.float64))
     e = row_exponent(np.max(np.abs(x), axis=1), TOP[fmt])

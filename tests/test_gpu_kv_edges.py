@@ -68,3 +68,25 @@ def test_elements_past_the_rotation_stay_as_they_are(fmt, d, rot, pairs):
             assert np.array_equal(a, b, equal_nan=True)
             real = ~np.isnan(b)
             assert np.array_equal(np.signbit(a)[real], np.signbit(b)[real])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("part", [False, True])
+def test_bf16_keys_are_rounded_once(d, pairs, part):
+    """Keys 2^-40 to either side of the middle between two bf16 values, which
+    binary32 does not hold."""
+    q = require_gpu()
+    say("bf16 keys", d, pairs, part)
+    rot = 32 if part else d
+    x = np.zeros((4, 3, d), dtype=np.float32)      # one query, key and value head
+    a, b = (0, 1) if pairs else (0, rot // 2)
+    x[:, 1, a] = 1 + np.array([1, 1, 3, 3]) / 256  # middles of 1, 1 + 2^-7, 1 + 2^-6
+    x[:, 1, b] = 2.0 ** -20 * np.array([-1, 1, -1, 1])
+    table = np.concatenate([np.ones((1, rot // 2)), np.full((1, rot // 2), 2.0 ** -20)], 1)
+    cache = q.KVCache(q.QL_KV_BF16, 1, 16, 1, d)
+    slots = torch.arange(4, device="cuda")
+    q.qkv_norm_rope_append(cache, on_gpu(x, False).flatten(1), 1, slots, slots.int(),
+                           _dev(table, torch.float32), interleaved=pairs)
+    k, _ = q.kv_gather(cache, slots, out_dtype=torch.float32)
+    assert k[:, 0, a].tolist() == [1 + 2.0 ** -7, 1.0, 1 + 2.0 ** -6, 1 + 2.0 ** -7]
