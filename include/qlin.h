@@ -498,8 +498,9 @@ int kv_gather(const ql_kv_cache *cache, const int64_t *slots, int64_t tokens, vo
  * The step between the qkv projection and the attention, in one pass over
  * the projection's output: RMS norm of every query and key head, rotation of
  * both by the token's position, queries out, K and V written to the cache
- * (as kv_append).  Queries are computed in binary32, keys in binary64 up to
- * the roundings of the row's format.
+ * (as kv_append).  Queries are computed in binary32 (their squares' sum must
+ * lie in its range: values from 1e-18 to 1e17, or any small ones with an eps
+ * that is not), keys in binary64 up to the roundings of the row's format.
  *   norm      x <- x / sqrt(mean(x^2) + eps) * weight
  *   rotation  (a, b) <- (a c - b s, b c + a s) for rot / 2 pairs of a head,
  *             a = x[i], b = x[i + rot / 2], or x[2 i], x[2 i + 1] with

@@ -90,3 +90,46 @@ def test_bf16_keys_are_rounded_once(d, pairs, part):
                            _dev(table, torch.float32), interleaved=pairs)
     k, _ = q.kv_gather(cache, slots, out_dtype=torch.float32)
     assert k[:, 0, a].tolist() == [1 + 2.0 ** -7, 1.0, 1 + 2.0 ** -6, 1 + 2.0 ** -7]
+
+
+@pytest.mark.parametrize("fmt,d", FD)
+@pytest.mark.parametrize("size", [1e-34, 1e-30, 1e-22, 1e20, 1e30, 1e35])
+def test_keys_are_normed_whatever_their_size(fmt, d, size):
+    """The mean of their squares may lie outside of binary32's range; eps = 0."""
+    q = require_gpu()
+    say("key size", fmt, d, size)
+    n_kv, slots = 2, np.arange(5)
+    x = rows(51, 5, 1 + 2 * n_kv, d, bf16=False)
+    x[:, 1:1 + n_kv] *= np.float32(size)
+    w = np.linspace(0.5, 1.5, d).astype(np.float32)
+    c = kv.Cache(FMTS[fmt], 1, 16, n_kv, d)
+    c.write("k", kv.norm_rope(x[:, 1:1 + n_kv], w, 0.0, None, None, False), slots)
+    c.write("v", x[:, 1 + n_kv:], slots)
+    cache = q.KVCache(FMTS[fmt], 1, 16, n_kv, d,
+                      data=torch.zeros(c.bytes.size, dtype=torch.uint8, device="cuda"))
+    q.qkv_norm_rope_append(cache, on_gpu(x, False).flatten(1), 1, _dev(slots, torch.int64),
+                           q_weight=_dev(w, torch.float32), k_weight=_dev(w, torch.float32), eps=0.0)
+    assert np.array_equal(cache.data.cpu().numpy(), c.bytes)
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_norms_of_zero_and_infinite_rows(fmt):
+    """x / sqrt(mean(x^2) + eps): an infinity gives NaN and makes the others 0, a
+    row of zeros is zero, or NaN with eps = 0; queries and keys alike."""
+    q = require_gpu()
+    say("norm ends", fmt)
+    d = 64
+    x = rows(52, 3, 3, d, bf16=False)
+    x[0, :, 5] = np.inf
+    x[1] = x[2] = 0
+    w = _dev(np.ones(d), torch.float32)
+    cache = q.KVCache(FMTS[fmt], 1, 16, 1, d)
+    for eps in (1e-6, 0.0):
+        y = q.qkv_norm_rope_append(cache, on_gpu(x, False).flatten(1), 1, torch.arange(3, device="cuda"),
+                                   q_weight=w, k_weight=w, eps=eps)
+        k, _ = q.kv_gather(cache, torch.arange(3, device="cuda"), out_dtype=torch.float32)
+        for got in (y[:, 0].float(), k[:, 0]):
+            bad = torch.isnan(got[0]).nonzero().flatten().tolist()
+            assert bad == (list(range(16)) if fmt == "nvfp4" and got.data_ptr() == k.data_ptr() else [5])
+            assert not got[0].nan_to_num().any()
+            assert torch.isnan(got[1:]).all() if eps == 0 else not got[1:].any()
