@@ -133,6 +133,13 @@ __device__ __forceinline__ uint32_t bad_halves(uint32_t w) {
 __device__ __forceinline__ uint32_t bad_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
+// In the upper two bits of each byte: not 0 where the row exponent lies outside
+// of [64, 127], that is of 2^-63 .. 1.
+__device__ __forceinline__ uint32_t far_bits(uint32_t w) { return w ^ 0x40404040u; }
+// 0xFF in byte k for bit k.
+__device__ __forceinline__ uint32_t byte_mask(uint32_t bits) {
+  return ((bits & 15u) * 0x00204081u & 0x01010101u) * 0xFFu;
+}
 template <int CTRL>
 __device__ __forceinline__ uint32_t row_or(uint32_t v) {   // another lane of the same 16
   return uint32_t(__builtin_amdgcn_mov_dpp(int(v), CTRL, 0xF, 0xF, true));
@@ -536,10 +543,18 @@ struct Rows {
 };
 
 // From z (scores, V's row exponent added) to the weights' operand p (BF16:
-// and p_lo); iv: 2 2^-ve.  MASKED: `seen` says which keys count.
+// and p_lo); iv: 2 2^-ve (its sign does not count if far).  MASKED: `seen` says which keys count.
+// The sum of weights takes w 2^-ve.  Where row exponents are at most 63 apart
+// (far_bits), a w below 2^-126, which is 0, has less than 2^-70 of the weights.
+// Otherwise (far: in this tile or an earlier one of this wave) it may have any
+// share, and the terms are made from their exponents, 8 more exponentials.  They
+// are as large as 2^116 or as small as 2^-112, whatever o is: l is rescaled in
+// two steps.  (Telling the two apart costs 0 to 5 %; with all rows far the 4-bit
+// batch takes 52 us and not 48, 16 trees of 63 drafts over 8-bit keys 63 and not
+// 53.)
 template <int FMT, int D, bool MASKED, bool IV>
 __device__ __forceinline__ void softmax_step(Rows<D>& r, float (&z)[8], const float (&iv)[8],
-                                             uint32_t seen, u32x4& p, u32x4& p_lo) {
+                                             bool far, uint32_t seen, u32x4& p, u32x4& p_lo) {
   if constexpr (MASKED) {
 #pragma unroll
     for (int x = 0; x < 8; ++x) z[x] = seen >> x & 1 ? z[x] : -__builtin_inff();
@@ -548,13 +563,26 @@ __device__ __forceinline__ void softmax_step(Rows<D>& r, float (&z)[8], const fl
 #pragma unroll
   for (int x = 1; x < 8; ++x) mx = __builtin_fmaxf(mx, z[x]);
   mx = column_max(mx);
-  if (__any(mx > r.m + kMost)) {
-    const float mn = __builtin_fmaxf(r.m, mx - kUp);
-    const float f = __builtin_amdgcn_exp2f(r.m - mn);
-    r.m = mn;
-    r.l *= f;
+  float l_far = 0.0f;
+  const bool anew = __any(mx > r.m + kMost);
+  // one way round for both: two would cut the step in three for the scheduler
+  if (anew || (IV && far)) {
+    if (anew) {
+      const float mn = __builtin_fmaxf(r.m, mx - kUp);
+      const float h = __builtin_amdgcn_exp2f(0.5f * (r.m - mn)), f = h * h;
+      r.m = mn;
+      r.l = r.l * h * h;
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) r.o[d] *= f;
+      for (int d = 0; d < D / 16; ++d) r.o[d] *= f;
+    }
+    if (IV && far) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float e = static_cast<float>(int(__float_as_uint(iv[x]) >> 23 & 0xFFu) - 127);
+        const float t = iv[x] != iv[x] ? iv[x] : __builtin_amdgcn_exp2f(z[x] - r.m + e);
+        l_far += !MASKED || (seen >> x & 1) ? t : 0.0f;
+      }
+    }
   }
   float w[8], l = 0.0f;
 #pragma unroll
@@ -567,6 +595,7 @@ __device__ __forceinline__ void softmax_step(Rows<D>& r, float (&z)[8], const fl
       l += w[x];
     }
   }
+  if (IV && far) l = l_far;
   r.l = FMT == QL_KV_BF16 ? r.l + l : __builtin_fmaf(l, kUnit / 2, r.l);   // iv: 2 2^-ve
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
@@ -627,6 +656,16 @@ struct Tile {
       ke[t] = e[0], ve[t] = e[1];
     }
   }
+  // Whether a V row (MASKED: of the keys in some lane's `seen`) has an exponent
+  // far from the usual.
+  template <bool MASKED>
+  __device__ __forceinline__ bool any_far(uint32_t seen) const {
+    uint32_t out = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      out |= MASKED ? far_bits(ve[t]) & byte_mask(seen >> (4 * t)) : far_bits(ve[t]);
+    return __any((out & 0xC0C0C0C0u) != 0);
+  }
 };
 
 // One tile.  n0, n1: how many of each block's 16 keys are there.  MASKED: some
@@ -635,7 +674,7 @@ struct Tile {
 template <int FMT, int D, bool MASKED>
 __device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&sm_q)[D / 32][64], float qs,
                                             Tile<FMT, D>& tile, int n0, int n1, uint32_t seen,
-                                            int lane) {
+                                            bool& far, int lane) {
   constexpr bool HALF = FMT == QL_KV_NVFP4;
   const int g = lane >> 4;
   // read again for every tile: held in registers they would cost waves
@@ -681,8 +720,9 @@ __device__ __forceinline__ void narrow_tile(Rows<D>& r, const u32x4 (&sm_q)[D / 
       tile.v[t].clear_v(keys);
     }
   }
+  if constexpr (FMT != QL_KV_BF16) far = far || tile.template any_far<MASKED>(seen);
   u32x4 p, p_lo;
-  softmax_step<FMT, D, MASKED, FMT != QL_KV_BF16>(r, z, iv, seen, p, p_lo);
+  softmax_step<FMT, D, MASKED, FMT != QL_KV_BF16>(r, z, iv, far, seen, p, p_lo);
   if constexpr (MASKED) {
     // A zero weight does not hide a NaN or an infinity in the product: they
     // are cleared, and the sum of weights of a row that sees one is made NaN.
@@ -803,7 +843,8 @@ __device__ __forceinline__ void finish(const KvAttnArgs& a, const Work& w, Rows<
       float l = 0.0f, v[8] = {};
 #pragma unroll
       for (int x = 0; x < kWaves; ++x) {
-        l += sm_l[x][row] * __builtin_amdgcn_exp2f(sm_m[x][row] - tm);
+        const float h = __builtin_amdgcn_exp2f(0.5f * (sm_m[x][row] - tm));
+        l += sm_l[x][row] * h * h;     // in two steps, as in softmax_step
 #pragma unroll
         for (int y = 0; y < 8; ++y) v[y] += sm_o[x][row][c + y];
       }
@@ -854,16 +895,18 @@ __global__ __launch_bounds__(64 * kWaves, narrow_waves(FMT, D)) void kv_attentio
 
   Walk<FMT, D> walk(a, w, wave, lane);
   Tile<FMT, D> tile;
+  bool far = false;
   int p0, p1;
   for (int i = 0; i < walk.partly; ++i) {
     walk.load(i, tile, p0, p1);
     const int base = walk.tile_of(i) * kTile, left = w.k1 - base;
     narrow_tile<FMT, D, true>(r, sm_q, qs, tile, p0 < 0 ? 0 : left, p1 < 0 ? 0 : left - 16,
-                              visible(rm, a.tree != nullptr, base, w.sq.ctx, g), lane);
+                              visible(rm, a.tree != nullptr, base, w.sq.ctx, g), far, lane);
   }
   for (int i = walk.partly; i < walk.count; ++i) {
     walk.load(i, tile, p0, p1);
-    if (p0 >= 0 || p1 >= 0) narrow_tile<FMT, D, false>(r, sm_q, qs, tile, p0 >= 0, p1 >= 0, 0, lane);
+    if (p0 >= 0 || p1 >= 0)
+      narrow_tile<FMT, D, false>(r, sm_q, qs, tile, p0 >= 0, p1 >= 0, 0, far, lane);
   }
 
   finish<FMT, D, DCH>(a, w, r, w.row0, sm_m, sm_l, sm_o);
@@ -885,7 +928,7 @@ constexpr int pair_waves(int fmt, int d) {
 template <int FMT, int D, bool MASKED>
 __device__ __forceinline__ void pair_tile(Rows<D> (&r)[2], const u32x4 (&sm_q)[2][D / 32][64],
                                           const float (&qs)[2], Tile<FMT, D>& tile, int n0, int n1,
-                                          uint32_t (&seen)[2], int lane) {
+                                          uint32_t (&seen)[2], bool& far, int lane) {
   constexpr bool HALF = FMT == QL_KV_NVFP4;
   const int g = lane >> 4;
   // read again for every tile: held in registers they would cost waves
@@ -920,6 +963,7 @@ __device__ __forceinline__ void pair_tile(Rows<D> (&r)[2], const u32x4 (&sm_q)[2
       tile.v[t].clear_v(keys);
     }
   }
+  if constexpr (FMT != QL_KV_BF16) far = far || tile.template any_far<MASKED>(seen[0] | seen[1]);
   u32x4 p[2], p_lo[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -938,7 +982,7 @@ __device__ __forceinline__ void pair_tile(Rows<D> (&r)[2], const u32x4 (&sm_q)[2
         z[x] = __builtin_fmaf(v, qs[i], static_cast<float>(b) + hide);
       }
     }
-    softmax_step<FMT, D, MASKED, FMT != QL_KV_BF16>(r[i], z, iv, seen[i], p[i], p_lo[i]);
+    softmax_step<FMT, D, MASKED, FMT != QL_KV_BF16>(r[i], z, iv, far, seen[i], p[i], p_lo[i]);
     in_order();
   }
   if constexpr (MASKED) {
@@ -997,6 +1041,7 @@ __global__ __launch_bounds__(64 * kWaves, pair_waves(FMT, D)) void kv_attention_
   r[1].clear();
   Walk<FMT, D> walk(a, w, wave, lane);
   Tile<FMT, D> tile;
+  bool far = false;
   int p0, p1;
   uint32_t seen[2] = {0, 0};
   for (int i = 0; i < walk.partly; ++i) {
@@ -1004,13 +1049,13 @@ __global__ __launch_bounds__(64 * kWaves, pair_waves(FMT, D)) void kv_attention_
     const int base = walk.tile_of(i) * kTile, left = w.k1 - base;
 #pragma unroll
     for (int x = 0; x < 2; ++x) seen[x] = visible(rm[x], a.tree != nullptr, base, w.sq.ctx, g);
-    pair_tile<FMT, D, true>(r, sm_q, qs, tile, p0 < 0 ? 0 : left, p1 < 0 ? 0 : left - 16, seen,
-                              lane);
+    pair_tile<FMT, D, true>(r, sm_q, qs, tile, p0 < 0 ? 0 : left, p1 < 0 ? 0 : left - 16, seen, far,
+                            lane);
   }
   for (int i = walk.partly; i < walk.count; ++i) {
     walk.load(i, tile, p0, p1);
     if (p0 >= 0 || p1 >= 0)
-      pair_tile<FMT, D, false>(r, sm_q, qs, tile, p0 >= 0, p1 >= 0, seen, lane);
+      pair_tile<FMT, D, false>(r, sm_q, qs, tile, p0 >= 0, p1 >= 0, seen, far, lane);
   }
 #pragma unroll
   for (int x = 0; x < 2; ++x) finish<FMT, D, DCH>(a, w, r[x], w.row0 + 16 * x, sm_m, sm_l, sm_o);
@@ -1024,7 +1069,8 @@ struct Shared {        // one tile's operands
   u32x4 k[2][D / 32][64];
   u32x4 v[D / 16][64];
   float ve[kTile];     // V's row exponent + 127; -inf: the key is missing
-  float iv[kTile];     // 2 2^-that exponent; NaN: the row holds a NaN or an infinity
+  float iv[kTile];     // 2 2^-that exponent, negative if it is far from the usual
+                       // (far_bits); NaN: the row holds a NaN or an infinity
 };
 
 // The quarter of a tile that a wave turns into operands: block t's K or V.
@@ -1073,7 +1119,10 @@ struct Quarter {
       }
       if (g == 0) {
         float ve = 0.0f, iv = 1.0f;
-        if constexpr (FMT != QL_KV_BF16) ve = static_cast<float>(mine), iv = power(255u - mine);
+        if constexpr (FMT != QL_KV_BF16) {
+          ve = static_cast<float>(mine), iv = power(255u - mine);
+          iv = far_bits(mine) & 0xC0u ? -iv : iv;
+        }
         sh.ve[16 * t + n] = n < keys ? ve : -__builtin_inff();
         sh.iv[16 * t + n] = n >= keys ? 0.0f : bad ? __builtin_nanf("") : iv;
       }
@@ -1083,7 +1132,7 @@ struct Quarter {
 
 template <int FMT, int D, bool MASKED>
 __device__ __forceinline__ void wide_tile(Rows<D>& r, const u32x4 (&q)[D / 32], float qs,
-                                          const Shared<FMT, D>& sh, uint32_t seen, int lane) {
+                                          const Shared<FMT, D>& sh, uint32_t seen, bool& far, int lane) {
   const int g = lane >> 4;
   f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
@@ -1103,8 +1152,14 @@ __device__ __forceinline__ void wide_tile(Rows<D>& r, const u32x4 (&q)[D / 32], 
       iv[4 * t + k] = b[k];
     }
   }
+  if constexpr (FMT != QL_KV_BF16) {
+    uint32_t signs = 0;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) signs |= __float_as_uint(iv[x]);
+    far = far || __any(int(signs) < 0);
+  }
   u32x4 p, p_lo;
-  softmax_step<FMT, D, MASKED, true>(r, z, iv, seen, p, p_lo);
+  softmax_step<FMT, D, MASKED, true>(r, z, iv, far, seen, p, p_lo);
 #pragma unroll
   for (int d = 0; d < D / 16; ++d) {
     r.o[d] = weigh<FMT>(sh.v[d][lane], p, p_lo, r.o[d]);
@@ -1135,6 +1190,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAtt
   load_query<FMT, D, false>(a, w, row0 + n, g, q, qs, rm);
   Rows<D> r;
   r.clear();
+  bool far = false;
 
   // The tiles in the order they are taken: the last ones, of which some key is
   // hidden from some row, before those that every row sees.
@@ -1190,13 +1246,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAtt
     if (active) {
       const uint32_t seen = visible(rm, a.tree != nullptr, tile_of(i) * kTile, w.sq.ctx, g);
       in_order();
-      wide_tile<FMT, D, true>(r, q, qs, sh[y], seen, lane);
+      wide_tile<FMT, D, true>(r, q, qs, sh[y], seen, far, lane);
     }
     __syncthreads();
   };
   auto open_tile = [&](int i, int y) {
     prepare(i + 1, (y + 1) % P);
-    if (active) wide_tile<FMT, D, false>(r, q, qs, sh[y], 0, lane);
+    if (active) wide_tile<FMT, D, false>(r, q, qs, sh[y], 0, far, lane);
     __syncthreads();
   };
   int i = 0;
@@ -1263,8 +1319,8 @@ __global__ __launch_bounds__(256) void kv_attention_join_kernel(KvAttnArgs a, in
     for (int off = 1; off < kLanes; off *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, off, 64));
     for (int s = part; s < nsplit; s += parts) {
       const int64_t at = s * step + row;
-      const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - top);
-      l = __builtin_fmaf(a.part_ml[2 * at + 1], f, l);
+      const float h = __builtin_amdgcn_exp2f(0.5f * (a.part_ml[2 * at] - top)), f = h * h;
+      l = __builtin_fmaf(a.part_ml[2 * at + 1] * h, h, l);     // in two steps, as in softmax_step
       v += *reinterpret_cast<const f32x4*>(a.part_o + at * D + 4 * lane) * f;
     }
   }

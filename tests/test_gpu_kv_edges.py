@@ -133,3 +133,42 @@ def test_norms_of_zero_and_infinite_rows(fmt):
             assert bad == (list(range(16)) if fmt == "nvfp4" and got.data_ptr() == k.data_ptr() else [5])
             assert not got[0].nan_to_num().any()
             assert torch.isnan(got[1:]).all() if eps == 0 else not got[1:].any()
+
+
+@pytest.mark.parametrize("fmt,d", FD)
+@pytest.mark.parametrize("nodes", [1, 20, 70])
+@pytest.mark.parametrize("far", ["anywhere", "by tile", "by part"])
+def test_value_rows_up_to_the_formats_ends(fmt, d, nodes, far):
+    """V rows 2^190 apart, in any order, in tiles of one wave or in parts of their
+    own: the small rows' weights stay in the sum of weights."""
+    q = require_gpu()
+    say("rows far apart", fmt, d, nodes, far)
+    lens = [nodes + 40, nodes + 1500]
+
+    def size(which, b, n):
+        if which == "k":
+            return np.ones(n)
+        at = np.arange(n)
+        big = {"anywhere": np.random.default_rng([6, b]).random(n) < 0.5,
+               "by tile": at // 32 % 2 == 0, "by part": at < n // 2}[far]
+        return 2.0 ** np.where(big, 95.0, -95.0)
+    b = Batch(FMTS[fmt], lens, [nodes] * 2, 4, 2, d, 32, seed=61, scale_rows=size)
+    b.check(b.run(q))
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("nodes", [1, 20])
+def test_a_large_row_of_little_weight(fmt, nodes):
+    """The largest V row has 2^-90 of the weight: the others give the result."""
+    q = require_gpu()
+    say("large row of little weight", fmt, nodes)
+    lens = [nodes + 90]
+    b = Batch(FMTS[fmt], lens, [nodes], 2, 1, 64, 16, seed=62,
+              scale_rows=lambda which, s, n: 2.0 ** np.where((np.arange(n) == 40) & (which == "v"), 60.0, -60.0)
+              if which == "v" else np.ones(n))
+    # one query direction: the large row's key lies against it
+    b.q[:] = np.float32(0.5)
+    k = rows(63, lens[0], 1, 64) * np.float32(0.05)
+    k[40] = -2.0
+    b.c.write("k", k, b.slots(0, np.arange(lens[0])))
+    b.check(b.run(q, scale=1.0), scale=1.0)
