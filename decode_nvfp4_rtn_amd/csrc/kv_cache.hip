@@ -170,14 +170,16 @@ struct EncRow {
 
 // Row exponent for a row of maximum amax (a bit pattern of a non-negative
 // float): the smallest e with amax <= Q 2^e, Q = 448 = 1.75 * 2^8 or
-// 2688 = 1.3125 * 2^11, as e + 127.
+// 2688 = 1.3125 * 2^11, as e + 127; at least kKvExpMin, which rows of zeros take
+// (with an e of 0 their weight in an attention would be that of rows that large,
+// and small rows beside them would lose their bits).
 template <int FMT>
 __device__ __forceinline__ uint32_t row_exponent(float amax) {
   const uint32_t u = __float_as_uint(amax), m = u & 0x7FFFFFu;
   constexpr int shift = FMT == QL_KV_E4M3 ? 8 : 11;
   constexpr uint32_t top = FMT == QL_KV_E4M3 ? 0x600000u : 0x280000u;
   const int b = int(u >> 23) - shift + (m > top ? 1 : 0);
-  return u == 0 ? 127u : uint32_t(b < kKvExpMin ? kKvExpMin : b);
+  return uint32_t(b < kKvExpMin ? kKvExpMin : b);
 }
 
 // A value in binary32 that rounds on to fewer bits as v itself does: where it

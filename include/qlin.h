@@ -417,7 +417,7 @@ int gemm_w4a16_sp24_ws(const void *x_bf16, const void *w_packed, int64_t m,
  * Formats of one row (the K or V vector of one token and head):
  *   QL_KV_BF16   the values, rounded to nearest even
  *   QL_KV_E4M3   E4M3 codes of x / 2^e; e is the smallest integer >= -100 with
- *                max|x| <= 448 * 2^e (0 for a row of zeros)
+ *                max|x| <= 448 * 2^e (-100 for a row of zeros)
  *   QL_KV_NVFP4  as quantize_nvfp4 with the row's own tensor scale 2^e: groups
  *                of 16, s_g = E4M3(max|x_g| / 2^e / 6), code =
  *                E2M1(x / 2^e * (1 / s_g)), each binary32 step rounded once;

@@ -12,7 +12,7 @@ scale.
 
 Steps for a row x of d values, binary32 (keys that were just normed: binary64),
 each rounded once to binary32:
-  e = the smallest integer >= -100 with max|x| <= Q 2^e, 0 for a row of zeros;
+  e = the smallest integer >= -100 with max|x| <= Q 2^e, -100 for a row of zeros;
       Q = 448 (E4M3) or 2688 = 6 * 448 (NVFP4); stored as the byte e + 127
   E4M3:  code = E4M3(x 2^-e)
   NVFP4: s_g = E4M3(rn32(max|x_g| 2^-e / 6)); code = E2M1(rn32(x 2^-e rn32(1 / s_g))),
@@ -38,7 +38,8 @@ def scale_bytes(fmt, d):
 
 
 def row_exponent(amax, top):
-    """The exponent e of rows of the given maxima (float64 array)."""
+    """The exponent e of rows of the given maxima (float64 array); 0 where there
+    is nothing to scale."""
     amax = np.asarray(amax, dtype=np.float64)
     e = np.zeros(amax.shape, dtype=np.int64)
     for i, a in np.ndenumerate(amax):
@@ -80,7 +81,8 @@ def quantize(fmt, x):
         bits = rn_bf16_bits(sticky32(x))
         return dict(row=bits.view(np.uint8).reshape(n, 2 * d), scales=None, exp=None,
                     value=bf16_bits_to_f32(bits).astype(np.float64))
-    e = row_exponent(np.max(np.abs(x), axis=1), TOP[fmt])
+    amax = np.max(np.abs(x), axis=1)
+    e = np.where(amax > 0, row_exponent(amax, TOP[fmt]), E_MIN)
     y = x.astype(np.float64) * 2.0 ** -e[:, None]
     stored = (e + 127).astype(np.uint8)
     p = 2.0 ** e[:, None].astype(np.float64)

@@ -172,3 +172,42 @@ def test_a_large_row_of_little_weight(fmt, nodes):
     k[40] = -2.0
     b.c.write("k", k, b.slots(0, np.arange(lens[0])))
     b.check(b.run(q, scale=1.0), scale=1.0)
+
+
+@pytest.mark.parametrize("fmt,d", FD)
+@pytest.mark.parametrize("nodes", [1, 20, 70])
+def test_zero_rows_beside_small_ones(fmt, d, nodes):
+    """A first key whose value is zero takes nearly all of the weight; the others'
+    values are small.  What is left keeps its bits."""
+    q = require_gpu()
+    say("zero rows", fmt, d, nodes)
+    lens = [nodes + 200]
+    b = Batch(FMTS[fmt], lens, [nodes], 4, 2, d, 16, seed=71,
+              scale_rows=lambda which, s, n: np.where(np.arange(n) == 0, 0.0, 2.0 ** -20)
+              if which == "v" else np.ones(n))
+    b.q[:] = np.abs(b.q)
+    k = rows(72, lens[0], 2, d) * np.float32(2.0 ** -3)
+    k[0] = 0.75
+    at = b.slots(0, np.arange(lens[0]))
+    b.c.write("k", k, at)
+    cache, v = device_cache(q, b.c), np.zeros((1, 2, d), dtype=np.float32)
+    q.kv_append(cache, on_gpu(k[:1], False), on_gpu(v, False), _dev(at[:1], torch.int64))
+    y = q.kv_attention(cache, on_gpu(b.q), torch.from_numpy(b.cu).cuda(), _dev(lens, torch.int32),
+                       torch.from_numpy(b.table).cuda(), nodes, lens[0])
+    b.check(y)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4"])
+def test_a_row_of_zeros_takes_the_smallest_exponent(fmt):
+    q = require_gpu()
+    say("zero row bytes", fmt)
+    c = kv.Cache(FMTS[fmt], 1, 16, 1, 64)
+    x = np.zeros((2, 1, 64), dtype=np.float32)
+    x[1, 0, ::2] = -0.0
+    for which in "kv":
+        c.write(which, x, [0, 1])
+    assert c.exp["v"][0, 0] == kv.E_MIN and c.exp["k"][1, 0] == kv.E_MIN
+    cache = q.KVCache(FMTS[fmt], 1, 16, 1, 64,
+                      data=torch.zeros(c.bytes.size, dtype=torch.uint8, device="cuda"))
+    q.kv_append(cache, on_gpu(x, False), on_gpu(x, False), _dev([0, 1], torch.int64))
+    assert np.array_equal(cache.data.cpu().numpy(), c.bytes)
