@@ -211,3 +211,28 @@ def test_a_row_of_zeros_takes_the_smallest_exponent(fmt):
                       data=torch.zeros(c.bytes.size, dtype=torch.uint8, device="cuda"))
     q.kv_append(cache, on_gpu(x, False), on_gpu(x, False), _dev([0, 1], torch.int64))
     assert np.array_equal(cache.data.cpu().numpy(), c.bytes)
+
+
+@pytest.mark.parametrize("fmt,d", [("nvfp4", 128), ("nvfp4", 256), ("e4m3", 128), ("bf16", 64)])
+def test_prompt_chunks_that_fill_the_chip(fmt, d):
+    """Chunks of prompts in blocks of 64 rows (4-bit 128-wide keys take 32 where
+    the blocks of 64 would not fill a round), the last one not full, with and
+    without context; a few of the sequences against the definition."""
+    q = require_gpu()
+    n_q, n_kv, seqs = 32, 4, 24
+    nodes = [70 - (5 * i) % 13 for i in range(seqs)]
+    lens = [n + (0, 33, 130, 7)[i % 4] for i, n in enumerate(nodes)]
+    say("full chip", fmt, d)
+    row_blocks = -(-max(nodes) * (n_q // n_kv) // 64)
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    assert max(nodes) > 64 and seqs * n_kv * row_blocks > 3 * cus
+    b = Batch(FMTS[fmt], lens, nodes, n_q, n_kv, d, 32, seed=81)
+    got = b.run(q).double().cpu().numpy()
+    assert np.all(np.isfinite(got))
+    for s in (0, 2, 13, 23):
+        t = slice(b.cu[s], b.cu[s + 1])
+        one = Batch.__new__(Batch)
+        one.__dict__.update(b.__dict__, lens=[lens[s]], nodes=[nodes[s]], table=b.table[s:s + 1],
+                            q=b.q[t], cu=np.array([0, nodes[s]], dtype=np.int32))
+        want, bound = one.reference()
+        assert np.all(np.abs(got[t] - want) <= bound)
