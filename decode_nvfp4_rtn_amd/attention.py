@@ -7,11 +7,12 @@ of its tokens are settled, and the integer arrays that the calls of a step take.
 
     qkv projection -> qkv_norm_rope_append -> kv_attention -> output projection
 
-with NVFP4 W4A4 projections for a prompt and INT4 weight-only ones for a few
-tokens, as the pages split a model between prefill and decode (Disaggregated
+with NVFP4 W4A4 projections for prompts and INT4 weight-only ones for decoding,
+as the pages split a model between prefill and decode (Disaggregated
 Quantization).  A step's new tokens are a chain (a chunk of a prompt, one token
 of decoding) or, for speculative decoding, a tree of drafts of which ``commit``
-keeps a path.  Every kernel is the library's; this module holds the weights,
+keeps a path.  Which weights a sequence's tokens meet goes by what they are, not
+by how many sequences share the step.  Every kernel is the library's; this module holds the weights,
 the cache and the order of the calls.
 """
 
@@ -22,14 +23,15 @@ import torch
 
 from . import qlin
 
-DECODE_TOKENS = 32      # the W4A16 projections are tuned up to here
+DECODE_TOKENS = 32      # rows up to which ``project`` takes INT4 weights if not told
 
 
 @dataclass
 class Step:
     """One step's arrays: new tokens per sequence, and on the device where they
     start, the lengths with them, the pages, each token's slot and position and
-    (a tree) which drafts it sees."""
+    (a tree) which drafts it sees.  prompt: for each sequence, whether its new
+    tokens are of its prompt (None: not said)."""
     nodes: list
     max_kv: int
     cu_q: torch.Tensor
@@ -38,6 +40,7 @@ class Step:
     slots: torch.Tensor
     positions: torch.Tensor
     tree: torch.Tensor
+    prompt: list = None
 
 
 class PagedSequences:
@@ -60,14 +63,20 @@ class PagedSequences:
         self.unused += reversed(self.pages.pop(s))
         del self.lens[s]
 
-    def step(self, seqs, nodes, tree=None):
+    def step(self, seqs, nodes, tree=None, prompt=None):
         """Room for `nodes` new tokens of each of `seqs` (distinct) and the
         step's arrays.  tree: for each sequence its drafts' ancestor masks
-        (integers, bit i of entry i set); None: chains."""
+        (integers, bit i of entry i set); None: chains.  prompt: for each
+        sequence whether these are tokens of its prompt; None: those of chains
+        that are longer than one token or begin a sequence."""
         if len(set(seqs)) != len(seqs) or len(nodes) != len(seqs) or min(nodes, default=1) < 0:
             raise ValueError("a step takes distinct sequences and a token count for each")
         if tree is not None and [len(m) for m in tree] != list(nodes):
             raise ValueError("a tree takes one mask for each new token")
+        if prompt is not None and len(prompt) != len(seqs):
+            raise ValueError("prompt takes a truth value for each sequence")
+        if prompt is None:
+            prompt = [tree is None and (n > 1 or self.lens[s] == 0) for s, n in zip(seqs, nodes)]
         total = [self.lens[s] + n for s, n in zip(seqs, nodes)]
         need = [max(0, -(-t // self.page_size) - len(self.pages[s])) for s, t in zip(seqs, total)]
         if sum(need) > len(self.unused):
@@ -94,7 +103,8 @@ class PagedSequences:
                     dev(np.concatenate([[0], np.cumsum(nodes)]), np.int32), dev(total, np.int32),
                     dev(table, np.int32), dev(np.concatenate(slots or [[]]), np.int64),
                     dev(np.concatenate(positions or [[]]), np.int32),
-                    None if tree is None else dev(np.array(masks, dtype=np.int64), np.int64))
+                    None if tree is None else dev(np.array(masks, dtype=np.int64), np.int64),
+                    [bool(p) for p in prompt])
 
     def settle(self, seqs, counts):
         """`counts` of the last step's tokens now belong to each sequence."""
@@ -111,8 +121,8 @@ def rope_table(max_pos, rot, base=10000.0, device="cuda"):
 
 class PagedAttention:
     """One layer.  wqkv fp32 [(n_q + 2 n_kv) * head_dim, hidden] and wo fp32
-    [hidden, n_q * head_dim] on the GPU are quantized to INT4 group-128 (steps
-    of up to 32 tokens) and NVFP4 (longer ones); rope as
+    [hidden, n_q * head_dim] on the GPU are quantized to INT4 group-128 (for
+    decoding) and NVFP4 (for prompts); rope as
     qlin.qkv_norm_rope_append takes it, q_weight and k_weight fp32 [head_dim]
     or None."""
 
@@ -132,23 +142,46 @@ class PagedAttention:
             many = qlin.repack_weights(qlin.QL_NVFP4, n, k, *qlin.quantize_nvfp4(w))
             self.weights.append((few, many, n, k))
 
-    def project(self, x, which):
+    def project(self, x, which, prompt=None, y=None):
+        """Projection `which` (0 qkv, 1 output) of x's rows: of a prompt (NVFP4
+        weights and activations, these under one tensor scale for all rows of
+        the call) or of decoding (INT4 weights).  Not told: by their number."""
         few, many, n, k = self.weights[which]
-        if x.shape[0] <= DECODE_TOKENS:
-            return qlin.gemm_w4a16(x, few, n, k)
-        return qlin.quantize_gemm_w4a4(x, many, n, out_dtype=torch.bfloat16)[0]
+        if x.shape[0] > DECODE_TOKENS if prompt is None else prompt:
+            return qlin.quantize_gemm_w4a4(x, many, n, y, out_dtype=torch.bfloat16)[0]
+        return qlin.gemm_w4a16(x, few, n, k, y)
+
+    def project_step(self, x, which, step):
+        """The same for a step's rows, each by its sequence's kind: one call for
+        every run of sequences of one kind."""
+        if step.prompt is None:
+            return self.project(x, which)
+        runs = []                                # [of a prompt, rows]
+        for p, n in zip(step.prompt, step.nodes):
+            if n and runs and runs[-1][0] == p:
+                runs[-1][1] += n
+            elif n:
+                runs.append([p, n])
+        if len(runs) < 2:
+            return self.project(x, which, runs[0][0] if runs else False)
+        y = torch.empty((x.shape[0], self.weights[which][2]), dtype=torch.bfloat16, device=x.device)
+        at = 0
+        for p, n in runs:
+            self.project(x[at:at + n], which, p, y[at:at + n])
+            at += n
+        return y
 
     def forward(self, x, step):
         """x bf16 [tokens, hidden], the step's new tokens sequence after
         sequence -> the layer's output [tokens, hidden].  Their keys and values
         are in the cache afterwards."""
-        qkv = self.project(x, 0)
+        qkv = self.project_step(x, 0, step)
         q = qlin.qkv_norm_rope_append(self.cache, qkv, self.n_q, step.slots, step.positions,
                                       self.rope, self.q_weight, self.k_weight, self.eps,
                                       self.interleaved)
         y = qlin.kv_attention(self.cache, q, step.cu_q, step.kv_lens, step.block_table,
                               max(step.nodes, default=0), step.max_kv, tree=step.tree)
-        return self.project(y.flatten(1), 1)
+        return self.project_step(y.flatten(1), 1, step)
 
     def commit(self, step, path):
         """After a tree's verification: path int32 [sequences, depth] on the
