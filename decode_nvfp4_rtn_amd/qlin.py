@@ -450,7 +450,8 @@ class KVCache:
     """One layer's paged cache of keys and values: a uint8 GPU tensor ``data``
     and what it holds.  fmt: QL_KV_BF16, QL_KV_E4M3 or QL_KV_NVFP4; page_size a
     power of two of 16..4096; head_dim 64, 128 or 256.  ``data`` is allocated
-    when not given and needs no initialisation."""
+    when not given and needs no initialisation.  The calls take its address as
+    it is here: the attributes cannot be assigned again."""
 
     def __init__(self, fmt, n_pages, page_size, n_kv, head_dim, data=None, device=None):
         nbytes = _lib.kv_cache_bytes(fmt, n_pages, page_size, n_kv, head_dim)
@@ -460,11 +461,15 @@ class KVCache:
         if data is None:
             data = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
         _bytes(data, "data", nbytes, torch.uint8)
-        self.fmt, self.n_pages, self.page_size = fmt, n_pages, page_size
-        self.n_kv, self.head_dim, self.data, self.device = n_kv, head_dim, data, data.device
-        self._struct = _KVStruct(fmt, n_kv, head_dim, page_size, n_pages, data.data_ptr(),
-                                 data.numel())
-        self._ref = ctypes.byref(self._struct)
+        struct = _KVStruct(fmt, n_kv, head_dim, page_size, n_pages, data.data_ptr(), data.numel())
+        self.__dict__.update(fmt=fmt, n_pages=n_pages, page_size=page_size, n_kv=n_kv,
+                             head_dim=head_dim, data=data, device=data.device, _struct=struct,
+                             _ref=ctypes.byref(struct))
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"KVCache.{name} is fixed: make another KVCache")
+        super().__setattr__(name, value)
 
 
 # The calls below are a few microseconds of GPU work each at decode sizes, so

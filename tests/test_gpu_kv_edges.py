@@ -236,3 +236,16 @@ def test_prompt_chunks_that_fill_the_chip(fmt, d):
                             q=b.q[t], cu=np.array([0, nodes[s]], dtype=np.int32))
         want, bound = one.reference()
         assert np.all(np.abs(got[t] - want) <= bound)
+
+
+def test_a_caches_buffer_is_fixed():
+    """The calls take the buffer that the cache was made with: another one cannot
+    be put in its place unnoticed."""
+    q = require_gpu()
+    say("cache buffer")
+    cache = q.KVCache(q.QL_KV_E4M3, 2, 16, 2, 64)
+    with pytest.raises(AttributeError):
+        cache.data = torch.zeros_like(cache.data)
+    for name in ("fmt", "n_pages", "page_size", "n_kv", "head_dim", "device"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name))
