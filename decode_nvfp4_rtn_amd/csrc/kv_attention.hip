@@ -462,6 +462,8 @@ __device__ __forceinline__ Work work_of(const KvAttnArgs& a) {
   }
   return w;
 }
+// Tiles that hold `keys` keys (up to 2^31 - 16 of them).
+__device__ __forceinline__ int tiles_of(int keys) { return int((uint32_t(keys) + kTile - 1) / kTile); }
 // Positions that every row from `row0` on sees.
 __device__ __forceinline__ int open_to(const KvAttnArgs& a, const Work& w, int row0) {
   const int o = a.tree ? w.sq.ctx : w.sq.ctx + row0 / w.group + 1;
@@ -770,7 +772,7 @@ struct Walk {
   __device__ __forceinline__ Walk(const KvAttnArgs& args, const Work& work, int wave, int ln)
       : a(args), w(work), lane(ln) {
     first = w.k0 / kTile + wave;
-    const int tiles = (w.k1 + kTile - 1) / kTile;
+    const int tiles = tiles_of(w.k1);
     count = tiles > first ? (tiles - first + kWaves - 1) / kWaves : 0;
     const int open = open_to(a, w, w.row0) / kTile;
     partly = count - (open > first ? (open - first + kWaves - 1) / kWaves : 0);
@@ -1194,7 +1196,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAtt
 
   // The tiles in the order they are taken: the last ones, of which some key is
   // hidden from some row, before those that every row sees.
-  const int first = w.k0 / kTile, tiles = (w.k1 + kTile - 1) / kTile;
+  const int first = w.k0 / kTile, tiles = tiles_of(w.k1);
   const int open = open_to(a, w, w.row0) / kTile;
   const int count = tiles > first ? tiles - first : 0;
   int partly = open > first ? tiles - open : count;

@@ -249,3 +249,21 @@ def test_a_caches_buffer_is_fixed():
     for name in ("fmt", "n_pages", "page_size", "n_kv", "head_dim", "device"):
         with pytest.raises(AttributeError):
             setattr(cache, name, getattr(cache, name))
+
+
+@pytest.mark.parametrize("n_q,d", [(1, 64), (33, 64), (33, 256)])
+def test_the_longest_length(n_q, d):
+    """2^31 - 16 positions, of which only the first and the last page are there."""
+    q = require_gpu()
+    say("longest", n_q, d)
+    cols = (2 ** 31 - 1) // 16
+    cache = q.KVCache(q.QL_KV_E4M3, 2, 16, 1, d)
+    k, v = on_gpu(rows(91, 32, 1, d)), on_gpu(rows(92, 32, 1, d))
+    q.kv_append(cache, k, v, torch.arange(32, device="cuda"))
+    k, v = (t[:, 0].double() for t in q.kv_gather(cache, torch.arange(32, device="cuda"), out_dtype=torch.float32))
+    table = torch.full((1, cols), -1, dtype=torch.int32, device="cuda")
+    table[0, 0], table[0, -1] = 0, 1
+    x = on_gpu(rows(93, 1, n_q, d))
+    y = q.kv_attention(cache, x, _dev([0, 1], torch.int32), _dev([16 * cols], torch.int32), table, 1, 2 ** 30)
+    want = torch.softmax(x[0].double() @ k.T * d ** -0.5, 1) @ v
+    assert torch.allclose(y[0].double(), want, rtol=2.0 ** -7, atol=2.0 ** -7)
