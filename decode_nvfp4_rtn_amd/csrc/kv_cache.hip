@@ -816,14 +816,36 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(KvGeom g, const int32_t*
 
 }  // namespace
 
+// A grid has less than 2^32 threads along x, so more tokens than this take
+// several launches: calls launch(first, count).
+template <typename F>
+static hipError_t by_launch(int64_t tokens, F&& launch) {
+  constexpr int64_t most = int64_t(1) << 25;
+  for (int64_t t = 0; t < tokens; t += most) {
+    launch(t, tokens - t < most ? tokens - t : most);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+// `rows` rows on from p.
+static const void* ahead(const void* p, int64_t rows, int64_t stride, int dtype) {
+  return static_cast<const uint8_t*>(p) + rows * stride * (dtype == QL_F32 ? 4 : 2);
+}
+static void* ahead(void* p, int64_t rows, int64_t stride, int dtype) {
+  return static_cast<uint8_t*>(p) + rows * stride * (dtype == QL_F32 ? 4 : 2);
+}
+
 hipError_t launch_kv_append(const KvGeom& g, int fmt, int d, const void* k, const void* v,
                             int x_dtype, int64_t tokens, int64_t k_stride, int64_t v_stride,
                             const int64_t* slots, hipStream_t s) {
-  const dim3 grid(quads(tokens), unsigned((2 * g.n_kv + kWaves - 1) / kWaves));
   return kv_dispatch(fmt, d, [&](auto f, auto n) {
-    kv_append_kernel<decltype(f)::value, decltype(n)::value><<<grid, 64 * kWaves, 0, s>>>(
-        g, k, v, x_dtype == QL_F32, tokens, k_stride, v_stride, slots);
-    return hipGetLastError();
+    return by_launch(tokens, [&](int64_t t, int64_t count) {
+      const dim3 grid(quads(count), unsigned((2 * g.n_kv + kWaves - 1) / kWaves));
+      kv_append_kernel<decltype(f)::value, decltype(n)::value><<<grid, 64 * kWaves, 0, s>>>(
+          g, ahead(k, t, k_stride, x_dtype), ahead(v, t, v_stride, x_dtype), x_dtype == QL_F32,
+          count, k_stride, v_stride, slots + t);
+    });
   });
 }
 
@@ -841,33 +863,37 @@ hipError_t launch_qkv_norm_rope_append(const KvGeom& g, int fmt, int d, const vo
   const int64_t waves = (tokens + 3) / 4 * heads, full = d == 256 ? 4096 : 8192;
   const int most = (heads + kWaves - 1) / kWaves;
   const int hpw = waves <= full ? 1 : waves / full < most ? int(waves / full) : most;
-  const NormArgs a{g, qkv, tokens, row_stride, n_q, hpw, q_weight,
-                   k_weight, eps, positions, rope, max_pos, rot, q_out, slots};
-  const dim3 grid(quads(tokens), unsigned((heads + kWaves * hpw - 1) / (kWaves * hpw)));
   return kv_dispatch(fmt, d, [&](auto f, auto n) {
     constexpr int FMT = decltype(f)::value, D = decltype(n)::value;
     auto go = [&](auto rot_c, auto f32_c) {
-      qkv_norm_rope_append_kernel<FMT, D, decltype(rot_c)::value, decltype(f32_c)::value>
-          <<<grid, 64 * kWaves, 0, s>>>(a);
+      return by_launch(tokens, [&](int64_t t, int64_t count) {
+        const NormArgs a{g, ahead(qkv, t, row_stride, x_dtype), count, row_stride, n_q, hpw,
+                         q_weight, k_weight, eps, positions ? positions + t : nullptr, rope,
+                         max_pos, rot, ahead(q_out, t, int64_t(n_q) * d, QL_BF16), slots + t};
+        const dim3 grid(quads(count), unsigned((heads + kWaves * hpw - 1) / (kWaves * hpw)));
+        qkv_norm_rope_append_kernel<FMT, D, decltype(rot_c)::value, decltype(f32_c)::value>
+            <<<grid, 64 * kWaves, 0, s>>>(a);
+      });
     };
     auto by_type = [&](auto rot_c) {
-      if (x_dtype == QL_F32) go(rot_c, std::true_type{});
-      else go(rot_c, std::false_type{});
+      return x_dtype == QL_F32 ? go(rot_c, std::true_type{}) : go(rot_c, std::false_type{});
     };
-    if (interleaved) by_type(std::integral_constant<int, kRotPairs>{});
-    else if (rot == D) by_type(std::integral_constant<int, kRotWhole>{});
-    else by_type(std::integral_constant<int, kRotPart>{});
-    return hipGetLastError();
+    return interleaved ? by_type(std::integral_constant<int, kRotPairs>{})
+           : rot == D  ? by_type(std::integral_constant<int, kRotWhole>{})
+                       : by_type(std::integral_constant<int, kRotPart>{});
   });
 }
 
 hipError_t launch_kv_gather(const KvGeom& g, int fmt, int d, const int64_t* slots, int64_t tokens,
                             void* k, void* v, int y_dtype, hipStream_t s) {
-  const dim3 grid(unsigned((tokens + 3) / 4), unsigned((2 * g.n_kv + kWaves - 1) / kWaves));
+  const int64_t row = int64_t(g.n_kv) * d;
   return kv_dispatch(fmt, d, [&](auto f, auto n) {
-    kv_gather_kernel<decltype(f)::value, decltype(n)::value><<<grid, 64 * kWaves, 0, s>>>(
-        g, slots, tokens, k, v, y_dtype == QL_F32);
-    return hipGetLastError();
+    return by_launch(tokens, [&](int64_t t, int64_t count) {
+      const dim3 grid(unsigned((count + 3) / 4), unsigned((2 * g.n_kv + kWaves - 1) / kWaves));
+      kv_gather_kernel<decltype(f)::value, decltype(n)::value><<<grid, 64 * kWaves, 0, s>>>(
+          g, slots + t, count, ahead(k, t, row, y_dtype), ahead(v, t, row, y_dtype),
+          y_dtype == QL_F32);
+    });
   });
 }
 

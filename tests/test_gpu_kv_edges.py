@@ -267,3 +267,36 @@ def test_the_longest_length(n_q, d):
     y = q.kv_attention(cache, x, _dev([0, 1], torch.int32), _dev([16 * cols], torch.int32), table, 1, 2 ** 30)
     want = torch.softmax(x[0].double() @ k.T * d ** -0.5, 1) @ v
     assert torch.allclose(y[0].double(), want, rtol=2.0 ** -7, atol=2.0 ** -7)
+
+
+def test_tokens_past_a_grids_rows():
+    """More tokens than one launch's grid holds: their last rows are written, normed
+    and read back like the first."""
+    q = require_gpu()
+    say("many tokens")
+    d, tokens = 64, (1 << 26) + 70
+    cache = q.KVCache(q.QL_KV_E4M3, 8, 16, 1, d)
+    slots = torch.full((tokens,), -1, dtype=torch.int64, device="cuda")
+    some = torch.tensor([0, 5, (1 << 26) - 9, (1 << 26) - 1, 1 << 26, tokens - 1], device="cuda")
+    slots[some] = torch.arange(6, device="cuda") * 3
+    k = torch.empty((tokens, 1, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    k[some], v[some] = on_gpu(rows(95, 6, 1, d)), on_gpu(rows(96, 6, 1, d))
+    q.kv_append(cache, k, v, slots)
+    few = q.KVCache(q.QL_KV_E4M3, 8, 16, 1, d)
+    q.kv_append(few, k[some], v[some], slots[some])
+    want = q.kv_gather(few, slots[some])
+    got = q.kv_gather(cache, slots[some])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    q.kv_gather(cache, slots, k=k, v=v)
+    assert torch.equal(k[some], want[0]) and torch.equal(v[some], want[1])
+    others = torch.ones(tokens, dtype=torch.bool, device="cuda")
+    others[some] = False
+    assert not k[others].any() and not v[others].any()
+    del k, v, others
+    qkv = torch.empty((tokens, 3 * d), dtype=torch.bfloat16, device="cuda")
+    qkv[some] = on_gpu(rows(97, 6, 3, d)).flatten(1)
+    out = q.qkv_norm_rope_append(cache, qkv, 1, slots)
+    assert torch.equal(out[some], q.qkv_norm_rope_append(few, qkv[some], 1, slots[some]))
+    got, want = q.kv_gather(cache, slots[some]), q.kv_gather(few, slots[some])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
