@@ -407,7 +407,7 @@ __device__ __forceinline__ Part part_of(const KvAttnArgs& a, int u) {
       const uint32_t v = __shfl_up(upto, off, 64);
       if (lane >= off) upto += v;
     }
-    if (blockIdx.x == 0 && threadIdx.x < 64 && b0 + lane < a.n_seqs) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 64 && b0 + lane < a.n_seqs) {
       a.first[b0 + lane] = int(before + upto - n);
       if (b0 + lane == a.n_seqs - 1) a.first[a.n_seqs] = int(before + upto);
     }
@@ -437,8 +437,9 @@ struct Work {
 template <int ROWS>
 __device__ __forceinline__ Work work_of(const KvAttnArgs& a) {
   Work w;
-  const int slot = int(blockIdx.x >> 3);
-  int unit = slot / a.row_blocks * 8 + int(blockIdx.x & 7);
+  const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x;
+  const int slot = int(id >> 3);
+  int unit = slot / a.row_blocks * 8 + int(id & 7);
   w.row0 = slot % a.row_blocks * ROWS;
   w.any = unit < a.units;
   if (!w.any) return w;
@@ -1403,7 +1404,7 @@ size_t kv_attention_ws_bytes(const KvAttnPlan& p, int64_t n_seqs, int64_t max_q,
 }
 
 template <int FMT, int D>
-static hipError_t launch_wide(const KvAttnArgs& a, unsigned blocks, hipStream_t s) {
+static hipError_t launch_wide(const KvAttnArgs& a, dim3 blocks, hipStream_t s) {
   constexpr int bytes = 2 * sizeof(Shared<FMT, D>);
   if constexpr (bytes > 64 * 1024) {
     static std::atomic<int> done[64];
@@ -1419,7 +1420,10 @@ hipError_t launch_kv_attention(int fmt, int d, const KvAttnPlan& p, KvAttnArgs a
   const int64_t units = p.parts * a.g.n_kv;
   a.units = int(units);
   a.row_blocks = int(p.row_blocks);
-  const unsigned blocks = unsigned((units + 7) / 8 * 8 * p.row_blocks);
+  // up to 2^30 (api_kv.cpp), while a grid has less than 2^32 threads along x; x is
+  // a multiple of 8, so that a block's number tells its XCD
+  const unsigned all = unsigned((units + 7) / 8 * 8 * p.row_blocks), most = 1u << 23;
+  const dim3 blocks(all < most ? all : most, (all + most - 1) / most);
   const hipError_t e = kv_dispatch(fmt, d, [&](auto f, auto n) {
     constexpr int FMT = decltype(f)::value, D = decltype(n)::value;
     if constexpr (wide_fits(FMT, D)) {

@@ -300,3 +300,23 @@ def test_tokens_past_a_grids_rows():
     assert torch.equal(out[some], q.qkv_norm_rope_append(few, qkv[some], 1, slots[some]))
     got, want = q.kv_gather(cache, slots[some]), q.kv_gather(few, slots[some])
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_more_blocks_than_a_grids_row(d):
+    """Many sequences under a max_q that is far above their token counts, as one
+    long chunk among them makes it: 2^24 thread blocks and more."""
+    q = require_gpu()
+    say("many blocks", d)
+    seqs, n_q = 515, 32
+    lens = [1 + (7 * i) % 40 for i in range(seqs)]
+    b = Batch(kv.E4M3, lens, [1] * seqs, n_q, 1, d, 16, seed=99)
+    most = 32768 if d == 64 else 65536
+    x = torch.zeros((most, n_q, d), dtype=torch.bfloat16, device="cuda")
+    x[:seqs] = on_gpu(b.q)
+    y = torch.zeros_like(x)
+    assert -(-most * n_q // (32 if d == 64 else 64)) * seqs > 1 << 24
+    q.kv_attention(device_cache(q, b.c), x, torch.from_numpy(b.cu).cuda(), _dev(lens, torch.int32),
+                   torch.from_numpy(b.table).cuda(), most, max(lens), y=y)
+    b.check(y[:seqs])
+    assert not y[seqs:].any()
