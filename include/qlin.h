@@ -544,8 +544,11 @@ int qkv_norm_rope_append(const ql_kv_cache *cache, const void *qkv, int x_dtype,
  *   y = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale q.k_p - max_p scale q.k_p)
  * A query that sees nothing gives zeros.  Rows that no query of a sequence
  * sees do not matter, whatever they hold; a NaN or infinity in a row hidden
- * from one query does not reach it.  One that a query sees makes its result
- * NaN in that element at least, and possibly in all.
+ * from one query does not reach it.  A NaN that a query sees makes its result
+ * NaN, in V's element at least and possibly in all.  An infinity that it sees
+ * in V makes the result infinite or NaN likewise; in a quantized cache it counts
+ * as its code's value, 1.75 2^128 (QL_KV_E4M3) or 1.3125 2^128, times its
+ * weight.  One in K gives an infinite score: a result of NaN, or no weight.
  *
  * Sums are binary32.  Keys, values and queries enter exactly (queries over
  * QL_KV_NVFP4 rounded to a multiple of 2^-38 of their row's largest value).

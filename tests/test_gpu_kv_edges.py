@@ -320,3 +320,39 @@ def test_more_blocks_than_a_grids_row(d):
                    torch.from_numpy(b.table).cuda(), most, max(lens), y=y)
     b.check(y[:seqs])
     assert not y[seqs:].any()
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("keys", [2, 64])
+def test_infinities_that_are_seen(fmt, keys):
+    """In V: infinite or NaN, or the value of the largest code; in K: a score of
+    that sign."""
+    q = require_gpu()
+    say("infinities", fmt, keys)
+    d = 64
+    cache = q.KVCache(FMTS[fmt], 4, 16, 1, d)
+    k = np.zeros((keys, 1, d), dtype=np.float32)
+    v = np.ones((keys, 1, d), dtype=np.float32)
+    v[0, 0, 3] = np.inf
+    slots = torch.arange(keys, device="cuda")
+    table, cu, lens = _dev([[0, 1, 2, 3]], torch.int32), _dev([0, 1], torch.int32), _dev([keys], torch.int32)
+
+    def run(x):
+        query = torch.full((1, 1, d), float(x), dtype=torch.bfloat16, device="cuda")
+        return q.kv_attention(cache, query, cu, lens, table, 1, keys)[0, 0].double().cpu().numpy()
+    q.kv_append(cache, on_gpu(k), on_gpu(v), slots)
+    one = q.kv_gather(cache, slots[1:2])[1][0, 0, 0].item()       # 1 in this format
+    y = run(1)
+    if fmt == "bf16":
+        assert not np.isfinite(y[3])
+        assert np.isnan(y).all() or (np.delete(y, 3) == 1).all()
+    else:
+        # the other rows' weights are far below 2^-31 of that row's times 2^e, so
+        # of the other elements nothing but their finiteness is stated
+        assert y[3] == {"e4m3": 1.75, "nvfp4": 1.3125}[fmt] * 2.0 ** 128 / keys
+        assert np.isfinite(y).all()
+    k[0, 0, 7] = np.inf
+    v[0, 0, 3] = 5
+    q.kv_append(cache, on_gpu(k), on_gpu(v), slots)
+    assert np.isnan(run(1)).all()
+    assert (run(-1) == one).all()
