@@ -53,13 +53,11 @@ __device__ __forceinline__ float fma_of(float a, float b, float c) { return __bu
 __device__ __forceinline__ double fma_of(double a, double b, double c) { return __builtin_fma(a, b, c); }
 __device__ __forceinline__ float rsqrt_of(float v) { return __builtin_amdgcn_rsqf(v); }
 __device__ __forceinline__ double rsqrt_of(double v) {
-  // One step of Newton's method from 24 bits, for v times a power of four that
-  // brings it near 1: v itself may lie outside of binary32's range (rows of
-  // below 1e-19 with eps = 0, or above 1e19).  0 and infinity: 1 / 0 and 0.
-  const int e = __builtin_amdgcn_frexp_exp(v) & ~1;
-  const double m = __builtin_amdgcn_ldexp(v, -e);
-  const double r = __builtin_amdgcn_rsqf(static_cast<float>(m));
-  const double y = __builtin_amdgcn_ldexp(r * (1.5 - 0.5 * m * r * r), -e / 2);
+  // One step of Newton's method from the instruction's 23 bits; v may
+  // lie outside of binary32's range (rows of below 1e-19 with eps = 0, or above
+  // 1e19).  0 and infinity: infinity and 0.
+  const double r = __builtin_amdgcn_rsq(v);
+  const double y = r * (1.5 - 0.5 * v * r * r);
   return r > 0.0 && r < __builtin_inf() ? y : r;
 }
 __device__ __forceinline__ float row_max(float v) {
