@@ -23,21 +23,23 @@
 //   bound by the cache's bytes (32 sequences of 2048 to 8192 keys, 32 / 8
 //   128-wide heads, with the join: bf16 130 us, 685 MB at 5.3 TB/s; 8-bit
 //   71 us, 4.9 TB/s), at 4 bits by each wave's chain of loads, unpacking,
-//   products and softmax (51 us, 195 MB at 3.8 TB/s; the vector unit issues in
-//   43 % of the cycles).
+//   products and softmax (52 us, 195 MB at 3.8 TB/s; the vector unit issues in
+//   46 % of the cycles).
 // pair (more rows, 64- and 128-wide heads): as narrow with 32 rows, so that a
 //   tile's operands serve two products each; bound by the chain of a tile as
 //   well (16 sequences of 63 drafts over up to 2000 8-bit 128-wide keys, 32 / 8
-//   heads: 51 us).
+//   heads: 53 us; a prompt's 4096 tokens over 8-bit keys 246 us, bf16 255, of 110
+//   for the operations).
 // wide (256-wide heads, whose 32 rows do not fit the registers, and mostly more
 //   than 32 rows over 4-bit 128-wide keys, whose unpacking counts for more): four
 //   waves share each tile.  Each turns a quarter of it into matrix operands in
 //   LDS, once for all, and takes 16 rows of its own; bound by what a tile takes
 //   a wave from barrier to barrier: operands made and stored, LDS reads,
 //   products, softmax (4 sequences of 6893 to 16063 4-bit 256-wide keys, 63
-//   drafts, 15 / 5 heads: 98 us and 9 for the join, 47 GFLOP).  A wave issues
-//   45 % of that time; without the operands' making and storing the case takes
-//   76 us, without LDS reads 101, without the softmax 99.
+//   drafts, 15 / 5 heads: 109 us with the join, 47 GFLOP; a prompt's 4096 tokens
+//   over 4-bit 128-wide keys 278 us).  A wave issues 44 % of that time; when the
+//   trees took 107 us, they took 76 without the operands' making and storing, 101
+//   without LDS reads, 99 without the softmax.
 //
 // Quantized rows.  K's row scale 2^ke goes into the bf16 operand where that
 // is free (narrow, NVFP4: it multiplies the score).  V's, 2^ve, joins the
@@ -552,9 +554,8 @@ struct Rows {
 // Otherwise (far: in this tile or an earlier one of this wave) it may have any
 // share, and the terms are made from their exponents, 8 more exponentials.  They
 // are as large as 2^116 or as small as 2^-112, whatever o is: l is rescaled in
-// two steps.  (Telling the two apart costs 0 to 5 %; with all rows far the 4-bit
-// batch takes 52 us and not 48, 16 trees of 63 drafts over 8-bit keys 63 and not
-// 53.)
+// two steps.  Telling the two apart costs 0 to 5 %; with all rows far the 4-bit
+// batch takes 8 % more, 16 trees of 63 drafts over 8-bit keys 20 %.
 template <int FMT, int D, bool MASKED, bool IV>
 __device__ __forceinline__ void softmax_step(Rows<D>& r, float (&z)[8], const float (&iv)[8],
                                              bool far, uint32_t seen, u32x4& p, u32x4& p_lo) {
@@ -1172,9 +1173,10 @@ __device__ __forceinline__ void wide_tile(Rows<D>& r, const u32x4 (&q)[D / 32], 
 
 // 16 rows to a wave, and so two or three waves on a SIMD, beat 32: a tile is a
 // chain of LDS reads, products and the softmax that takes a wave more than
-// twice the cycles it issues, so it is the other waves that fill the SIMD (16
-// sequences of 63 drafts over 2000 8-bit 128-wide keys: 56 us, and 77 us with 32
-// rows to a wave; eight waves to a block: 78 us).
+// twice the cycles it issues, so it is the other waves that fill the SIMD.
+// (Measured with 8-bit 128-wide keys before those had the pair kernel, 16
+// sequences of 63 drafts over 2000 keys: 56 us, with 32 rows to a wave 77, with
+// eight waves to a block 78.)
 template <int FMT, int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_wide_kernel(KvAttnArgs a) {
   using L = KvLayout<FMT, D>;

@@ -410,7 +410,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(
 // qkv_norm_rope_append: a wave takes four tokens and a run of heads, whose
 // rotation factors times weights it makes once; 16 lanes hold a row, so the sum
 // of squares is four steps within them.  Bound by the bytes: 8192 tokens of 32
-// query and 8 key heads of 128, bf16 in, 8-bit cache: 185 MB in 44.7 us,
+// query and 8 key heads of 128, bf16 in, 8-bit cache: 185 MB in 44.5 us,
 // 4.1 TB/s; a few tokens are one launch (3.9 us).
 // --------------------------------------------------------------------------
 struct NormArgs {
