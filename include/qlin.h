@@ -552,7 +552,8 @@ int qkv_norm_rope_append(const ql_kv_cache *cache, const void *qkv, int x_dtype,
  *
  * Sums are binary32.  Keys, values and queries enter exactly (queries over
  * QL_KV_NVFP4 rounded to a multiple of 2^-38 of their row's largest value).
- * Weights are rounded to 16 bits (QL_KV_BF16), or to 11 bits, those below
+ * Weights are rounded to 16 bits (QL_KV_BF16; those below 2^-120 of the largest
+ * lose bits, below 2^-133 all of them), or to 11 bits, those below
  * 2^-21 of the largest w_p 2^e_p (e_p: the exponent of V's row) to a multiple
  * of at most 2^-31 of it.  Weights below 2^-70 of the largest, or 2^(e - 130)
  * where a V row's exponent e is above 60, may be missing from their sum.
