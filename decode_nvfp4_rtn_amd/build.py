@@ -42,6 +42,11 @@ SOURCES = {
     "api_kv.cpp": [],
     "kv_cache.hip": ["-ffp-contract=off"],
     "kv_attention.hip": [],
+    "api_rows.cpp": [],
+    "rows_plan.hip": [],
+    "moe_w4a16.hip": [],
+    "moe_w4a4.hip": [],
+    "lora.hip": [],
 }
 
 COMMON = [

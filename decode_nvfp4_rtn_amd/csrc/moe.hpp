@@ -1,0 +1,127 @@
+// Internal declarations of the linear layers whose rows choose their own
+// weights (mixtures of experts, adapters).  Not part of the public ABI.
+#pragma once
+
+#include "qlin_internal.hpp"
+
+namespace qlin {
+
+constexpr int kMostGroups = 1024;   // experts or adapters of one call
+
+// A plan: the rows of a batch in the order of the weights they meet.  order
+// [rows]: the row at each place; offsets [groups + 1]: where each group's run
+// begins.  The rows of no group come last, from offsets[groups] on.
+struct RowPlan {
+  const int32_t* order;
+  const int32_t* offsets;
+  int groups;
+  int rows;
+};
+
+// A run of at most `tall` places of one group, found from a number: the tiles
+// of group 0, of group 1, ..., then those of the rows without a group (group
+// == groups).  The search is a wave's: each lane takes a group of 64, a prefix
+// sum over the lanes gives the tiles before it.  Offsets are held to 0 ..
+// rows, so that no plan makes a kernel leave its buffers.
+struct RowTile {
+  int group;   // -1: no such tile
+  int first;   // its first place
+  int count;   // 1 .. tall
+};
+
+__device__ __forceinline__ RowTile find_tile(const RowPlan& p, int tall, int number) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int g0 = 0; g0 <= p.groups; g0 += 64) {
+    const int g = g0 + lane;
+    const uint32_t most = uint32_t(p.rows);
+    int a = 0, b = 0;
+    if (g < p.groups) {
+      a = int(min(uint32_t(p.offsets[g]), most));
+      b = int(min(uint32_t(p.offsets[g + 1]), most));
+    } else if (g == p.groups) {
+      a = int(min(uint32_t(p.offsets[g]), most));
+      b = p.rows;
+    }
+    const int tiles = b > a ? (b - a + tall - 1) / tall : 0;
+    int sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(sum, d);
+      if (lane >= d) sum += v;
+    }
+    const uint64_t past = __ballot(before + sum > number);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      const int start = before + __shfl(sum, at) - __shfl(tiles, at);
+      const int first = __shfl(a, at) + (number - start) * tall;
+      const int end = __shfl(b, at);
+      return RowTile{__builtin_amdgcn_readfirstlane(g0 + at), __builtin_amdgcn_readfirstlane(first),
+                     __builtin_amdgcn_readfirstlane(min(end - first, tall))};
+    }
+    before += __shfl(sum, 63);
+  }
+  return RowTile{-1, 0, 0};
+}
+
+// How many such tiles there are.
+__device__ __forceinline__ int count_tiles(const RowPlan& p, int tall) {
+  const int lane = threadIdx.x & 63;
+  int sum = 0;
+  for (int g = lane; g <= p.groups; g += 64) {
+    const uint32_t most = uint32_t(p.rows);
+    const int a = int(min(uint32_t(p.offsets[g]), most));
+    const int b = g < p.groups ? int(min(uint32_t(p.offsets[g + 1]), most)) : p.rows;
+    sum += b > a ? (b - a + tall - 1) / tall : 0;
+  }
+#pragma unroll
+  for (int d = 32; d; d /= 2) sum += __shfl_xor(sum, d);
+  return __builtin_amdgcn_readfirstlane(sum);
+}
+
+// The most tiles that a plan of so many rows and groups can have.
+inline int64_t most_tiles(int64_t rows, int64_t groups, int64_t tall) {
+  return rows / tall + (rows < groups + 1 ? rows : groups + 1);
+}
+
+// ---------------------------------------------------------------------------
+// Launchers: arguments are checked by the caller.
+// ---------------------------------------------------------------------------
+size_t group_rows_ws_bytes(int64_t rows, int64_t top_k, int64_t groups);
+hipError_t launch_group_rows(const int32_t* ids, int64_t rows, int groups, int32_t* order,
+                             int32_t* where, int32_t* offsets, int32_t* ws, hipStream_t s);
+hipError_t launch_moe_route(const void* logits, int dtype, int64_t tokens, int experts,
+                            int64_t stride, int top_k, bool renormalize, int32_t* ids,
+                            float* weights, int32_t* order, int32_t* where, int32_t* offsets,
+                            int32_t* ws, hipStream_t s);
+hipError_t launch_moe_combine(const void* rows, int x_dtype, const RowPlan& p, const int32_t* where,
+                              const float* weights, int64_t tokens, int top_k, int64_t n, void* out,
+                              int out_dtype, hipStream_t s);
+
+struct MoeGemm {
+  RowPlan plan;
+  int top_k;              // with gather: the place's row of x is order / top_k
+  bool gather, silu_mul;
+  const uint8_t* experts; // blobs, `blob_stride` bytes apart
+  int64_t blob_stride;
+  int n, k;
+  void* y;
+  int y_dtype;
+};
+hipError_t launch_moe_gemm_w4a16(const MoeGemm& g, const void* x, hipStream_t s);
+hipError_t launch_moe_gemm_w4a4(const MoeGemm& g, const uint8_t* codes, const uint8_t* scales,
+                                const float* a_ts, hipStream_t s);
+
+struct LoraArgs {
+  RowPlan plan;
+  const void *x, *a, *b, *y;
+  const float* scale;
+  void* out;
+  int64_t x_stride, y_stride, out_stride;
+  int rank, n, k, y_dtype;
+  float* part;            // [parts][rows][rank]
+};
+size_t lora_ws_bytes(int64_t rows, int64_t groups, int rank, int64_t k);
+hipError_t launch_lora_add(const LoraArgs& a, hipStream_t s);
+
+}  // namespace qlin

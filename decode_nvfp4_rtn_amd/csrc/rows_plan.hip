@@ -1,0 +1,409 @@
+// Which rows meet which weights: the choice of a token's experts, the plan
+// that puts rows in the order of their weights, and the sum over a token's
+// experts.
+//
+// Plan: a stable counting sort.  A block takes a run of rows and counts its
+// groups; a second launch adds up the counts of the blocks before its own
+// (every block for itself: at most 256 blocks' counts, read from L2), and
+// writes each row's place.  Within a wave a row's rank among the rows of its
+// group comes from ballots over the bits of the group's number.  One block's
+// worth of rows takes one launch.  Whole numbers only, counted by integer
+// atomics in LDS whose order does not show: the plan is the same every time.
+#include "moe.hpp"
+
+#include <cmath>
+
+namespace qlin {
+namespace {
+
+constexpr int THREADS = 512, WAVES = THREADS / 64;
+constexpr int kMostBlocks = 256;
+
+struct PlanSmem {
+  int base[kMostGroups + 1];             // next place of each group
+  __attribute__((aligned(4))) uint8_t wave_count[WAVES][kMostGroups + 1];
+  int carry[WAVES];
+};
+
+__device__ __forceinline__ int group_of(int32_t id, int groups) {
+  return uint32_t(id) < uint32_t(groups) ? id : groups;
+}
+
+// base[g] = first place of group g (an exclusive sum of count over the
+// groups); every thread of the block takes part.
+__device__ __forceinline__ void scan_groups(PlanSmem& sm, int groups) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int before = 0;
+  for (int g0 = 0; g0 <= groups; g0 += THREADS) {
+    const int g = g0 + threadIdx.x;
+    const int own = g <= groups ? sm.base[g] : 0;
+    int sum = own;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(sum, d);
+      if (lane >= d) sum += v;
+    }
+    if (lane == 63) sm.carry[wave] = sum;
+    __syncthreads();
+    int at = before;
+    for (int w = 0; w < wave; ++w) at += sm.carry[w];
+    for (int w = 0; w < WAVES; ++w) before += sm.carry[w];
+    if (g <= groups) sm.base[g] = at + sum - own;
+    __syncthreads();
+  }
+}
+
+// Places of the rows [begin, end) from base on, which moves along.
+__device__ __forceinline__ void place_rows(PlanSmem& sm, const int32_t* __restrict__ ids, int begin,
+                                           int end, int groups, int32_t* __restrict__ order,
+                                           int32_t* __restrict__ where) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int bits = 32 - __clz(groups);   // groups itself is a number too
+  for (int r0 = begin; r0 < end; r0 += THREADS) {
+    static_assert(sizeof(sm.wave_count) % 4 == 0, "cleared by words");
+    for (int i = threadIdx.x; i < int(sizeof(sm.wave_count) / 4); i += THREADS)
+      reinterpret_cast<uint32_t*>(sm.wave_count)[i] = 0;
+    __syncthreads();
+    const int row = r0 + threadIdx.x;
+    const bool live = row < end;
+    const int g = live ? group_of(ids[row], groups) : 0;
+    uint64_t same = __ballot(live);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot((g >> b) & 1);
+      same &= (g >> b) & 1 ? set : ~set;
+    }
+    const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+    if (live && rank == 0) sm.wave_count[wave][g] = uint8_t(__popcll(same));
+    __syncthreads();
+    if (live) {
+      int at = sm.base[g] + rank;
+      for (int w = 0; w < wave; ++w) at += sm.wave_count[w][g];
+      order[at] = row;
+      where[row] = at;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i <= groups; i += THREADS) {
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) sum += sm.wave_count[w][i];
+      sm.base[i] += sum;
+    }
+    __syncthreads();
+  }
+}
+
+__device__ __forceinline__ void count_rows(PlanSmem& sm, const int32_t* __restrict__ ids, int begin,
+                                           int end, int groups) {
+  for (int i = threadIdx.x; i <= groups; i += THREADS) sm.base[i] = 0;
+  __syncthreads();
+  for (int r = begin + threadIdx.x; r < end; r += THREADS) atomicAdd(&sm.base[group_of(ids[r], groups)], 1);
+  __syncthreads();
+}
+
+__device__ __forceinline__ void write_offsets(const PlanSmem& sm, int groups,
+                                              int32_t* __restrict__ offsets) {
+  for (int i = threadIdx.x; i <= groups; i += THREADS) offsets[i] = sm.base[i];
+}
+
+// What a block does once its rows' groups are known: the whole plan where it
+// is the only block, or its counts.
+__device__ __forceinline__ void finish_block(PlanSmem& sm, const int32_t* ids, int begin, int end,
+                                             int groups, int32_t* order, int32_t* where,
+                                             int32_t* offsets, int32_t* counts) {
+  count_rows(sm, ids, begin, end, groups);
+  if (gridDim.x > 1) {
+    for (int i = threadIdx.x; i <= groups; i += THREADS)
+      counts[int64_t(blockIdx.x) * (groups + 1) + i] = sm.base[i];
+    return;
+  }
+  scan_groups(sm, groups);
+  write_offsets(sm, groups, offsets);
+  __syncthreads();
+  place_rows(sm, ids, begin, end, groups, order, where);
+}
+
+__global__ __launch_bounds__(THREADS) void group_count_kernel(const int32_t* __restrict__ ids, int rows,
+                                                              int per_block, int groups,
+                                                              int32_t* __restrict__ order,
+                                                              int32_t* __restrict__ where,
+                                                              int32_t* __restrict__ offsets,
+                                                              int32_t* __restrict__ counts) {
+  __shared__ PlanSmem sm;
+  const int64_t begin = int64_t(blockIdx.x) * per_block;
+  finish_block(sm, ids, int(begin), int(min(begin + per_block, int64_t(rows))), groups, order, where,
+               offsets, counts);
+}
+
+__global__ __launch_bounds__(THREADS) void group_place_kernel(const int32_t* __restrict__ ids, int rows,
+                                                              int per_block, int groups, int blocks,
+                                                              const int32_t* __restrict__ counts,
+                                                              int32_t* __restrict__ order,
+                                                              int32_t* __restrict__ where,
+                                                              int32_t* __restrict__ offsets) {
+  __shared__ PlanSmem sm;
+  const int own = blockIdx.x;
+  int mine[3] = {0, 0, 0};   // of the blocks before, for this thread's groups
+  static_assert(3 * THREADS > kMostGroups, "groups of a thread");
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const int g = j * THREADS + threadIdx.x;
+    if (g > groups) break;
+    int all = 0, before = 0;
+#pragma unroll 8
+    for (int b = 0; b < blocks; ++b) {
+      const int c = counts[int64_t(b) * (groups + 1) + g];
+      all += c;
+      before += b < own ? c : 0;
+    }
+    mine[j] = before;
+    sm.base[g] = all;
+  }
+  __syncthreads();
+  scan_groups(sm, groups);
+  if (own == 0) write_offsets(sm, groups, offsets);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const int g = j * THREADS + threadIdx.x;
+    if (g <= groups) sm.base[g] += mine[j];
+  }
+  __syncthreads();
+  const int64_t begin = int64_t(own) * per_block;
+  place_rows(sm, ids, int(begin), int(min(begin + per_block, int64_t(rows))), groups, order, where);
+}
+
+// A number that orders binary32 values as unsigned integers do; +0 and -0 are
+// one value, -infinity and NaN (an expert that may not be chosen) are 0.
+__device__ __forceinline__ uint32_t rank_of(float x) {
+  if (!(x > -INFINITY)) return 0;
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float value_of(uint32_t r) {
+  return __uint_as_float(r & 0x80000000u ? r & 0x7FFFFFFFu : ~r);
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int d = 32; d; d /= 2) v = max(v, uint32_t(__shfl_xor(int(v), d)));
+  return v;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d; d /= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
+// One wave to a token: lane l holds logits l, l + 64, ...; top_k times the
+// largest is found (of equals the lowest expert) and taken out.  The softmax's
+// terms are exp(l - largest); those of the largest are 1 whatever it is, so
+// that infinities share the weight.
+template <int PER, bool kBF16>
+__global__ __launch_bounds__(THREADS) void route_kernel(
+    const void* __restrict__ logits, int64_t stride, int tokens, int tokens_per_block, int experts,
+    int top_k, bool renormalize, int32_t* __restrict__ ids, float* __restrict__ weights,
+    int32_t* __restrict__ order, int32_t* __restrict__ where, int32_t* __restrict__ offsets,
+    int32_t* __restrict__ counts) {
+  __shared__ PlanSmem sm;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t0 = int64_t(blockIdx.x) * tokens_per_block;
+  const int64_t t1 = min(t0 + tokens_per_block, int64_t(tokens));
+  for (int64_t t = t0 + wave; t < t1; t += WAVES) {
+    uint32_t rank[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = i * 64 + lane;
+      float v = -INFINITY;
+      if (e < experts) {
+        if (kBF16)
+          v = __uint_as_float(uint32_t(static_cast<const uint16_t*>(logits)[t * stride + e]) << 16);
+        else
+          v = static_cast<const float*>(logits)[t * stride + e];
+      }
+      rank[i] = rank_of(v);
+    }
+    uint32_t most = rank[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) most = max(most, rank[i]);
+    const uint32_t top = wave_max(most);
+    const float largest = value_of(top);
+    auto term = [&](uint32_t r) { return r == top ? 1.0f : r ? expf(value_of(r) - largest) : 0.0f; };
+    float total = 0.0f;
+    if (!renormalize) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) total += top ? term(rank[i]) : 0.0f;
+      total = wave_sum(total);
+    }
+    uint32_t chosen = 0;   // lane j: the j-th choice
+    int expert = -1;
+    for (int j = 0; j < top_k; ++j) {
+      uint32_t best = rank[0];
+      int at = lane;
+#pragma unroll
+      for (int i = 1; i < PER; ++i)
+        if (rank[i] > best) best = rank[i], at = i * 64 + lane;
+      const uint32_t m = wave_max(best);
+      if (m == 0) break;
+      // the lowest expert of those with the largest rank
+      const int e = int(~wave_max(best == m ? ~uint32_t(at) : 0u));
+      if (lane == j) chosen = m, expert = e;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i * 64 + lane == e) rank[i] = 0;
+    }
+    const float w = chosen ? term(chosen) : 0.0f;
+    if (renormalize) total = wave_sum(lane < top_k ? w : 0.0f);
+    if (lane < top_k) {
+      ids[t * top_k + lane] = expert;
+      weights[t * top_k + lane] = chosen ? w / total : 0.0f;
+    }
+  }
+  __syncthreads();   // the block's ids, read back below
+  finish_block(sm, ids, int(t0 * top_k), int(t1 * top_k), experts, order, where, offsets, counts);
+}
+
+// Rows of a block: whole tokens, blocks of about THREADS rows, at most
+// kMostBlocks of them.
+int64_t block_rows(int64_t rows, int64_t top_k) {
+  const int64_t tokens = rows / top_k;
+  const int64_t least = THREADS / top_k;
+  const int64_t spread = (tokens + kMostBlocks - 1) / kMostBlocks;
+  return (spread > least ? spread : least) * top_k;
+}
+
+template <bool kBF16>
+hipError_t launch_route(const void* logits, int64_t tokens, int experts, int64_t stride, int top_k,
+                        bool renormalize, int32_t* ids, float* weights, int32_t* order,
+                        int32_t* where, int32_t* offsets, int32_t* ws, hipStream_t s) {
+  const int64_t per = block_rows(tokens * top_k, top_k) / top_k;
+  const int blocks = tokens ? int((tokens + per - 1) / per) : 1;   // no tokens: offsets of zero
+  auto run = [&](auto kern) {
+    kern<<<blocks, THREADS, 0, s>>>(logits, stride, int(tokens), int(per), experts, top_k, renormalize,
+                                    ids, weights, order, where, offsets, ws);
+    return hipGetLastError();
+  };
+  hipError_t e;
+  if (experts <= 64) e = run(route_kernel<1, kBF16>);
+  else if (experts <= 128) e = run(route_kernel<2, kBF16>);
+  else if (experts <= 256) e = run(route_kernel<4, kBF16>);
+  else if (experts <= 512) e = run(route_kernel<8, kBF16>);
+  else e = run(route_kernel<16, kBF16>);
+  if (e != hipSuccess || blocks == 1) return e;
+  group_place_kernel<<<blocks, THREADS, 0, s>>>(ids, int(tokens * top_k), int(per * top_k), experts,
+                                                blocks, ws, order, where, offsets);
+  return hipGetLastError();
+}
+
+// Each token's weighted sum over its experts' rows, in binary32 and in the
+// order of its choices.  A thread takes 8 columns; the rows of four choices
+// are under way at once.  A place that is no expert's adds nothing and is not
+// read.
+template <bool kBF16In, bool kBF16Out>
+__global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ rows,
+                                                      const int32_t* __restrict__ where,
+                                                      const float* __restrict__ weights,
+                                                      const int32_t* __restrict__ offsets, int groups,
+                                                      int n_rows, int top_k, int n,
+                                                      void* __restrict__ out) {
+  const int64_t t = blockIdx.x;
+  const int col = (blockIdx.y * 256 + threadIdx.x) * 8;
+  const int used = min(offsets[groups], n_rows);
+  if (col >= n) return;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < top_k; j0 += 4) {
+    uint4 v[4][kBF16In ? 1 : 2];
+    float w[4];
+    bool live[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int slot = min(j0 + j, top_k - 1);
+      const int at = where[t * top_k + slot];
+      live[j] = j0 + j < top_k && uint32_t(at) < uint32_t(max(used, 0));
+      w[j] = weights[t * top_k + slot];
+      const int64_t row = live[j] ? at : 0;
+      if (live[j]) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(rows) +
+                                                        (row * n + col) * (kBF16In ? 2 : 4));
+        v[j][0] = p[0];
+        if constexpr (!kBF16In) v[j][1] = p[1];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (!live[j]) continue;
+      float x[8];
+      if constexpr (kBF16In) {
+        const uint32_t d[4] = {v[j][0].x, v[j][0].y, v[j][0].z, v[j][0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = __uint_as_float(d[i] << 16);
+          x[2 * i + 1] = __uint_as_float(d[i] & 0xFFFF0000u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          x[4 * i] = __uint_as_float(v[j][i].x);
+          x[4 * i + 1] = __uint_as_float(v[j][i].y);
+          x[4 * i + 2] = __uint_as_float(v[j][i].z);
+          x[4 * i + 3] = __uint_as_float(v[j][i].w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], x[i], sum[i]);
+    }
+  }
+  uint8_t* o = static_cast<uint8_t*>(out) + (t * n + col) * (kBF16Out ? 2 : 4);
+  if constexpr (kBF16Out) {
+    *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]),
+                                              pack_bf16x2(sum[4], sum[5]), pack_bf16x2(sum[6], sum[7]));
+  } else {
+    reinterpret_cast<float4*>(o)[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    reinterpret_cast<float4*>(o)[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+  }
+}
+
+}  // namespace
+
+size_t group_rows_ws_bytes(int64_t rows, int64_t top_k, int64_t groups) {
+  const int64_t per = block_rows(rows, top_k);
+  const int64_t blocks = (rows + per - 1) / per;
+  return blocks > 1 ? size_t(blocks) * size_t(groups + 1) * sizeof(int32_t) : 0;
+}
+
+hipError_t launch_group_rows(const int32_t* ids, int64_t rows, int groups, int32_t* order,
+                             int32_t* where, int32_t* offsets, int32_t* ws, hipStream_t s) {
+  const int per = int(block_rows(rows, 1));
+  const int blocks = rows ? int((rows + per - 1) / per) : 1;   // no rows: offsets of zero
+  group_count_kernel<<<blocks, THREADS, 0, s>>>(ids, int(rows), per, groups, order, where, offsets, ws);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || blocks == 1) return e;
+  group_place_kernel<<<blocks, THREADS, 0, s>>>(ids, int(rows), per, groups, blocks, ws, order, where,
+                                                offsets);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_route(const void* logits, int dtype, int64_t tokens, int experts,
+                            int64_t stride, int top_k, bool renormalize, int32_t* ids,
+                            float* weights, int32_t* order, int32_t* where, int32_t* offsets,
+                            int32_t* ws, hipStream_t s) {
+  return dtype == 1 ? launch_route<true>(logits, tokens, experts, stride, top_k, renormalize, ids,
+                                         weights, order, where, offsets, ws, s)
+                    : launch_route<false>(logits, tokens, experts, stride, top_k, renormalize, ids,
+                                          weights, order, where, offsets, ws, s);
+}
+
+hipError_t launch_moe_combine(const void* rows, int x_dtype, const RowPlan& p, const int32_t* where,
+                              const float* weights, int64_t tokens, int top_k, int64_t n, void* out,
+                              int out_dtype, hipStream_t s) {
+  const dim3 grid(unsigned(tokens), unsigned((n / 8 + 255) / 256));
+  auto run = [&](auto kern) {
+    kern<<<grid, 256, 0, s>>>(rows, where, weights, p.offsets, p.groups, p.rows, top_k, int(n), out);
+    return hipGetLastError();
+  };
+  if (x_dtype == 1) return out_dtype == 1 ? run(combine_kernel<true, true>) : run(combine_kernel<true, false>);
+  return out_dtype == 1 ? run(combine_kernel<false, true>) : run(combine_kernel<false, false>);
+}
+
+}  // namespace qlin

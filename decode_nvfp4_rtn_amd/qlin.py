@@ -28,6 +28,8 @@ QL_NVFP4, QL_INT4_G128, QL_LUT2, QL_INT4_SP24 = 0, 1, 2, 3
 QL_STATIC_SCALE = 1
 QL_KV_BF16, QL_KV_E4M3, QL_KV_NVFP4 = 0, 1, 2
 QL_ROPE_INTERLEAVED = 1
+QL_ROUTE_RENORMALIZE = 1
+QL_ROWS_GATHER, QL_ROWS_SILU_MUL = 1, 2
 
 _vp, _i64, _sz, _int, _uint = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint
 
@@ -67,6 +69,19 @@ _SIGS = {
     "kv_attention": (_int, [_vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64,
                             _i64, _vp, ctypes.c_float, _vp, _vp, _sz, _vp]),
     "kv_commit": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp]),
+    "group_rows_workspace": (_sz, [_i64, _i64]),
+    "group_rows": (_int, [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_workspace": (_sz, [_i64, _i64, _i64]),
+    "moe_route": (_int, [_vp, _int, _i64, _i64, _i64, _i64, _uint, _vp, _vp, _vp, _vp, _vp, _vp,
+                         _sz, _vp]),
+    "moe_gemm_w4a16": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _uint, _vp,
+                              _int, _vp]),
+    "moe_gemm_w4a4": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i64,
+                             _uint, _vp, _int, _vp]),
+    "moe_combine": (_int, [_vp, _int, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _int, _vp]),
+    "lora_add_workspace": (_sz, [_i64, _i64, _i64, _i64]),
+    "lora_add": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64,
+                        _vp, _i64, _int, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -694,6 +709,273 @@ def kv_commit(cache, cu_q, kv_lens, block_table, path, stream=None):
                         path.data_ptr(), path.shape[1], _queue(stream, dev))
     if st:
         raise QlinError("kv_commit", st)
+
+
+# ---------------------------------------------------------------------------
+# Rows that choose their own weights: experts and adapters
+# ---------------------------------------------------------------------------
+
+class RowPlan:
+    """The rows of a batch in the order of the weights they meet, as
+    ``group_rows`` or ``moe_route`` makes it: int32 tensors ``order`` [rows] (the
+    row at each place), ``where`` (each row's place, in the shape of the choices)
+    and ``offsets`` [groups + 1] (where each group's run begins; rows of no group
+    from offsets[groups] on).  ``tokens`` rows of ``top_k`` choices each."""
+
+    __slots__ = ("order", "where", "offsets", "groups", "tokens", "top_k", "device")
+
+    def __init__(self, groups, tokens, top_k, dev, stream=None):
+        self.groups, self.tokens, self.top_k, self.device = groups, tokens, top_k, dev
+        self.order = _new((tokens * top_k,), torch.int32, dev, stream)
+        self.where = _new((tokens, top_k), torch.int32, dev, stream)
+        self.offsets = _new((groups + 1,), torch.int32, dev, stream)
+
+
+def _call(name, dev, *args):
+    """An entry point's call with `dev` current: launches and launch plans go by
+    the current device."""
+    if torch._C._cuda_getDevice() == dev.index:
+        st = getattr(_lib, name)(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(_lib, name)(*args)
+    if st:
+        raise QlinError(name, st)
+
+
+def _whole(x, name):
+    """x as an integer, or a refusal (a bool or a float is no count)."""
+    if isinstance(x, bool) or not hasattr(x, "__index__"):
+        raise ValueError(f"{name} must be a whole number, got {x!r}")
+    return x.__index__()
+
+
+def _workspace(workspace, need, dev, stream):
+    """(address, bytes, what keeps it alive) of a call's workspace."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = _new((need,), torch.uint8, dev, stream)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
+    else:
+        _bytes(workspace, "workspace", 0, torch.uint8)
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
+def _for_plan(plan, groups, tokens, top_k, dev, stream):
+    if plan is None:
+        return RowPlan(groups, tokens, top_k, dev, stream)
+    if (plan.groups, plan.tokens, plan.top_k, plan.device) != (groups, tokens, top_k, dev):
+        raise ValueError(f"plan is of {plan.tokens} x {plan.top_k} rows and {plan.groups} groups on "
+                         f"{plan.device}; the call needs {tokens} x {top_k}, {groups}, {dev}")
+    return plan
+
+
+def group_rows(ids, groups, plan=None, workspace=None, stream=None):
+    """The plan of given choices: ids int32 [rows] or [tokens, top_k], each the
+    row's group (an adapter, an expert) or, outside of 0 .. groups - 1, none.
+    plan: one of the same sizes to write (allocated when not given); workspace:
+    uint8 of group_rows_workspace(rows, groups) bytes, allocated when not given."""
+    if not ids.is_cuda or ids.dtype != torch.int32 or ids.dim() not in (1, 2) or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous int32 [rows] or [tokens, top_k] GPU tensor, got "
+                         f"{ids.dtype} {list(ids.shape)} on {ids.device}")
+    dev, groups = ids.device, _whole(groups, "groups")
+    tokens, top_k = ids.shape if ids.dim() == 2 else (ids.shape[0], 1)
+    if not 1 <= groups <= 1024 or not 1 <= top_k <= 64:
+        raise ValueError(f"1 .. 1024 groups and 1 .. 64 choices to a token, got {groups} and {top_k}")
+    plan = _for_plan(plan, groups, tokens, top_k, dev, stream)
+    rows = tokens * top_k
+    at, have, keep = _workspace(workspace, _lib.group_rows_workspace(rows, groups), dev, stream)
+    _call("group_rows", dev, ids.data_ptr(), rows, groups, plan.order.data_ptr(), plan.where.data_ptr(),
+          plan.offsets.data_ptr(), at, have, _queue(stream, dev))
+    return plan
+
+
+def group_rows_workspace(rows, groups):
+    return _lib.group_rows_workspace(rows, groups)
+
+
+def moe_route(logits, top_k, renormalize=True, ids=None, weights=None, plan=None, workspace=None,
+              stream=None):
+    """A router's choice: logits [tokens, experts] (fp32 or bf16; a row's experts
+    contiguous) -> (ids int32 [tokens, top_k], weights fp32 [tokens, top_k],
+    plan).  The top_k largest, of equal ones the lowest expert; softmax weights
+    over the chosen experts, or over all if not renormalize.  An expert at
+    -infinity or NaN is not chosen: its place holds -1 and weight 0.  ids,
+    weights, plan and workspace (uint8 of moe_route_workspace(...) bytes) are
+    allocated when not given."""
+    dt = _XDT.get(logits.dtype)
+    if dt is None or not logits.is_cuda or logits.dim() != 2:
+        raise ValueError(f"logits must be a float32 or bfloat16 [tokens, experts] GPU tensor, got "
+                         f"{logits.dtype} {list(logits.shape)} on {logits.device}")
+    dev, top_k = logits.device, _whole(top_k, "top_k")
+    tokens, experts = logits.shape
+    stride, inner = logits.stride()
+    if experts > 1 and inner != 1:
+        raise ValueError("logits: a token's experts must be contiguous")
+    if not 1 <= top_k <= min(64, experts) or experts > 1024:
+        raise ValueError(f"top_k of 1 .. min(64, experts) and at most 1024 experts, got {top_k} of {experts}")
+    plan = _for_plan(plan, experts, tokens, top_k, dev, stream)
+    shape = (tokens, top_k)
+    ids = _new(shape, torch.int32, dev, stream) if ids is None else _rows_out(ids, "ids", shape, (torch.int32,), dev)
+    weights = (_new(shape, torch.float32, dev, stream) if weights is None
+               else _rows_out(weights, "weights", shape, (torch.float32,), dev))
+    at, have, keep = _workspace(workspace, _lib.moe_route_workspace(tokens, experts, top_k), dev, stream)
+    _call("moe_route", dev, logits.data_ptr(), dt, tokens, experts, stride if tokens > 1 else experts, top_k,
+          QL_ROUTE_RENORMALIZE if renormalize else 0, ids.data_ptr(), weights.data_ptr(),
+          plan.order.data_ptr(), plan.where.data_ptr(), plan.offsets.data_ptr(), at, have,
+          _queue(stream, dev))
+    return ids, weights, plan
+
+
+def moe_route_workspace(tokens, experts, top_k):
+    return _lib.moe_route_workspace(tokens, experts, top_k)
+
+
+def _experts(experts, plan, fmt, n, k):
+    """Bytes between the blobs of a stack uint8 [experts, bytes]."""
+    if (experts.device != plan.device or experts.dtype != torch.uint8 or experts.dim() != 2
+            or experts.shape[0] != plan.groups):
+        raise ValueError(f"experts must be a uint8 [{plan.groups}, bytes] tensor on {plan.device}, got "
+                         f"{experts.dtype} {list(experts.shape)} on {experts.device}")
+    step, inner = experts.stride()
+    if inner != 1:
+        raise ValueError("experts: a blob's bytes must be contiguous")
+    if experts.shape[1] < _lib.repack_weights_bytes(fmt, n, k):
+        raise ValueError(f"experts hold {experts.shape[1]} bytes each; a format-{fmt} blob of [{n}, {k}] takes "
+                         f"{_lib.repack_weights_bytes(fmt, n, k)}")
+    return step if plan.groups > 1 else experts.shape[1] // 16 * 16
+
+
+def _operand(t, name, dtype, rows, cols, dev):
+    """Address of t, a contiguous [rows, cols] tensor of dtype on dev."""
+    if t.device != dev or t.dtype != dtype or t.shape != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} [{rows}, {cols}] tensor on {dev}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _product(plan, n, k, gather, silu_mul, y, out_dtype, stream):
+    """(n, k, rows of x, flags, y, its type) of an experts' product."""
+    n, k = _whole(n, "n"), _whole(k, "k")
+    pairs = plan.tokens * plan.top_k
+    shape = (pairs, n // 2 if silu_mul else n)
+    y = _new(shape, out_dtype, plan.device, stream) if y is None else _rows_out(y, "y", shape, _XDT, plan.device)
+    dt = _XDT.get(y.dtype)
+    if dt is None:
+        raise ValueError("y must be float32 or bfloat16")
+    flags = (QL_ROWS_GATHER if gather else 0) | (QL_ROWS_SILU_MUL if silu_mul else 0)
+    return n, k, plan.tokens if gather else pairs, flags, y, dt
+
+
+def moe_gemm_w4a16(x, experts, plan, n, k, gather=True, silu_mul=False, y=None,
+                   out_dtype=torch.bfloat16, stream=None):
+    """The plan's rows times their experts' INT4 weights: y [pairs, n] in the
+    plan's order.
+
+    x bf16: [tokens, k], the plan's tokens (gather), or [pairs, k] in the plan's
+    order.  experts: uint8 [experts, bytes], an INT4 blob of [n, k] each
+    (``repack_weights(..., packed=experts[e])``).  silu_mul: the weights' first
+    n / 2 rows are a gate, and y [pairs, n / 2] = silu(gate) * up.  Rows of y
+    whose pair has no expert are zero."""
+    n, k, rows, flags, y, dt = _product(plan, n, k, gather, silu_mul, y, out_dtype, stream)
+    x_at = _operand(x, "x", torch.bfloat16, rows, k, plan.device)
+    step = _experts(experts, plan, QL_INT4_G128, n, k)
+    _call("moe_gemm_w4a16", plan.device, x_at, experts.data_ptr(), plan.groups, step, plan.order.data_ptr(),
+          plan.offsets.data_ptr(), plan.tokens * plan.top_k, plan.top_k, n, k, flags,
+          y.data_ptr(), dt, _queue(stream, plan.device))
+    return y
+
+
+def moe_gemm_w4a4(a_codes, a_scales, a_tensor_scale, experts, plan, n, k, gather=True, silu_mul=False,
+                  y=None, out_dtype=torch.bfloat16, stream=None):
+    """moe_gemm_w4a16 for NVFP4 weights and activations: a_codes, a_scales and
+    a_tensor_scale are quantize_nvfp4's of x."""
+    n, k, rows, flags, y, dt = _product(plan, n, k, gather, silu_mul, y, out_dtype, stream)
+    dev = plan.device
+    c_at = _operand(a_codes, "a_codes", torch.uint8, rows, k // 2, dev)
+    s_at = _operand(a_scales, "a_scales", torch.uint8, rows, k // 16, dev)
+    t_at = _vector(a_tensor_scale, "a_tensor_scale", torch.float32, dev, 1)
+    step = _experts(experts, plan, QL_NVFP4, n, k)
+    _call("moe_gemm_w4a4", dev, c_at, s_at, t_at, experts.data_ptr(), plan.groups, step, plan.order.data_ptr(),
+          plan.offsets.data_ptr(), plan.tokens * plan.top_k, plan.top_k, n, k, flags,
+          y.data_ptr(), dt, _queue(stream, dev))
+    return y
+
+
+def moe_combine(rows, plan, weights, out=None, out_dtype=torch.bfloat16, stream=None):
+    """Back to the tokens: out[t] = sum_j weights[t, j] * rows[plan.where[t, j]],
+    rows [pairs, n] (fp32 or bf16) in the plan's order, weights fp32 [tokens,
+    top_k].  Pairs without an expert add nothing."""
+    dev = plan.device
+    if (rows.device != dev or rows.dtype not in _XDT or rows.dim() != 2 or not rows.is_contiguous()
+            or rows.shape[0] != plan.tokens * plan.top_k):
+        raise ValueError(f"rows must be a contiguous float32 or bfloat16 [{plan.tokens * plan.top_k}, n] tensor "
+                         f"on {dev}, got {rows.dtype} {list(rows.shape)} on {rows.device}")
+    n = rows.shape[1]
+    w_at = _operand(weights, "weights", torch.float32, plan.tokens, plan.top_k, dev)
+    shape = (plan.tokens, n)
+    out = _new(shape, out_dtype, dev, stream) if out is None else _rows_out(out, "out", shape, _XDT, dev)
+    dt = _XDT.get(out.dtype)
+    if dt is None:
+        raise ValueError("out must be float32 or bfloat16")
+    _call("moe_combine", dev, rows.data_ptr(), _XDT[rows.dtype], plan.where.data_ptr(), plan.offsets.data_ptr(),
+          plan.groups, w_at, plan.tokens, plan.top_k, n, out.data_ptr(), dt,
+          _queue(stream, dev))
+    return out
+
+
+def _strided(t, name, dtypes, rows, dev):
+    """Row stride and columns of t [rows, columns], a row's elements contiguous."""
+    if t.device != dev or t.dtype not in dtypes or t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be a [{rows}, columns] tensor on {dev} of "
+                         f"{' or '.join(map(str, dtypes))}, got {t.dtype} {list(t.shape)} on {t.device}")
+    step, inner = t.stride()
+    if t.shape[1] > 1 and inner != 1:
+        raise ValueError(f"{name}: a row must be contiguous")
+    return (step if rows > 1 else t.shape[1]), t.shape[1]
+
+
+def lora_add_workspace(rows, adapters, rank, k):
+    return _lib.lora_add_workspace(rows, adapters, rank, k)
+
+
+def lora_add(y, x, a, b, plan, scale=None, out=None, workspace=None, stream=None):
+    """Low-rank adapters beside a projection: out[t] = y[t] + scale[i] * B_i (A_i
+    x[t]), i the adapter of row t (plan: group_rows of the rows' adapters); rows
+    without one: out = y.
+
+    y [rows, n] (fp32 or bf16), x bf16 [rows, k]: a row's elements contiguous,
+    rows any stride (a slice of a fused projection will do).  a bf16 [adapters,
+    rank, k], b bf16 [adapters, n, rank], rank a multiple of 8 up to 128; scale
+    fp32 [adapters] (None: 1).  out: like y, y itself when not given."""
+    dev = plan.device
+    if plan.top_k != 1:
+        raise ValueError(f"a row has one adapter; the plan has {plan.top_k} choices to a row")
+    rows, adapters = plan.tokens, plan.groups
+    ys, n = _strided(y, "y", _XDT, rows, dev)
+    xs, k = _strided(x, "x", (torch.bfloat16,), rows, dev)
+    if (a.device != dev or a.dtype != torch.bfloat16 or a.dim() != 3 or a.shape[0] != adapters
+            or a.shape[2] != k or not a.is_contiguous()):
+        raise ValueError(f"a must be a contiguous bfloat16 [{adapters}, rank, {k}] tensor on {dev}, got "
+                         f"{a.dtype} {list(a.shape)} on {a.device}")
+    rank = a.shape[1]
+    if (b.device != dev or b.dtype != torch.bfloat16 or b.shape != (adapters, n, rank)
+            or not b.is_contiguous()):
+        raise ValueError(f"b must be a contiguous bfloat16 [{adapters}, {n}, {rank}] tensor on {dev}, got "
+                         f"{b.dtype} {list(b.shape)} on {b.device}")
+    s_at = None if scale is None else _vector(scale, "scale", torch.float32, dev, adapters)
+    if out is None:
+        out = y
+    os_, cols = (ys, n) if out is y else _strided(out, "out", (y.dtype,), rows, dev)
+    if cols != n:
+        raise ValueError(f"out must be [{rows}, {n}], got {list(out.shape)}")
+    at, have, keep = _workspace(workspace, _lib.lora_add_workspace(rows, adapters, rank, k), dev, stream)
+    _call("lora_add", dev, y.data_ptr(), ys, x.data_ptr(), xs, a.data_ptr(), b.data_ptr(), s_at, adapters, rank,
+          plan.order.data_ptr(), plan.offsets.data_ptr(), rows, n, k, out.data_ptr(), os_,
+          _XDT[y.dtype], at, have, _queue(stream, dev))
+    return out
 
 
 def raw():

@@ -603,6 +603,132 @@ int kv_commit(const ql_kv_cache *cache, int64_t n_seqs, const int32_t *cu_q,
               const int32_t *kv_lens, const int32_t *block_table, int64_t table_stride,
               int64_t table_cols, const int32_t *path, int64_t max_path, void *stream);
 
+/* ========================================================================
+ * Linear layers whose rows choose their own weights: mixtures of experts
+ * (each token meets the weights of its top_k experts) and low-rank adapters
+ * (each request has its own).  The calls run over a PLAN, the rows of a batch
+ * in the order of the weights they meet:
+ *
+ *   order   [rows]        the row at each place of that order
+ *   where   [rows]        the place of each row (the inverse)
+ *   offsets [groups + 1]  group g's run is the places offsets[g] ..
+ *                         offsets[g + 1] - 1, its rows in ascending order
+ *
+ * Rows of no group come last, from offsets[groups] on.  For a mixture the
+ * rows of a plan are the pairs (token, choice), pair = token * top_k + choice.
+ * Everything stays on the device: no call needs to know a group's size, and a
+ * captured graph may be replayed on other choices.  The arrays are as one of
+ * the two calls below wrote them; entries outside of the batch are held to it
+ * (no call reads or writes out of bounds for any contents), with results that
+ * mean nothing.
+ *
+ * At most 1024 groups, 2^24 - 1 rows, top_k <= 64.
+ * ===================================================================== */
+
+/* ------------------------------------------------------------------------
+ * The plan of given choices (the adapter of each row).
+ * ids   [rows]: the row's group; outside of 0 .. groups - 1: none.
+ * rows == 0 writes offsets of zero.  workspace: group_rows_workspace(rows,
+ * groups) bytes, 16-byte aligned (0: may be NULL), not read before it is
+ * written; calls that share one must be ordered.
+ * Errors: QL_EINVAL, QL_ESHAPE, QL_EALIGN (int32 pointers: 4 bytes),
+ * QL_EWORKSPACE, QL_EHIP.
+ * ---------------------------------------------------------------------- */
+size_t group_rows_workspace(int64_t rows, int64_t groups);
+int group_rows(const int32_t *ids, int64_t rows, int64_t groups, int32_t *order, int32_t *where,
+               int32_t *offsets, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A router's choice: for each token the top_k experts of largest logit (of
+ * equal ones the lowest expert first), their weights, and the plan of the
+ * pairs.
+ *   weight = exp(l - max) / sum exp(l' - max), in binary32, the sum over all
+ *   experts or, with QL_ROUTE_RENORMALIZE, over the chosen ones.
+ * An expert whose logit is -infinity or NaN is not chosen and takes no part in
+ * the sum: where fewer than top_k are left, the other choices are -1 with
+ * weight 0 and belong to no group.  Experts at +infinity share the weight.
+ *
+ * logits   [tokens, experts] QL_F32 or QL_BF16, rows row_stride elements apart.
+ * ids, weights  out [tokens, top_k].
+ * order, where, offsets  out: the plan of tokens * top_k pairs.
+ * workspace as group_rows.  Errors: as group_rows, and QL_EDTYPE.
+ * ---------------------------------------------------------------------- */
+#define QL_ROUTE_RENORMALIZE 1u
+size_t moe_route_workspace(int64_t tokens, int64_t experts, int64_t top_k);
+int moe_route(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t row_stride,
+              int64_t top_k, unsigned flags, int32_t *ids, float *weights, int32_t *order,
+              int32_t *where, int32_t *offsets, void *workspace, size_t workspace_bytes,
+              void *stream);
+
+/* ------------------------------------------------------------------------
+ * The pairs' products with their experts' weights: for place p of expert e
+ *   y[p, :] = x[row(p), :] W_e^T
+ * W4A16 (decoding; bf16 x, INT4 blobs) and W4A4 (prompts; x as quantize_nvfp4
+ * leaves it, under one tensor scale, NVFP4 blobs).
+ *
+ * row(p)   order[p] / top_k with QL_ROWS_GATHER (x holds a row for each token),
+ *          else p (x is in the plan's order; order may be NULL).
+ * experts  n_experts blobs of W_e [n, k] from repack_weights, expert_bytes
+ *          apart (a multiple of 16, at least repack_weights_bytes(...)).
+ * y        out [pairs, n] in the plan's order, QL_F32 or QL_BF16.
+ * QL_ROWS_SILU_MUL: the first n / 2 rows of W_e are a gate g, the others u,
+ *          and y [pairs, n / 2] = silu(g) * u, silu(g) = g / (1 + exp(-g)), in
+ *          binary32, rounded once.
+ * Rows of y of pairs without an expert are set to zero.
+ * Shapes: n % 16 == 0 (n % 32 with QL_ROWS_SILU_MUL), k % 128 == 0, n * k <=
+ * 2^31; W4A4: fewer than 2^32 / k rows of x.  A blob that is not of this
+ * format and (n, k) leaves its expert's rows untouched.
+ * Errors: QL_EINVAL, QL_ESHAPE, QL_EALIGN, QL_EDTYPE, QL_EWORKSPACE
+ * (expert_bytes too small), QL_EHIP.
+ * ---------------------------------------------------------------------- */
+#define QL_ROWS_GATHER 1u
+#define QL_ROWS_SILU_MUL 2u
+int moe_gemm_w4a16(const void *x_bf16, const void *experts, int64_t n_experts, int64_t expert_bytes,
+                   const int32_t *order, const int32_t *offsets, int64_t pairs, int64_t top_k,
+                   int64_t n, int64_t k, unsigned flags, void *y, int y_dtype, void *stream);
+int moe_gemm_w4a4(const uint8_t *a_codes, const uint8_t *a_scales, const float *a_tensor_scale,
+                  const void *experts, int64_t n_experts, int64_t expert_bytes,
+                  const int32_t *order, const int32_t *offsets, int64_t pairs, int64_t top_k,
+                  int64_t n, int64_t k, unsigned flags, void *y, int y_dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Back to the tokens: out[t, :] = sum_j weights[t, j] rows[where[t, j], :], in
+ * binary32 and in the order of the choices.  Places from offsets[n_experts] on
+ * (pairs without an expert) are not read and add nothing.
+ * rows  [tokens * top_k, n] and out [tokens, n], each QL_F32 or QL_BF16.
+ * Shapes: n % 8 == 0.  Errors: as the products.
+ * ---------------------------------------------------------------------- */
+int moe_combine(const void *rows, int x_dtype, const int32_t *where, const int32_t *offsets,
+                int64_t n_experts, const float *weights, int64_t tokens, int64_t top_k, int64_t n,
+                void *out, int out_dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Low-rank adapters beside a projection that all rows share:
+ *   out[t, :] = y[t, :] + scale[i] B_i (A_i x[t, :]),  i the adapter of row t
+ * binary32 accumulation; A x is kept in 16 bits of mantissa or more, and out is
+ * rounded once.  Rows without an adapter: out = y.
+ *
+ * y, out   [rows, n] QL_F32 or QL_BF16 (y_dtype for both), rows y_stride and
+ *          out_stride elements apart (slices of a fused projection will do).
+ *          out may be y; otherwise they do not overlap.
+ * x        [rows, k] bf16, rows x_stride apart.
+ * a, b     [adapters, rank, k] and [adapters, n, rank] bf16, contiguous.
+ * scale    [adapters] or NULL (1).
+ * order, offsets  the plan of the rows' adapters (group_rows).
+ * workspace  lora_add_workspace(rows, adapters, rank, k) bytes, 16-byte
+ *          aligned, not read before it is written; calls that share one must be
+ *          ordered.
+ * Shapes: n % 16 == 0, k % 128 == 0, rank a multiple of 8 up to 128 (smaller
+ * ranks: padded with zeros).  Row strides are multiples of 16 bytes.
+ * Errors: QL_EINVAL, QL_ESHAPE, QL_EALIGN, QL_EDTYPE, QL_EWORKSPACE, QL_EHIP.
+ * ---------------------------------------------------------------------- */
+size_t lora_add_workspace(int64_t rows, int64_t adapters, int64_t rank, int64_t k);
+int lora_add(const void *y, int64_t y_stride, const void *x_bf16, int64_t x_stride,
+             const void *a_bf16, const void *b_bf16, const float *scale, int64_t adapters,
+             int64_t rank, const int32_t *order, const int32_t *offsets, int64_t rows, int64_t n,
+             int64_t k, void *out, int64_t out_stride, int y_dtype, void *workspace,
+             size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
