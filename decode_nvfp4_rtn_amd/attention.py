@@ -128,6 +128,7 @@ class PagedAttention:
 
     def __init__(self, cache, wqkv, wo, n_q, rope, q_weight=None, k_weight=None, eps=1e-6,
                  interleaved=False):
+        self.adapters = (None, None)
         self.cache, self.n_q, self.rope, self.eps = cache, n_q, rope, eps
         self.q_weight, self.k_weight, self.interleaved = q_weight, k_weight, interleaved
         self.hidden = wqkv.shape[1]
@@ -171,17 +172,37 @@ class PagedAttention:
             at += n
         return y
 
-    def forward(self, x, step):
+    def set_adapters(self, qkv=None, out=None):
+        """Low-rank adapters beside the projections: for each an (a, b, scale) as
+        qlin.lora_add takes them, or None."""
+        for name, which, pair in (("qkv", 0, qkv), ("out", 1, out)):
+            n, k = self.weights[which][2:]
+            if pair is not None and (pair[0].dim() != 3 or pair[0].shape[2] != k or pair[1].dim() != 3
+                                     or pair[1].shape[1] != n):
+                raise ValueError(f"{name} adapters must be a [adapters, rank, {k}] and b [adapters, {n}, "
+                                 f"rank], got {list(pair[0].shape)}, {list(pair[1].shape)}")
+        self.adapters = (qkv, out)
+
+    def adapt(self, y, x, which, plan):
+        """y with the adapters of projection `which` added in place."""
+        if plan is not None and self.adapters[which] is not None:
+            a, b, scale = self.adapters[which]
+            qlin.lora_add(y, x, a, b, plan, scale=scale)
+        return y
+
+    def forward(self, x, step, adapters=None):
         """x bf16 [tokens, hidden], the step's new tokens sequence after
         sequence -> the layer's output [tokens, hidden].  Their keys and values
-        are in the cache afterwards."""
-        qkv = self.project_step(x, 0, step)
+        are in the cache afterwards.  adapters: the plan of the tokens' adapters
+        (qlin.group_rows), one for all layers of the step; None: none."""
+        qkv = self.adapt(self.project_step(x, 0, step), x, 0, adapters)
         q = qlin.qkv_norm_rope_append(self.cache, qkv, self.n_q, step.slots, step.positions,
                                       self.rope, self.q_weight, self.k_weight, self.eps,
                                       self.interleaved)
         y = qlin.kv_attention(self.cache, q, step.cu_q, step.kv_lens, step.block_table,
                               max(step.nodes, default=0), step.max_kv, tree=step.tree)
-        return self.project_step(y.flatten(1), 1, step)
+        y = y.flatten(1)
+        return self.adapt(self.project_step(y, 1, step), y, 1, adapters)
 
     def commit(self, step, path):
         """After a tree's verification: path int32 [sequences, depth] on the

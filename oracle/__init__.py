@@ -25,6 +25,8 @@ lut2     2-bit per-row codebook (K-means, Lloyd iterations).
 gemm     Matrix products on dequantized operands and the pass rule.
 kvcache  Row formats and layout of the paged key/value cache, head norm and
          rotation, attention over chains and trees of new tokens.
+rows     Layers whose rows choose their weights: plans, a router's choice,
+         experts' products and their sum, low-rank adapters.
 
 Pins (what ties each function to something other than itself) live in
 ``tests/test_oracle_*.py``.  ``lut2.lloyd`` is pinned to scikit-learn's
@@ -34,4 +36,4 @@ rule, final rounding and re-assignment are pinned by closed forms, brute
 force and special cases.
 """
 
-from . import formats, nvfp4, int4, sparse24, lut2, gemm, kvcache  # noqa: F401
+from . import formats, nvfp4, int4, sparse24, lut2, gemm, kvcache, rows  # noqa: F401
