@@ -18,6 +18,38 @@ struct RowPlan {
   int rows;
 };
 
+// Sums and largest values over a wave's lanes by DPP moves (8 cycles a step,
+// where a shuffle through LDS takes over 100): within rows of 16 lanes, then
+// from row to row.  Lanes without a source take 0.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int dpp0(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, kCtrl, kRows, 0xF, false);
+}
+
+// Inclusive prefix sum.
+__device__ __forceinline__ int wave_prefix(int v) {
+  v += dpp0<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8
+  v += dpp0<0x112, 0xF>(v);
+  v += dpp0<0x114, 0xF>(v);
+  v += dpp0<0x118, 0xF>(v);
+  v += dpp0<0x142, 0xA>(v);   // lane 15 of a row to the next, rows 1 and 3
+  v += dpp0<0x143, 0xC>(v);   // lane 31 to rows 2 and 3
+  return v;
+}
+
+__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+
+// The largest of unsigned values, the same for all lanes.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, uint32_t(dpp0<0x111, 0xF>(int(v))));
+  v = max(v, uint32_t(dpp0<0x112, 0xF>(int(v))));
+  v = max(v, uint32_t(dpp0<0x114, 0xF>(int(v))));
+  v = max(v, uint32_t(dpp0<0x118, 0xF>(int(v))));
+  v = max(v, uint32_t(dpp0<0x142, 0xA>(int(v))));
+  v = max(v, uint32_t(dpp0<0x143, 0xC>(int(v))));
+  return uint32_t(last_lane(int(v)));
+}
+
 // A run of at most `tall` places of one group, found from a number: the tiles
 // of group 0, of group 1, ..., then those of the rows without a group (group
 // == groups).  The search is a wave's: each lane takes a group of 64, a prefix
@@ -44,22 +76,15 @@ __device__ __forceinline__ RowTile find_tile(const RowPlan& p, int tall, int num
       b = p.rows;
     }
     const int tiles = b > a ? (b - a + tall - 1) / tall : 0;
-    int sum = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(sum, d);
-      if (lane >= d) sum += v;
-    }
+    const int sum = wave_prefix(tiles);
     const uint64_t past = __ballot(before + sum > number);
     if (past) {
       const int at = __builtin_ctzll(past);
-      const int start = before + __shfl(sum, at) - __shfl(tiles, at);
-      const int first = __shfl(a, at) + (number - start) * tall;
-      const int end = __shfl(b, at);
-      return RowTile{__builtin_amdgcn_readfirstlane(g0 + at), __builtin_amdgcn_readfirstlane(first),
-                     __builtin_amdgcn_readfirstlane(min(end - first, tall))};
+      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, at); };
+      const int first = of(a) + (number - before - of(sum) + of(tiles)) * tall;
+      return RowTile{g0 + at, first, min(of(b) - first, tall)};
     }
-    before += __shfl(sum, 63);
+    before += last_lane(sum);
   }
   return RowTile{-1, 0, 0};
 }
@@ -74,9 +99,7 @@ __device__ __forceinline__ int count_tiles(const RowPlan& p, int tall) {
     const int b = g < p.groups ? int(min(uint32_t(p.offsets[g + 1]), most)) : p.rows;
     sum += b > a ? (b - a + tall - 1) / tall : 0;
   }
-#pragma unroll
-  for (int d = 32; d; d /= 2) sum += __shfl_xor(sum, d);
-  return __builtin_amdgcn_readfirstlane(sum);
+  return last_lane(wave_prefix(sum));
 }
 
 // The most tiles that a plan of so many rows and groups can have.

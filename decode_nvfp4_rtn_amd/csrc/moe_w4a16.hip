@@ -8,14 +8,19 @@
 // reading their weights once.
 //
 // A block takes up to 16 MT places of one expert (its tile, found on the
-// device from the plan's offsets) and walks a part of the expert's 16-row
-// weight tiles.  The tile's rows of x lie in LDS as MFMA fragments, written
-// once; after that the waves share nothing: each streams weight tiles of its
-// own, whose groups are contiguous in memory, two sets of W groups deep, and
-// needs no barrier.  Operands are made as in the dense decode kernels: the
-// bf16 values 128 + u of the codes u = q + 8, accumulators that begin at -136
-// times the rows' sums (kept in LDS, one for each row and group) and the group
-// scale in binary32 after each group's four MFMAs.
+// device from the plan's offsets) and a part of the expert's 16-row weight
+// tiles.  The tile's rows of x lie in LDS as MFMA fragments, written once;
+// after that the waves share nothing: each streams weight tiles of its own,
+// two at a time and two sets of W groups deep, over the ends of tiles, and
+// needs no barrier.  The first set is under way before x is.  Operands are
+// made as in the dense decode kernels: the bf16 values 128 + u of the codes u =
+// q + 8, accumulators that begin at -136 times the rows' sums (kept in LDS, one
+// for each row and group) and the group scale in binary32 after each group's
+// four MFMAs.
+//
+// Where there are few tiles and places (a single sequence's step) KS waves
+// share a pair of weight tiles, a part of k each, and add up in LDS in a fixed
+// order.
 #include "moe.hpp"
 #include "decode_ops.hpp"
 
@@ -31,22 +36,26 @@ struct Args16 {
   int top_k, gather, n, k, walkers, chunk;   // chunk: groups of x in LDS at a time
 };
 
-// LDS: fragments [chunk][MT][4][64] x 16 bytes, then sums [chunk][MT][16].
-constexpr int frag_bytes(int mt) { return mt * 4096; }
-constexpr int group_bytes(int mt) { return mt * (4096 + 64); }
+constexpr int WAVES = 8, NT = 2;
+// LDS: fragments [chunk][MT][4 pieces][16 XR] x 16 bytes (XR rows to an
+// m-tile: 16, or 4 where a tile holds at most 4 places), then sums
+// [chunk][MT][XR], then (KS > 1) the waves' accumulators.
+constexpr int frag_bytes(int mt, int xr) { return mt * 256 * xr; }
+constexpr int group_bytes(int mt, int xr) { return mt * (256 * xr + 4 * xr); }
+constexpr int red_bytes(int mt, int ks) { return ks > 1 ? WAVES * NT * mt * 1024 : 0; }
 
 // The slot of row r's 16-byte piece c (k 8 c of the group) within a group's
-// 256 slots: piece 4 s + q of fragment s belongs to lanes of quarter q, which
-// read 16 rows in 16 slots of their own; rows are XORed with the piece so
-// that a row's 16 pieces, written together, fall on different banks.
-__device__ __forceinline__ int piece_slot(int r, int c) { return c * 16 + (r ^ c); }
+// slots: piece 4 s + q of fragment s belongs to lanes of quarter q, which read
+// XR rows in XR slots of their own; rows are XORed with the piece so that a
+// row's pieces, written together, fall on different banks.
+template <int XR>
+__device__ __forceinline__ int piece_slot(int r, int c) { return c * XR + (r ^ (c & (XR - 1))); }
 
-// NT weight tiles at a time: with silu_mul a gate tile and its up tile, else
-// one tile or two neighbours.
-template <int MT, int NT, int W, bool kSilu, bool kBF16Out>
-__global__ __launch_bounds__(512, 2) void moe_w4a16_kernel(Args16 A) {
+template <int MT, int XR, int KS, int W, bool kSilu, bool kBF16Out>
+__global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void moe_w4a16_kernel(Args16 A) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  constexpr int TALL = 16 * MT, WAVES = 8;
+  static_assert(XR == 16 || MT == 1, "tiles of 4 places are one m-tile");
+  constexpr int TALL = MT == 1 ? XR : 16 * MT, FB = frag_bytes(MT, XR);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int walker = blockIdx.x % A.walkers;
@@ -54,7 +63,7 @@ __global__ __launch_bounds__(512, 2) void moe_w4a16_kernel(Args16 A) {
   if (tile.group < 0) return;
   const int G = A.k / 128, T = A.n / 16;
   const int n_out = kSilu ? A.n / 2 : A.n;
-  const int units = kSilu ? T / 2 : (T + NT - 1) / NT;   // of NT weight tiles
+  const int units = kSilu ? T / 2 : (T + 1) / 2;   // of two weight tiles
   const int q = lane >> 4, r = lane & 15;
 
   if (tile.group == A.plan.groups) {   // rows without an expert: zeros
@@ -67,14 +76,40 @@ __global__ __launch_bounds__(512, 2) void moe_w4a16_kernel(Args16 A) {
     return;
   }
   const uint8_t* blob = A.experts + tile.group * A.blob_stride;
-  if (!blob_matches(blob, 1, A.n, A.k)) return;
+  const uint8_t* codes = blob + A.codes_off;
+  const uint8_t* scales = blob + A.sc_off;
 
-  float* const sums = reinterpret_cast<float*>(smem + size_t(A.chunk) * frag_bytes(MT));
+  // units of this wave: u0, u0 + step, ...
+  const int u0 = KS > 1 ? walker * (WAVES / KS) + wave / KS : walker * WAVES + wave;
+  const int step = A.walkers * WAVES;
+  const int mine = u0 < units ? KS > 1 ? 1 : (units - u0 + step - 1) / step : 0;
+  const bool once = A.chunk >= G;            // all of x fits
+  const int span = once ? mine : 1;          // units in a row over one piece of x
+
+  struct Batch {
+    uint4 w[W][NT];
+    uint2 s[W][NT];
+  };
+  // strand j of unit u: with silu_mul a gate tile and its up tile, else two
+  // neighbours
+  auto load = [&](Batch& B, int u, int g0, int g1) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int t = kSilu ? u + j * (T / 2) : min(u * NT + j, T - 1);
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const int64_t at = int64_t(t) * G + min(g0 + i, g1 - 1);
+        B.w[i][j] = load_nt16(codes + at * 1024 + lane * 16);
+        B.s[i][j] = *reinterpret_cast<const uint2*>(scales + at * 32 + 8 * q);
+      }
+    }
+  };
+
+  float* const sums = reinterpret_cast<float*>(smem + size_t(A.chunk) * FB);
   // the rows of groups [c0, c1) into LDS: 16 lanes to a row's group
   auto stage = [&](int c0, int c1) {
-    const int per_row = c1 - c0;
     const int rows = (tile.count + 3) / 4;
-    for (int i = wave; i < rows * per_row; i += WAVES) {
+    for (int i = wave; i < rows * (c1 - c0); i += WAVES) {
       const int g = i / rows, row = 4 * (i % rows) + q;
       const int place = tile.first + min(row, tile.count - 1);
       int64_t from = place;
@@ -87,45 +122,33 @@ __global__ __launch_bounds__(512, 2) void moe_w4a16_kernel(Args16 A) {
         s += __uint_as_float(d[j] << 16) + __uint_as_float(d[j] & 0xFFFF0000u);
 #pragma unroll
       for (int m = 8; m; m /= 2) s += __shfl_xor(s, m);
-      *reinterpret_cast<uint4*>(smem + g * frag_bytes(MT) + (row >> 4) * 4096 + piece_slot(row & 15, r) * 16) = v;
-      if (r == 0) sums[(g * MT + (row >> 4)) * 16 + (row & 15)] = -136.0f * s;
+      const int mt = XR == 16 ? row >> 4 : 0, rr = XR == 16 ? row & 15 : row;
+      *reinterpret_cast<uint4*>(smem + g * FB + mt * (256 * XR) + piece_slot<XR>(rr, r) * 16) = v;
+      if (r == 0) sums[(g * MT + mt) * XR + rr] = -136.0f * s;
     }
   };
   const uint32_t nib_mask = vconst(0x000F000Fu), bf16_128 = vconst(0x43004300u);
-  const uint8_t* codes = blob + A.codes_off;
-  const uint8_t* scales = blob + A.sc_off;
-
-  struct Batch {
-    uint4 w[W][NT];
-    uint2 s[W][NT];
-  };
-  // first weight tile of unit u's strand j
-  auto tile_of = [&](int u, int j) { return kSilu ? u + j * (T / 2) : min(u * NT + j, T - 1); };
-  auto load = [&](Batch& B, int u, int g0, int g1) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int64_t t = tile_of(u, j);
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const int64_t at = t * G + min(g0 + i, g1 - 1);
-        B.w[i][j] = load_nt16(codes + at * 1024 + lane * 16);
-        B.s[i][j] = *reinterpret_cast<const uint2*>(scales + at * 32 + 8 * q);
-      }
-    }
-  };
-  floatx4 tot[NT][MT];
+  const int rl = XR == 16 ? r : min(r, XR - 1);   // lanes past a tile of 4 read its last row
   int off[4];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) off[s] = piece_slot(r, 4 * s + q) * 16;
+  for (int s = 0; s < 4; ++s) off[s] = piece_slot<XR>(rl, 4 * s + q) * 16;
+
+  floatx4 tot[NT][MT];
+  auto clear = [&]() {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) tot[j][m] = floatx4{0.f, 0.f, 0.f, 0.f};
+  };
   auto compute = [&](const Batch& B, int g0, int g1, int c0) {
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       if (g0 + i >= g1) break;   // wave-uniform
-      const uint8_t* fr = smem + (g0 + i - c0) * frag_bytes(MT);
+      const uint8_t* fr = smem + (g0 + i - c0) * FB;
       floatx4 acc[NT][MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const float z = sums[((g0 + i - c0) * MT + m) * 16 + r];
+        const float z = sums[((g0 + i - c0) * MT + m) * XR + rl];
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[j][m] = floatx4{z, z, z, z};
       }
@@ -134,7 +157,7 @@ __global__ __launch_bounds__(512, 2) void moe_w4a16_kernel(Args16 A) {
         bf16x8_t f[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          f[m] = as_bf16x8(*reinterpret_cast<const u32x4*>(fr + m * 4096 + off[s]));
+          f[m] = as_bf16x8(*reinterpret_cast<const u32x4*>(fr + m * (256 * XR) + off[s]));
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const uint32_t d = s == 0 ? B.w[i][j].x : s == 1 ? B.w[i][j].y : s == 2 ? B.w[i][j].z : B.w[i][j].w;
@@ -182,63 +205,100 @@ __global__ __launch_bounds__(512, 2) void moe_w4a16_kernel(Args16 A) {
     }
   };
 
-  const int rounds = (units + WAVES * A.walkers - 1) / (WAVES * A.walkers);
-  const bool once = A.chunk >= G;
-  if (once) {
-    stage(0, G);
-    __syncthreads();
+  Batch P, Q;
+  const uint32_t hdr = header_word(blob);   // tested before the first store
+  bool ok = false;
+  clear();
+  const int most = KS > 1 ? 1 : (units + step - 1) / step;   // units of the block's first wave, at least
+  for (int rd = 0; rd < (once ? 1 : most); ++rd) {
+    for (int c0 = 0; c0 < G; c0 += A.chunk) {
+      const int c1 = min(c0 + A.chunk, G);
+      // this wave's part of the piece
+      const int ga = KS > 1 ? c0 + (c1 - c0) * (wave % KS) / KS : c0;
+      const int gb = KS > 1 ? c0 + (c1 - c0) * (wave % KS + 1) / KS : c1;
+      const bool busy = rd < mine && ga < gb;
+      int u = u0 + rd * step, g = ga;           // what P holds
+      const int u_end = u0 + (rd + span) * step;
+      if (busy) load(P, u, g, gb);
+      if (rd + c0 > 0) __syncthreads();         // the piece before is read
+      stage(c0, c1);
+      __syncthreads();
+      if (rd + c0 == 0) ok = header_word_ok(hdr, 1, A.n, A.k);
+      if (!busy) continue;
+      // steps of W groups, the next one's loads under way, over tiles' ends
+      auto walk = [&](const Batch& now, Batch& next) {
+        int nu = u, ng = g + W;
+        if (ng >= gb) nu += step, ng = ga;
+        load(next, min(nu, u_end - step), ng, gb);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(now, g, gb, c0);
+        if (ng == ga && KS == 1 && c1 == G) {
+          if (ok) finish(u);
+          clear();
+        }
+        u = nu;
+        g = ng;
+      };
+      while (u < u_end) {
+        walk(P, Q);
+        if (u >= u_end) break;
+        walk(Q, P);
+      }
+    }
   }
-  for (int rd = 0; rd < rounds; ++rd) {
-    const int u = (rd * A.walkers + walker) * WAVES + wave;
+  if constexpr (KS > 1) {
+    floatx4* const red = reinterpret_cast<floatx4*>(smem + size_t(A.chunk) * group_bytes(MT, XR));
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) tot[j][m] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int c0 = 0; c0 < G; c0 += A.chunk) {
-      const int c1 = min(c0 + A.chunk, G);
-      if (!once) {
-        __syncthreads();   // the chunk before is read
-        stage(c0, c1);
-        __syncthreads();
-      }
-      if (u >= units) continue;
-      Batch P, Q;
-      load(P, u, c0, c1);
-      for (int g0 = c0; g0 < c1; g0 += 2 * W) {
-        load(Q, u, min(g0 + W, c1 - 1), c1);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(P, g0, c1, c0);
-        load(P, u, min(g0 + 2 * W, c1 - 1), c1);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(Q, g0 + W, c1, c0);
-      }
-    }
-    if (u < units) finish(u);
+      for (int m = 0; m < MT; ++m) red[((wave * NT + j) * MT + m) * 64 + lane] = tot[j][m];
+    __syncthreads();
+    if (wave % KS || !mine || !ok) return;
+#pragma unroll
+    for (int w = 1; w < KS; ++w)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) tot[j][m] += red[(((wave + w) * NT + j) * MT + m) * 64 + lane];
+    finish(u0);
   }
 }
 
-template <int MT, int NT, int W, bool kSilu>
-hipError_t launch16(const Args16& a, int y_dtype, int blocks, hipStream_t s) {
-  const size_t lds = size_t(a.chunk) * group_bytes(MT);
-  static std::atomic<int> done[2][64];
+template <int MT, int XR, int KS>
+hipError_t launch16(Args16 a, const MoeGemm& g, hipStream_t s) {
+  constexpr int W = 2, TALL = MT == 1 ? XR : 16 * MT;
+  const int G = g.k / 128, T = g.n / 16;
+  const int most = (160 * 1024 - red_bytes(MT, KS)) / group_bytes(MT, XR);
+  a.chunk = G < most ? G : most;
+  const int64_t tiles = most_tiles(g.plan.rows, g.plan.groups, TALL);
+  const int64_t units = g.silu_mul ? T / 2 : (T + 1) / 2;
+  const int64_t widest = (units + WAVES / KS - 1) / (WAVES / KS);
+  const int cus = device_cu_count();
+  int64_t walkers = widest;
+  if (KS == 1) {   // two blocks to a CU, as far as there are units for their waves
+    walkers = (2 * (cus > 0 ? cus : 256) + tiles - 1) / tiles;
+    if (walkers > widest) walkers = widest;
+  }
+  a.walkers = int(walkers);
+  const size_t lds = size_t(a.chunk) * group_bytes(MT, XR) + red_bytes(MT, KS);
+  static std::atomic<int> done[4][64];
   auto run = [&](auto kern, std::atomic<int>* flag) {
     const hipError_t e = lds_limit_once(flag, reinterpret_cast<const void*>(kern), 160 * 1024);
     if (e != hipSuccess) return e;
-    kern<<<blocks, 512, lds, s>>>(a);
+    kern<<<unsigned(tiles * walkers), 512, lds, s>>>(a);
     return hipGetLastError();
   };
-  return y_dtype == 1 ? run(moe_w4a16_kernel<MT, NT, W, kSilu, true>, done[1])
-                      : run(moe_w4a16_kernel<MT, NT, W, kSilu, false>, done[0]);
+  if (g.silu_mul)
+    return g.y_dtype == 1 ? run(moe_w4a16_kernel<MT, XR, KS, W, true, true>, done[0])
+                          : run(moe_w4a16_kernel<MT, XR, KS, W, true, false>, done[1]);
+  return g.y_dtype == 1 ? run(moe_w4a16_kernel<MT, XR, KS, W, false, true>, done[2])
+                        : run(moe_w4a16_kernel<MT, XR, KS, W, false, false>, done[3]);
 }
 
 }  // namespace
 
 hipError_t launch_moe_gemm_w4a16(const MoeGemm& g, const void* x, hipStream_t s) {
   const BlobLayout L = blob_layout(1, g.n, g.k);
-  // the height of a tile: the rows that an expert has on average
-  const int64_t mean = g.plan.rows / g.plan.groups;
-  const int mt = mean > 32 ? 4 : mean > 12 ? 2 : 1;
-  const int G = g.k / 128;
   Args16 a{};
   a.plan = g.plan;
   a.x = static_cast<const uint16_t*>(x);
@@ -251,23 +311,22 @@ hipError_t launch_moe_gemm_w4a16(const MoeGemm& g, const void* x, hipStream_t s)
   a.gather = g.gather;
   a.n = g.n;
   a.k = g.k;
-  const int most = 160 * 1024 / group_bytes(mt);
-  a.chunk = G < most ? G : most;
-  const int64_t tiles = most_tiles(g.plan.rows, g.plan.groups, 16 * mt);
-  const int cus = device_cu_count();
-  const int64_t units = (g.n / 16 + 1) / 2;
-  int64_t walkers = (2 * (cus > 0 ? cus : 256) + tiles - 1) / tiles;
-  if (walkers > (units + 7) / 8) walkers = (units + 7) / 8;
-  a.walkers = int(walkers);
-  const int blocks = int(tiles * walkers);
-  if (g.silu_mul) {
-    if (mt == 1) return launch16<1, 2, 4, true>(a, g.y_dtype, blocks, s);
-    if (mt == 2) return launch16<2, 2, 4, true>(a, g.y_dtype, blocks, s);
-    return launch16<4, 2, 4, true>(a, g.y_dtype, blocks, s);
+  // Up to 4 tokens: no expert has more rows (a token chooses it once).
+  if (g.plan.rows <= 4 * g.top_k) {
+    // waves to a pair of weight tiles: until 8 waves to a CU have work, at
+    // least 4 groups each
+    const int cus = device_cu_count();
+    const int64_t pairs = most_tiles(g.plan.rows, g.plan.groups, 4) * ((g.n / 16 + 1) / 2);
+    int ks = 1;
+    while (ks < 8 && pairs * ks < 8 * (cus > 0 ? cus : 256) && g.k / 128 >= 8 * ks) ks *= 2;
+    if (ks == 8) return launch16<1, 4, 8>(a, g, s);
+    if (ks == 4) return launch16<1, 4, 4>(a, g, s);
+    if (ks == 2) return launch16<1, 4, 2>(a, g, s);
+    return launch16<1, 4, 1>(a, g, s);
   }
-  if (mt == 1) return launch16<1, 2, 4, false>(a, g.y_dtype, blocks, s);
-  if (mt == 2) return launch16<2, 2, 4, false>(a, g.y_dtype, blocks, s);
-  return launch16<4, 2, 4, false>(a, g.y_dtype, blocks, s);
+  // the height of a tile: by the rows that an expert has on average
+  if (g.plan.rows / g.plan.groups > 12) return launch16<2, 16, 1>(a, g, s);
+  return launch16<1, 16, 1>(a, g, s);
 }
 
 }  // namespace qlin

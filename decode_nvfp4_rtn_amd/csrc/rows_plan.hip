@@ -4,7 +4,7 @@
 //
 // Plan: a stable counting sort.  A block takes a run of rows and counts its
 // groups; a second launch adds up the counts of the blocks before its own
-// (every block for itself: at most 256 blocks' counts, read from L2), and
+// (every block for itself: at most 128 blocks' counts, read from L2), and
 // writes each row's place.  Within a wave a row's rank among the rows of its
 // group comes from ballots over the bits of the group's number.  One block's
 // worth of rows takes one launch.  Whole numbers only, counted by integer
@@ -16,8 +16,8 @@
 namespace qlin {
 namespace {
 
-constexpr int THREADS = 512, WAVES = THREADS / 64;
-constexpr int kMostBlocks = 256;
+constexpr int THREADS = 1024, WAVES = THREADS / 64;
+constexpr int kMostBlocks = 128;
 
 struct PlanSmem {
   int base[kMostGroups + 1];             // next place of each group
@@ -37,12 +37,7 @@ __device__ __forceinline__ void scan_groups(PlanSmem& sm, int groups) {
   for (int g0 = 0; g0 <= groups; g0 += THREADS) {
     const int g = g0 + threadIdx.x;
     const int own = g <= groups ? sm.base[g] : 0;
-    int sum = own;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(sum, d);
-      if (lane >= d) sum += v;
-    }
+    const int sum = wave_prefix(own);
     if (lane == 63) sm.carry[wave] = sum;
     __syncthreads();
     int at = before;
@@ -141,32 +136,29 @@ __global__ __launch_bounds__(THREADS) void group_place_kernel(const int32_t* __r
                                                               int32_t* __restrict__ where,
                                                               int32_t* __restrict__ offsets) {
   __shared__ PlanSmem sm;
+  __shared__ int before[kMostGroups + 1];   // of the blocks before this one
   const int own = blockIdx.x;
-  int mine[3] = {0, 0, 0};   // of the blocks before, for this thread's groups
-  static_assert(3 * THREADS > kMostGroups, "groups of a thread");
-#pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    const int g = j * THREADS + threadIdx.x;
-    if (g > groups) break;
-    int all = 0, before = 0;
+  for (int i = threadIdx.x; i <= groups; i += THREADS) sm.base[i] = before[i] = 0;
+  __syncthreads();
+  // several threads to a group, each a share of the blocks
+  const int wide = min((groups + 64) / 64 * 64, THREADS), shares = THREADS / wide;
+  const int share = threadIdx.x / wide;
+  for (int g = threadIdx.x % wide; g <= groups && share < shares; g += wide) {
+    int all = 0, mine = 0;
 #pragma unroll 8
-    for (int b = 0; b < blocks; ++b) {
+    for (int b = share; b < blocks; b += shares) {
       const int c = counts[int64_t(b) * (groups + 1) + g];
       all += c;
-      before += b < own ? c : 0;
+      mine += b < own ? c : 0;
     }
-    mine[j] = before;
-    sm.base[g] = all;
+    atomicAdd(&sm.base[g], all);
+    atomicAdd(&before[g], mine);
   }
   __syncthreads();
   scan_groups(sm, groups);
   if (own == 0) write_offsets(sm, groups, offsets);
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    const int g = j * THREADS + threadIdx.x;
-    if (g <= groups) sm.base[g] += mine[j];
-  }
+  for (int i = threadIdx.x; i <= groups; i += THREADS) sm.base[i] += before[i];
   __syncthreads();
   const int64_t begin = int64_t(own) * per_block;
   place_rows(sm, ids, int(begin), int(min(begin + per_block, int64_t(rows))), groups, order, where);
@@ -182,12 +174,6 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
 
 __device__ __forceinline__ float value_of(uint32_t r) {
   return __uint_as_float(r & 0x80000000u ? r & 0x7FFFFFFFu : ~r);
-}
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 32; d; d /= 2) v = max(v, uint32_t(__shfl_xor(int(v), d)));
-  return v;
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -240,18 +226,23 @@ __global__ __launch_bounds__(THREADS) void route_kernel(
     int expert = -1;
     for (int j = 0; j < top_k; ++j) {
       uint32_t best = rank[0];
-      int at = lane;
 #pragma unroll
-      for (int i = 1; i < PER; ++i)
-        if (rank[i] > best) best = rank[i], at = i * 64 + lane;
+      for (int i = 1; i < PER; ++i) best = max(best, rank[i]);
       const uint32_t m = wave_max(best);
       if (m == 0) break;
-      // the lowest expert of those with the largest rank
-      const int e = int(~wave_max(best == m ? ~uint32_t(at) : 0u));
-      if (lane == j) chosen = m, expert = e;
+      // the lowest expert of those with the largest rank: the first register,
+      // then the first lane that holds it
+      int e = -1;
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i * 64 + lane == e) rank[i] = 0;
+      for (int i = 0; i < PER; ++i) {
+        if (e >= 0) break;
+        const uint64_t with = __ballot(rank[i] == m);
+        if (!with) continue;
+        const int l = __builtin_ctzll(with);
+        e = i * 64 + l;
+        if (lane == l) rank[i] = 0;
+      }
+      if (lane == j) chosen = m, expert = e;
     }
     const float w = chosen ? term(chosen) : 0.0f;
     if (renormalize) total = wave_sum(lane < top_k ? w : 0.0f);

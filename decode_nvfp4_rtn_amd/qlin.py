@@ -718,17 +718,32 @@ def kv_commit(cache, cu_q, kv_lens, block_table, path, stream=None):
 class RowPlan:
     """The rows of a batch in the order of the weights they meet, as
     ``group_rows`` or ``moe_route`` makes it: int32 tensors ``order`` [rows] (the
-    row at each place), ``where`` (each row's place, in the shape of the choices)
-    and ``offsets`` [groups + 1] (where each group's run begins; rows of no group
-    from offsets[groups] on).  ``tokens`` rows of ``top_k`` choices each."""
+    row at each place), ``where`` [tokens, top_k] (each row's place) and
+    ``offsets`` [groups + 1] (where each group's run begins; rows of no group
+    from offsets[groups] on).  ``tokens`` rows of ``top_k`` choices each.  The
+    three are views of one allocation, made when asked for."""
 
-    __slots__ = ("order", "where", "offsets", "groups", "tokens", "top_k", "device")
+    __slots__ = ("groups", "tokens", "top_k", "device", "_data", "_order", "_where", "_offsets")
 
     def __init__(self, groups, tokens, top_k, dev, stream=None):
         self.groups, self.tokens, self.top_k, self.device = groups, tokens, top_k, dev
-        self.order = _new((tokens * top_k,), torch.int32, dev, stream)
-        self.where = _new((tokens, top_k), torch.int32, dev, stream)
-        self.offsets = _new((groups + 1,), torch.int32, dev, stream)
+        rows = tokens * top_k
+        self._data = _new((2 * rows + groups + 1,), torch.int32, dev, stream)
+        at = self._data.data_ptr()
+        self._order, self._where, self._offsets = at, at + 4 * rows, at + 8 * rows
+
+    @property
+    def order(self):
+        return self._data[:self.tokens * self.top_k]
+
+    @property
+    def where(self):
+        rows = self.tokens * self.top_k
+        return self._data[rows:2 * rows].view(self.tokens, self.top_k)
+
+    @property
+    def offsets(self):
+        return self._data[2 * self.tokens * self.top_k:]
 
 
 def _call(name, dev, *args):
@@ -787,8 +802,8 @@ def group_rows(ids, groups, plan=None, workspace=None, stream=None):
     plan = _for_plan(plan, groups, tokens, top_k, dev, stream)
     rows = tokens * top_k
     at, have, keep = _workspace(workspace, _lib.group_rows_workspace(rows, groups), dev, stream)
-    _call("group_rows", dev, ids.data_ptr(), rows, groups, plan.order.data_ptr(), plan.where.data_ptr(),
-          plan.offsets.data_ptr(), at, have, _queue(stream, dev))
+    _call("group_rows", dev, ids.data_ptr(), rows, groups, plan._order, plan._where,
+          plan._offsets, at, have, _queue(stream, dev))
     return plan
 
 
@@ -824,7 +839,7 @@ def moe_route(logits, top_k, renormalize=True, ids=None, weights=None, plan=None
     at, have, keep = _workspace(workspace, _lib.moe_route_workspace(tokens, experts, top_k), dev, stream)
     _call("moe_route", dev, logits.data_ptr(), dt, tokens, experts, stride if tokens > 1 else experts, top_k,
           QL_ROUTE_RENORMALIZE if renormalize else 0, ids.data_ptr(), weights.data_ptr(),
-          plan.order.data_ptr(), plan.where.data_ptr(), plan.offsets.data_ptr(), at, have,
+          plan._order, plan._where, plan._offsets, at, have,
           _queue(stream, dev))
     return ids, weights, plan
 
@@ -882,8 +897,8 @@ def moe_gemm_w4a16(x, experts, plan, n, k, gather=True, silu_mul=False, y=None,
     n, k, rows, flags, y, dt = _product(plan, n, k, gather, silu_mul, y, out_dtype, stream)
     x_at = _operand(x, "x", torch.bfloat16, rows, k, plan.device)
     step = _experts(experts, plan, QL_INT4_G128, n, k)
-    _call("moe_gemm_w4a16", plan.device, x_at, experts.data_ptr(), plan.groups, step, plan.order.data_ptr(),
-          plan.offsets.data_ptr(), plan.tokens * plan.top_k, plan.top_k, n, k, flags,
+    _call("moe_gemm_w4a16", plan.device, x_at, experts.data_ptr(), plan.groups, step, plan._order,
+          plan._offsets, plan.tokens * plan.top_k, plan.top_k, n, k, flags,
           y.data_ptr(), dt, _queue(stream, plan.device))
     return y
 
@@ -898,8 +913,8 @@ def moe_gemm_w4a4(a_codes, a_scales, a_tensor_scale, experts, plan, n, k, gather
     s_at = _operand(a_scales, "a_scales", torch.uint8, rows, k // 16, dev)
     t_at = _vector(a_tensor_scale, "a_tensor_scale", torch.float32, dev, 1)
     step = _experts(experts, plan, QL_NVFP4, n, k)
-    _call("moe_gemm_w4a4", dev, c_at, s_at, t_at, experts.data_ptr(), plan.groups, step, plan.order.data_ptr(),
-          plan.offsets.data_ptr(), plan.tokens * plan.top_k, plan.top_k, n, k, flags,
+    _call("moe_gemm_w4a4", dev, c_at, s_at, t_at, experts.data_ptr(), plan.groups, step, plan._order,
+          plan._offsets, plan.tokens * plan.top_k, plan.top_k, n, k, flags,
           y.data_ptr(), dt, _queue(stream, dev))
     return y
 
@@ -920,7 +935,7 @@ def moe_combine(rows, plan, weights, out=None, out_dtype=torch.bfloat16, stream=
     dt = _XDT.get(out.dtype)
     if dt is None:
         raise ValueError("out must be float32 or bfloat16")
-    _call("moe_combine", dev, rows.data_ptr(), _XDT[rows.dtype], plan.where.data_ptr(), plan.offsets.data_ptr(),
+    _call("moe_combine", dev, rows.data_ptr(), _XDT[rows.dtype], plan._where, plan._offsets,
           plan.groups, w_at, plan.tokens, plan.top_k, n, out.data_ptr(), dt,
           _queue(stream, dev))
     return out
@@ -973,7 +988,7 @@ def lora_add(y, x, a, b, plan, scale=None, out=None, workspace=None, stream=None
         raise ValueError(f"out must be [{rows}, {n}], got {list(out.shape)}")
     at, have, keep = _workspace(workspace, _lib.lora_add_workspace(rows, adapters, rank, k), dev, stream)
     _call("lora_add", dev, y.data_ptr(), ys, x.data_ptr(), xs, a.data_ptr(), b.data_ptr(), s_at, adapters, rank,
-          plan.order.data_ptr(), plan.offsets.data_ptr(), rows, n, k, out.data_ptr(), os_,
+          plan._order, plan._offsets, rows, n, k, out.data_ptr(), os_,
           _XDT[y.dtype], at, have, _queue(stream, dev))
     return out
 

@@ -51,15 +51,15 @@ def test_group_rows(lib):
                        (dict(rows=0, offsets=0), QL_EINVAL)):
         assert run(**kw) == status, kw
     # one block's rows need no workspace; more need their blocks' counts
-    assert lib.group_rows_workspace(512, 1024) == 0
-    need = lib.group_rows_workspace(513, 7)
+    assert lib.group_rows_workspace(1024, 1024) == 0
+    need = lib.group_rows_workspace(1025, 7)
     assert need == 2 * 8 * 4
-    assert run(rows=513) == QL_EINVAL
-    assert run(rows=513, ws=E + 8, wsb=need) == QL_EALIGN
-    assert run(rows=513, ws=E, wsb=need - 1) == QL_EWORKSPACE
+    assert run(rows=1025) == QL_EINVAL
+    assert run(rows=1025, ws=E + 8, wsb=need) == QL_EALIGN
+    assert run(rows=1025, ws=E, wsb=need - 1) == QL_EWORKSPACE
     # the counts stay small however many rows
-    assert 0 < lib.group_rows_workspace(MOST, 1024) <= 256 * 1025 * 4
-    for bad in ((-1, 7), (MOST + 1, 7), (600, 0), (600, 1025)):
+    assert 0 < lib.group_rows_workspace(MOST, 1024) <= 128 * 1025 * 4
+    for bad in ((-1, 7), (MOST + 1, 7), (2000, 0), (2000, 1025)):
         assert lib.group_rows_workspace(*bad) == 0
 
 
@@ -76,9 +76,9 @@ def test_route(lib):
                        (dict(experts=100, stride=100, top_k=65), QL_ESHAPE),
                        (dict(tokens=MOST // 2 + 1), QL_ESHAPE), (dict(x=A + 2), QL_EALIGN),
                        (dict(dt=QBF16, x=A + 1), QL_EALIGN), (dict(weights=C + 2), QL_EALIGN),
-                       (dict(tokens=300), QL_EINVAL)):
+                       (dict(tokens=600), QL_EINVAL)):
         assert run(**kw) == status, kw
-    assert lib.moe_route_workspace(256, 8, 2) == 0 < lib.moe_route_workspace(257, 8, 2)
+    assert lib.moe_route_workspace(512, 8, 2) == 0 < lib.moe_route_workspace(513, 8, 2)
     assert lib.moe_route_workspace(MOST // 2 + 1, 8, 2) == 0 == lib.moe_route_workspace(5, 8, 65)
 
 
