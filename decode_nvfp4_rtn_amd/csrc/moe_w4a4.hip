@@ -9,19 +9,25 @@
 // v_mfma_f32_16x16x32_f16, binary32 accumulation, every code dequantized once
 // per block.
 //
-// Block 256 (weight rows) x 256 (places of one expert), 8 wavefronts in 2 x 4,
-// each 128 x 64; K advances 64 per stage, the fp16 tiles double buffered in
-// LDS, the codes of stage s + 2 loaded at the start of stage s.  A thread
+// Block 256 (weight rows) x up to 256 (places of one expert), 8 wavefronts; K
+// advances 64 per stage, the fp16 tiles double buffered in LDS.  A thread
 // dequantizes one weight row or one activation row, whose address it looks up
 // once: activation rows come in the plan's order or through it from the
-// tokens.  Experts' runs are ragged: a wave whose 64 places lie past the run
-// skips its products (the block's waves then share fewer MFMAs, not fewer
-// weights), and one whose 64 activation rows do skips their dequantization.
+// tokens.  Codes are loaded 128 of k at a time (64 bytes of a row) into a ring
+// of RING such pairs of stages, 2 RING - 3 stages before their dequantization.
+//
+// Experts' runs are ragged.  A tile of more than 128 places has its waves 2 x
+// 4, each 128 x 64, as the dense kernel; a lower one 4 x 2, each 64 x 64, one
+// of a run's first 64 places on each SIMD, so that half the products take half
+// the time.  A wave whose 64 places lie past the run skips its products, one
+// whose activation rows do their dequantization.  Low tiles do little for each
+// weight and wait for memory: with their 64 accumulators the ring can be
+// deeper.
 //
 // With silu_mul the 256 weight rows are 128 gate rows and their 128 up rows,
 // alternating by 16, so that a wave holds both halves of an output in the same
-// lane and the product's epilogue writes h: a pass over 4 n bytes a place less
-// than writing g and u and reading them again.
+// lane and the epilogue writes h: 4 n bytes a place less to memory and back
+// than g and u.
 #include "moe.hpp"
 #include "w4a4_ops.hpp"
 
@@ -41,43 +47,28 @@ struct Args4 {
   int top_k, gather, n, k;
 };
 
-template <bool kSilu, bool kBF16Out>
-__global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // [2][W tile, X tile]
-  constexpr int TN = 8, TM = 4;
+// Columns [n0, n0 + cols) of a tile's rows, zeroed: pairs without an expert.
+template <bool kBF16Out>
+__device__ __forceinline__ void zero_rows(void* y, const RowTile& tile, int n0, int cols, int n_out) {
+  constexpr int size = kBF16Out ? 2 : 4;
+  const int per = cols * size / 16;
+  for (int i = threadIdx.x; i < tile.count * per; i += 512)
+    reinterpret_cast<uint4*>(static_cast<uint8_t*>(y) +
+                             (int64_t(tile.first + i / per) * n_out + n0) * size)[i % per] = make_uint4(0, 0, 0, 0);
+}
+
+// One tile.  WN wavefronts along the weight rows, 8 / WN along the places.
+template <int WN, int RING, bool kSilu, bool kBF16Out>
+__device__ __forceinline__ void w4a4_tile(const Args4& A, const RowTile& tile, int n0, uint8_t* smem) {
+  constexpr int TN = 16 / WN, TM = 4;   // 16 x 16 MFMA tiles of a wave
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = A.n, K = A.k, H = N / 2;
   const int n_out = kSilu ? H : N;
-  constexpr int OUT_WIDE = kSilu ? WIDE / 2 : WIDE;
-
-  // tile: XCD-major over the tiles that there are, groups of GROUP_M row
-  // tiles, weight tiles in order within a group
-  const int tiles_n = (n_out + OUT_WIDE - 1) / OUT_WIDE;
-  const int tiles_m = count_tiles(A.plan, TALL);
-  const int total = tiles_m * tiles_n, per = (total + 7) / 8;
-  const int in_xcd = blockIdx.x >> 3;
-  const int t = (blockIdx.x & 7) * per + in_xcd;
-  if (in_xcd >= per || t >= total) return;
-  const int in_group = GROUP_M * tiles_n;
-  const int first_m = (t / in_group) * GROUP_M;
-  const int gsz = min(tiles_m - first_m, GROUP_M);
-  const RowTile tile = find_tile(A.plan, TALL, first_m + (t % in_group) % gsz);
-  const int n0 = ((t % in_group) / gsz) * OUT_WIDE;   // first output column
-  if (tile.group < 0) return;
-
-  if (tile.group == A.plan.groups) {   // rows without an expert: zeros
-    const int cols = min(OUT_WIDE, n_out - n0) * (kBF16Out ? 2 : 4) / 16;
-    for (int i = tid; i < tile.count * cols; i += 512)
-      reinterpret_cast<uint4*>(static_cast<uint8_t*>(A.y) +
-                               (int64_t(tile.first + i / cols) * n_out + n0) * (kBF16Out ? 2 : 4))[i % cols] =
-          make_uint4(0, 0, 0, 0);
-    return;
-  }
   const uint8_t* blob = A.experts + tile.group * A.blob_stride;
   if (!blob_matches(blob, 0, N, K)) return;   // before any barrier: uniform
 
-  const int KT = K / 128, S = K / BK;
+  const int KT = K / 128;
   const __amdgpu_buffer_rsrc_t rcw = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(blob + A.wc_off), 0, 0x7FFFFFFF, 0x00020000);
   const __amdgpu_buffer_rsrc_t rsw = __builtin_amdgcn_make_buffer_rsrc(
@@ -86,16 +77,17 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
       const_cast<uint8_t*>(A.codes), 0, 0x7FFFFFFF, 0x00020000);
   const __amdgpu_buffer_rsrc_t rsx = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(A.scales), 0, 0x7FFFFFFF, 0x00020000);
-  // this thread's row: weight rows on the first four waves, places on the
-  // others; past the weights' or the run's end the last one (their products
-  // reach only outputs that are never stored)
-  const bool isw = wave < 4;
+  // this thread's row: four waves take the weight rows, four the places (low
+  // tiles: the waves with products take places); past the weights' or the
+  // run's end the last one (its products reach only outputs that are never
+  // stored)
+  const bool isw = WN == 2 ? wave < 4 : wave >= 4;
   const int lrow = tid & 255;
   uint32_t vc, vs;
   if (isw) {
     int wrow;
     if constexpr (kSilu) {
-      const int col = min(n0 + (lrow >> 7) * 64 + ((lrow >> 5) & 3) * 16 + (lrow & 15), H - 16 + (lrow & 15));
+      const int col = min(n0 + (lrow >> 5) * 16 + (lrow & 15), H - 16 + (lrow & 15));
       wrow = ((lrow >> 4) & 1) * H + col;
     } else {
       wrow = min(n0 + lrow, N - 16 + (lrow & 15));
@@ -110,29 +102,30 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
     vc = from * uint32_t(K / 2);
     vs = from * uint32_t(K / 16);
   }
-  const int wn = wave & 1, wm = wave >> 1;
+  const int wn = wave & (WN - 1), wm = wave / WN;
   const bool multiplies = wm * 64 < tile.count;
-  const bool dequantizes = isw || (wave - 4) * 64 < tile.count;
+  const bool dequantizes = isw || (wave & 3) * 64 < tile.count;
 
+  // codes and scales of 128 of k of this thread's row
   struct Regs {
-    uint4 c[2];
-    uint32_t sc;
+    u32x4 c[4];
+    uint32_t sc[2];
   };
-  Regs ra, rb;
+  Regs ring[RING];
   const __amdgpu_buffer_rsrc_t rc = isw ? rcw : rcx, rs = isw ? rsw : rsx;
-  auto gload = [&](Regs& R, int st) {
-    const int co = isw ? (st >> 1) * 1024 + (st & 1) * 32 : st * 32;
-    const int so = isw ? (st >> 1) * 128 + (st & 1) * 4 : st * 4;
-    const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(rc, vc, co, 0);
-    const u32x4 b = __builtin_amdgcn_raw_buffer_load_b128(rc, vc, co + 16, 0);
-    R.c[0] = make_uint4(a[0], a[1], a[2], a[3]);
-    R.c[1] = make_uint4(b[0], b[1], b[2], b[3]);
-    R.sc = __builtin_amdgcn_raw_buffer_load_b32(rs, vs, so, 0);
+  const int cstep = isw ? 1024 : 64, sstep = isw ? 128 : 8;
+  auto gload = [&](Regs& R, int p) {   // past the end: the last one again, never used
+    p = min(p, KT - 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) R.c[i] = __builtin_amdgcn_raw_buffer_load_b128(rc, vc, p * cstep + 16 * i, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) R.sc[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, vs, p * sstep + 4 * i, 0);
   };
   uint8_t* const own_row = smem + (isw ? 0 : TILE_BYTES) + lrow * RS;
-  auto dq_store = [&](const Regs& R, int buf, int d) {
-    *reinterpret_cast<u32x4*>(own_row + buf * 2 * TILE_BYTES + d * 16) =
-        dequant8(pick(R.c[d >> 2], d & 3), scale_h2(R.sc, d >> 1));
+  // eight values (of eight) of half `half` of a pair into LDS buffer `half`
+  auto dq_store = [&](const Regs& R, int half, int d) {
+    *reinterpret_cast<u32x4*>(own_row + half * 2 * TILE_BYTES + d * 16) =
+        dequant8(R.c[2 * half + (d >> 2)][d & 3], scale_h2(R.sc[half], d >> 1));
   };
 
   floatx4 acc[TN][TM];
@@ -141,20 +134,23 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  gload(ra, 0);
+#pragma unroll
+  for (int i = 0; i < RING; ++i) {
+    gload(ring[i], i);
+    __builtin_amdgcn_sched_barrier(0);   // in this order, which the waits below count on
+  }
   if (dequantizes) {
 #pragma unroll
-    for (int d = 0; d < 8; ++d) dq_store(ra, 0, d);
+    for (int d = 0; d < 8; ++d) dq_store(ring[0], 0, d);
   }
-  gload(rb, 1);   // K is a multiple of 128: an even number of stages
   __syncthreads();
 
   const int r = lane & 15, q = lane >> 4;
-  const int wbase = (wn * 128 + r) * RS + q * 16;
+  const int wbase = (wn * (TN * 16) + r) * RS + q * 16;
   const int xbase = (wm * 64 + r) * RS + q * 16;
 
-  // one stage: MFMAs on LDS buffer `buf` while `nxt` (the next stage's codes)
-  // is dequantized into the other buffer
+  // one stage: MFMAs on LDS buffer `buf` while half `buf ^ 1` of `nxt` is
+  // dequantized into the other buffer
   auto stage = [&](int buf, const Regs& nxt) {
     const uint8_t* wt = smem + buf * 2 * TILE_BYTES;
     const uint8_t* xt = wt + TILE_BYTES;
@@ -181,22 +177,30 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
         for (int j = 0; j < TM; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf, xf[j], acc[i][j], 0, 0, 0);
         const int it = s * TN + i;
-        if (it % 2 == 0) dq_store(nxt, buf ^ 1, it / 2);
+        if (it % (TN / 4) == 0) dq_store(nxt, buf ^ 1, it / (TN / 4));
         wf = wn_f;
       }
     }
   };
-  // prefetches are unconditional, their stage clamped to the last
-  for (int st = 0; st < S; st += 2) {
-    gload(ra, min(st + 2, S - 1));
-    __builtin_amdgcn_sched_barrier(0);
-    stage(0, rb);
+  // pair p lies in ring[p % RING]; its second half is dequantized during its
+  // first stage, after which its place in the ring is free.  On the last pair
+  // the second stage writes the idle buffer, which nothing reads again.
+  auto pair = [&](int p, int i) {
+    stage(0, ring[i]);
     __syncthreads();
-    gload(rb, min(st + 3, S - 1));
-    __builtin_amdgcn_sched_barrier(0);
-    stage(1, ra);
+    gload(ring[i], p + RING);
+    __builtin_amdgcn_sched_barrier(0);   // issue the loads here, not after the stage
+    stage(1, ring[(i + 1) % RING]);
     __syncthreads();
+  };
+  int p = 0;
+  for (; p + RING <= KT; p += RING) {
+#pragma unroll
+    for (int i = 0; i < RING; ++i) pair(p + i, i);
   }
+#pragma unroll
+  for (int i = 0; i < RING - 1; ++i)
+    if (p + i < KT) pair(p + i, i);
   if (!multiplies) return;   // no barrier follows
 
   const float stv = A.a_ts[0] * reinterpret_cast<const BlobHeader*>(blob)->tensor_scale;
@@ -227,6 +231,7 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
     // through a private LDS region, so that whole rows are stored (a lane
     // holds four columns of one row); a wave's LDS operations stay in order
     constexpr int ORS = TO * 32 + 32, LPR = TO * 2;   // row bytes, lanes to a row
+    static_assert(8 * 64 * ORS <= 4 * TILE_BYTES, "output staging fits in LDS");
     uint8_t* const ot = smem + wave * (64 * ORS);
 #pragma unroll
     for (int i = 0; i < TO; ++i)
@@ -258,6 +263,216 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
   }
 }
 
+template <bool kSilu, bool kBF16Out>
+__global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // [2][W tile, X tile]
+  const int n_out = kSilu ? A.n / 2 : A.n;
+  constexpr int OUT_WIDE = kSilu ? WIDE / 2 : WIDE;
+
+  // weight tiles in order within a row tile: consecutive blocks go to
+  // different XCDs, so each gets its share of every expert
+  const int tiles_n = (n_out + OUT_WIDE - 1) / OUT_WIDE;
+  const RowTile tile = find_tile(A.plan, TALL, blockIdx.x / tiles_n);
+  const int n0 = (blockIdx.x % tiles_n) * OUT_WIDE;   // first output column
+  if (tile.group < 0) return;
+
+  if (tile.group == A.plan.groups) {   // rows without an expert: zeros
+    zero_rows<kBF16Out>(A.y, tile, n0, min(OUT_WIDE, n_out - n0), n_out);
+    return;
+  }
+  if (tile.count > 128) w4a4_tile<2, 2, kSilu, kBF16Out>(A, tile, n0, smem);
+  else w4a4_tile<4, 4, kSilu, kBF16Out>(A, tile, n0, smem);
+}
+
+// Short runs: tiles of 16 TM places, one m-tile of 16 for each of TM products of
+// an operand, and weights that go from memory to a wave's registers and no
+// further.
+//
+// Block 8 waves x 2 weight tiles of 16 rows (with silu_mul a gate tile and its
+// up tile) x 16 TM places.  Of a weight tile's 128 of k a wave's load is one
+// contiguous KB, lane (row r, quarter q) k 32 q .. 32 q + 31; dword s of it is
+// the operand of step s, so step s contracts k 32 q + 8 s .. + 7 of each q, and
+// the activations' fragments lie in LDS in that order: a thread that
+// dequantizes 16 bytes of codes of a place stores one piece for each step,
+// lane after lane.  Activations are dequantized PIECE pairs (128 of k each) at
+// a time into the other of two buffers, one barrier to a piece; weights are
+// loaded RING pairs ahead.  16 TM x 128 of k of products to an operand of 16 x
+// 128: at 64 places the MFMAs take half the time of the weights' way from
+// memory.
+template <int TM, bool kSilu, bool kBF16Out>
+__global__ __launch_bounds__(512, 4) void moe_w4a4_low_kernel(Args4 A) {
+  constexpr int PIECE = 2, RING = 4, LOW = 16 * TM, FRAG = 1024;
+  static_assert(PIECE * TM % 8 == 0 || 8 % (PIECE * TM) == 0, "units of a piece over 8 waves");
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];   // [2][PIECE][TM][4][64 lanes] x 16 bytes
+  constexpr int BUF = PIECE * TM * 4 * FRAG;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n_out = kSilu ? A.n / 2 : A.n;
+  constexpr int OUT_WIDE = kSilu ? 128 : 256;
+  const int tiles_n = (n_out + OUT_WIDE - 1) / OUT_WIDE;
+  const RowTile tile = find_tile(A.plan, LOW, blockIdx.x / tiles_n);
+  const int n0 = (blockIdx.x % tiles_n) * OUT_WIDE;
+  if (tile.group < 0) return;
+  if (tile.group == A.plan.groups) {
+    zero_rows<kBF16Out>(A.y, tile, n0, min(OUT_WIDE, n_out - n0), n_out);
+    return;
+  }
+  const uint8_t* blob = A.experts + tile.group * A.blob_stride;
+  if (!blob_matches(blob, 0, A.n, A.k)) return;   // before any barrier: uniform
+
+  const int KT = A.k / 128, T = A.n / 16;
+  const int r = lane & 15, q = lane >> 4;
+  // this wave's weight tiles; past the last one again (not stored)
+  const uint8_t *wc[2], *ws[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int t = kSilu ? min(n0 / 16 + wave, T / 2 - 1) + j * (T / 2) : min(n0 / 16 + 2 * wave + j, T - 1);
+    wc[j] = blob + A.wc_off + int64_t(t) * KT * 1024 + r * 64 + q * 16;
+    ws[j] = blob + A.ws_off + int64_t(t) * KT * 128 + r * 8 + q * 2;
+  }
+  struct Regs {
+    uint4 c[2];
+    uint32_t s[2];
+  };
+  Regs ring[RING];
+  auto wload = [&](Regs& R, int p) {   // past the end: the last one again, not used
+    p = min(p, KT - 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      R.c[j] = load_nt16(wc[j] + int64_t(p) * 1024);
+      R.s[j] = *reinterpret_cast<const uint16_t*>(ws[j] + int64_t(p) * 128);
+    }
+  };
+  // Activations: the units (pair, m-tile) of a piece go round the waves; a
+  // unit is 16 bytes of codes of each of 16 places and 4 quarters.
+  constexpr int UNITS = PIECE * TM > 8 ? PIECE * TM / 8 : 1;
+  const uint8_t *xc[UNITS], *xs[UNITS];
+  bool active[UNITS];
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i) {
+    const int unit = wave + 8 * i, mt = unit % TM;
+    active[i] = unit < PIECE * TM && 16 * mt < tile.count;   // wave-uniform
+    const int place = tile.first + min(16 * mt + r, tile.count - 1);
+    int64_t from = place;
+    if (A.gather) from = min(uint32_t(A.plan.order[place]), uint32_t(A.plan.rows - 1)) / uint32_t(A.top_k);
+    xc[i] = A.codes + from * (A.k / 2) + q * 16;
+    xs[i] = A.scales + from * (A.k / 16) + q * 2;
+  }
+  struct XRegs {
+    uint4 c[UNITS];
+    uint32_t s[UNITS];
+  };
+  auto xload = [&](XRegs& R, int piece) {
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      const int64_t p = min(piece * PIECE + (wave + 8 * i) / TM % PIECE, KT - 1);
+      R.c[i] = *reinterpret_cast<const uint4*>(xc[i] + p * 64);
+      R.s[i] = *reinterpret_cast<const uint16_t*>(xs[i] + p * 8);
+    }
+  };
+  auto xstore = [&](const XRegs& R, int buf) {
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      if (!active[i]) continue;
+      uint8_t* to = smem + buf * BUF + (wave + 8 * i) * (4 * FRAG) + lane * 16;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        *reinterpret_cast<u32x4*>(to + s * FRAG) = dequant8(pick(R.c[i], s), scale_h2(R.s[i], s >> 1));
+    }
+  };
+
+  floatx4 acc[2][TM];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int m = 0; m < TM; ++m) acc[j][m] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const Regs& R, int buf, int in_piece) {
+    const uint8_t* x = smem + buf * BUF + in_piece * (TM * 4 * FRAG) + lane * 16;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      half8_t w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        w[j] = __builtin_bit_cast(half8_t, dequant8(pick(R.c[j], s), scale_h2(R.s[j], s >> 1)));
+#pragma unroll
+      for (int m = 0; m < TM; ++m) {
+        if (16 * m >= tile.count) break;   // uniform
+        const half8_t xf = *reinterpret_cast<const half8_t*>(x + (m * 4 + s) * FRAG);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[j][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[j], xf, acc[j][m], 0, 0, 0);
+      }
+    }
+  };
+
+  XRegs xa;
+  xload(xa, 0);
+#pragma unroll
+  for (int i = 0; i < RING; ++i) {
+    wload(ring[i], i);
+    __builtin_amdgcn_sched_barrier(0);   // in this order, which the waits count on
+  }
+  xstore(xa, 0);
+  xload(xa, 1);
+  __syncthreads();
+  // pieces two by two, so that ring and buffers have fixed places; pairs past
+  // the end are skipped
+  const int pieces = (KT + PIECE - 1) / PIECE;
+  for (int c = 0; c < pieces; c += RING / PIECE) {
+#pragma unroll
+    for (int h = 0; h < RING / PIECE; ++h) {
+      xstore(xa, (h & 1) ^ 1);
+      xload(xa, c + h + 2);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < PIECE; ++i) {
+        const int p = (c + h) * PIECE + i;
+        if (p < KT) compute(ring[h * PIECE + i], h & 1, i);
+        wload(ring[h * PIECE + i], p + RING);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __syncthreads();
+    }
+  }
+
+  const float stv = A.a_ts[0] * reinterpret_cast<const BlobHeader*>(blob)->tensor_scale;
+  // bf16 goes through LDS, so that whole rows are stored; [LOW places][OUT_WIDE]
+  constexpr int ORS = OUT_WIDE * 2 + 16;
+  static_assert(LOW * ORS <= 2 * BUF, "output staging fits in LDS");
+  auto put = [&](int col, int m, floatx4 v) {   // col: within the block
+    const int place = 16 * m + r;
+    if constexpr (kBF16Out) {
+      *reinterpret_cast<uint2*>(smem + place * ORS + col * 2) =
+          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else if (place < tile.count && n0 + col < n_out) {
+      *reinterpret_cast<floatx4*>(static_cast<float*>(A.y) + int64_t(tile.first + place) * n_out + n0 + col) = v;
+    }
+  };
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    if constexpr (kSilu) {
+      floatx4 h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float g = acc[0][m][e] * stv, u = acc[1][m][e] * stv;
+        h[e] = g / (1.0f + expf(-g)) * u;
+      }
+      put(wave * 16 + 4 * q, m, h);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) put((2 * wave + j) * 16 + 4 * q, m, acc[j][m] * stv);
+    }
+  }
+  if constexpr (kBF16Out) {
+    __syncthreads();
+    constexpr int LPR = OUT_WIDE / 8;   // lanes to a row
+    const int n = 8 * (threadIdx.x % LPR);
+    for (int place = threadIdx.x / LPR; place < tile.count; place += 512 / LPR)
+      if (n0 + n < n_out)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.y) + int64_t(tile.first + place) * n_out + n0 + n) =
+            *reinterpret_cast<const uint4*>(smem + place * ORS + n * 2);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_moe_gemm_w4a4(const MoeGemm& g, const uint8_t* codes, const uint8_t* scales,
@@ -277,19 +492,29 @@ hipError_t launch_moe_gemm_w4a4(const MoeGemm& g, const uint8_t* codes, const ui
   a.gather = g.gather;
   a.n = g.n;
   a.k = g.k;
-  const int64_t tiles = most_tiles(g.plan.rows, g.plan.groups, TALL) * ((g.n + WIDE - 1) / WIDE);
-  const int blocks = int((tiles + 7) / 8 * 8);
-  constexpr size_t lds = 2 * 2 * TILE_BYTES;
-  static std::atomic<int> done[4][64];
-  auto run = [&](auto kern, std::atomic<int>* flag) {
+  const int64_t wide = (g.n + WIDE - 1) / WIDE;
+  static std::atomic<int> done[8][64];
+  auto run = [&](auto kern, std::atomic<int>* flag, int tall, size_t lds) {
     const hipError_t e = lds_limit_once(flag, reinterpret_cast<const void*>(kern), int(lds));
     if (e != hipSuccess) return e;
-    kern<<<blocks, 512, lds, s>>>(a);
+    kern<<<unsigned(most_tiles(g.plan.rows, g.plan.groups, tall) * wide), 512, lds, s>>>(a);
     return hipGetLastError();
   };
+  const bool bf16 = g.y_dtype == 1;
+  if (g.plan.rows <= 96 * int64_t(g.plan.groups)) {
+    constexpr size_t lds = 2 * 2 * 4 * 4096;
+    if (g.silu_mul)
+      return bf16 ? run(moe_w4a4_low_kernel<4, true, true>, done[4], 64, lds)
+                  : run(moe_w4a4_low_kernel<4, true, false>, done[5], 64, lds);
+    return bf16 ? run(moe_w4a4_low_kernel<4, false, true>, done[6], 64, lds)
+                : run(moe_w4a4_low_kernel<4, false, false>, done[7], 64, lds);
+  }
+  constexpr size_t lds = 2 * 2 * TILE_BYTES;
   if (g.silu_mul)
-    return g.y_dtype == 1 ? run(moe_w4a4_kernel<true, true>, done[0]) : run(moe_w4a4_kernel<true, false>, done[1]);
-  return g.y_dtype == 1 ? run(moe_w4a4_kernel<false, true>, done[2]) : run(moe_w4a4_kernel<false, false>, done[3]);
+    return bf16 ? run(moe_w4a4_kernel<true, true>, done[0], TALL, lds)
+                : run(moe_w4a4_kernel<true, false>, done[1], TALL, lds);
+  return bf16 ? run(moe_w4a4_kernel<false, true>, done[2], TALL, lds)
+              : run(moe_w4a4_kernel<false, false>, done[3], TALL, lds);
 }
 
 }  // namespace qlin
