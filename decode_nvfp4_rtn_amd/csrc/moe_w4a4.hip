@@ -299,24 +299,19 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
 // loaded RING pairs ahead.  16 TM x 128 of k of products to an operand of 16 x
 // 128: at 64 places the MFMAs take half the time of the weights' way from
 // memory.
+constexpr int PIECE = 2, FRAG = 1024;
+constexpr int low_bytes(int tm) { return 2 * PIECE * tm * 4 * FRAG; }
+
 template <int TM, bool kSilu, bool kBF16Out>
-__global__ __launch_bounds__(512, 4) void moe_w4a4_low_kernel(Args4 A) {
-  constexpr int PIECE = 2, RING = 4, LOW = 16 * TM, FRAG = 1024;
+__device__ __forceinline__ void w4a4_low_tile(const Args4& A, const RowTile& tile, int n0, uint8_t* smem) {
+  constexpr int RING = 4, LOW = 16 * TM;
   static_assert(PIECE * TM % 8 == 0 || 8 % (PIECE * TM) == 0, "units of a piece over 8 waves");
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];   // [2][PIECE][TM][4][64 lanes] x 16 bytes
+  // smem: [2][PIECE][TM][4][64 lanes] x 16 bytes
   constexpr int BUF = PIECE * TM * 4 * FRAG;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n_out = kSilu ? A.n / 2 : A.n;
   constexpr int OUT_WIDE = kSilu ? 128 : 256;
-  const int tiles_n = (n_out + OUT_WIDE - 1) / OUT_WIDE;
-  const RowTile tile = find_tile(A.plan, LOW, blockIdx.x / tiles_n);
-  const int n0 = (blockIdx.x % tiles_n) * OUT_WIDE;
-  if (tile.group < 0) return;
-  if (tile.group == A.plan.groups) {
-    zero_rows<kBF16Out>(A.y, tile, n0, min(OUT_WIDE, n_out - n0), n_out);
-    return;
-  }
   const uint8_t* blob = A.experts + tile.group * A.blob_stride;
   if (!blob_matches(blob, 0, A.n, A.k)) return;   // before any barrier: uniform
 
@@ -396,7 +391,6 @@ __global__ __launch_bounds__(512, 4) void moe_w4a4_low_kernel(Args4 A) {
         w[j] = __builtin_bit_cast(half8_t, dequant8(pick(R.c[j], s), scale_h2(R.s[j], s >> 1)));
 #pragma unroll
       for (int m = 0; m < TM; ++m) {
-        if (16 * m >= tile.count) break;   // uniform
         const half8_t xf = *reinterpret_cast<const half8_t*>(x + (m * 4 + s) * FRAG);
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[j][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[j], xf, acc[j][m], 0, 0, 0);
@@ -437,7 +431,7 @@ __global__ __launch_bounds__(512, 4) void moe_w4a4_low_kernel(Args4 A) {
   const float stv = A.a_ts[0] * reinterpret_cast<const BlobHeader*>(blob)->tensor_scale;
   // bf16 goes through LDS, so that whole rows are stored; [LOW places][OUT_WIDE]
   constexpr int ORS = OUT_WIDE * 2 + 16;
-  static_assert(LOW * ORS <= 2 * BUF, "output staging fits in LDS");
+  static_assert(LOW * ORS <= low_bytes(4), "output staging fits in the launch's LDS");
   auto put = [&](int col, int m, floatx4 v) {   // col: within the block
     const int place = 16 * m + r;
     if constexpr (kBF16Out) {
@@ -473,6 +467,25 @@ __global__ __launch_bounds__(512, 4) void moe_w4a4_low_kernel(Args4 A) {
   }
 }
 
+template <bool kSilu, bool kBF16Out>
+__global__ __launch_bounds__(512, 4) void moe_w4a4_low_kernel(Args4 A) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int n_out = kSilu ? A.n / 2 : A.n;
+  constexpr int OUT_WIDE = kSilu ? 128 : 256;
+  const int tiles_n = (n_out + OUT_WIDE - 1) / OUT_WIDE;
+  const RowTile tile = find_tile(A.plan, 64, blockIdx.x / tiles_n);
+  const int n0 = (blockIdx.x % tiles_n) * OUT_WIDE;
+  if (tile.group < 0) return;
+  if (tile.group == A.plan.groups)
+    zero_rows<kBF16Out>(A.y, tile, n0, min(OUT_WIDE, n_out - n0), n_out);
+  else if (tile.count > 32)
+    w4a4_low_tile<4, kSilu, kBF16Out>(A, tile, n0, smem);
+  else if (tile.count > 16)
+    w4a4_low_tile<2, kSilu, kBF16Out>(A, tile, n0, smem);
+  else
+    w4a4_low_tile<1, kSilu, kBF16Out>(A, tile, n0, smem);
+}
+
 }  // namespace
 
 hipError_t launch_moe_gemm_w4a4(const MoeGemm& g, const uint8_t* codes, const uint8_t* scales,
@@ -502,12 +515,12 @@ hipError_t launch_moe_gemm_w4a4(const MoeGemm& g, const uint8_t* codes, const ui
   };
   const bool bf16 = g.y_dtype == 1;
   if (g.plan.rows <= 96 * int64_t(g.plan.groups)) {
-    constexpr size_t lds = 2 * 2 * 4 * 4096;
+    constexpr size_t lds = low_bytes(4);
     if (g.silu_mul)
-      return bf16 ? run(moe_w4a4_low_kernel<4, true, true>, done[4], 64, lds)
-                  : run(moe_w4a4_low_kernel<4, true, false>, done[5], 64, lds);
-    return bf16 ? run(moe_w4a4_low_kernel<4, false, true>, done[6], 64, lds)
-                : run(moe_w4a4_low_kernel<4, false, false>, done[7], 64, lds);
+      return bf16 ? run(moe_w4a4_low_kernel<true, true>, done[4], 64, lds)
+                  : run(moe_w4a4_low_kernel<true, false>, done[5], 64, lds);
+    return bf16 ? run(moe_w4a4_low_kernel<false, true>, done[6], 64, lds)
+                : run(moe_w4a4_low_kernel<false, false>, done[7], 64, lds);
   }
   constexpr size_t lds = 2 * 2 * TILE_BYTES;
   if (g.silu_mul)
