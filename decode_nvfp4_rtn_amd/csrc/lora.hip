@@ -6,17 +6,23 @@
 // with A_i [rank, k] and B_i [n, rank] in bf16.  Both products run over the
 // runs of a plan, so that a tile of rows meets one adapter.
 //
-// Two launches.  "down" makes u = A x: a block takes a tile of places and a
-// part of k, its waves take pieces of 128 of that part, all of the rank at
-// once; their sums are added in LDS in a fixed order and stored in binary32,
-// one buffer for each part.  "up" adds the parts in their order and makes
-// out = y + scale B u: each wave owns 128 columns of a tile of rows.  u enters
-// the second product as a sum of two bf16 values (16 bits of mantissa), which
-// is as good as binary32 beside the bf16 B and costs nothing that shows: the
-// second product is bound by reading y and writing out.  The MFMA's rows are
-// columns of out in an order that leaves each lane eight neighbours (tile
-// pair a, lane quarter q: columns 32 a + 8 q ..), so that y and out move in
-// 16-byte pieces, 64 bytes of a row at a time.
+// Adapters of few rows (a decode batch): one launch.  A block takes a tile of
+// 16 places and a part of the columns; its waves share k, add their sums of
+// u = A x in LDS in a fixed order, and make out = y + scale B u, each its own
+// columns.  A and x are read once for each part of the columns.
+//
+// Adapters of many rows (prompts): two launches.  "down" makes u: a block takes
+// 64 places and a part of k, each wave 16 places and all of the rank; A passes
+// through LDS, x goes from memory to registers.  u is stored in binary32, one
+// buffer for each part of k.  "up" adds the parts in their order and makes out
+// for 64 places and a part of the columns.
+//
+// u enters the second product as a sum of two bf16 values (16 bits of mantissa
+// or more), which costs nothing that shows: that product is bound by reading y
+// and writing out.  The MFMA's rows are columns of out in an order that leaves
+// each lane eight neighbours (of 32 columns: lane quarter q has 8 q ..), so
+// that y and out move in 16-byte pieces, 64 bytes of a row at a time; a step's
+// y and B are loaded a step ahead.
 //
 // Rows without an adapter come last in the plan: they are copied, or left
 // alone where out is y.
@@ -30,216 +36,389 @@ __device__ __forceinline__ floatx4 mfma(bf16x8_t a, bf16x8_t b, floatx4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ bf16x8_t load8(const uint16_t* p) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  return as_bf16x8(u32x4{v.x, v.y, v.z, v.w});
-}
+__device__ __forceinline__ u32x4 load16(const void* p) { return *static_cast<const u32x4*>(p); }
 
 __device__ __forceinline__ int row_of(const RowPlan& p, int place) {
   return int(min(uint32_t(p.order[place]), uint32_t(p.rows - 1)));
 }
 
-// MT tiles of 16 places, RT tiles of 16 of the rank (the last may be half).
-template <int MT, int RT>
-__global__ __launch_bounds__(512) void lora_down_kernel(LoraArgs A, int parts) {
-  constexpr int WAVES = 8;
-  __shared__ floatx4 red[WAVES][RT * MT][64];
+// eight binary32 values as two bf16 values each
+struct Split {
+  bf16x8_t hi, lo;
+};
+__device__ __forceinline__ Split split(floatx4 a, floatx4 b) {
+  Split s;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float v = e < 4 ? a[e & 3] : b[e & 3];
+    s.hi[e] = static_cast<__bf16>(v);
+    s.lo[e] = static_cast<__bf16>(v - static_cast<float>(s.hi[e]));
+  }
+  return s;
+}
+
+// One step of the second product: 32 columns of a tile's rows, its y and the
+// operand made of B.  Columns past n and a rank past the last are clamped: the
+// first are not stored, the second meet zeros of u.
+template <int MT, int KT, bool kBF16>
+struct Step {
+  u32x4 b[2][KT];
+  u32x4 y[MT][kBF16 ? 1 : 2];
+};
+
+template <int MT, int KT, bool kBF16>
+__device__ __forceinline__ void load_step(Step<MT, KT, kBF16>& S, const LoraArgs& A, const uint16_t* b,
+                                          const int64_t (&y_at)[MT], int col0) {
+  const int q = (threadIdx.x >> 4) & 3, r = threadIdx.x & 15;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const uint8_t* p = static_cast<const uint8_t*>(A.y) + (y_at[m] + min(col0 + 8 * q, A.n - 8)) * (kBF16 ? 2 : 4);
+    S.y[m][0] = load16(p);
+    if constexpr (!kBF16) S.y[m][1] = load16(p + 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t n = min(col0 + 8 * (r >> 2) + 4 * i + (r & 3), A.n - 1);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) S.b[i][kt] = load16(b + n * A.rank + min(32 * kt + 8 * q, A.rank - 8));
+  }
+}
+
+// out of one step; u(m, kt) gives the fragments of u.
+template <int MT, int KT, bool kBF16, typename U>
+__device__ __forceinline__ void finish_step(const Step<MT, KT, kBF16>& S, const LoraArgs& A, U u, float scale,
+                                            const int64_t (&out_at)[MT], int count, int col0) {
+  const int q = (threadIdx.x >> 4) & 3, r = threadIdx.x & 15;
+  floatx4 acc[2][MT];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const Split s = u(m, kt);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        acc[i][m] = mfma(as_bf16x8(S.b[i][kt]), s.hi, acc[i][m]);
+        acc[i][m] = mfma(as_bf16x8(S.b[i][kt]), s.lo, acc[i][m]);
+      }
+    }
+  const int col = col0 + 8 * q;
+  if (col >= A.n) return;   // n is a multiple of 16
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (16 * m + r >= count) continue;
+    if constexpr (kBF16) {
+      const u32x4 d = S.y[m][0];
+      u32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = pack_bf16x2(fmaf(scale, acc[e >> 1][m][2 * (e & 1)], __uint_as_float(d[e] << 16)),
+                           fmaf(scale, acc[e >> 1][m][2 * (e & 1) + 1], __uint_as_float(d[e] & 0xFFFF0000u)));
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(A.out) + out_at[m] + col) = o;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        floatx4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = fmaf(scale, acc[i][m][e], __uint_as_float(S.y[m][i][e]));
+        *reinterpret_cast<floatx4*>(static_cast<float*>(A.out) + out_at[m] + col + 4 * i) = o;
+      }
+    }
+  }
+}
+
+// Rows without an adapter: columns [c0, c1), copied by the block.
+template <int kThreads, bool kBF16>
+__device__ __forceinline__ void copy_rows(const LoraArgs& A, const RowTile& tile, int c0, int c1) {
+  constexpr int size = kBF16 ? 2 : 4;
+  const int per = (c1 - c0) * size / 16;
+  for (int i = threadIdx.x; i < tile.count * per; i += kThreads) {
+    const int64_t row = row_of(A.plan, tile.first + i / per), at = int64_t(c0) * size + i % per * 16;
+    *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(A.out) + row * A.out_stride * size + at) =
+        load16(static_cast<const uint8_t*>(A.y) + row * A.y_stride * size + at);
+  }
+}
+
+// RT tiles of 16 of the rank (the last may be half), one m-tile of places.
+template <int RT, bool kBF16>
+__global__ __launch_bounds__(512) void lora_few_kernel(LoraArgs A, int col_parts) {
+  constexpr int WAVES = 8, KT = (RT + 1) / 2;
+  __shared__ floatx4 red[WAVES][RT][64];
+  __shared__ __attribute__((aligned(16))) float us[16][32 * KT + 4];   // u, zero past the rank
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = blockIdx.x % col_parts;
+  const RowTile tile = find_tile(A.plan, 16, blockIdx.x / col_parts);
+  if (tile.group < 0) return;
+  const int steps = (A.n + 31) / 32;
+  const int s0 = int(int64_t(steps) * part / col_parts), s1 = int(int64_t(steps) * (part + 1) / col_parts);
+  if (tile.group == A.plan.groups) {
+    if (A.out != A.y) copy_rows<512, kBF16>(A, tile, 32 * s0, min(32 * s1, A.n));
+    return;
+  }
+  const int q = lane >> 4, r = lane & 15, G = A.k / 128;
+  const int64_t row = row_of(A.plan, tile.first + min(r, tile.count - 1));
+  const uint16_t* xr = static_cast<const uint16_t*>(A.x) + row * A.x_stride + 8 * q;
+  const uint16_t* ar[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    ar[i] = static_cast<const uint16_t*>(A.a) + (int64_t(tile.group) * A.rank + min(16 * i + r, A.rank - 1)) * A.k + 8 * q;
+
+  floatx4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int g = wave; g < G; g += WAVES) {
+    u32x4 xf[4], af[4][RT];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      xf[s] = load16(xr + g * 128 + 32 * s);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) af[s][i] = load16(ar[i] + g * 128 + 32 * s);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) acc[i] = mfma(as_bf16x8(af[s][i]), as_bf16x8(xf[s]), acc[i]);
+  }
+  // the first step's y and B are under way while u is added up
+  const uint16_t* b = static_cast<const uint16_t*>(A.b) + int64_t(tile.group) * A.n * A.rank;
+  const int64_t y_at[1] = {row * A.y_stride}, out_at[1] = {row * A.out_stride};
+  Step<1, KT, kBF16> S;
+  load_step<1, KT, kBF16>(S, A, b, y_at, 32 * min(s0 + wave, steps - 1));
+  const float scale = A.scale ? A.scale[tile.group] : 1.0f;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) red[wave][i][lane] = acc[i];
+  __syncthreads();
+  for (int t = threadIdx.x; t < 2 * KT * 64; t += 512) {
+    const int i = t / 64, ln = t % 64, j = 16 * i + 4 * (ln >> 4);
+    floatx4 sum = floatx4{0.f, 0.f, 0.f, 0.f};
+    if (j < A.rank) {   // the rank is a multiple of 8
+      sum = red[0][min(i, RT - 1)][ln];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) sum += red[w][min(i, RT - 1)][ln];
+    }
+    *reinterpret_cast<floatx4*>(&us[ln & 15][j]) = sum;
+  }
+  __syncthreads();
+  Split u[KT];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+    u[kt] = split(*reinterpret_cast<const floatx4*>(&us[r][32 * kt + 8 * q]),
+                  *reinterpret_cast<const floatx4*>(&us[r][32 * kt + 8 * q + 4]));
+  for (int st = s0 + wave; st < s1; st += WAVES) {
+    Step<1, KT, kBF16> next;
+    load_step<1, KT, kBF16>(next, A, b, y_at, 32 * min(st + WAVES, steps - 1));
+    finish_step<1, KT, kBF16>(S, A, [&](int, int kt) { return u[kt]; }, scale, out_at, tile.count, 32 * st);
+    S = next;
+  }
+}
+
+constexpr int TALL = 64, MT = TALL / 16;
+
+// the slot of row r's 16-byte piece c of 128 of k among a tile's 256: rows are
+// XORed with the piece so that a row's pieces, written together, and a
+// fragment's rows, read together, both fall on different banks
+__device__ __forceinline__ int piece_slot(int r, int c) { return c * 16 + (r ^ c); }
+
+template <int RT>
+__global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs A, int parts) {
+  constexpr int BUF = RT * 4096;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];   // two pieces of A
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = blockIdx.x % parts;
-  const RowTile tile = find_tile(A.plan, 16 * MT, blockIdx.x / parts);
+  const RowTile tile = find_tile(A.plan, TALL, blockIdx.x / parts);
   if (tile.group < 0 || tile.group == A.plan.groups) return;
   const int q = lane >> 4, r = lane & 15;
   const int G = A.k / 128;
   const int g0 = int(int64_t(G) * part / parts), g1 = int(int64_t(G) * (part + 1) / parts);
+  const bool busy = 16 * wave < tile.count;   // wave-uniform
 
-  const uint16_t* xr[MT];
+  const uint16_t* xr = static_cast<const uint16_t*>(A.x) +
+                       row_of(A.plan, tile.first + min(16 * wave + r, tile.count - 1)) * A.x_stride + 8 * q;
+  // of a piece of A this thread moves one 16-byte piece of every 16th row
+  const int ac = threadIdx.x & 15, an = threadIdx.x >> 4;
+  const uint16_t* a = static_cast<const uint16_t*>(A.a) + int64_t(tile.group) * A.rank * A.k + 8 * ac;
+  u32x4 av[RT];
+  auto aload = [&](int g) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-    xr[m] = static_cast<const uint16_t*>(A.x) +
-            row_of(A.plan, tile.first + min(16 * m + r, tile.count - 1)) * A.x_stride + 8 * q;
-  const uint16_t* ar[RT];
+    for (int i = 0; i < RT; ++i)
+      av[i] = load16(a + int64_t(min(16 * i + an, A.rank - 1)) * A.k + min(g, g1 - 1) * 128);
+  };
+  auto astore = [&](int buf) {
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-    ar[i] = static_cast<const uint16_t*>(A.a) +
-            (int64_t(tile.group) * A.rank + min(16 * i + r, A.rank - 1)) * A.k + 8 * q;
-
-  floatx4 acc[RT][MT];
+    for (int i = 0; i < RT; ++i)
+      *reinterpret_cast<u32x4*>(smem + buf * BUF + i * 4096 + piece_slot(an, ac) * 16) = av[i];
+  };
+  struct X {
+    u32x4 v[4];
+  };
+  auto xload = [&](X& x, int g) {
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+    for (int s = 0; s < 4; ++s) x.v[s] = load16(xr + min(g, g1 - 1) * 128 + 32 * s);
+  };
+  int off[4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0.f, 0.f, 0.f, 0.f};
-  for (int g = g0 + wave; g < g1; g += WAVES) {
+  for (int s = 0; s < 4; ++s) off[s] = piece_slot(r, 4 * s + q) * 16;
+  floatx4 acc[RT];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      bf16x8_t xf[MT];
+  for (int i = 0; i < RT; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const X& x, int buf) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xf[m] = load8(xr[m] + g * 128 + 32 * s);
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const bf16x8_t af = load8(ar[i] + g * 128 + 32 * s);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[i][m] = mfma(af, xf[m], acc[i][m]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) red[wave][i * MT + m][lane] = acc[i][m];
+      for (int i = 0; i < RT; ++i)
+        acc[i] = mfma(as_bf16x8(load16(smem + buf * BUF + i * 4096 + off[s])), as_bf16x8(x.v[s]), acc[i]);
+  };
+  X P, Q;
+  aload(g0);
+  xload(P, g0);
+  xload(Q, g0 + 1);
+  __builtin_amdgcn_sched_barrier(0);
+  astore(0);
+  aload(g0 + 1);
   __syncthreads();
-  for (int t = threadIdx.x; t < RT * MT * 64; t += 512) {
-    const int i = t / 64 / MT, m = t / 64 % MT, ln = t % 64;
-    floatx4 sum = red[0][t / 64][ln];
+  // two pieces to a turn, so that buffers and registers have fixed places
+  for (int g = g0; g < g1; g += 2) {
+    astore(1);
+    aload(g + 2);
+    if (busy) compute(P, 0);
+    xload(P, g + 2);
+    __syncthreads();
+    astore(0);
+    aload(g + 3);
+    if (busy && g + 1 < g1) compute(Q, 1);
+    xload(Q, g + 3);
+    __syncthreads();
+  }
+  const int place = 16 * wave + r;
+  if (place < tile.count) {
+    float* to = A.part + (int64_t(part) * A.plan.rows + tile.first + place) * A.rank;
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) sum += red[w][t / 64][ln];
-    const int place = 16 * m + (ln & 15), j = 16 * i + 4 * (ln >> 4);
-    if (place < tile.count && j < A.rank)   // the rank is a multiple of 8
-      *reinterpret_cast<floatx4*>(A.part + (int64_t(part) * A.plan.rows + tile.first + place) * A.rank + j) = sum;
+    for (int i = 0; i < RT; ++i)
+      if (16 * i + 4 * q < A.rank) *reinterpret_cast<floatx4*>(to + 16 * i + 4 * q) = acc[i];
   }
 }
 
 // KT pieces of 32 of the rank.
-template <int MT, int KT, bool kBF16>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs A, int parts, int col_blocks) {
+template <int KT, bool kBF16>
+__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs A, int parts, int col_parts) {
+  __shared__ __attribute__((aligned(16))) u32x4 frag[MT][KT][2][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col0 = (int(blockIdx.x % col_blocks) * 4 + wave) * 128;
-  const RowTile tile = find_tile(A.plan, 16 * MT, blockIdx.x / col_blocks);
-  if (tile.group < 0 || col0 >= A.n) return;
-  const bool bare = tile.group == A.plan.groups;
-  if (bare && A.out == A.y) return;
-  const int q = lane >> 4, r = lane & 15;
-
-  // u of the tile's places, in two bf16 values each
-  bf16x8_t hi[MT][KT], lo[MT][KT];
-  int row[MT];
+  const RowTile tile = find_tile(A.plan, TALL, blockIdx.x / col_parts);
+  if (tile.group < 0) return;
+  const int part = blockIdx.x % col_parts, steps = (A.n + 31) / 32;
+  const int s0 = int(int64_t(steps) * part / col_parts), s1 = int(int64_t(steps) * (part + 1) / col_parts);
+  if (tile.group == A.plan.groups) {
+    if (A.out != A.y) copy_rows<256, kBF16>(A, tile, 32 * s0, min(32 * s1, A.n));
+    return;
+  }
+  const int r = lane & 15;
+  int64_t y_at[MT], out_at[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int place = tile.first + min(16 * m + r, tile.count - 1);
-    row[m] = row_of(A.plan, place);
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      const int j = 32 * kt + 8 * q;
-      floatx4 u[2] = {floatx4{0.f, 0.f, 0.f, 0.f}, floatx4{0.f, 0.f, 0.f, 0.f}};
-      if (!bare && j < A.rank) {
-        const float* p = A.part + int64_t(place) * A.rank + j;
-        for (int s = 0; s < parts; ++s, p += int64_t(A.plan.rows) * A.rank) {
-          u[0] += *reinterpret_cast<const floatx4*>(p);
-          u[1] += *reinterpret_cast<const floatx4*>(p + 4);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = u[e >> 2][e & 3];
-        const __bf16 h = static_cast<__bf16>(v);
-        hi[m][kt][e] = h;
-        lo[m][kt][e] = static_cast<__bf16>(v - static_cast<float>(h));
-      }
-    }
+    const int64_t row = row_of(A.plan, tile.first + min(16 * m + r, tile.count - 1));
+    y_at[m] = row * A.y_stride;
+    out_at[m] = row * A.out_stride;
   }
-  const float scale = bare ? 0.f : A.scale ? A.scale[tile.group] : 1.0f;
-  const uint16_t* b = static_cast<const uint16_t*>(A.b) + int64_t(bare ? 0 : tile.group) * A.n * A.rank;
-#pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    const int col = col0 + 32 * a + 8 * q;   // this lane's eight columns
-    floatx4 acc[2][MT];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0.f, 0.f, 0.f, 0.f};
-    if (!bare) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int n = min(col0 + 32 * a + 8 * (r >> 2) + 4 * i + (r & 3), A.n - 1);
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-          const int j = 32 * kt + 8 * q;
-          bf16x8_t bf = as_bf16x8(u32x4{0u, 0u, 0u, 0u});
-          if (j < A.rank) bf = load8(b + int64_t(n) * A.rank + j);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            acc[i][m] = mfma(bf, hi[m][kt], acc[i][m]);
-            acc[i][m] = mfma(bf, lo[m][kt], acc[i][m]);
-          }
-        }
+  const uint16_t* b = static_cast<const uint16_t*>(A.b) + int64_t(tile.group) * A.n * A.rank;
+  const float scale = A.scale ? A.scale[tile.group] : 1.0f;
+  Step<MT, KT, kBF16> P, Q;
+  auto load = [&](Step<MT, KT, kBF16>& S, int st) { load_step<MT, KT, kBF16>(S, A, b, y_at, 32 * min(st, steps - 1)); };
+  load(P, s0 + wave);   // under way while u is made
+  for (int t = threadIdx.x; t < MT * KT * 64; t += 256) {
+    const int ln = t & 63, kt = t / 64 % KT, m = t / 64 / KT, j = 32 * kt + 8 * (ln >> 4);
+    const int place = tile.first + min(16 * m + (ln & 15), tile.count - 1);
+    floatx4 u[2] = {floatx4{0.f, 0.f, 0.f, 0.f}, floatx4{0.f, 0.f, 0.f, 0.f}};
+    if (j < A.rank) {
+      const float* p = A.part + int64_t(place) * A.rank + j;
+      for (int s = 0; s < parts; ++s, p += int64_t(A.plan.rows) * A.rank) {
+        u[0] += *reinterpret_cast<const floatx4*>(p);
+        u[1] += *reinterpret_cast<const floatx4*>(p + 4);
       }
     }
-    if (col >= A.n) continue;   // n is a multiple of 16
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (16 * m + r >= tile.count) continue;
-      if constexpr (kBF16) {
-        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.y) +
-                                                        row[m] * A.y_stride + col);
-        const uint32_t d[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = pack_bf16x2(
-              fmaf(scale, acc[e >> 1][m][2 * (e & 1)], __uint_as_float(d[e] << 16)),
-              fmaf(scale, acc[e >> 1][m][2 * (e & 1) + 1], __uint_as_float(d[e] & 0xFFFF0000u)));
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + row[m] * A.out_stride + col) =
-            bare ? v : make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        const floatx4* from = reinterpret_cast<const floatx4*>(static_cast<const float*>(A.y) + row[m] * A.y_stride + col);
-        floatx4* to = reinterpret_cast<floatx4*>(static_cast<float*>(A.out) + row[m] * A.out_stride + col);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const floatx4 v = from[i];
-          floatx4 o;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = fmaf(scale, acc[i][m][e], v[e]);
-          to[i] = bare ? v : o;
-        }
-      }
-    }
+    const Split s = split(u[0], u[1]);
+    frag[m][kt][0][ln] = __builtin_bit_cast(u32x4, s.hi);
+    frag[m][kt][1][ln] = __builtin_bit_cast(u32x4, s.lo);
+  }
+  __syncthreads();
+  auto u = [&](int m, int kt) { return Split{as_bf16x8(frag[m][kt][0][lane]), as_bf16x8(frag[m][kt][1][lane])}; };
+  auto finish = [&](const Step<MT, KT, kBF16>& S, int st) {
+    finish_step<MT, KT, kBF16>(S, A, u, scale, out_at, tile.count, 32 * st);
+  };
+  for (int st = s0 + wave; st < s1; st += 8) {
+    load(Q, st + 4);
+    __builtin_amdgcn_sched_barrier(0);   // before the step's own arithmetic
+    finish(P, st);
+    load(P, st + 8);
+    __builtin_amdgcn_sched_barrier(0);
+    if (st + 4 < s1) finish(Q, st + 4);
   }
 }
 
-// The height of a tile: 64 places (32 beside a rank over 64, whose sums would
-// not fit in LDS) where adapters have that many rows on average, else 16.
-int tall_of(int64_t rows, int64_t groups, int rank) {
-  return rows < 48 * groups ? 16 : rank > 64 ? 32 : 64;
-}
-
-// Parts of k: as many as fill the chip once, at least 512 of k each.
-int parts_of(int64_t rows, int64_t groups, int rank, int64_t k) {
+int cus_or(int otherwise) {
   const int cus = device_cu_count();
-  const int64_t tiles = most_tiles(rows, groups, tall_of(rows, groups, rank));
-  int64_t parts = (cus > 0 ? cus : 256) / (tiles > 0 ? tiles : 1);
+  return cus > 0 ? cus : otherwise;
+}
+
+// Adapters of few rows: less than 48 on average.
+bool few_rows(int64_t rows, int64_t groups) { return rows < 48 * groups; }
+
+// Parts of k of the first product: two blocks to a CU, at least 512 of k each.
+int parts_of(int64_t rows, int64_t groups, int64_t k) {
+  if (few_rows(rows, groups)) return 0;
+  const int64_t tiles = most_tiles(rows, groups, TALL);
+  int64_t parts = (2 * cus_or(256) + tiles - 1) / tiles;
   if (parts > k / 512) parts = k / 512;
   return parts < 1 ? 1 : int(parts);
 }
 
-template <int MT, int RT>
+// Parts of the columns: as many as give a CU `each` blocks, at least one step
+// of 32 columns for each of `waves` waves.
+int col_parts_of(int64_t tiles, int64_t n, int each, int waves) {
+  int64_t parts = (each * cus_or(256) + tiles - 1) / tiles;
+  const int64_t most = ((n + 31) / 32 + waves - 1) / waves;
+  return int(parts < most ? parts : most);
+}
+
+template <int RT>
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
-  const int parts = parts_of(a.plan.rows, a.plan.groups, a.rank, a.k);
-  const int64_t tiles = most_tiles(a.plan.rows, a.plan.groups, 16 * MT);
-  lora_down_kernel<MT, RT><<<unsigned(tiles * parts), 512, 0, s>>>(a, parts);
+  const bool bf16 = a.y_dtype == 1;
+  if (few_rows(a.plan.rows, a.plan.groups)) {
+    const int64_t tiles = most_tiles(a.plan.rows, a.plan.groups, 16);
+    const int cols = col_parts_of(tiles, a.n, 1, 8);
+    if (bf16) lora_few_kernel<RT, true><<<unsigned(tiles * cols), 512, 0, s>>>(a, cols);
+    else lora_few_kernel<RT, false><<<unsigned(tiles * cols), 512, 0, s>>>(a, cols);
+    return hipGetLastError();
+  }
+  const int64_t tiles = most_tiles(a.plan.rows, a.plan.groups, TALL);
+  const int parts = parts_of(a.plan.rows, a.plan.groups, a.k);
+  lora_down_kernel<RT><<<unsigned(tiles * parts), 256, 2 * RT * 4096, s>>>(a, parts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int cols = (a.n + 511) / 512;
   constexpr int KT = (RT + 1) / 2;
-  if (a.y_dtype == 1)
-    lora_up_kernel<MT, KT, true><<<unsigned(tiles * cols), 256, 0, s>>>(a, parts, cols);
-  else
-    lora_up_kernel<MT, KT, false><<<unsigned(tiles * cols), 256, 0, s>>>(a, parts, cols);
+  const int cols = col_parts_of(tiles, a.n, 3, 4);
+  if (bf16) lora_up_kernel<KT, true><<<unsigned(tiles * cols), 256, 0, s>>>(a, parts, cols);
+  else lora_up_kernel<KT, false><<<unsigned(tiles * cols), 256, 0, s>>>(a, parts, cols);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t lora_ws_bytes(int64_t rows, int64_t groups, int rank, int64_t k) {
-  return size_t(parts_of(rows, groups, rank, k)) * size_t(rows) * size_t(rank) * sizeof(float);
+  return size_t(parts_of(rows, groups, k)) * size_t(rows) * size_t(rank) * sizeof(float);
 }
 
 hipError_t launch_lora_add(const LoraArgs& a, hipStream_t s) {
-  const int tall = tall_of(a.plan.rows, a.plan.groups, a.rank);
-  if (a.rank <= 16) return tall == 16 ? launch_lora<1, 1>(a, s) : launch_lora<4, 1>(a, s);
-  if (a.rank <= 32) return tall == 16 ? launch_lora<1, 2>(a, s) : launch_lora<4, 2>(a, s);
-  if (a.rank <= 64) return tall == 16 ? launch_lora<1, 4>(a, s) : launch_lora<4, 4>(a, s);
-  return tall == 16 ? launch_lora<1, 8>(a, s) : launch_lora<2, 8>(a, s);
+  if (a.rank <= 16) return launch_lora<1>(a, s);
+  if (a.rank <= 32) return launch_lora<2>(a, s);
+  if (a.rank <= 64) return launch_lora<4>(a, s);
+  return launch_lora<8>(a, s);
 }
 
 }  // namespace qlin

@@ -272,8 +272,10 @@ def test_refusals():
                  lambda: q.lora_add(torch.zeros((64, 6), device="cuda").t(), x, a, b, plan)):
         with pytest.raises(ValueError):
             call()
-    small = torch.empty(16, dtype=torch.uint8, device="cuda")
-    for call in (lambda: q.lora_add(y, x, a, b, plan, workspace=small),
+    many = q.group_rows(torch.zeros(200, dtype=torch.int32, device="cuda"), 3)
+    assert q.lora_add_workspace(200, 3, 16, 256) > 16
+    for call in (lambda: q.lora_add(torch.zeros((200, 64), device="cuda"), x[:1].repeat(200, 1), a, b, many,
+                                    workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
                  lambda: q.lora_add(y, x, a[:, :12].contiguous(), b[:, :, :12].contiguous(), plan),
                  lambda: q.lora_add(torch.zeros((6, 66), device="cuda")[:, :64], x, a, b, plan)):
         with pytest.raises(q.QlinError):
