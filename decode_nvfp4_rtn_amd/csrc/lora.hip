@@ -19,10 +19,7 @@
 //
 // u enters the second product as a sum of two bf16 values (16 bits of mantissa
 // or more), which costs nothing that shows: that product is bound by reading y
-// and writing out.  The MFMA's rows are columns of out in an order that leaves
-// each lane eight neighbours (of 32 columns: lane quarter q has 8 q ..), so
-// that y and out move in 16-byte pieces, 64 bytes of a row at a time; a step's
-// y and B are loaded a step ahead.
+// and writing out.
 //
 // Rows without an adapter come last in the plan: they are copied, or left
 // alone where out is y.
@@ -57,25 +54,24 @@ __device__ __forceinline__ Split split(floatx4 a, floatx4 b) {
   return s;
 }
 
-// One step of the second product: 32 columns of a tile's rows, its y and the
-// operand made of B.  Columns past n and a rank past the last are clamped: the
-// first are not stored, the second meet zeros of u.
-template <int MT, int KT, bool kBF16>
+// Few rows: a step of 32 columns of the tile's rows, its y and the operand made
+// of B.  The MFMA's rows are columns of out in an order that leaves each lane
+// eight neighbours (lane quarter q: 8 q ..), so that y and out move in 16-byte
+// pieces.  Columns past n and a rank past the last are clamped: the first are
+// not stored, the second meet zeros of u.
+template <int KT, bool kBF16>
 struct Step {
   u32x4 b[2][KT];
-  u32x4 y[MT][kBF16 ? 1 : 2];
+  u32x4 y[kBF16 ? 1 : 2];
 };
 
-template <int MT, int KT, bool kBF16>
-__device__ __forceinline__ void load_step(Step<MT, KT, kBF16>& S, const LoraArgs& A, const uint16_t* b,
-                                          const int64_t (&y_at)[MT], int col0) {
+template <int KT, bool kBF16>
+__device__ __forceinline__ void load_step(Step<KT, kBF16>& S, const LoraArgs& A, const uint16_t* b, int64_t y_at,
+                                          int col0) {
   const int q = (threadIdx.x >> 4) & 3, r = threadIdx.x & 15;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const uint8_t* p = static_cast<const uint8_t*>(A.y) + (y_at[m] + min(col0 + 8 * q, A.n - 8)) * (kBF16 ? 2 : 4);
-    S.y[m][0] = load16(p);
-    if constexpr (!kBF16) S.y[m][1] = load16(p + 16);
-  }
+  const uint8_t* p = static_cast<const uint8_t*>(A.y) + (y_at + min(col0 + 8 * q, A.n - 8)) * (kBF16 ? 2 : 4);
+  S.y[0] = load16(p);
+  if constexpr (!kBF16) S.y[1] = load16(p + 16);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t n = min(col0 + 8 * (r >> 2) + 4 * i + (r & 3), A.n - 1);
@@ -84,48 +80,35 @@ __device__ __forceinline__ void load_step(Step<MT, KT, kBF16>& S, const LoraArgs
   }
 }
 
-// out of one step; u(m, kt) gives the fragments of u.
-template <int MT, int KT, bool kBF16, typename U>
-__device__ __forceinline__ void finish_step(const Step<MT, KT, kBF16>& S, const LoraArgs& A, U u, float scale,
-                                            const int64_t (&out_at)[MT], int count, int col0) {
+template <int KT, bool kBF16>
+__device__ __forceinline__ void finish_step(const Step<KT, kBF16>& S, const LoraArgs& A, const Split (&u)[KT],
+                                            float scale, int64_t out_at, int count, int col0) {
   const int q = (threadIdx.x >> 4) & 3, r = threadIdx.x & 15;
-  floatx4 acc[2][MT];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[i][m] = floatx4{0.f, 0.f, 0.f, 0.f};
+  floatx4 acc[2] = {floatx4{0.f, 0.f, 0.f, 0.f}, floatx4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const Split s = u(m, kt);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        acc[i][m] = mfma(as_bf16x8(S.b[i][kt]), s.hi, acc[i][m]);
-        acc[i][m] = mfma(as_bf16x8(S.b[i][kt]), s.lo, acc[i][m]);
-      }
+    for (int i = 0; i < 2; ++i) {
+      acc[i] = mfma(as_bf16x8(S.b[i][kt]), u[kt].hi, acc[i]);
+      acc[i] = mfma(as_bf16x8(S.b[i][kt]), u[kt].lo, acc[i]);
     }
   const int col = col0 + 8 * q;
-  if (col >= A.n) return;   // n is a multiple of 16
+  if (col >= A.n || r >= count) return;   // n is a multiple of 16
+  if constexpr (kBF16) {
+    const u32x4 d = S.y[0];
+    u32x4 o;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (16 * m + r >= count) continue;
-    if constexpr (kBF16) {
-      const u32x4 d = S.y[m][0];
-      u32x4 o;
+    for (int e = 0; e < 4; ++e)
+      o[e] = pack_bf16x2(fmaf(scale, acc[e >> 1][2 * (e & 1)], __uint_as_float(d[e] << 16)),
+                         fmaf(scale, acc[e >> 1][2 * (e & 1) + 1], __uint_as_float(d[e] & 0xFFFF0000u)));
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(A.out) + out_at + col) = o;
+  } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = pack_bf16x2(fmaf(scale, acc[e >> 1][m][2 * (e & 1)], __uint_as_float(d[e] << 16)),
-                           fmaf(scale, acc[e >> 1][m][2 * (e & 1) + 1], __uint_as_float(d[e] & 0xFFFF0000u)));
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(A.out) + out_at[m] + col) = o;
-    } else {
+    for (int i = 0; i < 2; ++i) {
+      floatx4 o;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        floatx4 o;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = fmaf(scale, acc[i][m][e], __uint_as_float(S.y[m][i][e]));
-        *reinterpret_cast<floatx4*>(static_cast<float*>(A.out) + out_at[m] + col + 4 * i) = o;
-      }
+      for (int e = 0; e < 4; ++e) o[e] = fmaf(scale, acc[i][e], __uint_as_float(S.y[i][e]));
+      *reinterpret_cast<floatx4*>(static_cast<float*>(A.out) + out_at + col + 4 * i) = o;
     }
   }
 }
@@ -186,9 +169,9 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraArgs A, int col_parts
   }
   // the first step's y and B are under way while u is added up
   const uint16_t* b = static_cast<const uint16_t*>(A.b) + int64_t(tile.group) * A.n * A.rank;
-  const int64_t y_at[1] = {row * A.y_stride}, out_at[1] = {row * A.out_stride};
-  Step<1, KT, kBF16> S;
-  load_step<1, KT, kBF16>(S, A, b, y_at, 32 * min(s0 + wave, steps - 1));
+  const int64_t y_at = row * A.y_stride, out_at = row * A.out_stride;
+  Step<KT, kBF16> S;
+  load_step<KT, kBF16>(S, A, b, y_at, 32 * min(s0 + wave, steps - 1));
   const float scale = A.scale ? A.scale[tile.group] : 1.0f;
 #pragma unroll
   for (int i = 0; i < RT; ++i) red[wave][i][lane] = acc[i];
@@ -210,14 +193,14 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraArgs A, int col_parts
     u[kt] = split(*reinterpret_cast<const floatx4*>(&us[r][32 * kt + 8 * q]),
                   *reinterpret_cast<const floatx4*>(&us[r][32 * kt + 8 * q + 4]));
   for (int st = s0 + wave; st < s1; st += WAVES) {
-    Step<1, KT, kBF16> next;
-    load_step<1, KT, kBF16>(next, A, b, y_at, 32 * min(st + WAVES, steps - 1));
-    finish_step<1, KT, kBF16>(S, A, [&](int, int kt) { return u[kt]; }, scale, out_at, tile.count, 32 * st);
+    Step<KT, kBF16> next;
+    load_step<KT, kBF16>(next, A, b, y_at, 32 * min(st + WAVES, steps - 1));
+    finish_step<KT, kBF16>(S, A, u, scale, out_at, tile.count, 32 * st);
     S = next;
   }
 }
 
-constexpr int TALL = 64, MT = TALL / 16;
+constexpr int TALL = 64;
 
 // the slot of row r's 16-byte piece c of 128 of k among a tile's 256: rows are
 // XORed with the piece so that a row's pieces, written together, and a
@@ -304,60 +287,150 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs A, int parts) {
   }
 }
 
-// KT pieces of 32 of the rank.
+// KT pieces of 32 of the rank.  The block's waves take 16 places each and share
+// the columns, 64 at a time: B's rows of them, contiguous in memory, pass
+// through LDS a step ahead (fragments loaded from memory, 64 bytes of each of 16
+// rows, cost the address unit twice as much and took 11 us of the 85 that this
+// product took of 8190 rows beside 7168 columns).  u stays in registers.  The
+// sums pass through an LDS region of the wave's own, so that y and out move in
+// whole lines, 128 bytes of 8 rows an instruction.
 template <int KT, bool kBF16>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs A, int parts, int col_parts) {
-  __shared__ __attribute__((aligned(16))) u32x4 frag[MT][KT][2][64];
+  constexpr int NB = 4, WIDE = 16 * NB;                             // columns of a step
+  constexpr int EPL = kBF16 ? 8 : 4;                                // a lane's columns
+  constexpr int LPR = WIDE / EPL, RPI = 64 / LPR, ITS = 16 / RPI;   // lanes to a row, rows and instructions
+  constexpr int BROW = 64 * KT + 16;                                // bytes of a row of B in LDS, at most
+  __shared__ __attribute__((aligned(16))) uint8_t bs[2][WIDE * BROW];
+  __shared__ __attribute__((aligned(16))) float st[4][16][WIDE + 4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const RowTile tile = find_tile(A.plan, TALL, blockIdx.x / col_parts);
   if (tile.group < 0) return;
-  const int part = blockIdx.x % col_parts, steps = (A.n + 31) / 32;
+  const int part = blockIdx.x % col_parts, steps = (A.n + WIDE - 1) / WIDE;
   const int s0 = int(int64_t(steps) * part / col_parts), s1 = int(int64_t(steps) * (part + 1) / col_parts);
   if (tile.group == A.plan.groups) {
-    if (A.out != A.y) copy_rows<256, kBF16>(A, tile, 32 * s0, min(32 * s1, A.n));
+    if (A.out != A.y) copy_rows<256, kBF16>(A, tile, WIDE * s0, min(WIDE * s1, A.n));
     return;
   }
-  const int r = lane & 15;
-  int64_t y_at[MT], out_at[MT];
+  const int q = lane >> 4, r = lane & 15;
+  const int first = 16 * wave, count = tile.count - first;   // this wave's places of the tile
+  const int lr = lane / LPR, lc = lane % LPR * EPL;          // this lane's row and first column of a piece
+  int64_t y_at[ITS], out_at[ITS];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int64_t row = row_of(A.plan, tile.first + min(16 * m + r, tile.count - 1));
-    y_at[m] = row * A.y_stride;
-    out_at[m] = row * A.out_stride;
+  for (int it = 0; it < ITS; ++it) {
+    const int64_t row = row_of(A.plan, tile.first + min(first + RPI * it + lr, tile.count - 1));
+    y_at[it] = row * A.y_stride * (kBF16 ? 2 : 4);
+    out_at[it] = (row * A.out_stride + lc) * (kBF16 ? 2 : 4);
   }
-  const uint16_t* b = static_cast<const uint16_t*>(A.b) + int64_t(tile.group) * A.n * A.rank;
-  const float scale = A.scale ? A.scale[tile.group] : 1.0f;
-  Step<MT, KT, kBF16> P, Q;
-  auto load = [&](Step<MT, KT, kBF16>& S, int st) { load_step<MT, KT, kBF16>(S, A, b, y_at, 32 * min(st, steps - 1)); };
-  load(P, s0 + wave);   // under way while u is made
-  for (int t = threadIdx.x; t < MT * KT * 64; t += 256) {
-    const int ln = t & 63, kt = t / 64 % KT, m = t / 64 / KT, j = 32 * kt + 8 * (ln >> 4);
-    const int place = tile.first + min(16 * m + (ln & 15), tile.count - 1);
-    floatx4 u[2] = {floatx4{0.f, 0.f, 0.f, 0.f}, floatx4{0.f, 0.f, 0.f, 0.f}};
-    if (j < A.rank) {
-      const float* p = A.part + int64_t(place) * A.rank + j;
-      for (int s = 0; s < parts; ++s, p += int64_t(A.plan.rows) * A.rank) {
-        u[0] += *reinterpret_cast<const floatx4*>(p);
-        u[1] += *reinterpret_cast<const floatx4*>(p + 4);
-      }
-    }
-    const Split s = split(u[0], u[1]);
-    frag[m][kt][0][ln] = __builtin_bit_cast(u32x4, s.hi);
-    frag[m][kt][1][ln] = __builtin_bit_cast(u32x4, s.lo);
-  }
-  __syncthreads();
-  auto u = [&](int m, int kt) { return Split{as_bf16x8(frag[m][kt][0][lane]), as_bf16x8(frag[m][kt][1][lane])}; };
-  auto finish = [&](const Step<MT, KT, kBF16>& S, int st) {
-    finish_step<MT, KT, kBF16>(S, A, u, scale, out_at, tile.count, 32 * st);
+  struct Y {
+    u32x4 v[ITS];
   };
-  for (int st = s0 + wave; st < s1; st += 8) {
-    load(Q, st + 4);
-    __builtin_amdgcn_sched_barrier(0);   // before the step's own arithmetic
-    finish(P, st);
-    load(P, st + 8);
-    __builtin_amdgcn_sched_barrier(0);
-    if (st + 4 < s1) finish(Q, st + 4);
+  auto yload = [&](Y& y, int step) {   // columns past n are clamped, and not stored
+    const int col = min(step * WIDE + lc, A.n - EPL) * (kBF16 ? 2 : 4);
+#pragma unroll
+    for (int it = 0; it < ITS; ++it) y.v[it] = load16(static_cast<const uint8_t*>(A.y) + y_at[it] + col);
+  };
+  // B: pieces of 16 bytes, 8 rank of them a step; a rank past the last meets
+  // zeros of u, so its place in LDS is clamped
+  const uint8_t* b = static_cast<const uint8_t*>(A.b) + int64_t(tile.group) * A.n * A.rank * 2;
+  const int pieces = 8 * A.rank, in_row = A.rank / 8, row_bytes = 2 * A.rank + 16;
+  int b_to[KT];
+#pragma unroll
+  for (int i = 0; i < KT; ++i) {
+    const int p = threadIdx.x + 256 * i;
+    b_to[i] = p / in_row * row_bytes + p % in_row * 16;
+  }
+  u32x4 bq[KT];
+  auto bload = [&](int step) {
+    const int64_t end = int64_t(A.n) * A.rank * 2 - 16;
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+      bq[i] = load16(b + min(int64_t(step) * pieces * 16 + (threadIdx.x + 256 * i) * 16, end));
+  };
+  auto bstore = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+      if (int(threadIdx.x) + 256 * i < pieces) *reinterpret_cast<u32x4*>(bs[buf] + b_to[i]) = bq[i];
+  };
+  int b_at[KT];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) b_at[kt] = r * row_bytes + 2 * min(32 * kt + 8 * q, A.rank - 8);
+
+  Y P, Q;
+  yload(P, s0);
+  bload(s0);
+  yload(Q, min(s0 + 1, steps - 1));
+  // u of the wave's places: the parts of k in their order
+  Split u[KT];
+  {
+    const int place = tile.first + min(first + r, tile.count - 1);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      const int j = 32 * kt + 8 * q;
+      floatx4 v[2] = {floatx4{0.f, 0.f, 0.f, 0.f}, floatx4{0.f, 0.f, 0.f, 0.f}};
+      if (j < A.rank) {
+        const float* p = A.part + int64_t(place) * A.rank + j;
+        for (int s = 0; s < parts; ++s, p += int64_t(A.plan.rows) * A.rank) {
+          v[0] += *reinterpret_cast<const floatx4*>(p);
+          v[1] += *reinterpret_cast<const floatx4*>(p + 4);
+        }
+      }
+      u[kt] = split(v[0], v[1]);
+    }
+  }
+  const float scale = A.scale ? A.scale[tile.group] : 1.0f;
+  bstore(0);
+  bload(min(s0 + 1, steps - 1));
+  __syncthreads();
+
+  auto work = [&](Y& y, int step, int buf) {
+    floatx4 d[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) d[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    if (count > 0) {   // wave-uniform
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const bf16x8_t bf = as_bf16x8(load16(bs[buf] + 16 * i * row_bytes + b_at[kt]));
+          d[i] = mfma(bf, u[kt].hi, d[i]);
+          d[i] = mfma(bf, u[kt].lo, d[i]);
+        }
+    }
+    bstore(buf ^ 1);   // read by nobody since the last barrier
+    bload(min(step + 2, steps - 1));
+    if (count > 0) {
+      // a wave's LDS operations stay in order
+#pragma unroll
+      for (int i = 0; i < NB; ++i) *reinterpret_cast<floatx4*>(&st[wave][r][16 * i + 4 * q]) = d[i];
+      __asm__ volatile("" ::: "memory");
+      const int64_t col = int64_t(step) * WIDE * (kBF16 ? 2 : 4);
+      const bool inside = step * WIDE + lc < A.n;
+#pragma unroll
+      for (int it = 0; it < ITS; ++it) {
+        const u32x4 v = y.v[it];
+        const floatx4 a0 = *reinterpret_cast<const floatx4*>(&st[wave][RPI * it + lr][lc]);
+        u32x4 o;
+        if constexpr (kBF16) {
+          const floatx4 a1 = *reinterpret_cast<const floatx4*>(&st[wave][RPI * it + lr][lc + 4]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[e] = pack_bf16x2(fmaf(scale, e < 2 ? a0[2 * e] : a1[2 * e - 4], __uint_as_float(v[e] << 16)),
+                               fmaf(scale, e < 2 ? a0[2 * e + 1] : a1[2 * e - 3], __uint_as_float(v[e] & 0xFFFF0000u)));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(fmaf(scale, a0[e], __uint_as_float(v[e])));
+        }
+        if (inside && RPI * it + lr < count)
+          *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(A.out) + out_at[it] + col) = o;
+      }
+      yload(y, min(step + 2, steps - 1));
+    }
+    __syncthreads();
+  };
+  for (int step = s0; step < s1; step += 2) {
+    work(P, step, 0);
+    if (step + 1 < s1) work(Q, step + 1, 1);
   }
 }
 
@@ -369,21 +442,21 @@ int cus_or(int otherwise) {
 // Adapters of few rows: less than 48 on average.
 bool few_rows(int64_t rows, int64_t groups) { return rows < 48 * groups; }
 
-// Parts of k of the first product: two blocks to a CU, at least 512 of k each.
+// Parts of k of the first product: a block to a CU, at least 512 of k each.
 int parts_of(int64_t rows, int64_t groups, int64_t k) {
   if (few_rows(rows, groups)) return 0;
   const int64_t tiles = most_tiles(rows, groups, TALL);
-  int64_t parts = (2 * cus_or(256) + tiles - 1) / tiles;
+  int64_t parts = (cus_or(256) + tiles - 1) / tiles;
   if (parts > k / 512) parts = k / 512;
   return parts < 1 ? 1 : int(parts);
 }
 
 // Parts of the columns: as many as give a CU `each` blocks, at least one step
-// of 32 columns for each of `waves` waves.
-int col_parts_of(int64_t tiles, int64_t n, int each, int waves) {
-  int64_t parts = (each * cus_or(256) + tiles - 1) / tiles;
-  const int64_t most = ((n + 31) / 32 + waves - 1) / waves;
-  return int(parts < most ? parts : most);
+// of `wide` columns for each of `waves` waves.
+int col_parts_of(int64_t tiles, int64_t n, int each, int waves, int wide) {
+  int64_t parts = each * cus_or(256) / tiles;
+  const int64_t most = ((n + wide - 1) / wide + waves - 1) / waves;
+  return int(parts < 1 ? 1 : parts < most ? parts : most);
 }
 
 template <int RT>
@@ -391,7 +464,7 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
   const bool bf16 = a.y_dtype == 1;
   if (few_rows(a.plan.rows, a.plan.groups)) {
     const int64_t tiles = most_tiles(a.plan.rows, a.plan.groups, 16);
-    const int cols = col_parts_of(tiles, a.n, 1, 8);
+    const int cols = col_parts_of(tiles, a.n, 1, 8, 32);
     if (bf16) lora_few_kernel<RT, true><<<unsigned(tiles * cols), 512, 0, s>>>(a, cols);
     else lora_few_kernel<RT, false><<<unsigned(tiles * cols), 512, 0, s>>>(a, cols);
     return hipGetLastError();
@@ -402,7 +475,7 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr int KT = (RT + 1) / 2;
-  const int cols = col_parts_of(tiles, a.n, 3, 4);
+  const int cols = col_parts_of(tiles, a.n, 8, 1, 256);
   if (bf16) lora_up_kernel<KT, true><<<unsigned(tiles * cols), 256, 0, s>>>(a, parts, cols);
   else lora_up_kernel<KT, false><<<unsigned(tiles * cols), 256, 0, s>>>(a, parts, cols);
   return hipGetLastError();
