@@ -129,7 +129,10 @@ __device__ __forceinline__ void copy_rows(const LoraArgs& A, const RowTile& tile
 template <int RT, bool kBF16>
 __global__ __launch_bounds__(512) void lora_few_kernel(LoraArgs A, int col_parts) {
   constexpr int WAVES = 8, KT = (RT + 1) / 2;
-  __shared__ floatx4 red[WAVES][RT][64];
+  __shared__ union {
+    __attribute__((aligned(16))) uint8_t stage[WAVES][4096];
+    floatx4 red[WAVES][RT][64];   // the waves' sums
+  } sm;
   __shared__ __attribute__((aligned(16))) float us[16][32 * KT + 4];   // u, zero past the rank
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -144,28 +147,69 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraArgs A, int col_parts
   }
   const int q = lane >> 4, r = lane & 15, G = A.k / 128;
   const int64_t row = row_of(A.plan, tile.first + min(r, tile.count - 1));
-  const uint16_t* xr = static_cast<const uint16_t*>(A.x) + row * A.x_stride + 8 * q;
-  const uint16_t* ar[RT];
+  // Rows of x and A are loaded whole (lane: row 4 i + q at k 8 r of a piece)
+  // and become fragments in a wave-private LDS tile of 16 rows x 256 bytes: as
+  // fragments straight from memory they cost the address unit two to four
+  // times as much, and of x only the rows that there are would be wanted.
+  const uint16_t* xr[4];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-    ar[i] = static_cast<const uint16_t*>(A.a) + (int64_t(tile.group) * A.rank + min(16 * i + r, A.rank - 1)) * A.k + 8 * q;
-
+  for (int i = 0; i < 4; ++i)
+    xr[i] = static_cast<const uint16_t*>(A.x) +
+            row_of(A.plan, tile.first + min(4 * i + q, tile.count - 1)) * A.x_stride + 8 * r;
+  const uint16_t* a = static_cast<const uint16_t*>(A.a) + int64_t(tile.group) * A.rank * A.k + 8 * r;
+  struct Piece {
+    u32x4 x[4], a[RT][4];
+  };
+  auto load = [&](Piece& P, int g) {   // past the end: the last piece again, not used
+    g = min(g, G - 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i == 0 || 4 * i < tile.count) P.x[i] = load16(xr[i] + g * 128);   // uniform
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) P.a[t][i] = load16(a + int64_t(min(16 * t + 4 * i + q, A.rank - 1)) * A.k + g * 128);
+  };
+  uint8_t* const stage = sm.stage[wave];
+  auto slot = [](int row, int piece) { return row * 256 + 16 * (piece ^ row); };
   floatx4 acc[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-  for (int g = wave; g < G; g += WAVES) {
-    u32x4 xf[4], af[4][RT];
+  auto compute = [&](const Piece& P) {   // a wave's LDS operations stay in order
+    u32x4 xf[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      xf[s] = load16(xr + g * 128 + 32 * s);
+    for (int i = 0; i < 4; ++i)
+      if (i == 0 || 4 * i < tile.count) *reinterpret_cast<u32x4*>(stage + slot(4 * i + q, r)) = P.x[i];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) af[s][i] = load16(ar[i] + g * 128 + 32 * s);
+    for (int s = 0; s < 4; ++s) xf[s] = load16(stage + slot(r, 4 * s + q));
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      __asm__ volatile("" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(stage + slot(4 * i + q, r)) = P.a[t][i];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        acc[t] = mfma(as_bf16x8(load16(stage + slot(r, 4 * s + q))), as_bf16x8(xf[s]), acc[t]);
     }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < RT; ++i) acc[i] = mfma(as_bf16x8(af[s][i]), as_bf16x8(xf[s]), acc[i]);
+    __asm__ volatile("" ::: "memory");
+  };
+  Piece P;
+  load(P, wave);
+  if constexpr (RT <= 4) {
+    Piece Q;
+    for (int g = wave; g < G; g += 2 * WAVES) {
+      load(Q, g + WAVES);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(P);
+      load(P, g + 2 * WAVES);
+      __builtin_amdgcn_sched_barrier(0);
+      if (g + WAVES < G) compute(Q);
+    }
+  } else {   // two pieces would not fit in the registers
+    for (int g = wave; g < G; g += WAVES) {
+      compute(P);
+      load(P, g + WAVES);
+    }
   }
   // the first step's y and B are under way while u is added up
   const uint16_t* b = static_cast<const uint16_t*>(A.b) + int64_t(tile.group) * A.n * A.rank;
@@ -173,16 +217,17 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraArgs A, int col_parts
   Step<KT, kBF16> S;
   load_step<KT, kBF16>(S, A, b, y_at, 32 * min(s0 + wave, steps - 1));
   const float scale = A.scale ? A.scale[tile.group] : 1.0f;
+  __syncthreads();   // the sums go where the rows were
 #pragma unroll
-  for (int i = 0; i < RT; ++i) red[wave][i][lane] = acc[i];
+  for (int i = 0; i < RT; ++i) sm.red[wave][i][lane] = acc[i];
   __syncthreads();
   for (int t = threadIdx.x; t < 2 * KT * 64; t += 512) {
     const int i = t / 64, ln = t % 64, j = 16 * i + 4 * (ln >> 4);
     floatx4 sum = floatx4{0.f, 0.f, 0.f, 0.f};
     if (j < A.rank) {   // the rank is a multiple of 8
-      sum = red[0][min(i, RT - 1)][ln];
+      sum = sm.red[0][min(i, RT - 1)][ln];
 #pragma unroll
-      for (int w = 1; w < WAVES; ++w) sum += red[w][min(i, RT - 1)][ln];
+      for (int w = 1; w < WAVES; ++w) sum += sm.red[w][min(i, RT - 1)][ln];
     }
     *reinterpret_cast<floatx4*>(&us[ln & 15][j]) = sum;
   }
