@@ -36,13 +36,15 @@ struct Args16 {
   int top_k, gather, n, k, walkers, chunk;   // chunk: groups of x in LDS at a time
 };
 
-constexpr int WAVES = 8, NT = 2;
+constexpr int NT = 2;
+// Waves of a block: 16 where its rows fill the LDS of a CU.
+constexpr int waves_of(int mt) { return mt == 1 ? 8 : 16; }
 // LDS: fragments [chunk][MT][4 pieces][16 XR] x 16 bytes (XR rows to an
 // m-tile: 16, or 4 where a tile holds at most 4 places), then sums
 // [chunk][MT][XR], then (KS > 1) the waves' accumulators.
 constexpr int frag_bytes(int mt, int xr) { return mt * 256 * xr; }
 constexpr int group_bytes(int mt, int xr) { return mt * (256 * xr + 4 * xr); }
-constexpr int red_bytes(int mt, int ks) { return ks > 1 ? WAVES * NT * mt * 1024 : 0; }
+constexpr int red_bytes(int mt, int ks) { return ks > 1 ? waves_of(mt) * NT * mt * 1024 : 0; }
 
 // The slot of row r's 16-byte piece c (k 8 c of the group) within a group's
 // slots: piece 4 s + q of fragment s belongs to lanes of quarter q, which read
@@ -52,10 +54,10 @@ template <int XR>
 __device__ __forceinline__ int piece_slot(int r, int c) { return c * XR + (r ^ (c & (XR - 1))); }
 
 template <int MT, int XR, int KS, int W, bool kSilu, bool kBF16Out>
-__global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void moe_w4a16_kernel(Args16 A) {
+__global__ __launch_bounds__(waves_of(MT) * 64, 4) void moe_w4a16_kernel(Args16 A) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   static_assert(XR == 16 || MT == 1, "tiles of 4 places are one m-tile");
-  constexpr int TALL = MT == 1 ? XR : 16 * MT, FB = frag_bytes(MT, XR);
+  constexpr int WAVES = waves_of(MT), TALL = MT == 1 ? XR : 16 * MT, FB = frag_bytes(MT, XR);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int walker = blockIdx.x % A.walkers;
@@ -70,7 +72,7 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void moe_w4a16_kernel(Args16 
     const int64_t bytes = int64_t(n_out) * (kBF16Out ? 2 : 4);
     for (int i = 0; i < tile.count; ++i) {
       uint4* row = reinterpret_cast<uint4*>(static_cast<uint8_t*>(A.y) + (tile.first + i) * bytes);
-      for (int64_t j = walker * 512 + threadIdx.x; j < bytes / 16; j += A.walkers * 512)
+      for (int64_t j = walker * WAVES * 64 + threadIdx.x; j < bytes / 16; j += A.walkers * WAVES * 64)
         row[j] = make_uint4(0, 0, 0, 0);
     }
     return;
@@ -266,7 +268,7 @@ __global__ __launch_bounds__(512, MT == 1 ? 4 : 2) void moe_w4a16_kernel(Args16 
 
 template <int MT, int XR, int KS>
 hipError_t launch16(Args16 a, const MoeGemm& g, hipStream_t s) {
-  constexpr int W = 2, TALL = MT == 1 ? XR : 16 * MT;
+  constexpr int W = 2, WAVES = waves_of(MT), TALL = MT == 1 ? XR : 16 * MT;
   const int G = g.k / 128, T = g.n / 16;
   const int most = (160 * 1024 - red_bytes(MT, KS)) / group_bytes(MT, XR);
   a.chunk = G < most ? G : most;
@@ -275,8 +277,8 @@ hipError_t launch16(Args16 a, const MoeGemm& g, hipStream_t s) {
   const int64_t widest = (units + WAVES / KS - 1) / (WAVES / KS);
   const int cus = device_cu_count();
   int64_t walkers = widest;
-  if (KS == 1) {   // two blocks to a CU, as far as there are units for their waves
-    walkers = (2 * (cus > 0 ? cus : 256) + tiles - 1) / tiles;
+  if (KS == 1) {   // 16 waves to a CU, as far as there are units for them
+    walkers = (16 / WAVES * (cus > 0 ? cus : 256) + tiles - 1) / tiles;
     if (walkers > widest) walkers = widest;
   }
   a.walkers = int(walkers);
@@ -285,7 +287,7 @@ hipError_t launch16(Args16 a, const MoeGemm& g, hipStream_t s) {
   auto run = [&](auto kern, std::atomic<int>* flag) {
     const hipError_t e = lds_limit_once(flag, reinterpret_cast<const void*>(kern), 160 * 1024);
     if (e != hipSuccess) return e;
-    kern<<<unsigned(tiles * walkers), 512, lds, s>>>(a);
+    kern<<<unsigned(tiles * walkers), WAVES * 64, lds, s>>>(a);
     return hipGetLastError();
   };
   if (g.silu_mul)
