@@ -293,8 +293,10 @@ def _run_own(state):
         ids, weights, plan = qlin.moe_route(state["logits"], case["top_k"], renormalize=case["renorm"])
         return ids, weights, plan.order, plan.where, plan.offsets
     if op == "lora":
+        # binary32 rows are added to in place, as the plain form adds to what no cast copies
+        out = state["out"] if case["out"] == "bf16" else state["y"]
         return qlin.lora_add(state["y"], state["x"], state["a"], state["b"], state["plan"],
-                             scale=state["scale"], out=state["out"])
+                             scale=state["scale"], out=out)
     if op == "combine":
         return qlin.moe_combine(state["rows"], state["plan"], state["weights"],
                                 out_dtype=_dtype(case["out"]))
