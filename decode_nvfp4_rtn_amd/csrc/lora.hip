@@ -17,9 +17,9 @@
 // buffer for each part of k.  "up" adds the parts in their order and makes out
 // for 64 places and a part of the columns.
 //
-// u enters the second product as a sum of two bf16 values (16 bits of mantissa
-// or more), which costs nothing that shows: that product is bound by reading y
-// and writing out.
+// u enters the second product as a sum of bf16 values, two beside a bf16 y (16
+// bits of mantissa or more), three beside a binary32 one (all of it): that
+// product is bound by reading y and writing out, so they cost nothing that shows.
 //
 // Rows without an adapter come last in the plan: they are copied, or left
 // alone where out is y.
@@ -39,20 +39,27 @@ __device__ __forceinline__ int row_of(const RowPlan& p, int place) {
   return int(min(uint32_t(p.order[place]), uint32_t(p.rows - 1)));
 }
 
-// eight binary32 values as two bf16 values each
+// Eight binary32 values, each a sum of kTerms bf16 values: two keep 16 bits of
+// the mantissa or more, three all of it.
+template <int kTerms>
 struct Split {
-  bf16x8_t hi, lo;
+  bf16x8_t term[kTerms];
 };
-__device__ __forceinline__ Split split(floatx4 a, floatx4 b) {
-  Split s;
+template <int kTerms>
+__device__ __forceinline__ Split<kTerms> split(floatx4 a, floatx4 b) {
+  Split<kTerms> s;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float v = e < 4 ? a[e & 3] : b[e & 3];
-    s.hi[e] = static_cast<__bf16>(v);
-    s.lo[e] = static_cast<__bf16>(v - static_cast<float>(s.hi[e]));
+    float v = e < 4 ? a[e & 3] : b[e & 3];
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) {
+      s.term[t][e] = static_cast<__bf16>(v);
+      v -= static_cast<float>(s.term[t][e]);
+    }
   }
   return s;
 }
+constexpr int terms_of(bool bf16) { return bf16 ? 2 : 3; }
 
 // Few rows: a step of 32 columns of the tile's rows, its y and the operand made
 // of B.  The MFMA's rows are columns of out in an order that leaves each lane
@@ -81,17 +88,15 @@ __device__ __forceinline__ void load_step(Step<KT, kBF16>& S, const LoraArgs& A,
 }
 
 template <int KT, bool kBF16>
-__device__ __forceinline__ void finish_step(const Step<KT, kBF16>& S, const LoraArgs& A, const Split (&u)[KT],
-                                            float scale, int64_t out_at, int count, int col0) {
+__device__ __forceinline__ void finish_step(const Step<KT, kBF16>& S, const LoraArgs& A, const Split<terms_of(kBF16)> (&u)[KT], float scale, int64_t out_at, int count, int col0) {
   const int q = (threadIdx.x >> 4) & 3, r = threadIdx.x & 15;
   floatx4 acc[2] = {floatx4{0.f, 0.f, 0.f, 0.f}, floatx4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      acc[i] = mfma(as_bf16x8(S.b[i][kt]), u[kt].hi, acc[i]);
-      acc[i] = mfma(as_bf16x8(S.b[i][kt]), u[kt].lo, acc[i]);
-    }
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int t = 0; t < terms_of(kBF16); ++t) acc[i] = mfma(as_bf16x8(S.b[i][kt]), u[kt].term[t], acc[i]);
   const int col = col0 + 8 * q;
   if (col >= A.n || r >= count) return;   // n is a multiple of 16
   if constexpr (kBF16) {
@@ -232,10 +237,10 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraArgs A, int col_parts
     *reinterpret_cast<floatx4*>(&us[ln & 15][j]) = sum;
   }
   __syncthreads();
-  Split u[KT];
+  Split<terms_of(kBF16)> u[KT];
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
-    u[kt] = split(*reinterpret_cast<const floatx4*>(&us[r][32 * kt + 8 * q]),
+    u[kt] = split<terms_of(kBF16)>(*reinterpret_cast<const floatx4*>(&us[r][32 * kt + 8 * q]),
                   *reinterpret_cast<const floatx4*>(&us[r][32 * kt + 8 * q + 4]));
   for (int st = s0 + wave; st < s1; st += WAVES) {
     Step<KT, kBF16> next;
@@ -406,7 +411,7 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs A, int parts, int
   bload(s0);
   yload(Q, min(s0 + 1, steps - 1));
   // u of the wave's places: the parts of k in their order
-  Split u[KT];
+  Split<terms_of(kBF16)> u[KT];
   {
     const int place = tile.first + min(first + r, tile.count - 1);
 #pragma unroll
@@ -420,7 +425,7 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs A, int parts, int
           v[1] += *reinterpret_cast<const floatx4*>(p + 4);
         }
       }
-      u[kt] = split(v[0], v[1]);
+      u[kt] = split<terms_of(kBF16)>(v[0], v[1]);
     }
   }
   const float scale = A.scale ? A.scale[tile.group] : 1.0f;
@@ -438,8 +443,8 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs A, int parts, int
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           const bf16x8_t bf = as_bf16x8(load16(bs[buf] + 16 * i * row_bytes + b_at[kt]));
-          d[i] = mfma(bf, u[kt].hi, d[i]);
-          d[i] = mfma(bf, u[kt].lo, d[i]);
+#pragma unroll
+          for (int t = 0; t < terms_of(kBF16); ++t) d[i] = mfma(bf, u[kt].term[t], d[i]);
         }
     }
     bstore(buf ^ 1);   // read by nobody since the last barrier

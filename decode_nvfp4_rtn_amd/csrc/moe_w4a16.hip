@@ -53,6 +53,12 @@ constexpr int red_bytes(int mt, int ks) { return ks > 1 ? waves_of(mt) * NT * mt
 template <int XR>
 __device__ __forceinline__ int piece_slot(int r, int c) { return c * XR + (r ^ (c & (XR - 1))); }
 
+// v of the lane N places on in the same row of 16 lanes
+template <int N>
+__device__ __forceinline__ float row_rotated(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xF, 0xF, false));
+}
+
 template <int MT, int XR, int KS, int W, bool kSilu, bool kBF16Out>
 __global__ __launch_bounds__(waves_of(MT) * 64, 4) void moe_w4a16_kernel(Args16 A) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -108,25 +114,43 @@ __global__ __launch_bounds__(waves_of(MT) * 64, 4) void moe_w4a16_kernel(Args16 
   };
 
   float* const sums = reinterpret_cast<float*>(smem + size_t(A.chunk) * FB);
-  // the rows of groups [c0, c1) into LDS: 16 lanes to a row's group
+  // the rows of groups [c0, c1) into LDS: 16 lanes to a row's group, a wave to
+  // four rows and a share of the groups, four loads under way
+  const int quads = (tile.count + 3) / 4, shares = WAVES / quads;
+  const int row = 4 * (wave % quads) + q, share = wave / quads;
+  const uint16_t* x_row;
+  {
+    const int place = tile.first + min(row, tile.count - 1);
+    int64_t from = place;
+    if (A.gather) from = min(uint32_t(A.plan.order[place]), uint32_t(A.plan.rows - 1)) / uint32_t(A.top_k);
+    x_row = A.x + from * A.k + 8 * r;
+  }
   auto stage = [&](int c0, int c1) {
-    const int rows = (tile.count + 3) / 4;
-    for (int i = wave; i < rows * (c1 - c0); i += WAVES) {
-      const int g = i / rows, row = 4 * (i % rows) + q;
-      const int place = tile.first + min(row, tile.count - 1);
-      int64_t from = place;
-      if (A.gather) from = min(uint32_t(A.plan.order[place]), uint32_t(A.plan.rows - 1)) / uint32_t(A.top_k);
-      const uint4 v = *reinterpret_cast<const uint4*>(A.x + from * A.k + (c0 + g) * 128 + 8 * r);
-      const uint32_t d[4] = {v.x, v.y, v.z, v.w};
-      float s = 0.f;
+    if (share >= shares) return;
+    const int mt = XR == 16 ? row >> 4 : 0, rr = XR == 16 ? row & 15 : row;
+    uint8_t* const to = smem + mt * (256 * XR) + piece_slot<XR>(rr, r) * 16;
+    for (int g0 = c0 + share; g0 < c1; g0 += 4 * shares) {
+      uint4 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        s += __uint_as_float(d[j] << 16) + __uint_as_float(d[j] & 0xFFFF0000u);
+      for (int i = 0; i < 4; ++i)
+        v[i] = *reinterpret_cast<const uint4*>(x_row + min(g0 + i * shares, c1 - 1) * 128);
 #pragma unroll
-      for (int m = 8; m; m /= 2) s += __shfl_xor(s, m);
-      const int mt = XR == 16 ? row >> 4 : 0, rr = XR == 16 ? row & 15 : row;
-      *reinterpret_cast<uint4*>(smem + g * FB + mt * (256 * XR) + piece_slot<XR>(rr, r) * 16) = v;
-      if (r == 0) sums[(g * MT + mt) * XR + rr] = -136.0f * s;
+      for (int i = 0; i < 4; ++i) {
+        const int g = g0 + i * shares - c0;
+        if (g >= c1 - c0) break;   // wave-uniform
+        const uint32_t d[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s += __uint_as_float(d[j] << 16) + __uint_as_float(d[j] & 0xFFFF0000u);
+        // over the row's 16 lanes
+        s += row_rotated<8>(s);
+        s += row_rotated<4>(s);
+        s += row_rotated<2>(s);
+        s += row_rotated<1>(s);
+        *reinterpret_cast<uint4*>(to + g * FB) = v[i];
+        if (r == 0) sums[(g * MT + mt) * XR + rr] = -136.0f * s;
+      }
     }
   };
   const uint32_t nib_mask = vconst(0x000F000Fu), bf16_128 = vconst(0x43004300u);
@@ -313,8 +337,10 @@ hipError_t launch_moe_gemm_w4a16(const MoeGemm& g, const void* x, hipStream_t s)
   a.gather = g.gather;
   a.n = g.n;
   a.k = g.k;
-  // Up to 4 tokens: no expert has more rows (a token chooses it once).
-  if (g.plan.rows <= 4 * g.top_k) {
+  // Tiles of 4 places: up to 4 tokens (no expert has more rows, a token chooses
+  // it once), or where experts have 2 rows on average, so that few take a second
+  // tile.  x then leaves room in LDS for a second block on the CU.
+  if (g.plan.rows <= 4 * g.top_k || g.plan.rows <= 2 * g.plan.groups) {
     // waves to a pair of weight tiles: until 8 waves to a CU have work, at
     // least 4 groups each
     const int cus = device_cu_count();

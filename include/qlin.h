@@ -705,8 +705,9 @@ int moe_combine(const void *rows, int x_dtype, const int32_t *where, const int32
 /* ------------------------------------------------------------------------
  * Low-rank adapters beside a projection that all rows share:
  *   out[t, :] = y[t, :] + scale[i] B_i (A_i x[t, :]),  i the adapter of row t
- * binary32 accumulation; A x is kept in 16 bits of mantissa or more, and out is
- * rounded once.  Rows without an adapter: out = y.
+ * binary32 accumulation; A x is kept in 16 bits of mantissa or more (all 24
+ * where y is binary32), and out is rounded once.  Rows without an adapter: out =
+ * y.
  *
  * y, out   [rows, n] QL_F32 or QL_BF16 (y_dtype for both), rows y_stride and
  *          out_stride elements apart (slices of a fused projection will do).

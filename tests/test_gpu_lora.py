@@ -28,12 +28,14 @@ def on(v, dtype=BF):
 
 def bound_of(y, x, a, b, scale, ids, dtype):
     """(reference, bound).  A x: k binary32 steps of at most 2^-23 each, at
-    least 16 bits kept of the result; B u: rank steps; the last sum rounds by
-    2^-24 of its terms; then the output's rounding."""
+    least 16 bits kept of the result (24 beside binary32 rows); B u: a step for
+    each of the rank and of up to three terms; the last sum rounds by 2^-24 of
+    its terms; then the output's rounding."""
     rank, k = a.shape[1:]
     want, mid, far = rows.lora(y, x.astype(np.float64), a.astype(np.float64), b.astype(np.float64),
                                scale.astype(np.float64), ids)
-    slack = k * 2.0 ** -23 * far + (2.0 ** -16 + (2 * rank + 2) * 2.0 ** -23) * mid + 2.0 ** -23 * np.abs(want)
+    kept = 2.0 ** -16 if dtype == BF else 2.0 ** -23
+    slack = k * 2.0 ** -23 * far + (kept + (3 * rank + 2) * 2.0 ** -23) * mid + 2.0 ** -23 * np.abs(want)
     slack[(np.asarray(ids) < 0) | (np.asarray(ids) >= a.shape[0])] = 0
     return want, slack + half_step(np.abs(want) + slack, dtype)
 
