@@ -4,7 +4,7 @@
 //
 // Plan: a stable counting sort.  A block takes a run of rows and counts its
 // groups; a second launch adds up the counts of the blocks before its own
-// (every block for itself: at most 128 blocks' counts, read from L2), and
+// (every block for itself: at most 256 blocks' counts, read from L2), and
 // writes each row's place.  Within a wave a row's rank among the rows of its
 // group comes from ballots over the bits of the group's number.  One block's
 // worth of rows takes one launch.  Whole numbers only, counted by integer
@@ -17,13 +17,19 @@ namespace qlin {
 namespace {
 
 constexpr int THREADS = 1024, WAVES = THREADS / 64;
-constexpr int kMostBlocks = 128;
+constexpr int kMostBlocks = 256;
+
+constexpr int kHeld = 1024;   // rows of a block whose choices stay in LDS
 
 struct PlanSmem {
   int base[kMostGroups + 1];             // next place of each group
+  int32_t held[kHeld];                   // the block's choices, where they fit
   __attribute__((aligned(4))) uint8_t wave_count[WAVES][kMostGroups + 1];
   int carry[WAVES];
 };
+
+// Counts of a block: rows of groups + 1 numbers, padded to whole 16 bytes.
+__host__ __device__ constexpr int count_stride(int groups) { return (groups + 4) / 4 * 4; }
 
 __device__ __forceinline__ int group_of(int32_t id, int groups) {
   return uint32_t(id) < uint32_t(groups) ? id : groups;
@@ -48,12 +54,19 @@ __device__ __forceinline__ void scan_groups(PlanSmem& sm, int groups) {
   }
 }
 
+// The choices of rows [begin, end) into LDS, where they fit (a barrier follows).
+__device__ __forceinline__ void hold_rows(PlanSmem& sm, const int32_t* __restrict__ ids, int begin, int end) {
+  if (end - begin <= kHeld)
+    for (int r = begin + threadIdx.x; r < end; r += THREADS) sm.held[r - begin] = ids[r];
+}
+
 // Places of the rows [begin, end) from base on, which moves along.
 __device__ __forceinline__ void place_rows(PlanSmem& sm, const int32_t* __restrict__ ids, int begin,
                                            int end, int groups, int32_t* __restrict__ order,
                                            int32_t* __restrict__ where) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int bits = 32 - __clz(groups);   // groups itself is a number too
+  const bool held = end - begin <= kHeld;
   for (int r0 = begin; r0 < end; r0 += THREADS) {
     static_assert(sizeof(sm.wave_count) % 4 == 0, "cleared by words");
     for (int i = threadIdx.x; i < int(sizeof(sm.wave_count) / 4); i += THREADS)
@@ -61,7 +74,7 @@ __device__ __forceinline__ void place_rows(PlanSmem& sm, const int32_t* __restri
     __syncthreads();
     const int row = r0 + threadIdx.x;
     const bool live = row < end;
-    const int g = live ? group_of(ids[row], groups) : 0;
+    const int g = live ? group_of(held ? sm.held[row - begin] : ids[row], groups) : 0;
     uint64_t same = __ballot(live);
     for (int b = 0; b < bits; ++b) {
       const uint64_t set = __ballot((g >> b) & 1);
@@ -91,7 +104,9 @@ __device__ __forceinline__ void count_rows(PlanSmem& sm, const int32_t* __restri
                                            int end, int groups) {
   for (int i = threadIdx.x; i <= groups; i += THREADS) sm.base[i] = 0;
   __syncthreads();
-  for (int r = begin + threadIdx.x; r < end; r += THREADS) atomicAdd(&sm.base[group_of(ids[r], groups)], 1);
+  const bool held = end - begin <= kHeld;
+  for (int r = begin + threadIdx.x; r < end; r += THREADS)
+    atomicAdd(&sm.base[group_of(held ? sm.held[r - begin] : ids[r], groups)], 1);
   __syncthreads();
 }
 
@@ -108,7 +123,7 @@ __device__ __forceinline__ void finish_block(PlanSmem& sm, const int32_t* ids, i
   count_rows(sm, ids, begin, end, groups);
   if (gridDim.x > 1) {
     for (int i = threadIdx.x; i <= groups; i += THREADS)
-      counts[int64_t(blockIdx.x) * (groups + 1) + i] = sm.base[i];
+      counts[blockIdx.x * count_stride(groups) + i] = sm.base[i];
     return;
   }
   scan_groups(sm, groups);
@@ -124,9 +139,9 @@ __global__ __launch_bounds__(THREADS) void group_count_kernel(const int32_t* __r
                                                               int32_t* __restrict__ offsets,
                                                               int32_t* __restrict__ counts) {
   __shared__ PlanSmem sm;
-  const int64_t begin = int64_t(blockIdx.x) * per_block;
-  finish_block(sm, ids, int(begin), int(min(begin + per_block, int64_t(rows))), groups, order, where,
-               offsets, counts);
+  const int64_t begin = int64_t(blockIdx.x) * per_block, end = min(begin + per_block, int64_t(rows));
+  hold_rows(sm, ids, int(begin), int(end));
+  finish_block(sm, ids, int(begin), int(end), groups, order, where, offsets, counts);
 }
 
 __global__ __launch_bounds__(THREADS) void group_place_kernel(const int32_t* __restrict__ ids, int rows,
@@ -140,19 +155,29 @@ __global__ __launch_bounds__(THREADS) void group_place_kernel(const int32_t* __r
   const int own = blockIdx.x;
   for (int i = threadIdx.x; i <= groups; i += THREADS) sm.base[i] = before[i] = 0;
   __syncthreads();
-  // several threads to a group, each a share of the blocks
-  const int wide = min((groups + 64) / 64 * 64, THREADS), shares = THREADS / wide;
-  const int share = threadIdx.x / wide;
-  for (int g = threadIdx.x % wide; g <= groups && share < shares; g += wide) {
-    int all = 0, mine = 0;
+  const int64_t begin = int64_t(own) * per_block, end = min(begin + per_block, int64_t(rows));
+  hold_rows(sm, ids, int(begin), int(end));
+  // a thread to four groups and a share of the blocks
+  const int stride = count_stride(groups), quads = stride / 4, shares = THREADS / quads;
+  const int g = threadIdx.x % quads * 4, share = threadIdx.x / quads;
+  if (share < shares) {
+    int all[4] = {0, 0, 0, 0}, mine[4] = {0, 0, 0, 0};
 #pragma unroll 8
     for (int b = share; b < blocks; b += shares) {
-      const int c = counts[int64_t(b) * (groups + 1) + g];
-      all += c;
-      mine += b < own ? c : 0;
+      const int4 c = *reinterpret_cast<const int4*>(counts + b * stride + g);
+      const int v[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        all[i] += v[i];
+        mine[i] += b < own ? v[i] : 0;
+      }
     }
-    atomicAdd(&sm.base[g], all);
-    atomicAdd(&before[g], mine);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (g + i <= groups) {   // past it: padding, never written
+        atomicAdd(&sm.base[g + i], all[i]);
+        atomicAdd(&before[g + i], mine[i]);
+      }
   }
   __syncthreads();
   scan_groups(sm, groups);
@@ -160,8 +185,7 @@ __global__ __launch_bounds__(THREADS) void group_place_kernel(const int32_t* __r
   __syncthreads();
   for (int i = threadIdx.x; i <= groups; i += THREADS) sm.base[i] += before[i];
   __syncthreads();
-  const int64_t begin = int64_t(own) * per_block;
-  place_rows(sm, ids, int(begin), int(min(begin + per_block, int64_t(rows))), groups, order, where);
+  place_rows(sm, ids, int(begin), int(end), groups, order, where);
 }
 
 // A number that orders binary32 values as unsigned integers do; +0 and -0 are
@@ -182,84 +206,116 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// One wave to a token: lane l holds logits l, l + 64, ...; top_k times the
-// largest is found (of equals the lowest expert) and taken out.  The softmax's
-// terms are exp(l - largest); those of the largest are 1 whatever it is, so
-// that infinities share the weight.
+// Two tokens at a time to a wave: lane l holds logits l, l + 64, ...; top_k times
+// the largest is found (of equals the lowest expert) and taken out.  A choice is
+// a chain of some twenty dependent steps; two tokens' chains fill each other's
+// waits, and the next two tokens' logits are under way.  The softmax's terms
+// are exp(l - largest); those of the largest are 1 whatever it is, so that
+// infinities share the weight.
 template <int PER, bool kBF16>
 __global__ __launch_bounds__(THREADS) void route_kernel(
     const void* __restrict__ logits, int64_t stride, int tokens, int tokens_per_block, int experts,
     int top_k, bool renormalize, int32_t* __restrict__ ids, float* __restrict__ weights,
     int32_t* __restrict__ order, int32_t* __restrict__ where, int32_t* __restrict__ offsets,
     int32_t* __restrict__ counts) {
+  constexpr int TOK = 2;
   __shared__ PlanSmem sm;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t0 = int64_t(blockIdx.x) * tokens_per_block;
   const int64_t t1 = min(t0 + tokens_per_block, int64_t(tokens));
-  for (int64_t t = t0 + wave; t < t1; t += WAVES) {
-    uint32_t rank[PER];
+  float raw[TOK][PER];
+  auto load = [&](int64_t t) {   // past the end: the last token again, not stored
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = i * 64 + lane;
-      float v = -INFINITY;
-      if (e < experts) {
-        if (kBF16)
-          v = __uint_as_float(uint32_t(static_cast<const uint16_t*>(logits)[t * stride + e]) << 16);
-        else
-          v = static_cast<const float*>(logits)[t * stride + e];
-      }
-      rank[i] = rank_of(v);
-    }
-    uint32_t most = rank[0];
-#pragma unroll
-    for (int i = 1; i < PER; ++i) most = max(most, rank[i]);
-    const uint32_t top = wave_max(most);
-    const float largest = value_of(top);
-    auto term = [&](uint32_t r) { return r == top ? 1.0f : r ? expf(value_of(r) - largest) : 0.0f; };
-    float total = 0.0f;
-    if (!renormalize) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) total += top ? term(rank[i]) : 0.0f;
-      total = wave_sum(total);
-    }
-    uint32_t chosen = 0;   // lane j: the j-th choice
-    int expert = -1;
-    for (int j = 0; j < top_k; ++j) {
-      uint32_t best = rank[0];
-#pragma unroll
-      for (int i = 1; i < PER; ++i) best = max(best, rank[i]);
-      const uint32_t m = wave_max(best);
-      if (m == 0) break;
-      // the lowest expert of those with the largest rank: the first register,
-      // then the first lane that holds it
-      int e = -1;
+    for (int u = 0; u < TOK; ++u) {
+      const int64_t at = min(t + u * WAVES, t1 - 1) * stride;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        if (e >= 0) break;
-        const uint64_t with = __ballot(rank[i] == m);
-        if (!with) continue;
-        const int l = __builtin_ctzll(with);
-        e = i * 64 + l;
-        if (lane == l) rank[i] = 0;
+        const int e = min(i * 64 + lane, experts - 1);
+        if (kBF16)
+          raw[u][i] = __uint_as_float(uint32_t(static_cast<const uint16_t*>(logits)[at + e]) << 16);
+        else
+          raw[u][i] = static_cast<const float*>(logits)[at + e];
       }
-      if (lane == j) chosen = m, expert = e;
     }
-    const float w = chosen ? term(chosen) : 0.0f;
-    if (renormalize) total = wave_sum(lane < top_k ? w : 0.0f);
-    if (lane < top_k) {
-      ids[t * top_k + lane] = expert;
-      weights[t * top_k + lane] = chosen ? w / total : 0.0f;
+  };
+  if (t0 + wave < t1) load(t0 + wave);
+  for (int64_t t = t0 + wave; t < t1; t += TOK * WAVES) {
+    uint32_t rank[TOK][PER], top[TOK];
+    float total[TOK];
+#pragma unroll
+    for (int u = 0; u < TOK; ++u)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) rank[u][i] = i * 64 + lane < experts ? rank_of(raw[u][i]) : 0;
+    load(t + TOK * WAVES);
+    auto most = [&](int u) {
+      uint32_t v = rank[u][0];
+#pragma unroll
+      for (int i = 1; i < PER; ++i) v = max(v, rank[u][i]);
+      return wave_max(v);
+    };
+    auto term = [&](int u, uint32_t r) {
+      return r == top[u] ? 1.0f : r ? expf(value_of(r) - value_of(top[u])) : 0.0f;
+    };
+    uint32_t chosen[TOK];   // lane j: the j-th choice
+    int expert[TOK];
+#pragma unroll
+    for (int u = 0; u < TOK; ++u) {
+      top[u] = most(u);
+      chosen[u] = 0;
+      expert[u] = -1;
+      total[u] = 0.0f;
+    }
+    if (!renormalize) {
+#pragma unroll
+      for (int u = 0; u < TOK; ++u) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) total[u] += top[u] ? term(u, rank[u][i]) : 0.0f;
+        total[u] = wave_sum(total[u]);
+      }
+    }
+    for (int j = 0; j < top_k; ++j) {
+      uint32_t m[TOK];
+      int e[TOK];
+#pragma unroll
+      for (int u = 0; u < TOK; ++u) m[u] = j == 0 ? top[u] : most(u);
+      // the lowest expert of those with the largest rank: of the first register
+      // that holds it the first lane
+#pragma unroll
+      for (int u = 0; u < TOK; ++u) {
+        e[u] = -1;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) {
+          const uint64_t with = __ballot(rank[u][i] == m[u]);
+          e[u] = with ? i * 64 + __builtin_ctzll(with) : e[u];
+        }
+        if (m[u] == 0) e[u] = -1;   // none is left
+#pragma unroll
+        for (int i = 0; i < PER; ++i) rank[u][i] = i * 64 + lane == e[u] ? 0 : rank[u][i];
+        if (lane == j) chosen[u] = m[u], expert[u] = e[u];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < TOK; ++u) {
+      const int64_t at = t + u * WAVES;
+      const float w = chosen[u] ? term(u, chosen[u]) : 0.0f;
+      if (renormalize) total[u] = wave_sum(lane < top_k ? w : 0.0f);
+      if (lane < top_k && at < t1) {
+        ids[at * top_k + lane] = expert[u];
+        const int in_block = int(at - t0) * top_k + lane;
+        if (in_block < kHeld) sm.held[in_block] = expert[u];
+        weights[at * top_k + lane] = chosen[u] ? w / total[u] : 0.0f;
+      }
     }
   }
-  __syncthreads();   // the block's ids, read back below
+  __syncthreads();   // the block's choices, read back below
   finish_block(sm, ids, int(t0 * top_k), int(t1 * top_k), experts, order, where, offsets, counts);
 }
 
-// Rows of a block: whole tokens, blocks of about THREADS rows, at most
-// kMostBlocks of them.
+// Rows of a block, whole tokens: one block up to kHeld rows, else blocks of
+// about half as many (a CU each for a long prompt), at most kMostBlocks.
 int64_t block_rows(int64_t rows, int64_t top_k) {
   const int64_t tokens = rows / top_k;
-  const int64_t least = THREADS / top_k;
+  const int64_t least = (rows <= kHeld ? kHeld : kHeld / 2) / top_k;
   const int64_t spread = (tokens + kMostBlocks - 1) / kMostBlocks;
   return (spread > least ? spread : least) * top_k;
 }
@@ -360,7 +416,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ r
 size_t group_rows_ws_bytes(int64_t rows, int64_t top_k, int64_t groups) {
   const int64_t per = block_rows(rows, top_k);
   const int64_t blocks = (rows + per - 1) / per;
-  return blocks > 1 ? size_t(blocks) * size_t(groups + 1) * sizeof(int32_t) : 0;
+  return blocks > 1 ? size_t(blocks) * size_t(count_stride(int(groups))) * sizeof(int32_t) : 0;
 }
 
 hipError_t launch_group_rows(const int32_t* ids, int64_t rows, int groups, int32_t* order,
