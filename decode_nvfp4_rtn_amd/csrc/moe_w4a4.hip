@@ -44,7 +44,7 @@ struct Args4 {
   const uint8_t* experts;
   int64_t blob_stride, wc_off, ws_off;
   void* y;
-  int top_k, gather, n, k;
+  int top_k, gather, n, k, cus;
 };
 
 // Columns [n0, n0 + cols) of a tile's rows, zeroed: pairs without an expert.
@@ -57,10 +57,12 @@ __device__ __forceinline__ void zero_rows(void* y, const RowTile& tile, int n0, 
                              (int64_t(tile.first + i / per) * n_out + n0) * size)[i % per] = make_uint4(0, 0, 0, 0);
 }
 
-// One tile.  WN wavefronts along the weight rows, 8 / WN along the places.
-template <int WN, int RING, bool kSilu, bool kBF16Out>
+// One tile.  WN wavefronts along the weight rows, TN x 16 of them each, and 8 /
+// WN along the places, 64 each.
+template <int WN, int TN, int RING, bool kSilu, bool kBF16Out>
 __device__ __forceinline__ void w4a4_tile(const Args4& A, const RowTile& tile, int n0, uint8_t* smem) {
-  constexpr int TN = 16 / WN, TM = 4;   // 16 x 16 MFMA tiles of a wave
+  constexpr int TM = 4;                 // m-tiles of a wave
+  constexpr int WROWS = WN * TN * 16;   // weight rows of the block
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = A.n, K = A.k, H = N / 2;
@@ -104,7 +106,7 @@ __device__ __forceinline__ void w4a4_tile(const Args4& A, const RowTile& tile, i
   }
   const int wn = wave & (WN - 1), wm = wave / WN;
   const bool multiplies = wm * 64 < tile.count;
-  const bool dequantizes = isw || (wave & 3) * 64 < tile.count;
+  const bool dequantizes = (wave & 3) * 64 < (isw ? WROWS : tile.count);
 
   // codes and scales of 128 of k of this thread's row
   struct Regs {
@@ -176,8 +178,9 @@ __device__ __forceinline__ void w4a4_tile(const Args4& A, const RowTile& tile, i
 #pragma unroll
         for (int j = 0; j < TM; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf, xf[j], acc[i][j], 0, 0, 0);
-        const int it = s * TN + i;
-        if (it % (TN / 4) == 0) dq_store(nxt, buf ^ 1, it / (TN / 4));
+        constexpr int ITS = 2 * TN;   // eight stores over them
+#pragma unroll
+        for (int d = (s * TN + i) * 8 / ITS; d < (s * TN + i + 1) * 8 / ITS; ++d) dq_store(nxt, buf ^ 1, d);
         wf = wn_f;
       }
     }
@@ -204,6 +207,7 @@ __device__ __forceinline__ void w4a4_tile(const Args4& A, const RowTile& tile, i
   if (!multiplies) return;   // no barrier follows
 
   const float stv = A.a_ts[0] * reinterpret_cast<const BlobHeader*>(blob)->tensor_scale;
+  static_assert(!kSilu || TN % 2 == 0, "a wave has whole pairs of gate and up");
   constexpr int TO = kSilu ? TN / 2 : TN;   // 16-column tiles of the wave's output
   if constexpr (kSilu) {
 #pragma unroll
@@ -263,6 +267,9 @@ __device__ __forceinline__ void w4a4_tile(const Args4& A, const RowTile& tile, i
   }
 }
 
+// A block to a CU at a time: what comes after the last whole round of tiles would
+// take a round of its own with most CUs idle, so those tiles are cut into 2 or 4
+// parts along the weight rows, as far as the CUs go.
 template <bool kSilu, bool kBF16Out>
 __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // [2][W tile, X tile]
@@ -272,16 +279,33 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
   // weight tiles in order within a row tile: consecutive blocks go to
   // different XCDs, so each gets its share of every expert
   const int tiles_n = (n_out + OUT_WIDE - 1) / OUT_WIDE;
-  const RowTile tile = find_tile(A.plan, TALL, blockIdx.x / tiles_n);
-  const int n0 = (blockIdx.x % tiles_n) * OUT_WIDE;   // first output column
+  const int total = count_tiles(A.plan, TALL) * tiles_n;
+  const int whole = total / A.cus * A.cus, rest = total - whole;
+  const int cut = 4 * rest <= A.cus ? 4 : 2 * rest <= A.cus ? 2 : 1;
+  int t = blockIdx.x, part = 0, parts = 1;
+  if (t >= whole) {
+    part = (t - whole) % cut;
+    t = whole + (t - whole) / cut;
+    parts = cut;
+  }
+  const RowTile tile = find_tile(A.plan, TALL, t / tiles_n);
   if (tile.group < 0) return;
-
-  if (tile.group == A.plan.groups) {   // rows without an expert: zeros
-    zero_rows<kBF16Out>(A.y, tile, n0, min(OUT_WIDE, n_out - n0), n_out);
+  const int wide = OUT_WIDE / parts, n0 = t % tiles_n * OUT_WIDE + part * wide;   // output columns
+  if (n0 >= n_out) return;
+  if (tile.group == A.plan.groups) {   // rows without an expert
+    zero_rows<kBF16Out>(A.y, tile, n0, min(wide, n_out - n0), n_out);
     return;
   }
-  if (tile.count > 128) w4a4_tile<2, 2, kSilu, kBF16Out>(A, tile, n0, smem);
-  else w4a4_tile<4, 4, kSilu, kBF16Out>(A, tile, n0, smem);
+  const bool low = tile.count <= 128;
+  if (parts == 1) {
+    if (low) w4a4_tile<4, 4, 4, kSilu, kBF16Out>(A, tile, n0, smem);
+    else w4a4_tile<2, 8, 2, kSilu, kBF16Out>(A, tile, n0, smem);
+  } else if (parts == 2) {
+    if (low) w4a4_tile<4, 2, 4, kSilu, kBF16Out>(A, tile, n0, smem);
+    else w4a4_tile<2, 4, 4, kSilu, kBF16Out>(A, tile, n0, smem);
+  } else {
+    w4a4_tile<2, 2, 4, kSilu, kBF16Out>(A, tile, n0, smem);
+  }
 }
 
 // Short runs: tiles of 16 TM places, one m-tile of 16 for each of TM products of
@@ -507,10 +531,14 @@ hipError_t launch_moe_gemm_w4a4(const MoeGemm& g, const uint8_t* codes, const ui
   a.k = g.k;
   const int64_t wide = (g.n + WIDE - 1) / WIDE;
   static std::atomic<int> done[8][64];
+  const int cus = device_cu_count();
+  a.cus = cus > 0 ? cus : 256;
   auto run = [&](auto kern, std::atomic<int>* flag, int tall, size_t lds) {
     const hipError_t e = lds_limit_once(flag, reinterpret_cast<const void*>(kern), int(lds));
     if (e != hipSuccess) return e;
-    kern<<<unsigned(most_tiles(g.plan.rows, g.plan.groups, tall) * wide), 512, lds, s>>>(a);
+    // with room for a last round of parts of tiles
+    const int64_t blocks = most_tiles(g.plan.rows, g.plan.groups, tall) * wide + (tall == TALL ? a.cus : 0);
+    kern<<<unsigned(blocks), 512, lds, s>>>(a);
     return hipGetLastError();
   };
   const bool bf16 = g.y_dtype == 1;

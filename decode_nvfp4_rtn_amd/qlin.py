@@ -734,16 +734,15 @@ class RowPlan:
 
     @property
     def order(self):
-        return self._data[:self.tokens * self.top_k]
+        return self._data.as_strided((self.tokens * self.top_k,), (1,), 0)
 
     @property
     def where(self):
-        rows = self.tokens * self.top_k
-        return self._data[rows:2 * rows].view(self.tokens, self.top_k)
+        return self._data.as_strided((self.tokens, self.top_k), (self.top_k, 1), self.tokens * self.top_k)
 
     @property
     def offsets(self):
-        return self._data[2 * self.tokens * self.top_k:]
+        return self._data.as_strided((self.groups + 1,), (1,), 2 * self.tokens * self.top_k)
 
 
 def _call(name, dev, *args):
