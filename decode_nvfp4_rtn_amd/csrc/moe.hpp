@@ -50,55 +50,97 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return uint32_t(last_lane(int(v)));
 }
 
-// A run of at most `tall` places of one group, found from a number: the tiles
-// of group 0, of group 1, ..., then those of the rows without a group (group
-// == groups).  The search is a wave's: each lane takes a group of 64, a prefix
-// sum over the lanes gives the tiles before it.  Offsets are held to 0 ..
-// rows, so that no plan makes a kernel leave its buffers.
+// A run of at most `tall` places of one group.
 struct RowTile {
-  int group;   // -1: no such tile
+  int group;   // -1: no such tile; `groups`: rows without a group
   int first;   // its first place
   int count;   // 1 .. tall
 };
 
-__device__ __forceinline__ RowTile find_tile(const RowPlan& p, int tall, int number) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int g0 = 0; g0 <= p.groups; g0 += 64) {
-    const int g = g0 + lane;
-    const uint32_t most = uint32_t(p.rows);
-    int a = 0, b = 0;
-    if (g < p.groups) {
-      a = int(min(uint32_t(p.offsets[g]), most));
-      b = int(min(uint32_t(p.offsets[g + 1]), most));
-    } else if (g == p.groups) {
-      a = int(min(uint32_t(p.offsets[g]), most));
-      b = p.rows;
-    }
-    const int tiles = b > a ? (b - a + tall - 1) / tall : 0;
-    const int sum = wave_prefix(tiles);
-    const uint64_t past = __ballot(before + sum > number);
-    if (past) {
-      const int at = __builtin_ctzll(past);
-      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, at); };
-      const int first = of(a) + (number - before - of(sum) + of(tiles)) * tall;
-      return RowTile{g0 + at, first, min(of(b) - first, tall)};
-    }
-    before += last_lane(sum);
+// The places of a group (group == groups: those of no group).  Offsets are held
+// to 0 .. rows, so that no plan makes a kernel leave its buffers.
+struct GroupRun {
+  int first, end;
+};
+__device__ __forceinline__ GroupRun run_of(const RowPlan& p, int g) {
+  if (g > p.groups) return GroupRun{0, 0};
+  const uint32_t most = uint32_t(p.rows);
+  const int a = int(min(uint32_t(p.offsets[g]), most));
+  const int b = g < p.groups ? int(min(uint32_t(p.offsets[g + 1]), most)) : p.rows;
+  return GroupRun{a, max(a, b)};
+}
+
+// The tile of a number.  All tiles: those of group 0, of group 1, ..., then
+// those of the rows without a group.  Or the full tiles of all groups in that
+// order, or the ends of all groups that are not whole tiles.  The search is a
+// wave's: each lane takes a group of 64, a prefix sum over the lanes gives the
+// tiles before it.
+enum TileKind { kAllTiles, kFullTiles, kEndTiles };
+
+template <TileKind kKind>
+__device__ __forceinline__ int tiles_of(GroupRun run, int tall) {
+  const int rows = run.end - run.first, full = rows / tall;
+  return kKind == kFullTiles ? full : kKind == kEndTiles ? rows != full * tall : (rows + tall - 1) / tall;
+}
+
+// A plan's runs as a wave searches them: those of the first 192 groups are read
+// once, at the same time (a read takes a microsecond where the plan was written
+// by another XCD's blocks).
+struct PlanRuns {
+  static constexpr int kHeld = 3;
+  const RowPlan& p;
+  GroupRun held[kHeld];
+
+  __device__ __forceinline__ explicit PlanRuns(const RowPlan& plan) : p(plan) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) held[i] = run_of(p, i * 64 + (threadIdx.x & 63));
   }
-  return RowTile{-1, 0, 0};
+
+  // f(first group, run of this lane's group) for each 64 groups, until it says true
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * 64 <= p.groups && f(i * 64, held[i])) return;
+    for (int g0 = kHeld * 64; g0 <= p.groups; g0 += 64)
+      if (f(g0, run_of(p, g0 + (threadIdx.x & 63)))) return;
+  }
+};
+
+template <TileKind kKind = kAllTiles>
+__device__ __forceinline__ RowTile find_tile(const PlanRuns& runs, int tall, int number) {
+  int before = 0;
+  RowTile tile{-1, 0, 0};
+  runs.each([&](int g0, GroupRun run) {
+    const int tiles = tiles_of<kKind>(run, tall), sum = wave_prefix(tiles);
+    const uint64_t past = __ballot(before + sum > number);
+    if (!past) {
+      before += last_lane(sum);
+      return false;
+    }
+    const int at = __builtin_ctzll(past);
+    auto of = [&](int v) { return __builtin_amdgcn_readlane(v, at); };
+    const int in_group =
+        kKind == kEndTiles ? (of(run.end) - of(run.first)) / tall : number - before - of(sum) + of(tiles);
+    const int first = of(run.first) + in_group * tall;
+    tile = RowTile{g0 + at, first, min(of(run.end) - first, tall)};
+    return true;
+  });
+  return tile;
+}
+
+__device__ __forceinline__ RowTile find_tile(const RowPlan& p, int tall, int number) {
+  return find_tile(PlanRuns(p), tall, number);
 }
 
 // How many such tiles there are.
-__device__ __forceinline__ int count_tiles(const RowPlan& p, int tall) {
-  const int lane = threadIdx.x & 63;
+template <TileKind kKind>
+__device__ __forceinline__ int count_tiles(const PlanRuns& runs, int tall) {
   int sum = 0;
-  for (int g = lane; g <= p.groups; g += 64) {
-    const uint32_t most = uint32_t(p.rows);
-    const int a = int(min(uint32_t(p.offsets[g]), most));
-    const int b = g < p.groups ? int(min(uint32_t(p.offsets[g + 1]), most)) : p.rows;
-    sum += b > a ? (b - a + tall - 1) / tall : 0;
-  }
+  runs.each([&](int, GroupRun run) {
+    sum += tiles_of<kKind>(run, tall);
+    return false;
+  });
   return last_lane(wave_prefix(sum));
 }
 

@@ -58,8 +58,9 @@ __device__ __forceinline__ void zero_rows(void* y, const RowTile& tile, int n0, 
 }
 
 // One tile.  WN wavefronts along the weight rows, TN x 16 of them each, and 8 /
-// WN along the places, 64 each.
-template <int WN, int TN, int RING, bool kSilu, bool kBF16Out>
+// WN along the places, 64 each.  kAll: every wave has places (a branch around its
+// products costs 4 % of a full tile's time).
+template <int WN, int TN, int RING, bool kAll, bool kSilu, bool kBF16Out>
 __device__ __forceinline__ void w4a4_tile(const Args4& A, const RowTile& tile, int n0, uint8_t* smem) {
   constexpr int TM = 4;                 // m-tiles of a wave
   constexpr int WROWS = WN * TN * 16;   // weight rows of the block
@@ -105,8 +106,8 @@ __device__ __forceinline__ void w4a4_tile(const Args4& A, const RowTile& tile, i
     vs = from * uint32_t(K / 16);
   }
   const int wn = wave & (WN - 1), wm = wave / WN;
-  const bool multiplies = wm * 64 < tile.count;
-  const bool dequantizes = (wave & 3) * 64 < (isw ? WROWS : tile.count);
+  const bool multiplies = kAll || wm * 64 < tile.count;
+  const bool dequantizes = kAll && WROWS == 256 ? true : (wave & 3) * 64 < (isw ? WROWS : tile.count);
 
   // codes and scales of 128 of k of this thread's row
   struct Regs {
@@ -276,10 +277,15 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
   const int n_out = kSilu ? A.n / 2 : A.n;
   constexpr int OUT_WIDE = kSilu ? WIDE / 2 : WIDE;
 
-  // weight tiles in order within a row tile: consecutive blocks go to
-  // different XCDs, so each gets its share of every expert
+  // Full tiles first: XCD-major (consecutive blocks go to different XCDs, so
+  // each gets a contiguous run of tiles), in groups of GROUP_M row tiles with
+  // the weight tiles in order, as the dense kernel's, so that an XCD's blocks
+  // share panels in its L2.  Then the experts' ends, whose costs differ, spread
+  // over the XCDs as they come.
   const int tiles_n = (n_out + OUT_WIDE - 1) / OUT_WIDE;
-  const int total = count_tiles(A.plan, TALL) * tiles_n;
+  const PlanRuns runs(A.plan);
+  const int full_m = count_tiles<kFullTiles>(runs, TALL);
+  const int full = full_m * tiles_n, total = full + count_tiles<kEndTiles>(runs, TALL) * tiles_n;
   const int whole = total / A.cus * A.cus, rest = total - whole;
   const int cut = 4 * rest <= A.cus ? 4 : 2 * rest <= A.cus ? 2 : 1;
   int t = blockIdx.x, part = 0, parts = 1;
@@ -288,9 +294,21 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
     t = whole + (t - whole) / cut;
     parts = cut;
   }
-  const RowTile tile = find_tile(A.plan, TALL, t / tiles_n);
+  if (t >= total) return;
+  RowTile tile;
+  int at_n;
+  if (t < full) {
+    const int even = min(full, whole) & ~7;
+    if (t < even) t = (t & 7) * (even >> 3) + (t >> 3);
+    const int in_group = GROUP_M * tiles_n, first_m = t / in_group * GROUP_M, tall = min(full_m - first_m, GROUP_M);
+    tile = find_tile<kFullTiles>(runs, TALL, first_m + t % in_group % tall);
+    at_n = t % in_group / tall;
+  } else {
+    tile = find_tile<kEndTiles>(runs, TALL, (t - full) / tiles_n);
+    at_n = (t - full) % tiles_n;
+  }
   if (tile.group < 0) return;
-  const int wide = OUT_WIDE / parts, n0 = t % tiles_n * OUT_WIDE + part * wide;   // output columns
+  const int wide = OUT_WIDE / parts, n0 = at_n * OUT_WIDE + part * wide;   // output columns
   if (n0 >= n_out) return;
   if (tile.group == A.plan.groups) {   // rows without an expert
     zero_rows<kBF16Out>(A.y, tile, n0, min(wide, n_out - n0), n_out);
@@ -298,13 +316,14 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
   }
   const bool low = tile.count <= 128;
   if (parts == 1) {
-    if (low) w4a4_tile<4, 4, 4, kSilu, kBF16Out>(A, tile, n0, smem);
-    else w4a4_tile<2, 8, 2, kSilu, kBF16Out>(A, tile, n0, smem);
+    if (tile.count > 192) w4a4_tile<2, 8, 2, true, kSilu, kBF16Out>(A, tile, n0, smem);
+    else if (low) w4a4_tile<4, 4, 4, false, kSilu, kBF16Out>(A, tile, n0, smem);
+    else w4a4_tile<2, 8, 2, false, kSilu, kBF16Out>(A, tile, n0, smem);
   } else if (parts == 2) {
-    if (low) w4a4_tile<4, 2, 4, kSilu, kBF16Out>(A, tile, n0, smem);
-    else w4a4_tile<2, 4, 4, kSilu, kBF16Out>(A, tile, n0, smem);
+    if (low) w4a4_tile<4, 2, 4, false, kSilu, kBF16Out>(A, tile, n0, smem);
+    else w4a4_tile<2, 4, 4, false, kSilu, kBF16Out>(A, tile, n0, smem);
   } else {
-    w4a4_tile<2, 2, 4, kSilu, kBF16Out>(A, tile, n0, smem);
+    w4a4_tile<2, 2, 4, false, kSilu, kBF16Out>(A, tile, n0, smem);
   }
 }
 
