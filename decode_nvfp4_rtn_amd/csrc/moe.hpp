@@ -70,19 +70,6 @@ __device__ __forceinline__ GroupRun run_of(const RowPlan& p, int g) {
   return GroupRun{a, max(a, b)};
 }
 
-// The tile of a number.  All tiles: those of group 0, of group 1, ..., then
-// those of the rows without a group.  Or the full tiles of all groups in that
-// order, or the ends of all groups that are not whole tiles.  The search is a
-// wave's: each lane takes a group of 64, a prefix sum over the lanes gives the
-// tiles before it.
-enum TileKind { kAllTiles, kFullTiles, kEndTiles };
-
-template <TileKind kKind>
-__device__ __forceinline__ int tiles_of(GroupRun run, int tall) {
-  const int rows = run.end - run.first, full = rows / tall;
-  return kKind == kFullTiles ? full : kKind == kEndTiles ? rows != full * tall : (rows + tall - 1) / tall;
-}
-
 // A plan's runs as a wave searches them: those of the first 192 groups are read
 // once, at the same time (a read takes a microsecond where the plan was written
 // by another XCD's blocks).
@@ -107,38 +94,47 @@ struct PlanRuns {
   }
 };
 
-template <TileKind kKind = kAllTiles>
-__device__ __forceinline__ RowTile find_tile(const PlanRuns& runs, int tall, int number) {
-  int before = 0;
-  RowTile tile{-1, 0, 0};
+// The tile of a number among those that tiles(group, run) counts for each group,
+// in the order of the groups; a group's are its first ones, or its last one
+// (kLast).  The search is a wave's: each lane takes a group of 64, a prefix sum
+// over the lanes gives the tiles before it.  Not found: the number less what
+// there is.
+template <bool kLast, typename F>
+__device__ __forceinline__ bool search_tiles(const PlanRuns& runs, int tall, int& number, RowTile& tile, F tiles) {
+  bool found = false;
   runs.each([&](int g0, GroupRun run) {
-    const int tiles = tiles_of<kKind>(run, tall), sum = wave_prefix(tiles);
-    const uint64_t past = __ballot(before + sum > number);
+    const int here = tiles(g0 + int(threadIdx.x & 63), run), sum = wave_prefix(here);
+    const uint64_t past = __ballot(sum > number);
     if (!past) {
-      before += last_lane(sum);
+      number -= last_lane(sum);
       return false;
     }
     const int at = __builtin_ctzll(past);
     auto of = [&](int v) { return __builtin_amdgcn_readlane(v, at); };
-    const int in_group =
-        kKind == kEndTiles ? (of(run.end) - of(run.first)) / tall : number - before - of(sum) + of(tiles);
+    const int in_group = kLast ? (of(run.end) - of(run.first) - 1) / tall : number - of(sum) + of(here);
     const int first = of(run.first) + in_group * tall;
     tile = RowTile{g0 + at, first, min(of(run.end) - first, tall)};
+    found = true;
     return true;
   });
+  return found;
+}
+
+// All tiles: those of group 0, of group 1, ..., then those of the rows without a
+// group.
+__device__ __forceinline__ RowTile find_tile(const RowPlan& p, int tall, int number) {
+  RowTile tile{-1, 0, 0};
+  search_tiles<false>(PlanRuns(p), tall, number, tile,
+                      [&](int, GroupRun run) { return (run.end - run.first + tall - 1) / tall; });
   return tile;
 }
 
-__device__ __forceinline__ RowTile find_tile(const RowPlan& p, int tall, int number) {
-  return find_tile(PlanRuns(p), tall, number);
-}
-
-// How many such tiles there are.
-template <TileKind kKind>
-__device__ __forceinline__ int count_tiles(const PlanRuns& runs, int tall) {
+// How many tiles that counts.
+template <typename F>
+__device__ __forceinline__ int count_tiles(const PlanRuns& runs, F tiles) {
   int sum = 0;
-  runs.each([&](int, GroupRun run) {
-    sum += tiles_of<kKind>(run, tall);
+  runs.each([&](int g0, GroupRun run) {
+    sum += tiles(g0 + int(threadIdx.x & 63), run);
     return false;
   });
   return last_lane(wave_prefix(sum));

@@ -284,8 +284,10 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
   // over the XCDs as they come.
   const int tiles_n = (n_out + OUT_WIDE - 1) / OUT_WIDE;
   const PlanRuns runs(A.plan);
-  const int full_m = count_tiles<kFullTiles>(runs, TALL);
-  const int full = full_m * tiles_n, total = full + count_tiles<kEndTiles>(runs, TALL) * tiles_n;
+  auto fulls = [](int, GroupRun run) { return (run.end - run.first) / TALL; };
+  auto ends = [](int, GroupRun run) { return (run.end - run.first) % TALL ? 1 : 0; };
+  const int full_m = count_tiles(runs, fulls);
+  const int full = full_m * tiles_n, total = full + count_tiles(runs, ends) * tiles_n;
   const int whole = total / A.cus * A.cus, rest = total - whole;
   const int cut = 4 * rest <= A.cus ? 4 : 2 * rest <= A.cus ? 2 : 1;
   int t = blockIdx.x, part = 0, parts = 1;
@@ -295,17 +297,19 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
     parts = cut;
   }
   if (t >= total) return;
-  RowTile tile;
-  int at_n;
+  RowTile tile{-1, 0, 0};
+  int at_n, at_m;
   if (t < full) {
     const int even = min(full, whole) & ~7;
     if (t < even) t = (t & 7) * (even >> 3) + (t >> 3);
     const int in_group = GROUP_M * tiles_n, first_m = t / in_group * GROUP_M, tall = min(full_m - first_m, GROUP_M);
-    tile = find_tile<kFullTiles>(runs, TALL, first_m + t % in_group % tall);
+    at_m = first_m + t % in_group % tall;
     at_n = t % in_group / tall;
+    search_tiles<false>(runs, TALL, at_m, tile, fulls);
   } else {
-    tile = find_tile<kEndTiles>(runs, TALL, (t - full) / tiles_n);
+    at_m = (t - full) / tiles_n;
     at_n = (t - full) % tiles_n;
+    search_tiles<true>(runs, TALL, at_m, tile, ends);
   }
   if (tile.group < 0) return;
   const int wide = OUT_WIDE / parts, n0 = at_n * OUT_WIDE + part * wide;   // output columns
@@ -348,7 +352,6 @@ constexpr int low_bytes(int tm) { return 2 * PIECE * tm * 4 * FRAG; }
 template <int TM, bool kSilu, bool kBF16Out>
 __device__ __forceinline__ void w4a4_low_tile(const Args4& A, const RowTile& tile, int n0, uint8_t* smem) {
   constexpr int RING = 4, LOW = 16 * TM;
-  static_assert(PIECE * TM % 8 == 0 || 8 % (PIECE * TM) == 0, "units of a piece over 8 waves");
   // smem: [2][PIECE][TM][4][64 lanes] x 16 bytes
   constexpr int BUF = PIECE * TM * 4 * FRAG;
   const int lane = threadIdx.x & 63;
@@ -383,7 +386,7 @@ __device__ __forceinline__ void w4a4_low_tile(const Args4& A, const RowTile& til
   };
   // Activations: the units (pair, m-tile) of a piece go round the waves; a
   // unit is 16 bytes of codes of each of 16 places and 4 quarters.
-  constexpr int UNITS = PIECE * TM > 8 ? PIECE * TM / 8 : 1;
+  constexpr int UNITS = (PIECE * TM + 7) / 8;
   const uint8_t *xc[UNITS], *xs[UNITS];
   bool active[UNITS];
 #pragma unroll
@@ -516,13 +519,31 @@ __global__ __launch_bounds__(512, 4) void moe_w4a4_low_kernel(Args4 A) {
   const int n_out = kSilu ? A.n / 2 : A.n;
   constexpr int OUT_WIDE = kSilu ? 128 : 256;
   const int tiles_n = (n_out + OUT_WIDE - 1) / OUT_WIDE;
-  const RowTile tile = find_tile(A.plan, 64, blockIdx.x / tiles_n);
   const int n0 = (blockIdx.x % tiles_n) * OUT_WIDE;
-  if (tile.group < 0) return;
+  // tiles by their height, the highest first, so that the last blocks of the
+  // launch are short ones; then the rows without an expert
+  RowTile tile{-1, 0, 0};
+  int number = blockIdx.x / tiles_n;
+  const PlanRuns runs(A.plan);
+  const int groups = A.plan.groups;
+  bool found = search_tiles<false>(runs, 64, number, tile, [&](int g, GroupRun run) {
+    return g < groups ? (run.end - run.first) / 64 : 0;
+  });
+  for (int low = 48; low >= 0 && !found; low -= 16)
+    found = search_tiles<true>(runs, 64, number, tile, [&](int g, GroupRun run) {
+      const int rows = (run.end - run.first) % 64;
+      return g < groups && rows > low && rows <= low + 16 ? 1 : 0;
+    });
+  if (!found && !search_tiles<false>(runs, 64, number, tile, [&](int g, GroupRun run) {
+        return g == groups ? (run.end - run.first + 63) / 64 : 0;
+      }))
+    return;
   if (tile.group == A.plan.groups)
     zero_rows<kBF16Out>(A.y, tile, n0, min(OUT_WIDE, n_out - n0), n_out);
-  else if (tile.count > 32)
+  else if (tile.count > 48)
     w4a4_low_tile<4, kSilu, kBF16Out>(A, tile, n0, smem);
+  else if (tile.count > 32)
+    w4a4_low_tile<3, kSilu, kBF16Out>(A, tile, n0, smem);
   else if (tile.count > 16)
     w4a4_low_tile<2, kSilu, kBF16Out>(A, tile, n0, smem);
   else

@@ -873,6 +873,8 @@ def _operand(t, name, dtype, rows, cols, dev):
 def _product(plan, n, k, gather, silu_mul, y, out_dtype, stream):
     """(n, k, rows of x, flags, y, its type) of an experts' product."""
     n, k = _whole(n, "n"), _whole(k, "k")
+    if n < 1 or k < 1:
+        raise ValueError(f"an expert's weights are [n, k] of 1 or more, got [{n}, {k}]")
     pairs = plan.tokens * plan.top_k
     shape = (pairs, n // 2 if silu_mul else n)
     y = _new(shape, out_dtype, plan.device, stream) if y is None else _rows_out(y, "y", shape, _XDT, plan.device)
@@ -965,6 +967,9 @@ def lora_add(y, x, a, b, plan, scale=None, out=None, workspace=None, stream=None
     rank, k], b bf16 [adapters, n, rank], rank a multiple of 8 up to 128; scale
     fp32 [adapters] (None: 1).  out: like y, y itself when not given."""
     dev = plan.device
+    if torch._C._cuda_getDevice() != dev.index:   # the workspace goes by the device too
+        with torch.cuda.device(dev):
+            return lora_add(y, x, a, b, plan, scale, out, workspace, stream)
     if plan.top_k != 1:
         raise ValueError(f"a row has one adapter; the plan has {plan.top_k} choices to a row")
     rows, adapters = plan.tokens, plan.groups

@@ -53,7 +53,16 @@ CASES = [(1, 1, 1, 32, 128, True, False, F32, {}),
          (300, 1000, 3, 32, 128, True, False, BF, {}),
          (130, 2, 1, 64, 1408, True, True, BF, dict(spare=48)),     # blobs with room between them
          (3, 2, 1, 32, 8192, True, False, F32, {}),                 # x in pieces
-         (100, 2, 2, 64, 4224, True, True, BF, {})]
+         (100, 2, 2, 64, 4224, True, True, BF, {}),
+         (12, 2, 1, 32, 8192, False, False, BF, {}),
+         (3, 2, 1, 32, 20480, True, False, BF, {}),
+         (1, 8, 2, 64, 1024, True, True, BF, {}),                   # k shared by 2, 4, 8 waves
+         (1, 8, 3, 64, 2048, True, False, F32, {}),
+         (4, 9, 3, 96, 4096, True, True, BF, {}),
+         (2, 5, 2, 48, 4096, True, False, BF, {}),
+         (1200, 3, 1, 4096, 128, True, False, BF, {}),              # tiles in halves, and whole
+         (1200, 3, 1, 4096, 128, True, True, F32, {}),
+         (1300, 3, 1, 8192, 128, False, False, BF, dict(idle=0.2))]
 
 
 @pytest.mark.parametrize("fmt", ["int4", "nvfp4"])
@@ -63,10 +72,27 @@ def test_product(fmt, case):
 
 
 @pytest.mark.parametrize("fmt", ["int4", "nvfp4"])
-@pytest.mark.parametrize("rows_each", [1, 4, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 129, 191, 193, 255, 256, 257])
+@pytest.mark.parametrize("rows_each", [1, 4, 15, 16, 17, 31, 32, 33, 48, 49, 63, 64, 65, 127, 129, 191, 192, 193, 255,
+                                       256, 257])
 def test_run_lengths(fmt, rows_each):
     """Two experts' runs of each length around the tiles' borders."""
     run(fmt, rows_each, 3, 2, 64, 256, True, rows_each % 2 == 0, BF, only=[0, 2])
+
+
+@pytest.mark.parametrize("fmt", ["int4", "nvfp4"])
+@pytest.mark.parametrize("tokens", [3, 50])
+def test_an_expert_chosen_twice(fmt, tokens):
+    """All choices of every token are one expert: its run holds every row top_k times."""
+    q = require_gpu()
+    ids = np.full((tokens, 8), 2, dtype=np.int32)
+    order, where, offsets = rows.plan(ids, 4)
+    stack = Stack(q, fmt, 5, 4, 64, 1024)
+    x, values = operand(q, fmt, bf16_rows(tokens, tokens, 1024)[0])
+    say("chosen twice", fmt, tokens)
+    plan = q.group_rows(torch.from_numpy(ids).cuda(), 4)
+    y = product(q, fmt, *x, stack.blobs, plan, 64, 1024)
+    ref = rows.experts_product(values, stack.values, order, offsets, 8, True)
+    check(y, ref, product_bound(ref, BF))
 
 
 @pytest.mark.parametrize("fmt", ["int4", "nvfp4"])
