@@ -6,12 +6,12 @@
 // with A_i [rank, k] and B_i [n, rank] in bf16.  Both products run over the
 // runs of a plan, so that a tile of rows meets one adapter.
 //
-// Adapters of few rows (a decode batch): one launch.  A block takes a tile of
+// Adapters of few rows and a low rank (a decode batch): one launch.  A block takes a tile of
 // 16 places and a part of the columns; its waves share k, add their sums of
 // u = A x in LDS in a fixed order, and make out = y + scale B u, each its own
 // columns.  A and x are read once for each part of the columns.
 //
-// Adapters of many rows (prompts): two launches.  "down" makes u: a block takes
+// Other adapters (prompts): two launches.  "down" makes u: a block takes
 // 64 places and a part of k, each wave 16 places and all of the rank; A passes
 // through LDS, x goes from memory to registers.  u is stored in binary32, one
 // buffer for each part of k.  "up" adds the parts in their order and makes out
@@ -198,23 +198,15 @@ __global__ __launch_bounds__(512) void lora_few_kernel(LoraArgs A, int col_parts
     }
     __asm__ volatile("" ::: "memory");
   };
-  Piece P;
+  Piece P, Q;
   load(P, wave);
-  if constexpr (RT <= 4) {
-    Piece Q;
-    for (int g = wave; g < G; g += 2 * WAVES) {
-      load(Q, g + WAVES);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(P);
-      load(P, g + 2 * WAVES);
-      __builtin_amdgcn_sched_barrier(0);
-      if (g + WAVES < G) compute(Q);
-    }
-  } else {   // two pieces would not fit in the registers
-    for (int g = wave; g < G; g += WAVES) {
-      compute(P);
-      load(P, g + WAVES);
-    }
+  for (int g = wave; g < G; g += 2 * WAVES) {
+    load(Q, g + WAVES);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(P);
+    load(P, g + 2 * WAVES);
+    __builtin_amdgcn_sched_barrier(0);
+    if (g + WAVES < G) compute(Q);
   }
   // the first step's y and B are under way while u is added up
   const uint16_t* b = static_cast<const uint16_t*>(A.b) + int64_t(tile.group) * A.n * A.rank;
@@ -489,12 +481,15 @@ int cus_or(int otherwise) {
   return cus > 0 ? cus : otherwise;
 }
 
-// Adapters of few rows: less than 48 on average.
-bool few_rows(int64_t rows, int64_t groups) { return rows < 48 * groups; }
+// Adapters of few rows, less than 48 on average: one launch, which makes u again
+// for each part of the columns.  It pays up to a rank of 32 (64 tokens over 32
+// adapters of rank 16 beside 6144 x 4096: 9 us, in two launches 13; 18 tokens
+// over 60 of rank 64: 20 and 15).
+bool few_rows(int64_t rows, int64_t groups, int rank) { return rank <= 32 && rows < 48 * groups; }
 
 // Parts of k of the first product: a block to a CU, at least 512 of k each.
-int parts_of(int64_t rows, int64_t groups, int64_t k) {
-  if (few_rows(rows, groups)) return 0;
+int parts_of(int64_t rows, int64_t groups, int rank, int64_t k) {
+  if (few_rows(rows, groups, rank)) return 0;
   const int64_t tiles = most_tiles(rows, groups, TALL);
   int64_t parts = (cus_or(256) + tiles - 1) / tiles;
   if (parts > k / 512) parts = k / 512;
@@ -512,7 +507,7 @@ int col_parts_of(int64_t tiles, int64_t n, int each, int waves, int wide) {
 template <int RT>
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
   const bool bf16 = a.y_dtype == 1;
-  if (few_rows(a.plan.rows, a.plan.groups)) {
+  if constexpr (RT <= 2) if (few_rows(a.plan.rows, a.plan.groups, a.rank)) {
     const int64_t tiles = most_tiles(a.plan.rows, a.plan.groups, 16);
     const int cols = col_parts_of(tiles, a.n, 1, 8, 32);
     if (bf16) lora_few_kernel<RT, true><<<unsigned(tiles * cols), 512, 0, s>>>(a, cols);
@@ -520,7 +515,7 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   const int64_t tiles = most_tiles(a.plan.rows, a.plan.groups, TALL);
-  const int parts = parts_of(a.plan.rows, a.plan.groups, a.k);
+  const int parts = parts_of(a.plan.rows, a.plan.groups, a.rank, a.k);
   lora_down_kernel<RT><<<unsigned(tiles * parts), 256, 2 * RT * 4096, s>>>(a, parts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -534,7 +529,7 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t lora_ws_bytes(int64_t rows, int64_t groups, int rank, int64_t k) {
-  return size_t(parts_of(rows, groups, k)) * size_t(rows) * size_t(rank) * sizeof(float);
+  return size_t(parts_of(rows, groups, rank, k)) * size_t(rows) * size_t(rank) * sizeof(float);
 }
 
 hipError_t launch_lora_add(const LoraArgs& a, hipStream_t s) {

@@ -312,7 +312,10 @@ hipError_t launch16(Args16 a, const MoeGemm& g, hipStream_t s) {
   const int64_t widest = (units + WAVES / KS - 1) / (WAVES / KS);
   const int cus = device_cu_count();
   int64_t walkers = widest;
-  if (KS == 1) {   // 16 waves to a CU, as far as there are units for them
+  // 16 waves to a CU, as far as there are units for them.  Where x passes through
+  // LDS in pieces it does so for every unit of a wave, and one unit to a wave is
+  // best (660 rows over 16 experts of 3840 x 3840: 73 -> 48 us).
+  if (KS == 1 && a.chunk >= G) {
     walkers = (16 / WAVES * (cus > 0 ? cus : 256) + tiles - 1) / tiles;
     if (walkers > widest) walkers = widest;
   }

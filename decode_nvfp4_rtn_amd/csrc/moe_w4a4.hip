@@ -582,7 +582,11 @@ hipError_t launch_moe_gemm_w4a4(const MoeGemm& g, const uint8_t* codes, const ui
     return hipGetLastError();
   };
   const bool bf16 = g.y_dtype == 1;
-  if (g.plan.rows <= 96 * int64_t(g.plan.groups)) {
+  // Tiles of 64 places up to 256 rows of an expert on average: 1362 rows over 8
+  // experts (gate and up of 4096 x 4096) 62 us, in tiles of 256 103; 2610 over 16
+  // (3840 x 1920) 53 and 77; 28000 over 128 (1536 x 2048) 244 and 252; but 9800
+  // over 32 (5120 x 1280) 185 and 179.
+  if (g.plan.rows <= 256 * int64_t(g.plan.groups)) {
     constexpr size_t lds = low_bytes(4);
     if (g.silu_mul)
       return bf16 ? run(moe_w4a4_low_kernel<true, true>, done[4], 64, lds)
