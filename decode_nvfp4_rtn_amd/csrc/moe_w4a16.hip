@@ -318,6 +318,11 @@ hipError_t launch16(Args16 a, const MoeGemm& g, hipStream_t s) {
   if (KS == 1 && a.chunk >= G) {
     walkers = (16 / WAVES * (cus > 0 ? cus : 256) + tiles - 1) / tiles;
     if (walkers > widest) walkers = widest;
+    // Then as few blocks as do these units in the nearest whole number of rounds
+    // (692 rows over 16 experts of 3840 x 1920: 36 -> 28 us; the others as before).
+    const int64_t in_round = WAVES * walkers;
+    const int64_t near = (2 * units + in_round) / (2 * in_round), rounds = near > 0 ? near : 1;
+    walkers = (units + WAVES * rounds - 1) / (WAVES * rounds);
   }
   a.walkers = int(walkers);
   const size_t lds = size_t(a.chunk) * group_bytes(MT, XR) + red_bytes(MT, KS);
