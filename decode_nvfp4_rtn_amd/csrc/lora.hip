@@ -21,6 +21,10 @@
 // bits of mantissa or more), three beside a binary32 one (all of it): that
 // product is bound by reading y and writing out, so they cost nothing that shows.
 //
+// 64 tokens over 32 adapters of rank 16 beside 6144 x 4096: 9.2 us, one block's
+// chain.  8190 tokens over 8 adapters of rank 64 beside 7168 x 5120: 28 us down (84
+// MB of x at 3 TB/s) and 64 up (235 MB of y and out at 3.6 TB/s).
+//
 // Rows without an adapter come last in the plan: they are copied, or left
 // alone where out is y.
 #include "moe.hpp"

@@ -22,6 +22,12 @@
 // Where there are few tiles and places (a single sequence's step) KS waves
 // share a pair of weight tiles, a part of k each, and add up in LDS in a fixed
 // order.
+//
+// 48 tokens that choose 8 of 128 experts of 2048 x 768: 19.7 us, 94.6 MB at 4.8
+// TB/s.  One token and 8 experts of 2048 x 4096: 10.2 us, 34.6 MB; a launch's
+// start and one wave's chain are half of it.  509 tokens, 4 of 60 experts of
+// 2816 x 2048 (34 rows each): 55 us, 186 MB at 3.4 TB/s; experts of more than 32
+// rows have a second tile, whose weights are read once more.
 #include "moe.hpp"
 #include "decode_ops.hpp"
 

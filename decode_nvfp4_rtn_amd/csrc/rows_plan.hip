@@ -9,6 +9,11 @@
 // group comes from ballots over the bits of the group's number.  One block's
 // worth of rows takes one launch.  Whole numbers only, counted by integer
 // atomics in LDS whose order does not show: the plan is the same every time.
+//
+// 16384 tokens, 8 of 256 experts, binary32 scores: the choice with its counts 16.4
+// us (18.9 MB; the chain of choices in a wave bounds it), the places 8.3.  32
+// tokens, 8 of 128: 8.3, one block's chain.  The sum of 8 rows of 4096 for 8192
+// tokens: 118 us, 604 MB at 5.1 TB/s.
 #include "moe.hpp"
 
 #include <cmath>
