@@ -47,6 +47,35 @@ int check_product(int64_t pairs, int64_t top_k, int64_t n_experts, int64_t exper
   return -1;
 }
 
+// Rows of `width` bytes, `stride` bytes apart, that a call reads or writes.
+struct Rows {
+  const void* at;
+  int64_t count, stride, width;
+};
+
+// Whether two sets of rows share bytes.  Rows of one stride may lie side by side
+// (slices of a fused projection); of two strides, where one set lies within the
+// other's, they count as shared.
+bool overlap(const Rows& a, const Rows& b) {
+  const uint64_t at = reinterpret_cast<uintptr_t>(a.at), bt = reinterpret_cast<uintptr_t>(b.at);
+  const uint64_t a_all = uint64_t((a.count - 1) * a.stride + a.width);
+  const uint64_t b_all = uint64_t((b.count - 1) * b.stride + b.width);
+  if (bt >= at ? bt - at >= a_all : at - bt >= b_all) return false;
+  if (a.stride != b.stride) return true;
+  const uint64_t s = uint64_t(a.stride);
+  const uint64_t b_past = bt >= at ? (bt - at) % s : (s - (at - bt) % s) % s;   // b's column in a's rows
+  return b_past < uint64_t(a.width) || b_past + uint64_t(b.width) > s;
+}
+
+Rows whole(const void* at, int64_t rows, int64_t width) { return Rows{at, rows, width, width}; }
+
+int64_t bytes_of(int dtype) { return dtype == QL_F32 ? 4 : 2; }
+
+// The rows that a product writes.
+Rows written(int64_t pairs, int64_t n, unsigned flags, const void* y, int y_dtype) {
+  return whole(y, pairs, (flags & QL_ROWS_SILU_MUL ? n / 2 : n) * bytes_of(y_dtype));
+}
+
 MoeGemm product(const void* experts, int64_t n_experts, int64_t expert_bytes, const int32_t* order,
                 const int32_t* offsets, int64_t pairs, int64_t top_k, int64_t n, int64_t k,
                 unsigned flags, void* y, int y_dtype) {
@@ -119,6 +148,8 @@ int moe_gemm_w4a16(const void* x_bf16, const void* experts, int64_t n_experts, i
   if (!x_bf16 || !experts || !offsets || !y || (!order && (flags & QL_ROWS_GATHER))) return QL_EINVAL;
   if (!aligned16(x_bf16) || !aligned16(experts) || !aligned16(y) || !aligned(order, 4) || !aligned(offsets, 4))
     return QL_EALIGN;
+  const int64_t rows = flags & QL_ROWS_GATHER ? pairs / top_k : pairs;
+  if (overlap(written(pairs, n, flags, y, y_dtype), whole(x_bf16, rows, 2 * k))) return QL_EINVAL;
   return launch_status(launch_moe_gemm_w4a16(
       product(experts, n_experts, expert_bytes, order, offsets, pairs, top_k, n, k, flags, y, y_dtype),
       x_bf16, as_stream(stream)));
@@ -140,6 +171,8 @@ int moe_gemm_w4a4(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(experts) || !aligned16(y) ||
       !aligned(a_tensor_scale, 4) || !aligned(order, 4) || !aligned(offsets, 4))
     return QL_EALIGN;
+  const Rows out = written(pairs, n, flags, y, y_dtype);
+  if (overlap(out, whole(a_codes, rows, k / 2)) || overlap(out, whole(a_scales, rows, k / 16))) return QL_EINVAL;
   return launch_status(launch_moe_gemm_w4a4(
       product(experts, n_experts, expert_bytes, order, offsets, pairs, top_k, n, k, flags, y, y_dtype),
       a_codes, a_scales, a_tensor_scale, as_stream(stream)));
@@ -156,6 +189,8 @@ int moe_combine(const void* rows, int x_dtype, const int32_t* where, const int32
   if (!rows || !where || !offsets || !weights || !out) return QL_EINVAL;
   if (!aligned16(rows) || !aligned16(out) || !aligned(where, 4) || !aligned(offsets, 4) || !aligned(weights, 4))
     return QL_EALIGN;
+  if (overlap(whole(out, tokens, n * bytes_of(out_dtype)), whole(rows, tokens * top_k, n * bytes_of(x_dtype))))
+    return QL_EINVAL;
   const RowPlan p{nullptr, offsets, int(n_experts), int(tokens * top_k)};
   return launch_status(launch_moe_combine(rows, x_dtype, p, where, weights, tokens, int(top_k), n, out,
                                           out_dtype, as_stream(stream)));
@@ -179,7 +214,7 @@ int lora_add(const void* y, int64_t y_stride, const void* x_bf16, int64_t x_stri
   const int64_t most = int64_t(1) << 40;
   if (x_stride < k || y_stride < n || out_stride < n || x_stride > most || y_stride > most || out_stride > most)
     return QL_ESHAPE;
-  const int size = y_dtype == QL_F32 ? 4 : 2;
+  const int64_t size = bytes_of(y_dtype);
   if (x_stride * 2 % 16 || y_stride * size % 16 || out_stride * size % 16) return QL_EALIGN;
   if (rows == 0) return QL_OK;
   if (!y || !x_bf16 || !a_bf16 || !b_bf16 || !order || !offsets || !out) return QL_EINVAL;
@@ -190,6 +225,9 @@ int lora_add(const void* y, int64_t y_stride, const void* x_bf16, int64_t x_stri
   if (most_tiles(rows, adapters, 16) * ((n + 511) / 512) > (int64_t(1) << 24) - 1) return QL_ESHAPE;
   const int st = check_workspace(lora_add_workspace(rows, adapters, rank, k), workspace, workspace_bytes);
   if (st != QL_OK) return st;
+  const Rows to{out, rows, out_stride * size, n * size};
+  if (out != y && overlap(to, Rows{y, rows, y_stride * size, n * size})) return QL_EINVAL;
+  if (overlap(to, Rows{x_bf16, rows, x_stride * 2, k * 2})) return QL_EINVAL;   // x of other blocks' rows
   LoraArgs g{};
   g.plan = RowPlan{order, offsets, int(adapters), int(rows)};
   g.x = x_bf16;

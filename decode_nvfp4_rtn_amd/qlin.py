@@ -965,7 +965,9 @@ def lora_add(y, x, a, b, plan, scale=None, out=None, workspace=None, stream=None
     y [rows, n] (fp32 or bf16), x bf16 [rows, k]: a row's elements contiguous,
     rows any stride (a slice of a fused projection will do).  a bf16 [adapters,
     rank, k], b bf16 [adapters, n, rank], rank a multiple of 8 up to 128; scale
-    fp32 [adapters] (None: 1).  out: like y, y itself when not given."""
+    fp32 [adapters] (None: 1).  out: like y, y itself when not given; it shares no
+    memory with x, or with y in part (slices side by side of one buffer's rows will
+    do)."""
     dev = plan.device
     if torch._C._cuda_getDevice() != dev.index:   # the workspace goes by the device too
         with torch.cuda.device(dev):

@@ -670,7 +670,8 @@ int moe_route(const void *logits, int dtype, int64_t tokens, int64_t experts, in
  *          else p (x is in the plan's order; order may be NULL).
  * experts  n_experts blobs of W_e [n, k] from repack_weights, expert_bytes
  *          apart (a multiple of 16, at least repack_weights_bytes(...)).
- * y        out [pairs, n] in the plan's order, QL_F32 or QL_BF16.
+ * y        out [pairs, n] in the plan's order, QL_F32 or QL_BF16; shares no
+ *          bytes with x (QL_EINVAL).
  * QL_ROWS_SILU_MUL: the first n / 2 rows of W_e are a gate g, the others u,
  *          and y [pairs, n / 2] = silu(g) * u, silu(g) = g / (1 + exp(-g)), in
  *          binary32, rounded once.
@@ -695,7 +696,8 @@ int moe_gemm_w4a4(const uint8_t *a_codes, const uint8_t *a_scales, const float *
  * Back to the tokens: out[t, :] = sum_j weights[t, j] rows[where[t, j], :], in
  * binary32 and in the order of the choices.  Places from offsets[n_experts] on
  * (pairs without an expert) are not read and add nothing.
- * rows  [tokens * top_k, n] and out [tokens, n], each QL_F32 or QL_BF16.
+ * rows  [tokens * top_k, n] and out [tokens, n], each QL_F32 or QL_BF16, out
+ *       sharing no bytes with rows (QL_EINVAL).
  * Shapes: n % 8 == 0.  Errors: as the products.
  * ---------------------------------------------------------------------- */
 int moe_combine(const void *rows, int x_dtype, const int32_t *where, const int32_t *offsets,
@@ -711,7 +713,8 @@ int moe_combine(const void *rows, int x_dtype, const int32_t *where, const int32
  *
  * y, out   [rows, n] QL_F32 or QL_BF16 (y_dtype for both), rows y_stride and
  *          out_stride elements apart (slices of a fused projection will do).
- *          out may be y; otherwise they do not overlap.
+ *          out may be y; otherwise they share no bytes, and out none with x
+ *          (QL_EINVAL; slices side by side of rows of one stride will do).
  * x        [rows, k] bf16, rows x_stride apart.
  * a, b     [adapters, rank, k] and [adapters, n, rank] bf16, contiguous.
  * scale    [adapters] or NULL (1).

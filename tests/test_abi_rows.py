@@ -155,3 +155,28 @@ def test_lora(lib):
         assert run(**kw) == status, kw
     for bad in ((0, 3, 16, 256), (10, 0, 16, 256), (10, 3, 12, 256), (10, 3, 136, 256), (10, 3, 16, 100)):
         assert lib.lora_add_workspace(*bad) == 0
+
+
+MB = 1 << 20      # addresses that no call below reads
+
+
+def test_outputs_that_share_bytes_with_inputs_are_refused(lib):
+    """Refused whatever part is shared; each call has all else in order."""
+    each = lib.repack_weights_bytes(1, 256, 256)
+    for y, dt in ((64 * MB, QBF16), (64 * MB + 512, QBF16), (64 * MB - 512, QBF16), (64 * MB - 7 * 1024, QF32)):
+        assert lib.moe_gemm_w4a16(64 * MB, A, 6, each, B, C, 8, 1, 256, 256, 1, y, dt, 0) == QL_EINVAL, (y, dt)
+    each = lib.repack_weights_bytes(0, 256, 256)
+    for y in (64 * MB, 64 * MB + 128 * 7, 80 * MB + 16 * 7):
+        assert lib.moe_gemm_w4a4(64 * MB, 80 * MB, A, B, 6, each, B, C, 8, 1, 256, 256, 1, y, QBF16, 0) == QL_EINVAL
+    for out in (64 * MB, 64 * MB + 5 * 128, 64 * MB - 2 * 128):
+        assert lib.moe_combine(64 * MB, QBF16, B, C, 6, D, 3, 2, 64, out, QBF16, 0) == QL_EINVAL
+
+    def lora(y=64 * MB, ys=256, x=80 * MB, xs=256, out=64 * MB, os_=256, dt=QBF16, n=256, rows=10):
+        return lib.lora_add(y, ys, x, xs, A, B, 0, 3, 16, C, D, rows, n, 256, out, os_, dt, 0, 0, 0)
+    for kw in (dict(x=64 * MB), dict(out=80 * MB), dict(out=80 * MB + 512 * 9), dict(out=80 * MB - 512 * 9 - 16),
+               dict(out=64 * MB + 16), dict(out=64 * MB + 512), dict(out=64 * MB - 512),
+               dict(out=64 * MB, y=64 * MB + 256, n=144, ys=256),              # half a column of the same rows
+               dict(x=64 * MB + 256, xs=512, ys=512, os_=512),                 # columns 128 .. 255 are both's
+               dict(x=64 * MB + 512 + 496, xs=512, ys=512, os_=512, n=512),    # wraps into the next row
+               dict(x=64 * MB + 512, xs=264)):                                 # of two strides
+        assert lora(**kw) == QL_EINVAL, kw

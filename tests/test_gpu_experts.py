@@ -210,6 +210,17 @@ def test_layer_step_by_step(tokens, prompt):
     assert not out[tokens // 2].any()
 
 
+@pytest.mark.parametrize("prompt", [None, False, True])
+def test_layer_of_no_tokens(prompt):
+    require_gpu()
+    from decode_nvfp4_rtn_amd.experts import RoutedExperts
+    up, down = weights_of(1, 4, 128, 256)
+    layer = RoutedExperts(torch.from_numpy(up).cuda(), torch.from_numpy(down).cuda(), 2)
+    say("layer of no tokens", prompt)
+    out = layer.forward(torch.zeros((0, 256), dtype=BF, device="cuda"), torch.zeros((0, 4), device="cuda"), prompt)
+    assert out.shape == (0, 256)
+
+
 def test_graph_replays_on_other_choices():
     """One captured layer, replayed with other tokens and other experts'
     sizes; eager work through the same memory between the replays."""

@@ -282,3 +282,25 @@ def test_refusals():
                  lambda: q.lora_add(torch.zeros((6, 66), device="cuda")[:, :64], x, a, b, plan)):
         with pytest.raises(q.QlinError):
             call()
+
+
+def test_x_and_y_of_one_buffer():
+    """Slices side by side; an output that would be x is refused, since blocks
+    read rows of x that others have written."""
+    q = require_gpu()
+    for rows in (5, 300):
+        ids = np.arange(rows, dtype=np.int32) % 4 - 1
+        n, k = 128, 128
+        bits, x = bf16_rows(1, rows, k)
+        y = synth.bf16_bits_as_f32(bf16_rows(2, rows, n)[0])
+        a, b, scale = adapters_of(1, 3, 16, n, k)
+        both = torch.cat((dev_bf16(bits), on(y)), 1)
+        say("one buffer", rows)
+        plan = q.group_rows(torch.from_numpy(ids).cuda(), 3)
+        q.lora_add(both[:, k:], both[:, :k], on(a), on(b), plan, scale=on(scale, F32))
+        want, bound = bound_of(y, x, a, b, scale, ids, BF)
+        assert np.all(np.abs(host_f64(both[:, k:]) - want) <= bound)
+        assert torch.equal(both[:, :k], dev_bf16(bits))
+        for out, z in ((both[:, :n], both[:, :k]), (both[:, 64:64 + n], both[:, :k])):
+            with pytest.raises(q.QlinError):
+                q.lora_add(out, z, on(a), on(b), plan)
