@@ -145,6 +145,8 @@ int moe_gemm_w4a16(const void* x_bf16, const void* experts, int64_t n_experts, i
                    int64_t n, int64_t k, unsigned flags, void* y, int y_dtype, void* stream) {
   const int st = check_product(pairs, top_k, n_experts, expert_bytes, QL_INT4_G128, n, k, flags, y_dtype);
   if (st >= QL_OK) return st;
+  // at most a block of 1024 threads for each 32 places and 512 rows of the weights
+  if (most_tiles(pairs, n_experts, 32) * ((n + 511) / 512) >= int64_t(1) << 22) return QL_ESHAPE;
   if (!x_bf16 || !experts || !offsets || !y || (!order && (flags & QL_ROWS_GATHER))) return QL_EINVAL;
   if (!aligned16(x_bf16) || !aligned16(experts) || !aligned16(y) || !aligned(order, 4) || !aligned(offsets, 4))
     return QL_EALIGN;

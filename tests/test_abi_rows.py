@@ -180,3 +180,13 @@ def test_outputs_that_share_bytes_with_inputs_are_refused(lib):
                dict(x=64 * MB + 512 + 496, xs=512, ys=512, os_=512, n=512),    # wraps into the next row
                dict(x=64 * MB + 512, xs=264)):                                 # of two strides
         assert lora(**kw) == QL_EINVAL, kw
+
+
+def test_more_blocks_than_a_launch_has_are_refused(lib):
+    def run(pairs, n, k=4096, count=6):
+        each = lib.repack_weights_bytes(1, n, k)
+        return lib.moe_gemm_w4a16(64 * MB, A, count, each, B, C, pairs, 1, n, k, 1, 0, QBF16, 0)
+    # y is missing, which is seen only where the sizes are in order
+    for pairs, n, status in ((32 * 131072, 16384, QL_ESHAPE), (32 * 131064, 16384, QL_EINVAL),
+                             (MOST, 8 * 512, QL_ESHAPE), (MOST, 7 * 512, QL_EINVAL)):
+        assert run(pairs, n) == status, (pairs, n)
