@@ -166,7 +166,8 @@ int moe_gemm_w4a4(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
   // a row's place among the codes is a 31-bit offset
   const int64_t rows = flags & QL_ROWS_GATHER ? pairs / top_k : pairs;
   if (rows > (int64_t(1) << 32) / k - 1) return QL_ESHAPE;
-  if (most_tiles(pairs, n_experts, 64) * ((n + 255) / 256) > (int64_t(1) << 23) - 4096) return QL_ESHAPE;
+  // a block of 512 threads for each tile, and room for one more to a CU
+  if (w4a4_tiles(pairs, n_experts, n) > (int64_t(1) << 23) - 4096) return QL_ESHAPE;
   if (!a_codes || !a_scales || !a_tensor_scale || !experts || !offsets || !y ||
       (!order && (flags & QL_ROWS_GATHER)))
     return QL_EINVAL;

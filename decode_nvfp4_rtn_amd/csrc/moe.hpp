@@ -169,6 +169,15 @@ struct MoeGemm {
   void* y;
   int y_dtype;
 };
+// W4A4: places of a tile, and the tiles of 256 weight rows that a launch has blocks
+// for.  Tiles of 64 places up to 256 rows of an expert on average: 1362 rows over 8
+// experts (gate and up of 4096 x 4096) 62 us, in tiles of 256 103; 2610 over 16
+// (3840 x 1920) 53 and 77; 28000 over 128 (1536 x 2048) 244 and 252; but 9800
+// over 32 (5120 x 1280) 185 and 179.
+inline int w4a4_tall(int64_t rows, int64_t groups) { return rows <= 256 * groups ? 64 : 256; }
+inline int64_t w4a4_tiles(int64_t rows, int64_t groups, int64_t n) {
+  return most_tiles(rows, groups, w4a4_tall(rows, groups)) * ((n + 255) / 256);
+}
 hipError_t launch_moe_gemm_w4a16(const MoeGemm& g, const void* x, hipStream_t s);
 hipError_t launch_moe_gemm_w4a4(const MoeGemm& g, const uint8_t* codes, const uint8_t* scales,
                                 const float* a_ts, hipStream_t s);

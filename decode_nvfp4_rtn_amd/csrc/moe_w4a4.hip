@@ -295,8 +295,10 @@ __global__ __launch_bounds__(512, 1) void moe_w4a4_kernel(Args4 A) {
   const PlanRuns runs(A.plan);
   auto fulls = [](int, GroupRun run) { return (run.end - run.first) / TALL; };
   auto ends = [](int, GroupRun run) { return (run.end - run.first) % TALL ? 1 : 0; };
-  const int full_m = count_tiles(runs, fulls);
-  const int full = full_m * tiles_n, total = full + count_tiles(runs, ends) * tiles_n;
+  // no plan has more than these, whatever the offsets hold
+  const int full_m = min(count_tiles(runs, fulls), A.plan.rows / TALL);
+  const int end_m = min(count_tiles(runs, ends), A.plan.groups + 1);
+  const int full = full_m * tiles_n, total = full + end_m * tiles_n;
   const int whole = total / A.cus * A.cus, rest = total - whole;
   const int cut = 4 * rest <= A.cus ? 4 : 2 * rest <= A.cus ? 2 : 1;
   int t = blockIdx.x, part = 0, parts = 1;
@@ -578,37 +580,35 @@ hipError_t launch_moe_gemm_w4a4(const MoeGemm& g, const uint8_t* codes, const ui
   a.gather = g.gather;
   a.n = g.n;
   a.k = g.k;
-  const int64_t wide = (g.n + WIDE - 1) / WIDE;
+  static_assert(TALL == 256 && WIDE == 256, "as w4a4_tall and w4a4_tiles count them");
+  const int tall = w4a4_tall(g.plan.rows, g.plan.groups);
+  const int64_t tiles = w4a4_tiles(g.plan.rows, g.plan.groups, g.n);
   static std::atomic<int> done[8][64];
   const int cus = device_cu_count();
   a.cus = cus > 0 ? cus : 256;
-  auto run = [&](auto kern, std::atomic<int>* flag, int tall, size_t lds) {
+  auto run = [&](auto kern, std::atomic<int>* flag, size_t lds) {
     const hipError_t e = lds_limit_once(flag, reinterpret_cast<const void*>(kern), int(lds));
     if (e != hipSuccess) return e;
-    // with room for a last round of parts of tiles
-    const int64_t blocks = most_tiles(g.plan.rows, g.plan.groups, tall) * wide + (tall == TALL ? a.cus : 0);
+    // tiles of 256 places: with room for a last round of parts of tiles
+    const int64_t blocks = tiles + (tall == TALL ? a.cus : 0);
     kern<<<unsigned(blocks), 512, lds, s>>>(a);
     return hipGetLastError();
   };
   const bool bf16 = g.y_dtype == 1;
-  // Tiles of 64 places up to 256 rows of an expert on average: 1362 rows over 8
-  // experts (gate and up of 4096 x 4096) 62 us, in tiles of 256 103; 2610 over 16
-  // (3840 x 1920) 53 and 77; 28000 over 128 (1536 x 2048) 244 and 252; but 9800
-  // over 32 (5120 x 1280) 185 and 179.
-  if (g.plan.rows <= 256 * int64_t(g.plan.groups)) {
+  if (tall < TALL) {
     constexpr size_t lds = low_bytes(4);
     if (g.silu_mul)
-      return bf16 ? run(moe_w4a4_low_kernel<true, true>, done[4], 64, lds)
-                  : run(moe_w4a4_low_kernel<true, false>, done[5], 64, lds);
-    return bf16 ? run(moe_w4a4_low_kernel<false, true>, done[6], 64, lds)
-                : run(moe_w4a4_low_kernel<false, false>, done[7], 64, lds);
+      return bf16 ? run(moe_w4a4_low_kernel<true, true>, done[4], lds)
+                  : run(moe_w4a4_low_kernel<true, false>, done[5], lds);
+    return bf16 ? run(moe_w4a4_low_kernel<false, true>, done[6], lds)
+                : run(moe_w4a4_low_kernel<false, false>, done[7], lds);
   }
   constexpr size_t lds = 2 * 2 * TILE_BYTES;
   if (g.silu_mul)
-    return bf16 ? run(moe_w4a4_kernel<true, true>, done[0], TALL, lds)
-                : run(moe_w4a4_kernel<true, false>, done[1], TALL, lds);
-  return bf16 ? run(moe_w4a4_kernel<false, true>, done[2], TALL, lds)
-              : run(moe_w4a4_kernel<false, false>, done[3], TALL, lds);
+    return bf16 ? run(moe_w4a4_kernel<true, true>, done[0], lds)
+                : run(moe_w4a4_kernel<true, false>, done[1], lds);
+  return bf16 ? run(moe_w4a4_kernel<false, true>, done[2], lds)
+              : run(moe_w4a4_kernel<false, false>, done[3], lds);
 }
 
 }  // namespace qlin

@@ -677,7 +677,9 @@ int moe_route(const void *logits, int dtype, int64_t tokens, int64_t experts, in
  *          binary32, rounded once.
  * Rows of y of pairs without an expert are set to zero.
  * Shapes: n % 16 == 0 (n % 32 with QL_ROWS_SILU_MUL), k % 128 == 0, n * k <=
- * 2^31; W4A4: fewer than 2^32 / k rows of x; W4A16: (pairs / 32 + n_experts + 1)
+ * 2^31; W4A4: fewer than 2^32 / k rows of x, and (pairs / T + n_experts + 1)
+ * (n / 256, rounded up) at most 2^23 - 4096, T = 64 up to 256 pairs an expert
+ * (pairs <= 256 n_experts), else 256; W4A16: (pairs / 32 + n_experts + 1)
  * (n / 512, rounded up) below 2^22.  A blob that is not of this
  * format and (n, k) leaves its expert's rows untouched.
  * Errors: QL_EINVAL, QL_ESHAPE, QL_EALIGN, QL_EDTYPE, QL_EWORKSPACE

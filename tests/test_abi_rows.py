@@ -190,3 +190,18 @@ def test_more_blocks_than_a_launch_has_are_refused(lib):
     for pairs, n, status in ((32 * 131072, 16384, QL_ESHAPE), (32 * 131064, 16384, QL_EINVAL),
                              (MOST, 8 * 512, QL_ESHAPE), (MOST, 7 * 512, QL_EINVAL)):
         assert run(pairs, n) == status, (pairs, n)
+
+
+def test_w4a4_blocks_are_those_of_the_launch(lib):
+    """Tiles of 64 places up to 256 rows of an expert on average, of 256 above."""
+    def run(pairs, n, k=128, count=6, y=0):
+        each = lib.repack_weights_bytes(0, n, k)
+        return lib.moe_gemm_w4a4(64 * MB, A, B, A, count, each, C, D, pairs, 1, n, k, 1, y, QBF16, 0)
+    # y is missing, which is seen only where the sizes are in order
+    for pairs, n, count, status in ((MOST, 127 * 256, 6, QL_EINVAL), (MOST, 128 * 256, 6, QL_ESHAPE),
+                                    (1 << 22, 32768, 6, QL_EINVAL), (1 << 22, 511 * 256, 6, QL_EINVAL),
+                                    (1 << 22, 512 * 256, 6, QL_ESHAPE),
+                                    (256 * 1024, 1637 * 256, 1024, QL_EINVAL),
+                                    (256 * 1024, 1638 * 256, 1024, QL_ESHAPE),
+                                    (256 * 1024 + 1, 4000 * 256, 1024, QL_EINVAL)):
+        assert run(pairs, n, count=count) == status, (pairs, n, count)

@@ -163,3 +163,26 @@ def test_w4a16_sums_within_a_group_are_exact(tokens, k):
         size += np.abs(part)
     steps = 1 if groups == 1 else groups + 8
     check(y, ref, steps * 2.0 ** -24 * size)
+
+
+def test_as_many_tiles_as_a_launch_has():
+    """2^21 tiles of 256 x 256, an output of 128 GiB: its first, middle and last rows."""
+    q = require_gpu()
+    n, k, pairs, base = 32768, 128, 1 << 22, 1024
+    if torch.cuda.mem_get_info()[0] < 140 << 30:
+        pytest.skip("needs 140 GiB of GPU memory")
+    stack = Stack(q, "nvfp4", 12, 2, n, k)
+    (codes, scales, ts), values = operand(q, "nvfp4", bf16_rows(5, base, k)[0])
+    ids = torch.zeros(pairs, dtype=torch.int32, device="cuda")
+    ids[-500:] = 1
+    say("128 GiB")
+    plan = q.group_rows(ids, 2)
+    y = q.moe_gemm_w4a4(codes.repeat(pairs // base, 1), scales.repeat(pairs // base, 1), ts, stack.blobs, plan, n, k,
+                        silu_mul=True)
+    assert y.numel() == 1 << 36
+    for first, e in ((0, 0), (pairs // 2 + 77, 0), (pairs - 700, 0), (pairs - 100, 1)):
+        at = np.arange(first, first + 100)
+        ref = values[at % base] @ stack.values[e].T
+        check(y[first:first + 100], *silu_bound(ref[:, :n // 2], ref[:, n // 2:], BF), first)
+    del y
+    torch.cuda.empty_cache()
