@@ -18,6 +18,7 @@ hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 constexpr int64_t kMostRows = (int64_t(1) << 24) - 1;   // a launch has fewer than 2^32 threads
 constexpr int64_t kMostTopK = 64;
+constexpr int64_t kMostSpan = int64_t(1) << 47;          // bytes of strided rows: no address space has more
 
 bool dtype_ok(int d) { return d == QL_F32 || d == QL_BF16; }
 
@@ -214,10 +215,11 @@ int lora_add(const void* y, int64_t y_stride, const void* x_bf16, int64_t x_stri
   if (!dtype_ok(y_dtype)) return QL_EDTYPE;
   if (!groups_ok(adapters) || rank < 8 || rank > 128 || rank % 8 || rows > kMostRows) return QL_ESHAPE;
   if (n == 0 || k == 0 || n % 16 || k % 128 || n > (int64_t(1) << 24) || k > (int64_t(1) << 20)) return QL_ESHAPE;
-  const int64_t most = int64_t(1) << 40;
-  if (x_stride < k || y_stride < n || out_stride < n || x_stride > most || y_stride > most || out_stride > most)
-    return QL_ESHAPE;
   const int64_t size = bytes_of(y_dtype);
+  const int64_t most = kMostSpan / (rows ? rows : 1);   // bytes between rows
+  if (x_stride < k || y_stride < n || out_stride < n || x_stride > most / 2 || y_stride > most / size ||
+      out_stride > most / size)
+    return QL_ESHAPE;
   if (x_stride * 2 % 16 || y_stride * size % 16 || out_stride * size % 16) return QL_EALIGN;
   if (rows == 0) return QL_OK;
   if (!y || !x_bf16 || !a_bf16 || !b_bf16 || !order || !offsets || !out) return QL_EINVAL;
@@ -225,7 +227,6 @@ int lora_add(const void* y, int64_t y_stride, const void* x_bf16, int64_t x_stri
       !aligned(scale, 4) || !aligned(order, 4) || !aligned(offsets, 4))
     return QL_EALIGN;
   if (out == y && out_stride != y_stride) return QL_EINVAL;
-  if (most_tiles(rows, adapters, 16) * ((n + 511) / 512) > (int64_t(1) << 24) - 1) return QL_ESHAPE;
   const int st = check_workspace(lora_add_workspace(rows, adapters, rank, k), workspace, workspace_bytes);
   if (st != QL_OK) return st;
   const Rows to{out, rows, out_stride * size, n * size};

@@ -726,7 +726,8 @@ int moe_combine(const void *rows, int x_dtype, const int32_t *where, const int32
  *          aligned, not read before it is written; calls that share one must be
  *          ordered.
  * Shapes: n % 16 == 0, k % 128 == 0, rank a multiple of 8 up to 128 (smaller
- * ranks: padded with zeros).  Row strides are multiples of 16 bytes.
+ * ranks: padded with zeros).  Row strides are multiples of 16 bytes; rows times
+ * a stride is at most 2^47 bytes.
  * Errors: QL_EINVAL, QL_ESHAPE, QL_EALIGN, QL_EDTYPE, QL_EWORKSPACE, QL_EHIP.
  * ---------------------------------------------------------------------- */
 size_t lora_add_workspace(int64_t rows, int64_t adapters, int64_t rank, int64_t k);

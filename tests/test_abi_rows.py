@@ -205,3 +205,21 @@ def test_w4a4_blocks_are_those_of_the_launch(lib):
                                     (256 * 1024, 1638 * 256, 1024, QL_ESHAPE),
                                     (256 * 1024 + 1, 4000 * 256, 1024, QL_EINVAL)):
         assert run(pairs, n, count=count) == status, (pairs, n, count)
+
+
+def test_lora_sizes_are_those_of_memory(lib):
+    """What a call's rows span is limited (2^47 bytes), not the blocks of a launch."""
+    def run(rows, n=64, xs=128, ys=None, os_=None, dt=QBF16):
+        ys = n if ys is None else ys
+        return lib.lora_add(A, ys, B, xs, C, D, 0, 3, 16, E, A, rows, n, 128, 1 << 50, os_ or ys, dt, 1 << 49, 0, 0)
+    # the workspace is too small, which is seen only where the sizes are in order
+    for rows, kw, status in ((1 << 22, dict(n=32768), QL_EWORKSPACE), (MOST, dict(n=16384), QL_EWORKSPACE),
+                             (MOST, dict(n=1 << 24), QL_ESHAPE),
+                             (1 << 20, dict(xs=1 << 26), QL_EWORKSPACE), (1 << 20, dict(xs=(1 << 26) + 8), QL_ESHAPE),
+                             (1 << 20, dict(ys=1 << 26), QL_EWORKSPACE), (1 << 20, dict(ys=(1 << 26) + 8), QL_ESHAPE),
+                             (1 << 20, dict(ys=1 << 25, dt=QF32), QL_EWORKSPACE),
+                             (1 << 20, dict(ys=(1 << 25) + 4, dt=QF32), QL_ESHAPE),
+                             (1 << 20, dict(os_=(1 << 26) + 8), QL_ESHAPE),
+                             (MOST, dict(xs=1 << 40), QL_ESHAPE), (MOST, dict(ys=1 << 40), QL_ESHAPE),
+                             (1 << 20, dict(xs=1 << 62), QL_ESHAPE)):
+        assert run(rows, **kw) == status, (rows, kw)
