@@ -72,6 +72,13 @@ Rows whole(const void* at, int64_t rows, int64_t width) { return Rows{at, rows, 
 
 int64_t bytes_of(int dtype) { return dtype == QL_F32 ? 4 : 2; }
 
+// Whether a plan's arrays share bytes with what the plan is made from.
+bool plan_over(const Rows& from, const int32_t* order, const int32_t* where, const int32_t* offsets,
+               int64_t rows, int64_t groups) {
+  return overlap(whole(order, 1, 4 * rows), from) || overlap(whole(where, 1, 4 * rows), from) ||
+         overlap(whole(offsets, 1, 4 * (groups + 1)), from);
+}
+
 // The rows that a product writes.
 Rows written(int64_t pairs, int64_t n, unsigned flags, const void* y, int y_dtype) {
   return whole(y, pairs, (flags & QL_ROWS_SILU_MUL ? n / 2 : n) * bytes_of(y_dtype));
@@ -111,6 +118,7 @@ int group_rows(const int32_t* ids, int64_t rows, int64_t groups, int32_t* order,
   if (!aligned(ids, 4) || !aligned(order, 4) || !aligned(where, 4) || !aligned(offsets, 4)) return QL_EALIGN;
   const int st = check_workspace(group_rows_workspace(rows, groups), workspace, workspace_bytes);
   if (st != QL_OK) return st;
+  if (rows && plan_over(whole(ids, 1, 4 * rows), order, where, offsets, rows, groups)) return QL_EINVAL;
   return launch_status(launch_group_rows(ids, rows, int(groups), order, where, offsets,
                                          static_cast<int32_t*>(workspace), as_stream(stream)));
 }
@@ -136,6 +144,13 @@ int moe_route(const void* logits, int dtype, int64_t tokens, int64_t experts, in
     return QL_EALIGN;
   const int st = check_workspace(moe_route_workspace(tokens, experts, top_k), workspace, workspace_bytes);
   if (st != QL_OK) return st;
+  if (tokens) {
+    const int64_t size = bytes_of(dtype), pairs = tokens * top_k;
+    const Rows from{logits, tokens, row_stride * size, experts * size};
+    if (overlap(whole(ids, 1, 4 * pairs), from) || overlap(whole(weights, 1, 4 * pairs), from) ||
+        plan_over(from, order, where, offsets, pairs, experts))
+      return QL_EINVAL;
+  }
   return launch_status(launch_moe_route(logits, dtype, tokens, int(experts), row_stride, int(top_k),
                                         (flags & QL_ROUTE_RENORMALIZE) != 0, ids, weights, order, where,
                                         offsets, static_cast<int32_t*>(workspace), as_stream(stream)));

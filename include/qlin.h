@@ -628,6 +628,7 @@ int kv_commit(const ql_kv_cache *cache, int64_t n_seqs, const int32_t *cu_q,
 /* ------------------------------------------------------------------------
  * The plan of given choices (the adapter of each row).
  * ids   [rows]: the row's group; outside of 0 .. groups - 1: none.
+ * The plan's arrays share no bytes with ids (QL_EINVAL).
  * rows == 0 writes offsets of zero.  workspace: group_rows_workspace(rows,
  * groups) bytes, 16-byte aligned (0: may be NULL), not read before it is
  * written; calls that share one must be ordered.
@@ -650,7 +651,8 @@ int group_rows(const int32_t *ids, int64_t rows, int64_t groups, int32_t *order,
  *
  * logits   [tokens, experts] QL_F32 or QL_BF16, rows row_stride elements apart.
  * ids, weights  out [tokens, top_k].
- * order, where, offsets  out: the plan of tokens * top_k pairs.
+ * order, where, offsets  out: the plan of tokens * top_k pairs.  No output shares
+ *          bytes with the logits (QL_EINVAL).
  * workspace as group_rows.  Errors: as group_rows, and QL_EDTYPE.
  * ---------------------------------------------------------------------- */
 #define QL_ROUTE_RENORMALIZE 1u

@@ -223,3 +223,20 @@ def test_lora_sizes_are_those_of_memory(lib):
                              (MOST, dict(xs=1 << 40), QL_ESHAPE), (MOST, dict(ys=1 << 40), QL_ESHAPE),
                              (1 << 20, dict(xs=1 << 62), QL_ESHAPE)):
         assert run(rows, **kw) == status, (rows, kw)
+
+
+def test_plans_written_over_their_input_are_refused(lib):
+    """Blocks read choices, and logits, that other blocks would have written over."""
+    def group(order=2 * MB, where=3 * MB, offsets=4 * MB, rows=1000):
+        return lib.group_rows(MB, rows, 7, order, where, offsets, 0, 0, 0)
+    for kw in (dict(order=MB), dict(order=MB + 3996), dict(order=MB - 3996), dict(where=MB), dict(where=MB + 4),
+               dict(offsets=MB + 400), dict(offsets=MB - 28)):
+        assert group(**kw) == QL_EINVAL, kw
+
+    def route(ids=2 * MB, weights=3 * MB, order=4 * MB, where=5 * MB, offsets=6 * MB, dt=QF32, stride=100):
+        return lib.moe_route(MB, dt, 50, 100, stride, 4, 1, ids, weights, order, where, offsets, 0, 0, 0)
+    end = MB + 4 * (49 * 100 + 100)
+    for kw in (dict(ids=MB), dict(weights=MB), dict(weights=end - 4), dict(order=MB + 8), dict(where=MB - 796),
+               dict(offsets=MB + 4000), dict(offsets=MB - 400), dict(ids=end, stride=101),
+               dict(dt=QBF16, weights=MB + 2 * (49 * 100 + 98))):
+        assert route(**kw) == QL_EINVAL, kw
