@@ -42,6 +42,19 @@ class Step:
     tree: torch.Tensor
     prompt: list = None
 
+    def runs(self):
+        """(of prompts, rows) of each run of sequences of one kind, in order; None
+        where the step does not say."""
+        if self.prompt is None:
+            return None
+        runs = []
+        for p, n in zip(self.prompt, self.nodes):
+            if n and runs and runs[-1][0] == p:
+                runs[-1] = (p, runs[-1][1] + n)
+            elif n:
+                runs.append((p, n))
+        return runs
+
 
 class PagedSequences:
     """Sequences over the pages of a cache.  A sequence keeps its pages until
@@ -155,14 +168,9 @@ class PagedAttention:
     def project_step(self, x, which, step):
         """The same for a step's rows, each by its sequence's kind: one call for
         every run of sequences of one kind."""
-        if step.prompt is None:
+        runs = step.runs()
+        if runs is None:
             return self.project(x, which)
-        runs = []                                # [of a prompt, rows]
-        for p, n in zip(step.prompt, step.nodes):
-            if n and runs and runs[-1][0] == p:
-                runs[-1][1] += n
-            elif n:
-                runs.append([p, n])
         if len(runs) < 2:
             return self.project(x, which, runs[0][0] if runs else False)
         y = torch.empty((x.shape[0], self.weights[which][2]), dtype=torch.bfloat16, device=x.device)

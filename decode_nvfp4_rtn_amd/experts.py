@@ -54,17 +54,38 @@ class RoutedExperts:
             return qlin.moe_gemm_w4a4(*qlin.quantize_nvfp4(x), many, plan, n, k, gather=up, silu_mul=up)
         return qlin.moe_gemm_w4a16(x, few, plan, n, k, gather=up, silu_mul=up)
 
-    def forward(self, x, logits, prompt=None):
+    def forward(self, x, logits, prompt=None, step=None):
         """x bf16 [tokens, hidden] and the router's logits [tokens, experts] (an
         expert at -infinity is not chosen; a token that may choose none gets
         zeros) -> bf16 [tokens, hidden].  prompt: whether these are tokens of
         prompts (NVFP4 weights and activations, these under one tensor scale for
-        all rows of a product) or of decoding (INT4 weights); not told: by their
-        number."""
+        all rows of a product) or of decoding (INT4 weights).  step: instead, the
+        attention.Step whose new tokens they are, each sequence's by its kind, with
+        the calls made for every run of sequences of one kind.  Neither told: by
+        their number."""
         if logits.shape[1] != self.experts or logits.shape[0] != x.shape[0]:
             raise ValueError(f"logits must be [{x.shape[0]}, {self.experts}], got {list(logits.shape)}")
-        if prompt is None:
+        runs = None
+        if step is not None:
+            if prompt is not None or sum(step.nodes) != x.shape[0]:
+                raise ValueError(f"a step of {sum(step.nodes)} new tokens takes as many rows, got {x.shape[0]}, "
+                                 f"and no prompt")
+            runs = step.runs()
+        if runs is not None and len(runs) < 2:
+            prompt = runs[0][0] if runs else False
+        elif runs is not None:
+            out = torch.empty((x.shape[0], self.hidden), dtype=torch.bfloat16, device=x.device)
+            at = 0
+            for kind, n in runs:
+                self._rows(x[at:at + n], logits[at:at + n], kind, out[at:at + n])
+                at += n
+            return out
+        elif prompt is None:
             prompt = x.shape[0] > DECODE_TOKENS
+        return self._rows(x, logits, prompt)
+
+    def _rows(self, x, logits, prompt, out=None):
+        """The layer of rows of one kind."""
         _, weights, plan = qlin.moe_route(logits, self.top_k, self.renormalize)
         h = self.product(x, 0, plan, prompt)
-        return qlin.moe_combine(self.product(h, 1, plan, prompt), plan, weights)
+        return qlin.moe_combine(self.product(h, 1, plan, prompt), plan, weights, out)

@@ -17,3 +17,16 @@ def test_kind_of_a_steps_tokens():
     with pytest.raises(ValueError):
         p.step([a, b], [3, 1], prompt=[True])
     assert p.step([], []).prompt == []
+
+
+def test_runs_of_a_step():
+    p = PagedSequences(40, 16, device="cpu")
+    seqs = [p.add() for _ in range(5)]
+    p.settle(seqs[:4], [1] * 4)
+    step = p.step(seqs, [1, 1, 20, 0, 3])
+    assert step.prompt == [False, False, True, False, True]
+    assert step.runs() == [(False, 2), (True, 23)]          # a sequence without tokens parts no run
+    assert p.step(seqs, [1, 9, 1, 1, 0]).runs() == [(False, 1), (True, 9), (False, 2)]
+    assert p.step([], []).runs() == [] == p.step(seqs[:2], [0, 0]).runs()
+    step.prompt = None
+    assert step.runs() is None
