@@ -31,11 +31,12 @@ class RoutedExperts:
         self.experts, self.top_k, self.renormalize = experts, top_k, renormalize
         self.hidden, self.inter = hidden, rows // 2
         self.weights = []
-        for w in (up, down):
-            n, k = w.shape[1:]
-            few = self._stack(w, qlin.QL_INT4_G128, qlin.quantize_int4_g128)
-            many = self._stack(w, qlin.QL_NVFP4, qlin.quantize_nvfp4)
-            self.weights.append((few, many, n, k))
+        with torch.cuda.device(up.device):     # the quantizers go by the current device
+            for w in (up, down):
+                n, k = w.shape[1:]
+                few = self._stack(w, qlin.QL_INT4_G128, qlin.quantize_int4_g128)
+                many = self._stack(w, qlin.QL_NVFP4, qlin.quantize_nvfp4)
+                self.weights.append((few, many, n, k))
 
     def _stack(self, w, fmt, quantize):
         n, k = w.shape[1:]
@@ -63,6 +64,9 @@ class RoutedExperts:
         attention.Step whose new tokens they are, each sequence's by its kind, with
         the calls made for every run of sequences of one kind.  Neither told: by
         their number."""
+        if torch._C._cuda_getDevice() != x.device.index:   # the quantizer goes by the current device
+            with torch.cuda.device(x.device):
+                return self.forward(x, logits, prompt, step)
         if logits.shape[1] != self.experts or logits.shape[0] != x.shape[0]:
             raise ValueError(f"logits must be [{x.shape[0]}, {self.experts}], got {list(logits.shape)}")
         runs = None
