@@ -105,12 +105,11 @@ __global__ __launch_bounds__(waves_of(MT) * 64, 4) void moe_w4a16_kernel(Args16 
   const uint8_t* codes = blob + A.codes_off;
   const uint8_t* scales = blob + A.sc_off;
 
-  // units of this wave: u0, u0 + step, ...
+  // units of this wave: u0, u0 + step, ...; one at most where x comes in pieces, as
+  // where waves share k
   const int u0 = KS > 1 ? walker * (WAVES / KS) + wave / KS : walker * WAVES + wave;
   const int step = A.walkers * WAVES;
   const int mine = u0 < units ? KS > 1 ? 1 : (units - u0 + step - 1) / step : 0;
-  const bool once = A.chunk >= G;            // all of x fits
-  const int span = once ? mine : 1;          // units in a row over one piece of x
 
   struct Batch {
     uint4 w[W][NT];
@@ -253,41 +252,38 @@ __global__ __launch_bounds__(waves_of(MT) * 64, 4) void moe_w4a16_kernel(Args16 
   const uint32_t hdr = header_word(blob);   // tested before the first store
   bool ok = false;
   clear();
-  const int most = KS > 1 ? 1 : (units + step - 1) / step;   // units of the block's first wave, at least
-  for (int rd = 0; rd < (once ? 1 : most); ++rd) {
-    for (int c0 = 0; c0 < G; c0 += A.chunk) {
-      const int c1 = min(c0 + A.chunk, G);
-      // this wave's part of the piece
-      const int ga = KS > 1 ? c0 + (c1 - c0) * (wave % KS) / KS : c0;
-      const int gb = KS > 1 ? c0 + (c1 - c0) * (wave % KS + 1) / KS : c1;
-      const bool busy = rd < mine && ga < gb;
-      int u = u0 + rd * step, g = ga;           // what P holds
-      const int u_end = u0 + (rd + span) * step;
-      if (busy) load(P, u, g, gb);
-      if (rd + c0 > 0) __syncthreads();         // the piece before is read
-      stage(c0, c1);
-      __syncthreads();
-      if (rd + c0 == 0) ok = header_word_ok(hdr, 1, A.n, A.k);
-      if (!busy) continue;
-      // steps of W groups, the next one's loads under way, over tiles' ends
-      auto walk = [&](const Batch& now, Batch& next) {
-        int nu = u, ng = g + W;
-        if (ng >= gb) nu += step, ng = ga;
-        load(next, min(nu, u_end - step), ng, gb);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(now, g, gb, c0);
-        if (ng == ga && KS == 1 && c1 == G) {
-          if (ok) finish(u);
-          clear();
-        }
-        u = nu;
-        g = ng;
-      };
-      while (u < u_end) {
-        walk(P, Q);
-        if (u >= u_end) break;
-        walk(Q, P);
+  const int u_end = u0 + mine * step;
+  for (int c0 = 0; c0 < G; c0 += A.chunk) {
+    const int c1 = min(c0 + A.chunk, G);
+    // this wave's part of the piece
+    const int ga = KS > 1 ? c0 + (c1 - c0) * (wave % KS) / KS : c0;
+    const int gb = KS > 1 ? c0 + (c1 - c0) * (wave % KS + 1) / KS : c1;
+    const bool busy = mine > 0 && ga < gb;
+    int u = u0, g = ga;                       // what P holds
+    if (busy) load(P, u, g, gb);
+    if (c0 > 0) __syncthreads();              // the piece before is read
+    stage(c0, c1);
+    __syncthreads();
+    if (c0 == 0) ok = header_word_ok(hdr, 1, A.n, A.k);
+    if (!busy) continue;
+    // steps of W groups, the next one's loads under way, over tiles' ends
+    auto walk = [&](const Batch& now, Batch& next) {
+      int nu = u, ng = g + W;
+      if (ng >= gb) nu += step, ng = ga;
+      load(next, min(nu, u_end - step), ng, gb);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(now, g, gb, c0);
+      if (ng == ga && KS == 1 && c1 == G) {
+        if (ok) finish(u);
+        clear();
       }
+      u = nu;
+      g = ng;
+    };
+    while (u < u_end) {
+      walk(P, Q);
+      if (u >= u_end) break;
+      walk(Q, P);
     }
   }
   if constexpr (KS > 1) {
