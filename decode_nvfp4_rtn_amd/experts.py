@@ -60,7 +60,8 @@ class RoutedExperts:
         expert at -infinity is not chosen; a token that may choose none gets
         zeros) -> bf16 [tokens, hidden].  prompt: whether these are tokens of
         prompts (NVFP4 weights and activations, these under one tensor scale for
-        all rows of a product) or of decoding (INT4 weights).  step: instead, the
+        all rows of a product, so that rows of tokens without an expert have to be
+        finite too) or of decoding (INT4 weights).  step: instead, the
         attention.Step whose new tokens they are, each sequence's by its kind, with
         the calls made for every run of sequences of one kind.  Neither told: by
         their number."""

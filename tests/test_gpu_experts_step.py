@@ -73,3 +73,16 @@ def test_refusals():
                  lambda: layer.forward(x[:4], logits[:4], step=step), lambda: layer.forward(x, logits[:4])):
         with pytest.raises(ValueError):
             call()
+
+
+def test_tokens_without_experts_may_hold_anything_when_decoding():
+    """Masked tokens' rows of NaN and infinities reach no other token."""
+    layer, step, x, logits = layer_and_step([1] * 40, [5] * 40)
+    say("masked rows")
+    masked = torch.arange(40, device="cuda") % 3 == 1
+    logits[masked] = float("-inf")
+    want = layer.forward(x, logits, step=step)
+    x[masked] = float("nan")
+    x[1] = float("inf")
+    out = layer.forward(x, logits, step=step)
+    assert torch.equal(out, want) and not out[masked].any() and out[~masked].any(1).all()
