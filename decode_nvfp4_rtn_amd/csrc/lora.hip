@@ -21,8 +21,8 @@
 // bits of mantissa or more), three beside a binary32 one (all of it): that
 // product is bound by reading y and writing out, so they cost nothing that shows.
 //
-// 64 tokens over 32 adapters of rank 16 beside 6144 x 4096: 9.2 us, one block's
-// chain.  8190 tokens over 8 adapters of rank 64 beside 7168 x 5120: 28 us down (84
+// 64 tokens over 32 adapters of rank 16 beside 6144 x 4096: 9.2 us (10.5 with all of
+// it from memory), one block's chain.  8190 tokens over 8 adapters of rank 64 beside 7168 x 5120: 28 us down (84
 // MB of x at 3 TB/s) and 64 up (235 MB of y and out at 3.6 TB/s).
 //
 // Rows without an adapter come last in the plan: they are copied, or left
@@ -485,8 +485,11 @@ int cus_or(int otherwise) {
   return cus > 0 ? cus : otherwise;
 }
 
-// Adapters of few rows, less than 48 on average: one launch, which makes u again
-// for each part of the columns.  It pays up to a rank of 32 (64 tokens over 32
+// Adapters of few rows, less than 48 on average over all that the call is given, met
+// or not (how many are met only the device knows): one launch, which makes u again
+// for each part of the columns.  Of long runs it reads A and B again for every 16
+// rows: 8000 rows over 8 adapters of rank 16 beside 7168 x 5120 take 84 us where the
+// call is given 200 adapters, and 72 - 74 in two launches where it is given up to 100.  It pays up to a rank of 32 (64 tokens over 32
 // adapters of rank 16 beside 6144 x 4096: 9 us, in two launches 13; 18 tokens
 // over 60 of rank 64: 20 and 15).
 bool few_rows(int64_t rows, int64_t groups, int rank) { return rank <= 32 && rows < 48 * groups; }

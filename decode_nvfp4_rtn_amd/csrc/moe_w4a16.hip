@@ -24,8 +24,9 @@
 // order.
 //
 // 48 tokens that choose 8 of 128 experts of 2048 x 768: 19.7 us, 94.6 MB at 4.8
-// TB/s.  One token and 8 experts of 2048 x 4096: 10.2 us, 34.6 MB; a launch's
-// start and one wave's chain are half of it.  509 tokens, 4 of 60 experts of
+// TB/s, on weights that the Infinity Cache may hold; 23.9 us, 4.0 TB/s, on weights
+// that it does not.  One token and 8 experts of 2048 x 4096: 10.2 us (11.4), 34.6 MB;
+// a launch's start and one wave's chain are half of it.  509 tokens, 4 of 60 experts of
 // 2816 x 2048 (34 rows each): 55 us, 186 MB at 3.4 TB/s; experts of more than 32
 // rows have a second tile on another XCD, whose weights come past its L2 again
 // (284 MB in all, 5.1 TB/s).

@@ -32,11 +32,13 @@
 // Few rows of an expert: a second kernel, tiles of 64 places, weights from memory
 // to registers (below).
 //
-// 8192 tokens, 8 of 64 experts of 2048 x 4096: 977 us, 1125 TFLOP/s (the dense
-// kernel's rate for a tile; runs padded to whole 64s are 12 % of the products).
-// 4095 tokens, 2 of 8 experts of 4096 x 2048: 147 us, 933 TFLOP/s in 2.3 rounds of
-// tiles.  1000 tokens, 4 of 60 experts of 2816 x 2048, by the second kernel: 71 us,
-// 207 MB at 2.9 TB/s and 580 TFLOP/s; the first took 139.
+// 8192 tokens, 8 of 64 experts of 2048 x 4096: 977 - 995 us, 1105 - 1125 TFLOP/s
+// (the dense kernel's rate for a tile; runs padded to whole 64s are 12 % of the
+// products).  4095 tokens, 2 of 8 experts of 4096 x 2048: 147 - 153 us, 900 - 933
+// TFLOP/s in 2.3 rounds of tiles.  1000 tokens, 4 of 60 experts of 2816 x 2048, by the
+// second kernel: 71 - 75 us, 207 MB at 2.8 - 2.9 TB/s and 550 - 580 TFLOP/s (85 us on
+// weights that the Infinity Cache does not hold); the first took 139.  313 MB come past
+// the L2s: an expert's weights once for each of its tiles.
 #include "moe.hpp"
 #include "w4a4_ops.hpp"
 
